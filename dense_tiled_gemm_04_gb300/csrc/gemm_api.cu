@@ -14,21 +14,19 @@
 #include <vector>
 
 #include "gemm.h"
+#include "host/handle.cuh"
 #include "kernel_set.cuh"
 
 namespace {
 
 using dtg::KernelChoice;
 using dtg::KernelParams;
+using namespace dtg::host;
 
 constexpr int64_t kGroupPanelBytes = 48ll << 20;  // automatic raster group: A bytes of a group's tile rows
 constexpr int64_t kMaxAutoGroup = 16;             // and at most this many tile rows
-constexpr int64_t kTimeoutDefaultNs = 2000000000LL;  // 2 s per wait
 constexpr int kTmapCacheMax = 64;
 constexpr int32_t kTmapBytes = -1;  // get_tmap element type: raw bytes (side data)
-constexpr int kNumSlots = 96;  // 4 configurations x 12 operand/output types x 2 layouts
-constexpr int64_t kMinStreamKBlocks = 8;   // default shortest stream-K share (GEMM_OPT_SK_MIN_BLOCKS)
-constexpr int64_t kMinSplitBlocks = 32;    // default shortest share of a split under one wave (GEMM_OPT_SPLIT_MIN_BLOCKS)
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -46,19 +44,6 @@ bool load_encode_fn()
     return g_encode != nullptr;
 }
 
-struct TmapKey {
-    const void* ptr;
-    uint64_t inner, outer, pitch_bytes;
-    uint32_t box_inner, box_outer;
-    int32_t dtype;
-    int32_t swizzle;
-    bool operator==(const TmapKey& o) const
-    {
-        return ptr == o.ptr && inner == o.inner && outer == o.outer && pitch_bytes == o.pitch_bytes &&
-               box_inner == o.box_inner && box_outer == o.box_outer && dtype == o.dtype && swizzle == o.swizzle;
-    }
-};
-
 // Epilogue of a launch: C = alpha * A·B + beta * C, C row-major or column-major, of
 // type `out` (< 0: the operand type).
 struct Epilogue {
@@ -71,94 +56,11 @@ struct Epilogue {
     const void* meta = nullptr;  // 2:4 sparsity metadata: A is the compressed (M x K/2) matrix
 };
 
-struct TmapEntry {
-    TmapKey key;
-    CUtensorMap map;
-};
-
-// Tunables a launch reads (a handle's options, or the defaults).
-struct LaunchOptions {
-    int64_t config = GEMM_CONFIG_AUTO;
-    int64_t timeout_ns = kTimeoutDefaultNs;
-    int64_t max_ctas = 0;
-    int64_t raster_group = 0;  // 0: automatic
-    int64_t fault_inject = 0;
-    int64_t stream_k = 1;
-    int64_t sk_min_blocks = kMinStreamKBlocks;
-    int64_t split_min_blocks = kMinSplitBlocks;
-    int64_t k_snake = 1;
-    int64_t host_row_chunks = 8;
-    int64_t host_col_chunks = 4;
-};
-
-// Per-device facts and lazily-set per-kernel state.  Guarded by `mu`.
-struct DeviceState {
-    int num_sms = 0;
-    std::mutex mu;
-    bool attrs_set[kNumSlots] = {};
-    int max_clusters[kNumSlots] = {};  // pair kernels: co-resident clusters (0 = not yet queried)
-};
-
-// Streams and events of gemm_run_host's copy/compute pipeline (created on first use).
-struct HostPipe {
-    static constexpr int kMaxRowChunks = 16;  // row chunks of A (and C)
-    static constexpr int kMaxColChunks = 8;   // column chunks of C (B's rows for TN, columns for NN)
-    static constexpr int kMaxPieces = kMaxRowChunks + kMaxColChunks;
-    bool ready = false;
-    cudaStream_t in = nullptr, out = nullptr;  // host -> device copies, in order; device -> host copies
-    cudaEvent_t start = nullptr, done = nullptr;
-    cudaEvent_t arrived[kMaxPieces] = {};      // per input piece, in transfer order
-    cudaEvent_t computed[kMaxPieces] = {};     // per GEMM launch
-};
-
-// Stream-K workspace: fp32 partial sums and arrival counters (see gemm_kernel.cuh).
-struct Workspace {
-    float* partials = nullptr;
-    int32_t* counters = nullptr;
-    size_t partial_floats = 0;  // capacity
-    int64_t counter_count = 0;  // capacity
-};
-
 }  // namespace
 
-struct gemm_handle_s {
-    int device = 0;
-    int32_t* d_err = nullptr;  // 4 ints
-    int32_t last_info[4] = {0, 0, 0, 0};
-    LaunchOptions opts;
-    DeviceState dev;
-    Workspace ws;
-    std::vector<TmapEntry> tmaps;
-    // gemm_run_host staging and pipeline
-    void* d_stage = nullptr;
-    size_t stage_bytes = 0;
-    HostPipe pipe;
-};
-
-namespace {
-
-// Keeps the caller's current device unchanged across a call made on h->device.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
-// Encode a 2-D row-major tensor map: `inner` contiguous elements per row, `outer` rows
-// `pitch_bytes` apart, box = box_inner x box_outer, 128-byte swizzle (or none), zero fill
-// outside.  With a cache (a handle's), identical requests reuse the earlier encoding.
-bool get_tmap(std::vector<TmapEntry>* cache, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
-              uint32_t box_inner, uint32_t box_outer, int32_t dtype, CUtensorMap* out,
-              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+bool dtg::host::get_tmap(std::vector<TmapEntry>* cache, const void* ptr, uint64_t inner, uint64_t outer,
+                         uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, int32_t dtype, CUtensorMap* out,
+                         CUtensorMapSwizzle swizzle)
 {
     const TmapKey key{ptr, inner, outer, pitch_bytes, box_inner, box_outer, dtype, static_cast<int32_t>(swizzle)};
     if (cache)
@@ -176,6 +78,7 @@ bool get_tmap(std::vector<TmapEntry>* cache, const void* ptr, uint64_t inner, ui
     // kTmapBytes: raw bytes (side data).
     const CUtensorMapDataType dt = dtype == GEMM_DTYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : dtype == GEMM_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                   : dtype == GEMM_DTYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (g_encode(out, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -187,14 +90,7 @@ bool get_tmap(std::vector<TmapEntry>* cache, const void* ptr, uint64_t inner, ui
     return true;
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool is_f8(gemm_dtype_t t) { return t == GEMM_DTYPE_E4M3 || t == GEMM_DTYPE_E5M2; }
-int elem_bytes(gemm_dtype_t t) { return is_f8(t) ? 1 : 2; }
-
-// Kernel families beyond the dense one: block-scaled 8-bit operands, 2:4-sparse A (each with
-// the one-CTA 128 x 256 tile and the CTA pair).
-enum Family { kDense = 0, kBlockScaled = 1, kSparse24 = 2 };
+namespace {
 
 // `out` is the type of C: equal to `in` for 16-bit operands, F16 or BF16 for 8-bit ones.
 KernelChoice kernel_choice(int config, gemm_dtype_t in, gemm_dtype_t out, gemm_layout_t layout, int family = kDense)
@@ -220,9 +116,9 @@ int slot_of(int config, gemm_dtype_t in, gemm_dtype_t out, gemm_layout_t layout,
     return (c * 12 + types) * 2 + (layout == GEMM_LAYOUT_NN ? 1 : 0);
 }
 
-// Opt the kernel into its shared memory and, for pair kernels, ask how many clusters can
-// be resident at once (the persistent grid never exceeds that).  Once per device and slot.
-gemm_status_t ensure_kernel_ready(DeviceState& dev, const KernelChoice& kc, int slot)
+}  // namespace
+
+gemm_status_t dtg::host::ensure_kernel_ready(DeviceState& dev, const KernelChoice& kc, int slot)
 {
     std::lock_guard<std::mutex> lock(dev.mu);
     if (!dev.attrs_set[slot]) {
@@ -250,7 +146,7 @@ gemm_status_t ensure_kernel_ready(DeviceState& dev, const KernelChoice& kc, int 
     return GEMM_OK;
 }
 
-int pick_config(const LaunchOptions& o, const DeviceState& dev, int64_t M, int64_t N, int64_t K)
+int dtg::host::pick_config(const LaunchOptions& o, const DeviceState& dev, int64_t M, int64_t N, int64_t K)
 {
     if (o.config == GEMM_CONFIG_128x256 || o.config == GEMM_CONFIG_128x128 || o.config == GEMM_CONFIG_256x256 ||
         o.config == GEMM_CONFIG_128x64)
@@ -271,6 +167,8 @@ int pick_config(const LaunchOptions& o, const DeviceState& dev, int64_t M, int64
     return GEMM_CONFIG_128x64;
 }
 
+namespace {
+
 // Workspace a stream-K plan with `units` work units needs (see the kernel's slot layout).
 size_t sk_partial_floats(int64_t units, const KernelChoice& kc)
 {
@@ -279,9 +177,10 @@ size_t sk_partial_floats(int64_t units, const KernelChoice& kc)
 
 int64_t sk_counter_count(int64_t sk_tiles, const KernelChoice& kc) { return sk_tiles * kc.cluster; }
 
-// `ws` == nullptr: no workspace, every tile is done whole (data-parallel).
-void fill_plan(const LaunchOptions& o, const DeviceState& dev, int max_clusters, const Workspace* ws, int64_t M,
-               int64_t N, int64_t K, const KernelChoice& kc, int family, gemm_plan_t* plan)
+}  // namespace
+
+void dtg::host::fill_plan(const LaunchOptions& o, const DeviceState& dev, int max_clusters, const Workspace* ws,
+                          int64_t M, int64_t N, int64_t K, const KernelChoice& kc, int family, gemm_plan_t* plan)
 {
     std::memset(plan, 0, sizeof(*plan));
     plan->config = kc.config;
@@ -358,6 +257,8 @@ void fill_plan(const LaunchOptions& o, const DeviceState& dev, int max_clusters,
     plan->threads = kc.threads;
     plan->smem_bytes = kc.smem;
 }
+
+namespace {
 
 // c_col_major: C is stored N x M (C[m, n] at C + n * ldc + m), so ldc must cover M.
 // out_dtype < 0: gemm_run's rule, 16-bit operands and C of the same type.  Otherwise any

@@ -6,6 +6,7 @@ or the device is not an sm_103 GPU, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -15,13 +16,16 @@ from . import build as _build
 
 API_VERSION = 3  # GEMM_API_VERSION the structures below are laid out for
 LAYOUT_NN, LAYOUT_TN = 0, 1
-DTYPE_F16, DTYPE_BF16, DTYPE_E4M3, DTYPE_E5M2 = 0, 1, 2, 3
+DTYPE_F16, DTYPE_BF16, DTYPE_E4M3, DTYPE_E5M2, DTYPE_F32 = 0, 1, 2, 3, 4
 LAYOUTS = {"NN": LAYOUT_NN, "TN": LAYOUT_TN}
 DTYPES = {"f16": DTYPE_F16, "bf16": DTYPE_BF16, "e4m3": DTYPE_E4M3, "e5m2": DTYPE_E5M2}
 KINDS = {"dense": 0, "block_scaled": 1, "sparse24": 2}  # gemm_kind_t
 TORCH_TO_DTYPE = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
 # 8-bit operand types (gemm_run_ex only).
 TORCH_TO_DTYPE_EX = {**TORCH_TO_DTYPE, torch.float8_e4m3fn: DTYPE_E4M3, torch.float8_e5m2: DTYPE_E5M2}
+# Biases, bias gradients and weight gradients (the linear-layer entry points).
+TORCH_TO_DTYPE_F32 = {**TORCH_TO_DTYPE, torch.float32: DTYPE_F32}
+ACTS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # gemm_act_t
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ARCH, ERR_CUDA, ERR_TIMEOUT = range(6)
 OPT_CONFIG, OPT_TIMEOUT_NS, OPT_MAX_CTAS, OPT_RASTER_GROUP, OPT_FAULT_INJECT, OPT_STREAM_K, \
@@ -45,6 +49,41 @@ class gemm_args_t(ctypes.Structure):
                 ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("c_col_major", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("scale_a", ctypes.c_float), ("scale_b", ctypes.c_float)]
+
+
+class gemm_linear_args_t(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("W", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("Z", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("ldz", ctypes.c_int64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("bias_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("alpha", ctypes.c_float)]
+
+
+class gemm_dgrad_args_t(ctypes.Structure):
+    _fields_ = [("dY", ctypes.c_void_p), ("W", ctypes.c_void_p), ("Z", ctypes.c_void_p), ("dX", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("lddy", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldz", ctypes.c_int64), ("lddx", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dbias_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta_bias", ctypes.c_float)]
+
+
+class gemm_wgrad_args_t(ctypes.Structure):
+    _fields_ = [("dY", ctypes.c_void_p), ("X", ctypes.c_void_p), ("dW", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("lddy", ctypes.c_int64), ("ldx", ctypes.c_int64), ("lddw", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float)]
+
+
+class gemm_act_grad_args_t(ctypes.Structure):
+    _fields_ = [("dY", ctypes.c_void_p), ("Z", ctypes.c_void_p), ("dZ", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("lddy", ctypes.c_int64), ("ldz", ctypes.c_int64), ("lddz", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dbias_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("beta_bias", ctypes.c_float)]
 
 
 class GemmError(RuntimeError):
@@ -90,6 +129,11 @@ def load() -> ctypes.CDLL:
         "gemm_check_args": ([p, p, p, i64, i64, i64, i64, i64, i64, i32, i32], i32),
         "gemm_tile_coord": ([i64, i64, i64, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)], i32),
         "gemm_run_noalloc": ([p, p, p, i64, i64, i64, i64, i64, i64, i32, i32, p, ctypes.POINTER(i32)], i32),
+        "gemm_run_linear": ([p, ctypes.POINTER(gemm_linear_args_t), p], i32),
+        "gemm_run_linear_dgrad": ([p, ctypes.POINTER(gemm_dgrad_args_t), p], i32),
+        "gemm_run_linear_wgrad": ([p, ctypes.POINTER(gemm_wgrad_args_t), p], i32),
+        "gemm_run_act_grad": ([p, ctypes.POINTER(gemm_act_grad_args_t), p], i32),
+        "gemm_bias_grad_workspace_bytes": ([i64, i64], i64),
         "gemm_status_string": ([i32], ctypes.c_char_p),
         "gemm_api_version": ([], i32),
     }
@@ -123,6 +167,11 @@ def sp_meta_bytes(M: int, K: int) -> int:
     return int(load().gemm_sp_meta_bytes(M, K))
 
 
+def bias_grad_workspace_bytes(M: int, cols: int) -> int:
+    """Bytes of workspace for the column sums of an M x cols matrix."""
+    return int(load().gemm_bias_grad_workspace_bytes(M, cols))
+
+
 def tile_coord(tile: int, tiles_m: int, tiles_n: int, group_m: int):
     tm, tn = ctypes.c_int64(), ctypes.c_int64()
     st = load().gemm_tile_coord(tile, tiles_m, tiles_n, group_m, ctypes.byref(tm), ctypes.byref(tn))
@@ -153,6 +202,54 @@ def empty_output(M: int, N: int, dtype: torch.dtype, device) -> torch.Tensor:
     """An M x N output whose row pitch is a multiple of 8 elements (TMA alignment)."""
     ldc = max(-(-N // 8) * 8, 8)
     return torch.empty((M, ldc), dtype=dtype, device=device)[:, :N]
+
+
+def _matrix(t: torch.Tensor, what: str, shape, dtype, device) -> int:
+    """Check a 2-D tensor argument and return its leading dimension."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    return _ld(t)
+
+
+def _vector(t: torch.Tensor, what: str, n: int, dtypes, device) -> int:
+    """Check a dense 1-D tensor argument and return its element type's code."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be one of {dtypes}, not {t.dtype}")
+    if t.dim() != 1 or t.size(0) != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a dense vector of {n} elements")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    return TORCH_TO_DTYPE_F32[t.dtype]
+
+
+def _act(name) -> int:
+    if name not in ACTS:
+        raise ValueError(f"unknown activation {name!r}: one of {sorted(k for k in ACTS if k)}")
+    return ACTS[name]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr() or None
+
+
+def _on_stream(stream, device):
+    """A context in which new tensors belong to `stream` (None: the current stream), so that their
+    memory is not handed out again while the stream still uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                             torch.cuda.ExternalStream(int(stream), device=device))
+
+
+def _padded_output(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """A rows x cols output whose row pitch is a multiple of 16 bytes."""
+    align = 4 if dtype == torch.float32 else 8
+    ld = max(-(-cols // align) * align, align)
+    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
 
 
 class Gemm:
@@ -393,6 +490,140 @@ class Gemm:
                                            _ld(A), _ld(B), _ld(C), LAYOUTS[layout], TORCH_TO_DTYPE[A.dtype],
                                            _stream_ptr(stream) or None))
 
+    # -------------------------------------------------------------- linear layers
+    def _device(self) -> torch.device:
+        return torch.device("cuda", self.device.index or 0)
+
+    def _stream(self, stream) -> int:
+        if stream is None:
+            return torch.cuda.current_stream(self._device()).cuda_stream
+        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+    def linear(self, X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = None,
+               residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               preact: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, alpha: float = 1.0,
+               stream=None) -> torch.Tensor:
+        """Y = act(alpha * X·W^T + bias) + residual (gemm_run_linear): X (M x K) and W (N x K) 16-bit or
+        8-bit floats, Y, residual and preact float16 or bfloat16, bias float32 or Y's type.  ``preact``, if
+        given, receives alpha * X·W^T + bias; ``out`` may be ``residual`` itself.  Async on `stream`."""
+        if X.dtype != W.dtype or X.dtype not in TORCH_TO_DTYPE_EX:
+            raise TypeError("X and W must have the same 16-bit or 8-bit float type")
+        if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
+            raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
+        dev = self._device()
+        (M, K), N = X.shape, W.shape[0]
+        if out_dtype is None:
+            out_dtype = out.dtype if out is not None else (X.dtype if X.dtype in TORCH_TO_DTYPE else torch.bfloat16)
+        if out_dtype not in TORCH_TO_DTYPE or (X.dtype in TORCH_TO_DTYPE and out_dtype != X.dtype):
+            raise TypeError("Y must be float16 or bfloat16, and of the operands' type if that is 16-bit")
+        ldx, ldw = _matrix(X, "X", (M, K), X.dtype, dev), _matrix(W, "W", (N, K), X.dtype, dev)
+        bias_dtype = 0 if bias is None else _vector(bias, "bias", N, (torch.float32, out_dtype), dev)
+        ldr = 0 if residual is None else _matrix(residual, "residual", (M, N), out_dtype, dev)
+        ldz = 0 if preact is None else _matrix(preact, "preact", (M, N), out_dtype, dev)
+        if out is None:
+            with _on_stream(stream, dev):
+                out = _padded_output(M, N, out_dtype, dev)
+        ldy = _matrix(out, "out", (M, N), out_dtype, dev)
+        a = gemm_linear_args_t(_ptr(X), _ptr(W), _ptr(out), _ptr(bias), _ptr(residual), _ptr(preact), M, N, K, ldx, ldw,
+                               ldy, ldr, ldz, TORCH_TO_DTYPE_EX[X.dtype], TORCH_TO_DTYPE[out_dtype], bias_dtype,
+                               _act(act), alpha)
+        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), self._stream(stream) or None)
+        if st != OK:
+            raise GemmError(st, "gemm_run_linear")
+        return out
+
+    def linear_dgrad(self, dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
+                     out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
+                     beta_bias: float = 0.0, stream=None) -> torch.Tensor:
+        """dX = (alpha * dY·W) * act'(Z) (gemm_run_linear_dgrad): dY (M x N), W (N x K), Z (M x K, what the
+        layer below kept) of one 16-bit type.  ``dbias`` (K, float32 or that type), if given, becomes
+        beta_bias * dbias + the column sums of dX.  Async on `stream`."""
+        if dY.dtype != W.dtype or dY.dtype not in TORCH_TO_DTYPE:
+            raise TypeError("dY and W must both be float16 or both bfloat16")
+        if dY.dim() != 2 or W.dim() != 2 or dY.shape[1] != W.shape[0]:
+            raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, W {tuple(W.shape)}")
+        code, dev, dt = _act(act), self._device(), dY.dtype
+        (M, N), K = dY.shape, W.shape[1]
+        if (Z is None) != (code == 0):
+            raise ValueError("Z is the pre-activation of act: both or neither")
+        lddy, ldw = _matrix(dY, "dY", (M, N), dt, dev), _matrix(W, "W", (N, K), dt, dev)
+        ldz = 0 if Z is None else _matrix(Z, "Z", (M, K), dt, dev)
+        dbias_dtype = 0 if dbias is None else _vector(dbias, "dbias", K, (torch.float32, dt), dev)
+        with _on_stream(stream, dev):
+            if out is None:
+                out = _padded_output(M, K, dt, dev)
+            ws, ws_bytes = self._sums_workspace(dbias, M, K, dev)
+        lddx = _matrix(out, "out", (M, K), dt, dev)
+        a = gemm_dgrad_args_t(_ptr(dY), _ptr(W), _ptr(Z), _ptr(out), _ptr(dbias), _ptr(ws), ws_bytes, M, N, K, lddy, ldw,
+                              ldz, lddx, TORCH_TO_DTYPE[dt], dbias_dtype, code, alpha, beta_bias)
+        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), self._stream(stream) or None)
+        if st != OK:
+            raise GemmError(st, "gemm_run_linear_dgrad")
+        return out
+
+    def linear_wgrad(self, dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = None,
+                     out_dtype: torch.dtype | None = None, alpha: float = 1.0, beta: float = 0.0,
+                     stream=None) -> torch.Tensor:
+        """dW = alpha * dY^T·X + beta * dW (gemm_run_linear_wgrad): dY (M x N) and X (M x K) of one 16-bit
+        type, dW (N x K) float32 (the default) or that type.  Async on `stream`."""
+        if dY.dtype != X.dtype or dY.dtype not in TORCH_TO_DTYPE:
+            raise TypeError("dY and X must both be float16 or both bfloat16")
+        if dY.dim() != 2 or X.dim() != 2 or dY.shape[0] != X.shape[0]:
+            raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, X {tuple(X.shape)}")
+        if out is None and beta != 0.0:
+            raise ValueError("beta adds to an existing dW: pass it as out")
+        dev, dt = self._device(), dY.dtype
+        (M, N), K = dY.shape, X.shape[1]
+        if out_dtype is None:
+            out_dtype = out.dtype if out is not None else torch.float32
+        if out_dtype not in (torch.float32, dt):
+            raise TypeError("dW must be float32 or of the operands' type")
+        lddy, ldx = _matrix(dY, "dY", (M, N), dt, dev), _matrix(X, "X", (M, K), dt, dev)
+        if out is None:
+            with _on_stream(stream, dev):
+                out = _padded_output(N, K, out_dtype, dev)
+        lddw = _matrix(out, "out", (N, K), out_dtype, dev)
+        a = gemm_wgrad_args_t(_ptr(dY), _ptr(X), _ptr(out), M, N, K, lddy, ldx, lddw, TORCH_TO_DTYPE[dt],
+                              TORCH_TO_DTYPE_F32[out_dtype], alpha, beta)
+        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), self._stream(stream) or None)
+        if st != OK:
+            raise GemmError(st, "gemm_run_linear_wgrad")
+        return out
+
+    def act_grad(self, dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
+                 out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, beta_bias: float = 0.0,
+                 sums_only: bool = False, stream=None) -> torch.Tensor | None:
+        """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N) of one 16-bit type; ``out`` may be dY itself.
+        ``dbias`` as for linear_dgrad, with N columns.  With ``sums_only`` dZ is not written (and None is
+        returned).  Async on `stream`."""
+        if dY.dtype not in TORCH_TO_DTYPE or dY.dim() != 2:
+            raise TypeError("dY must be a 2-D float16 or bfloat16 tensor")
+        code, dev, dt = _act(act), self._device(), dY.dtype
+        M, N = dY.shape
+        if (Z is None) != (code == 0):
+            raise ValueError("Z is the pre-activation of act: both or neither")
+        if sums_only and (out is not None or dbias is None):
+            raise ValueError("sums_only writes dbias and no dZ")
+        lddy = _matrix(dY, "dY", (M, N), dt, dev)
+        ldz = 0 if Z is None else _matrix(Z, "Z", (M, N), dt, dev)
+        dbias_dtype = 0 if dbias is None else _vector(dbias, "dbias", N, (torch.float32, dt), dev)
+        with _on_stream(stream, dev):
+            if out is None and not sums_only:
+                out = _padded_output(M, N, dt, dev)
+            ws, ws_bytes = self._sums_workspace(dbias, M, N, dev)
+        lddz = 0 if out is None else _matrix(out, "out", (M, N), dt, dev)
+        a = gemm_act_grad_args_t(_ptr(dY), _ptr(Z), _ptr(out), _ptr(dbias), _ptr(ws), ws_bytes, M, N, lddy, ldz, lddz,
+                                 TORCH_TO_DTYPE[dt], dbias_dtype, code, beta_bias)
+        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), self._stream(stream) or None)
+        if st != OK:
+            raise GemmError(st, "gemm_run_act_grad")
+        return out
+
+    def _sums_workspace(self, dbias, M: int, cols: int, device):
+        """(workspace, bytes) of a call that writes dbias, (None, 0) without."""
+        n = 0 if dbias is None else int(self._lib.gemm_bias_grad_workspace_bytes(M, cols))
+        return (torch.empty(n, dtype=torch.uint8, device=device), n) if n else (None, 0)
+
     def sync_status(self, stream=None) -> int:
         return int(self._lib.gemm_sync_status(self._h, _stream_ptr(stream) or None))
 
@@ -400,10 +631,35 @@ class Gemm:
 _default: dict = {}
 
 
+def _default_handle(device: torch.device) -> Gemm:
+    """The handle that matmul and the linear-layer functions use on a device."""
+    dev = device.index if device.index is not None else torch.cuda.current_device()
+    if dev not in _default:
+        _default[dev] = Gemm(dev)
+    return _default[dev]
+
+
 def matmul(A: torch.Tensor, B: torch.Tensor, layout: str = "NN", out: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
     """C = A·B with the library's kernel, on a per-device default handle."""
-    dev = A.device.index if A.device.index is not None else torch.cuda.current_device()
-    if dev not in _default:
-        _default[dev] = Gemm(dev)
-    return _default[dev].run(A, B, out, layout, stream)
+    return _default_handle(A.device).run(A, B, out, layout, stream)
+
+
+def linear(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, **kw) -> torch.Tensor:
+    """Gemm.linear on a per-device default handle."""
+    return _default_handle(X.device).linear(X, W, bias, **kw)
+
+
+def linear_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, **kw) -> torch.Tensor:
+    """Gemm.linear_dgrad on a per-device default handle."""
+    return _default_handle(dY.device).linear_dgrad(dY, W, Z, **kw)
+
+
+def linear_wgrad(dY: torch.Tensor, X: torch.Tensor, **kw) -> torch.Tensor:
+    """Gemm.linear_wgrad on a per-device default handle."""
+    return _default_handle(dY.device).linear_wgrad(dY, X, **kw)
+
+
+def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, **kw) -> torch.Tensor | None:
+    """Gemm.act_grad on a per-device default handle."""
+    return _default_handle(dY.device).act_grad(dY, Z, **kw)

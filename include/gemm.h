@@ -51,9 +51,10 @@ enum { GEMM_LAYOUT_NN = 0, GEMM_LAYOUT_TN = 1 };
 
 /* Element types.  F16 and BF16 serve as operand and output types; E4M3 and E5M2 (8-bit
  * floats: 1-4-3 with bias 7 and no infinities, 1-5-2 with bias 15) are operand types only,
- * accepted by gemm_run_ex. */
+ * accepted by gemm_run_ex and gemm_run_linear.  F32 is the type of biases, of bias gradients
+ * and of weight gradients (the linear-layer entry points), never of A or B. */
 typedef int32_t gemm_dtype_t;
-enum { GEMM_DTYPE_F16 = 0, GEMM_DTYPE_BF16 = 1, GEMM_DTYPE_E4M3 = 2, GEMM_DTYPE_E5M2 = 3 };
+enum { GEMM_DTYPE_F16 = 0, GEMM_DTYPE_BF16 = 1, GEMM_DTYPE_E4M3 = 2, GEMM_DTYPE_E5M2 = 3, GEMM_DTYPE_F32 = 4 };
 
 typedef int32_t gemm_status_t;
 enum {
@@ -356,6 +357,133 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C,
                                int64_t lda, int64_t ldb, int64_t ldc,
                                gemm_layout_t layout, gemm_dtype_t dtype, void* stream,
                                int32_t* watchdog_info);
+
+/* ---------------------------------------------------------------- linear layers
+ *
+ * The products of a linear layer Y = act(alpha X W^T + bias) + residual, forward and backward,
+ * with what surrounds them done where the product is written.  X is M tokens x K features and
+ * W is N x K, as a layer stores it.  The pages have no counterpart beyond the products themselves.
+ *
+ * act(z) and its derivative act'(z), in fp32:
+ *   NONE       z                            1
+ *   RELU       z < 0 ? 0 : z                z <= 0 ? 0 : 1
+ *   GELU       z Phi(z)                     Phi(z) + z phi(z)    (Phi, phi: normal distribution, density)
+ *   GELU_TANH  z s(2u)                      s + z s (1 - s) 2u'  (u = sqrt(2/pi)(z + 0.044715 z^3), s = s(2u))
+ *   SILU       z s(z)                       s (1 + z (1 - s))    (s(t) = 1 / (1 + exp(-t)))
+ * NaN stays NaN.  The derivatives of +-infinity are their limits; GELU, GELU_TANH and SILU of
+ * -infinity are NaN, as the formulas say.
+ *
+ * Sums run in fp32, in an order that depends on the sizes and the handle's options alone, so a
+ * call's results do not change from one call to the next.  Every matrix is row-major, with the
+ * alignment rules of gemm_run (bases of 16 bytes; row pitches that are multiples of 16 bytes);
+ * bias and dbias are dense vectors of any alignment their type allows.  An output may not
+ * overlap an input, except where it is said below.  Like gemm_run these calls enqueue on
+ * `stream` and return; they share the handle's workspace, so the rule on overlapping launches
+ * is the same, and so are the status codes and the watchdog (gemm_sync_status). */
+typedef int32_t gemm_act_t;
+enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3, GEMM_ACT_SILU = 4 };
+
+/* Y = act(z) + residual with z = alpha X W^T + bias; each output rounded once from fp32.
+ *   - dtype: type of X and W (F16, BF16, E4M3, E5M2; row pitches of 8-bit operands are multiples
+ *     of 16 elements).  out_dtype: type of Y, residual and Z (F16 or BF16; equal to dtype for
+ *     16-bit operands).  alpha carries the operands' scales, if they have any; it must be finite.
+ *   - bias: N values of bias_dtype (F32, or out_dtype), or NULL.
+ *   - residual: M x N, pitch ldr, or NULL.  Y may be the residual itself (same pointer and pitch).
+ *   - Z: M x N, pitch ldz, or NULL: receives z, which a backward pass reads.
+ *   - M == 0 or N == 0 is a no-op; with K == 0 the product is zero. */
+typedef struct {
+    const void* X;
+    const void* W;
+    void* Y;
+    const void* bias;
+    const void* residual;
+    void* Z;
+    int64_t M, N, K;
+    int64_t ldx, ldw, ldy, ldr, ldz;
+    gemm_dtype_t dtype;
+    gemm_dtype_t out_dtype;
+    gemm_dtype_t bias_dtype;
+    gemm_act_t act;
+    float alpha;
+} gemm_linear_args_t;
+
+gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, void* stream);
+
+/* Backward through the weights and the activation below them: dX = d rounded, with
+ * d = (alpha dY W) * act'(Z), and dbias[k] = beta_bias * dbias[k] + sum over m of d[m, k]
+ * (the fp32 d, before its rounding).
+ *   - dY: M x N, W: N x K, Z: M x K (the pre-activations that the layer below saved; NULL when
+ *     act is NONE, and not read then), dX: M x K, all of type dtype (F16 or BF16).
+ *   - dbias: K values of dbias_dtype (F32, or dtype), or NULL.  With beta_bias == 0 it is not
+ *     read.  workspace: gemm_bias_grad_workspace_bytes(M, K) bytes, 16-byte aligned, that the
+ *     call may overwrite until its kernels are done; needed with dbias only (too small, or NULL:
+ *     INVALID_ARG).
+ *   - K == 0 is a no-op; with M == 0 dbias becomes beta_bias * dbias; with N == 0 d is zero. */
+typedef struct {
+    const void* dY;
+    const void* W;
+    const void* Z;
+    void* dX;
+    void* dbias;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t M, N, K;
+    int64_t lddy, ldw, ldz, lddx;
+    gemm_dtype_t dtype;
+    gemm_dtype_t dbias_dtype;
+    gemm_act_t act;
+    float alpha;
+    float beta_bias;
+} gemm_dgrad_args_t;
+
+gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* args, void* stream);
+
+/* The weights' gradient: dW = alpha dY^T X + beta dW, with dY M x N, X M x K (F16 or BF16), dW
+ * N x K of out_dtype (F32, or dtype; an F32 row pitch is a multiple of 4 elements).  With
+ * beta == 0 dW is not read.  N == 0 or K == 0 is a no-op; with M == 0 dW becomes beta * dW. */
+typedef struct {
+    const void* dY;
+    const void* X;
+    void* dW;
+    int64_t M, N, K;
+    int64_t lddy, ldx, lddw;
+    gemm_dtype_t dtype;
+    gemm_dtype_t out_dtype;
+    float alpha;
+    float beta;
+} gemm_wgrad_args_t;
+
+gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* args, void* stream);
+
+/* An activation's backward pass where no product comes before it: dZ = d rounded, with
+ * d = dY * act'(Z), and dbias[n] = beta_bias * dbias[n] + sum over m of d[m, n].
+ *   - dY, Z, dZ: M x N of type dtype (F16 or BF16); Z is NULL when act is NONE.  dZ may be NULL
+ *     (the sums alone are wanted), or dY itself (same pointer and pitch).
+ *   - dbias, workspace: as for gemm_run_linear_dgrad, with N columns
+ *     (gemm_bias_grad_workspace_bytes(M, N)).
+ *   - N == 0 is a no-op; with M == 0 dbias becomes beta_bias * dbias. */
+typedef struct {
+    const void* dY;
+    const void* Z;
+    void* dZ;
+    void* dbias;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t M, N;
+    int64_t lddy, ldz, lddz;
+    gemm_dtype_t dtype;
+    gemm_dtype_t dbias_dtype;
+    gemm_act_t act;
+    float beta_bias;
+} gemm_act_grad_args_t;
+
+gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* args, void* stream);
+
+/* Bytes of workspace for the column sums of an M x cols matrix: 4 * ceil(M / 32) * (cols rounded
+ * up to 64); 0 when M or cols is 0. */
+int64_t gemm_bias_grad_workspace_bytes(int64_t M, int64_t cols);
+
+/* ---------------------------------------------------------------- status and version */
 
 /* Static description of a status code.  Never NULL. */
 const char* gemm_status_string(gemm_status_t s);

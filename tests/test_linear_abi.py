@@ -1,0 +1,57 @@
+"""The linear-layer entry points without a GPU: struct layouts, workspace sizes, null handles."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+
+STRUCTS = ["gemm_linear_args_t", "gemm_dgrad_args_t", "gemm_wgrad_args_t", "gemm_act_grad_args_t"]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dense_tiled_gemm_04_gb300 import build, native
+
+    build.build()
+    return native
+
+
+def test_structs_are_laid_out_as_the_c_compiler_does(lib, tmp_path):
+    lines = []
+    for s in STRUCTS:
+        lines.append(f'printf("%zu\\n", sizeof({s}));')
+        lines += [f'printf("%zu\\n", offsetof({s}, {f}));' for f, _ in getattr(lib, s)._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("#include <stdio.h>\n#include <stddef.h>\n#include \"gemm.h\"\nint main(void) {\n" + "\n".join(lines) + "\nreturn 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    want = []
+    for s in STRUCTS:
+        cls = getattr(lib, s)
+        want.append(ctypes.sizeof(cls))
+        want += [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want
+
+
+@pytest.mark.parametrize("M,cols,want", [(0, 5, 0), (5, 0, 0), (-1, 8, 0), (1, 1, 256), (32, 64, 256), (33, 65, 1024),
+                                         (16384, 8192, 4 * 512 * 8192), ((1 << 31) - 1, 1 << 20, 4 << 46)])
+def test_workspace_bytes(lib, M, cols, want):
+    assert lib.bias_grad_workspace_bytes(M, cols) == want
+
+
+def test_null_handles_and_arguments(lib):
+    so = lib.load()
+    for name, cls in (("gemm_run_linear", lib.gemm_linear_args_t), ("gemm_run_linear_dgrad", lib.gemm_dgrad_args_t),
+                      ("gemm_run_linear_wgrad", lib.gemm_wgrad_args_t), ("gemm_run_act_grad", lib.gemm_act_grad_args_t)):
+        assert getattr(so, name)(None, None, None) == lib.ERR_INVALID_ARG
+        assert getattr(so, name)(None, ctypes.byref(cls()), None) == lib.ERR_INVALID_ARG
+
+
+def test_activation_codes_match_the_header(lib):
+    text = open(os.path.join(ROOT, "include", "gemm.h")).read()
+    for name, code in lib.ACTS.items():
+        if name:
+            assert f"GEMM_ACT_{name.upper()} = {code}" in text
