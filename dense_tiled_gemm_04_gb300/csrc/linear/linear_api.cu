@@ -1,14 +1,18 @@
 // Host side of the linear-layer entry points of include/gemm.h: argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
+#include "elementwise.cuh"
 #include "gemm.h"
 #include "host/handle.cuh"
-#include "simple.cuh"
+#include "tile_set.cuh"
 
 using namespace dtg::host;
+using dtg::KernelChoice;
 
 namespace {
 
@@ -57,20 +61,187 @@ void check_sums(Checks& c, const void* dbias, gemm_dtype_t t, const void* ws, in
 
 int64_t sum_pitch(int64_t cols) { return cdiv(cols, kSumAlign) * kSumAlign; }
 
-gemm_status_t launched() { return cudaPeekAtLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA; }
-
-gemm_status_t launch_product(const dtg::linear::SimpleParams& p, cudaStream_t s)
+// Kernels that start while the stream's previous kernel finishes (they wait for it themselves).
+template <class... P, class... A>
+gemm_status_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args)
 {
-    dtg::linear::simple_product_kernel<<<static_cast<unsigned>(cdiv(p.M, 32) * cdiv(p.N, 32)), dim3(32, 32), 0, s>>>(p);
-    return launched();
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-gemm_status_t launch_sums(const float* partials, int64_t M, int64_t cols, void* dbias, gemm_dtype_t t, float beta,
+// dbias = beta * dbias + the sums of `rows` rows of partial sums.
+gemm_status_t launch_sums(const void* partials, int64_t rows, int64_t cols, void* dbias, gemm_dtype_t t, float beta,
                           cudaStream_t s)
 {
-    dtg::linear::simple_column_sum_kernel<<<static_cast<unsigned>(cdiv(cols, 128)), 128, 0, s>>>(
-        partials, cdiv(M, kSumRows), sum_pitch(cols), cols, dbias, t, beta);
-    return launched();
+    const auto fn = t == GEMM_DTYPE_F32    ? &dtg::linear::column_sum_kernel<dtg::linear::kOutF32>
+                    : t == GEMM_DTYPE_BF16 ? &dtg::linear::column_sum_kernel<dtg::linear::kOutBf16>
+                                           : &dtg::linear::column_sum_kernel<dtg::linear::kOutF16>;
+    return launch_after(fn, dim3(static_cast<unsigned>(cdiv(cols, 32))), dim3(256), 0, s, static_cast<const float*>(partials),
+                        rows, sum_pitch(cols), cols, dbias, beta);
+}
+
+// One product: rows x cols over `depth`, as linear_tile_kernel names them.
+struct Product {
+    int mode;                  // dtg::linear::kForward, kDgrad, kWgrad
+    gemm_dtype_t in, out;
+    int64_t rows, cols, depth;
+    const void *A, *B;
+    int64_t lda, ldb;
+    void* C;
+    int64_t ldc;
+    float alpha, beta;
+    gemm_act_t act;
+    const void* bias;
+    gemm_dtype_t bias_dtype;
+    const void* src;           // residual, pre-activations or dW; null: none
+    int64_t ldsrc;
+    void* Z;
+    int64_t ldz;
+    float* partials;
+};
+
+KernelChoice tile_kernel(const Product& q, int config)
+{
+    const bool bf16 = q.out == GEMM_DTYPE_BF16, f32 = q.out == GEMM_DTYPE_F32;
+    if (q.mode == dtg::linear::kDgrad) return dtg::linear::dgrad_16(config, bf16);
+    if (q.mode == dtg::linear::kWgrad)
+        return q.in == GEMM_DTYPE_BF16 ? dtg::linear::wgrad_bf16(config, f32) : dtg::linear::wgrad_f16(config, f32);
+    switch (q.in) {
+    case GEMM_DTYPE_BF16: return dtg::linear::forward_bf16(config);
+    case GEMM_DTYPE_E4M3: return dtg::linear::forward_e4m3(config, bf16);
+    case GEMM_DTYPE_E5M2: return dtg::linear::forward_e5m2(config, bf16);
+    default: return dtg::linear::forward_f16(config);
+    }
+}
+
+// Launch-state slot of a tile kernel: 12 operators and types x 3 configurations.
+int tile_slot(const Product& q, int config)
+{
+    int op;
+    if (q.mode == dtg::linear::kForward)
+        op = is_f8(q.in) ? 2 + 2 * (q.in - GEMM_DTYPE_E4M3) + (q.out == GEMM_DTYPE_BF16) : q.in;
+    else if (q.mode == dtg::linear::kDgrad)
+        op = 6 + q.in;
+    else
+        op = 8 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
+    return kLinearSlot0 + 3 * op + (config - 1);
+}
+
+// K blocks per chunk of the accumulation (see tile_kernel.cuh).  Where an fp32 result is wanted (a weight
+// gradient, or sums of the product's values) 8 blocks of 64 keep the truncation of the tensor core's
+// accumulator at 6e-7; a 16-bit result rounds at 2e-4 or more, and 32 blocks do.
+int chunk_blocks(const Product& q) { return q.out == GEMM_DTYPE_F32 || q.partials ? 8 : 32; }
+
+gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t stream)
+{
+    const LaunchOptions& o = h->opts;
+    int config = pick_config(o, h->dev, q.rows, q.cols, q.depth);
+    if (config == GEMM_CONFIG_128x64) config = GEMM_CONFIG_128x128;
+    const KernelChoice kc = tile_kernel(q, config);
+    const int slot = tile_slot(q, kc.config);
+    if (!h->dev.attrs_set[slot]) {
+        // The kernel's warps share out the registers it starts with: fewer than it counts on would leave the
+        // epilogue waiting for registers forever.
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kc.fn) != cudaSuccess || fa.numRegs < dtg::linear::kTileLaunchRegs)
+            return GEMM_ERR_CUDA;
+    }
+    const gemm_status_t ready = ensure_kernel_ready(h->dev, kc, slot);
+    if (ready != GEMM_OK) return ready;
+    gemm_plan_t plan;
+    fill_plan(o, h->dev, h->dev.max_clusters[slot], &h->ws, q.rows, q.cols, q.depth, kc, kDense, &plan);
+
+    const uint64_t eb = static_cast<uint64_t>(elem_bytes(q.in));
+    const uint32_t sk = static_cast<uint32_t>(kc.stage_k), nb = static_cast<uint32_t>(kc.n_block);
+    const uint64_t oe = static_cast<uint64_t>(bytes_of(q.out));
+    CUtensorMap tA, tB, tC, tZ;
+    if (!get_tmap(nullptr, q.C, q.cols, q.rows, q.ldc * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tC))
+        return GEMM_ERR_CUDA;
+    tA = tB = tZ = tC;  // those that are not used name a valid tensor
+    if (q.Z && !get_tmap(nullptr, q.Z, q.cols, q.rows, q.ldz * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tZ))
+        return GEMM_ERR_CUDA;
+    if (q.depth > 0) {
+        const bool at = q.mode == dtg::linear::kWgrad, bt = q.mode != dtg::linear::kForward;
+        if (!(at ? get_tmap(nullptr, q.A, q.rows, q.depth, q.lda * eb, nb, sk, q.in, &tA)
+                 : get_tmap(nullptr, q.A, q.depth, q.rows, q.lda * eb, sk, dtg::kBM, q.in, &tA)) ||
+            !(bt ? get_tmap(nullptr, q.B, q.cols, q.depth, q.ldb * eb, nb, sk, q.in, &tB)
+                 : get_tmap(nullptr, q.B, q.depth, q.cols, q.ldb * eb, sk, static_cast<uint32_t>(kc.b_box), q.in, &tB)))
+            return GEMM_ERR_CUDA;
+    }
+
+    dtg::linear::TileParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = static_cast<int32_t>(q.rows);
+    p.N = static_cast<int32_t>(q.cols);
+    p.K = static_cast<int32_t>(q.depth);
+    p.tiles_m = static_cast<int32_t>(plan.tiles_m);
+    p.tiles_n = static_cast<int32_t>(plan.tiles_n);
+    p.num_kb = static_cast<int32_t>(plan.k_blocks);
+    p.num_tiles = static_cast<int32_t>(plan.tiles_m * plan.tiles_n);
+    p.group_m = static_cast<int32_t>(plan.raster_group);
+    p.fault_inject = static_cast<int32_t>(o.fault_inject);
+    p.k_snake = static_cast<int32_t>(plan.k_snake);
+    p.timeout_ns = static_cast<uint64_t>(o.timeout_ns);
+    p.err = h->d_err;
+    p.C = q.C;
+    p.ldc = q.ldc;
+    p.dp_tiles = static_cast<int32_t>(plan.dp_tiles);
+    p.sk_base = plan.sk_base;
+    p.sk_extra = plan.sk_extra;
+    p.ws = h->ws.partials;
+    p.counters = h->ws.counters;
+    p.alpha = q.alpha;
+    p.beta = q.beta;
+    p.chunk_kb = chunk_blocks(q);
+    p.act = q.act;
+    p.bias = q.bias;
+    p.bias_f32 = q.bias_dtype == GEMM_DTYPE_F32;
+    p.in = q.src;
+    p.ldin = q.ldsrc;
+    p.Z = q.Z;
+    p.ldz = q.ldz;
+    p.partials = q.partials;
+    p.pitch = sum_pitch(q.cols);
+
+    void* args[] = {&tA, &tB, &tC, &tZ, &p};
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(kc.threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(kc.smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (kc.cluster > 1) {
+        attrs[1].id = cudaLaunchAttributeClusterDimension;
+        attrs[1].val.clusterDim.x = static_cast<unsigned>(kc.cluster);
+        attrs[1].val.clusterDim.y = 1;
+        attrs[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cfg.attrs = attrs;
+    return cudaLaunchKernelExC(&cfg, kc.fn, args) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+template <bool BF16>
+gemm_status_t launch_act_grad(const dtg::linear::ActGradParams& p, gemm_act_t act, dim3 grid, cudaStream_t s)
+{
+    using namespace dtg::linear;
+    void (*fn)(const ActGradParams) = nullptr;
+    DTG_ACT_SWITCH(act, fn = (&act_grad_kernel<BF16, ACT>));
+    return launch_after(fn, grid, dim3(kActWarps * 32), 0, s, p);
 }
 
 }  // namespace
@@ -106,29 +277,28 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, v
     if (c.st != GEMM_OK) return c.st;
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
-    dtg::linear::SimpleParams p = {};
-    p.A = a.X;
-    p.B = a.W;
-    p.C = a.Y;
-    p.bias = a.bias;
-    p.in = a.residual;
-    p.Z = a.Z;
-    p.M = a.M;
-    p.N = a.N;
-    p.K = a.K;
-    p.a_m = a.ldx;
-    p.a_k = 1;
-    p.b_k = 1;
-    p.b_n = a.ldw;
-    p.ldc = a.ldy;
-    p.ldin = a.ldr;
-    p.ldz = a.ldz;
-    p.dtype = a.dtype;
-    p.out = a.out_dtype;
-    p.bias_dtype = a.bias_dtype;
-    p.act = a.act;
-    p.alpha = a.alpha;
-    return launch_product(p, static_cast<cudaStream_t>(stream));
+    Product q = {};
+    q.mode = dtg::linear::kForward;
+    q.in = a.dtype;
+    q.out = a.out_dtype;
+    q.rows = a.M;
+    q.cols = a.N;
+    q.depth = a.K;
+    q.A = a.X;
+    q.lda = a.ldx;
+    q.B = a.W;
+    q.ldb = a.ldw;
+    q.C = a.Y;
+    q.ldc = a.ldy;
+    q.alpha = a.alpha;
+    q.act = a.act;
+    q.bias = a.bias;
+    q.bias_dtype = a.bias_dtype;
+    q.src = a.residual;
+    q.ldsrc = a.ldr;
+    q.Z = a.Z;
+    q.ldz = a.ldz;
+    return launch_product(h, q, static_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* args, void* stream)
@@ -156,32 +326,28 @@ gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* ar
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.M > 0) {
-        dtg::linear::SimpleParams p = {};
-        p.A = a.dY;
-        p.B = a.W;
-        p.C = a.dX;
-        p.in = a.act != GEMM_ACT_NONE ? a.Z : nullptr;
-        p.partials = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
-        p.pitch = sum_pitch(a.K);
-        p.M = a.M;
-        p.N = a.K;
-        p.K = a.N;
-        p.a_m = a.lddy;
-        p.a_k = 1;
-        p.b_k = a.ldw;
-        p.b_n = 1;
-        p.ldc = a.lddx;
-        p.ldin = a.ldz;
-        p.dtype = a.dtype;
-        p.out = a.dtype;
-        p.act = a.act;
-        p.slope = 1;
-        p.alpha = a.alpha;
-        const gemm_status_t st = launch_product(p, s);
+        Product q = {};
+        q.mode = dtg::linear::kDgrad;
+        q.in = q.out = a.dtype;
+        q.rows = a.M;
+        q.cols = a.K;
+        q.depth = a.N;
+        q.A = a.dY;
+        q.lda = a.lddy;
+        q.B = a.W;
+        q.ldb = a.ldw;
+        q.C = a.dX;
+        q.ldc = a.lddx;
+        q.alpha = a.alpha;
+        q.act = a.act;
+        q.src = a.act != GEMM_ACT_NONE ? a.Z : nullptr;
+        q.ldsrc = a.ldz;
+        q.partials = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
+        const gemm_status_t st = launch_product(h, q, s);
         if (st != GEMM_OK) return st;
     }
     if (!a.dbias) return GEMM_OK;
-    return launch_sums(static_cast<const float*>(a.workspace), a.M, a.K, a.dbias, a.dbias_dtype, a.beta_bias, s);
+    return launch_sums(a.workspace, cdiv(a.M, kSumRows), a.K, a.dbias, a.dbias_dtype, a.beta_bias, s);
 }
 
 gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* args, void* stream)
@@ -202,23 +368,24 @@ gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* ar
     if (c.st != GEMM_OK) return c.st;
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
-    dtg::linear::SimpleParams p = {};
-    p.A = a.dY;
-    p.B = a.X;
-    p.C = a.dW;
-    p.M = a.N;
-    p.N = a.K;
-    p.K = a.M;
-    p.a_m = 1;
-    p.a_k = a.lddy;
-    p.b_k = a.ldx;
-    p.b_n = 1;
-    p.ldc = a.lddw;
-    p.dtype = a.dtype;
-    p.out = a.out_dtype;
-    p.alpha = a.alpha;
-    p.beta = a.beta;
-    return launch_product(p, static_cast<cudaStream_t>(stream));
+    Product q = {};
+    q.mode = dtg::linear::kWgrad;
+    q.in = a.dtype;
+    q.out = a.out_dtype;
+    q.rows = a.N;
+    q.cols = a.K;
+    q.depth = a.M;
+    q.A = a.dY;
+    q.lda = a.lddy;
+    q.B = a.X;
+    q.ldb = a.ldx;
+    q.C = a.dW;
+    q.ldc = a.lddw;
+    q.alpha = a.alpha;
+    q.beta = a.beta;
+    q.src = a.beta != 0.0f ? a.dW : nullptr;
+    q.ldsrc = a.lddw;
+    return launch_product(h, q, static_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* args, void* stream)
@@ -241,26 +408,30 @@ gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* arg
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Blocks of 128 rows, down to the 32 that the workspace has room for when they would not fill the GPU.
+    const int64_t strips = cdiv(a.N, dtg::linear::kActCols);
+    const int64_t block_rows = strips * cdiv(a.M, 128) >= 2 * h->dev.num_sms ? 128 : kSumRows;
+    const int64_t blocks = cdiv(a.M, block_rows);
     if (a.M > 0 && (a.dZ || a.dbias)) {
-        dtg::linear::SimpleParams p = {};
-        p.A = a.dY;
-        p.C = a.dZ;
-        p.in = a.act != GEMM_ACT_NONE ? a.Z : nullptr;
+        dtg::linear::ActGradParams p;
+        p.dY = static_cast<const uint16_t*>(a.dY);
+        p.Z = static_cast<const uint16_t*>(a.Z);
+        p.dZ = static_cast<uint16_t*>(a.dZ);
         p.partials = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
-        p.pitch = sum_pitch(a.N);
         p.M = a.M;
         p.N = a.N;
-        p.a_m = a.lddy;
-        p.ldc = a.lddz;
-        p.ldin = a.ldz;
-        p.dtype = a.dtype;
-        p.act = a.act;
-        dtg::linear::simple_act_grad_kernel<<<static_cast<unsigned>(cdiv(a.M, 32) * cdiv(a.N, 32)), dim3(32, 32), 0, s>>>(p);
-        const gemm_status_t st = launched();
+        p.lddy = a.lddy;
+        p.ldz = a.ldz;
+        p.lddz = a.lddz;
+        p.pitch = sum_pitch(a.N);
+        p.block_rows = block_rows;
+        const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(std::min<int64_t>(blocks, 65535)));
+        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_act_grad<true>(p, a.act, grid, s)
+                                                            : launch_act_grad<false>(p, a.act, grid, s);
         if (st != GEMM_OK) return st;
     }
     if (!a.dbias) return GEMM_OK;
-    return launch_sums(static_cast<const float*>(a.workspace), a.M, a.N, a.dbias, a.dbias_dtype, a.beta_bias, s);
+    return launch_sums(a.workspace, blocks, a.N, a.dbias, a.dbias_dtype, a.beta_bias, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,717 @@
+// The linear-layer products on tcgen05: persistent, warp-specialised tile kernels with the
+// operator's arithmetic in the epilogue.
+//
+//   kForward  rows = tokens M, columns = outputs N, contraction K:   z = alpha X W^T + bias (kept on
+//             request), Y = act(z) + residual.            X and W are K-major.
+//   kDgrad    rows = tokens M, columns = inputs K, contraction N:    d = (alpha dY W) * act'(Z), dX = d,
+//             and the sums of d over each warp's 32 rows.  dY is K-major, W N-major (its rows are the contraction).
+//   kWgrad    rows = outputs N, columns = inputs K, contraction M:   dW = alpha dY^T X + beta dW.
+//             Both operands have the contraction as rows: A is M-major, B N-major.
+//
+// The work schedule (tile raster, stream-K shares, backwards K walks, CTA pairs), the operand
+// ring and the bounded waits are those of gemm_tcgen05_kernel.  What differs:
+//
+// Accumulation.  The tensor core's fp32 accumulator truncates: over one chain of 8192 products of
+// N(0, 1) data it ends 9.5e-6 (relative, in norm) below the exact sum, 4.5e-6 over 4096, 2.9e-7 over
+// 256, where fp32 fused multiply-adds stay at 1.6e-6 (8192).  So an item's K blocks run in chunks of
+// chunk_kb; each chunk overwrites one of the two TMEM accumulators, and the epilogue warps
+// add it to a running sum in their registers, rounding to nearest.  The MMAs of the next chunk
+// run meanwhile, so the tensor pipe does not wait, and an item's accumulator is free as soon as its last
+// chunk has been read, before any of the epilogue's arithmetic.
+//
+// Epilogue.  Eight warps, two per TMEM lane quadrant, each holding 32 rows x BN/2 columns of sums
+// (128 registers at BN = 256).  Four warps would need 256 registers each for the sums alone.  Per box of 128 bytes of output columns: bias through the warp's staging
+// buffer (every lane needs the same 64 values), residual or pre-activations straight from
+// global memory (16 bytes a load, a row's 128 bytes per lane), then the 128-byte-swizzled staging and TMA store.
+//
+// Column sums (kDgrad): the 32 lanes' rows are summed by five exchange steps that halve the columns
+// a lane holds each time, which leaves two finished columns per lane and a fixed order of additions.
+#pragma once
+
+#include "activation.cuh"
+#include "gemm_kernel.cuh"
+
+namespace dtg {
+namespace linear {
+
+constexpr int kForward = 0, kDgrad = 1, kWgrad = 2;
+constexpr int kOutF16 = 0, kOutBf16 = 1, kOutF32 = 2;
+// Warps 0-3: producer, MMA and two idle ones; warps 4-11: epilogue.  setmaxnreg moves registers
+// between them by warpgroup: the block starts with 384 x 168 = 64512, the first four warps go down
+// to 64, the epilogue's eight up to 216 (128 x 64 + 256 x 216 = 63488).
+constexpr int kTileThreads = 384;
+constexpr int kTileLaunchRegs = 168;
+constexpr int kTileMainRegs = 64;
+constexpr int kTileEpiRegs = 216;
+static_assert(128 * kTileMainRegs + 256 * kTileEpiRegs <= kTileThreads * kTileLaunchRegs, "the pool covers both shares");
+constexpr int kTileEpiWarp0 = 4;
+constexpr int kTileEpiWarps = 8;
+constexpr int kTileStgBytes = 4096;   // one warp's 32 rows x 128 bytes
+constexpr int kTileEpiBarrier = 1;
+
+struct TileParams : KernelParams {
+    int32_t chunk_kb;     // K blocks accumulated in TMEM before they join the fp32 registers' sums
+    int32_t act;          // gemm_act_t
+    const void* bias;     // forward; null: none
+    int32_t bias_f32;     // bias is fp32 (else of the output type)
+    const void* in;       // forward: residual; dgrad: pre-activations; wgrad: dW when beta != 0; null: none
+    int64_t ldin;
+    void* Z;              // forward: where z is kept; null: nowhere
+    int64_t ldz;
+    float* partials;      // dgrad: sums of 32-row blocks, `pitch` columns a row; null: none
+    int64_t pitch;
+};
+
+template <int B_ROWS, int STAGES>
+struct TileSmem {
+    static constexpr int kABytes = kBM * kRowBytes;
+    static constexpr int kStageBytes = kABytes + B_ROWS * kRowBytes;
+    static constexpr int kStgOff = STAGES * kStageBytes;
+    static constexpr int kBarOff = kStgOff + kTileEpiWarps * kTileStgBytes;
+    static constexpr int kNumBars = 2 * STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+    static constexpr int kTotal = kMiscOff + 16;  // tmem slot, abort flag, stream-K "last" flag
+    static constexpr int kAlloc = kTotal + 1024;  // slack for aligning the base to 1 KB
+    static_assert(kStageBytes % 1024 == 0 && kStgOff % 1024 == 0, "swizzle atoms need 1 KB alignment");
+    static_assert(kAlloc <= 227 * 1024, "fits an SM");
+};
+
+template <int N>
+__device__ __forceinline__ void registers_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void registers_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tile_epi_sync()
+{
+    asm volatile("bar.sync %0, %1;" ::"n"(kTileEpiBarrier), "n"(kTileEpiWarps * 32) : "memory");
+}
+
+// Barrier of the eight epilogue warps that also ANDs a flag over their threads.
+__device__ __forceinline__ bool tile_epi_and(bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\t"
+        "setp.ne.u32 pi, %1, 0;\n\t"
+        "bar.red.and.pred po, %2, %3, pi;\n\t"
+        "selp.u32 %0, 1, 0, po;\n\t}\n"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u), "n"(kTileEpiBarrier), "n"(kTileEpiWarps * 32)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ float unpack_lo(uint32_t w)
+{
+    if constexpr (BF16) return __uint_as_float(w << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xFFFFu)));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float unpack_hi(uint32_t w)
+{
+    if constexpr (BF16) return __uint_as_float(w & 0xFFFF0000u);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+}
+
+// Elements [col, col + 64) of a 16-bit row, two per word; zeros from column N on.
+__device__ __forceinline__ void load_row16(uint32_t (&r)[32], const uint16_t* row, int64_t col, int64_t N)
+{
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        const int64_t c = col + ch * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c + 8 <= N) {
+            v = *reinterpret_cast<const uint4*>(row + c);
+        } else if (c < N) {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < N) w[e >> 1] |= static_cast<uint32_t>(row[c + e]) << ((e & 1) * 16);
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        r[4 * ch] = v.x;
+        r[4 * ch + 1] = v.y;
+        r[4 * ch + 2] = v.z;
+        r[4 * ch + 3] = v.w;
+    }
+}
+
+// Elements [col, col + 32) of an fp32 row; zeros from column N on.
+__device__ __forceinline__ void load_row32(float (&r)[32], const float* row, int64_t col, int64_t N)
+{
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        const int64_t c = col + ch * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c + 4 <= N) {
+            v = *reinterpret_cast<const float4*>(row + c);
+        } else if (c < N) {
+            v.x = row[c];
+            if (c + 1 < N) v.y = row[c + 1];
+            if (c + 2 < N) v.z = row[c + 2];
+        }
+        r[4 * ch] = v.x;
+        r[4 * ch + 1] = v.y;
+        r[4 * ch + 2] = v.z;
+        r[4 * ch + 3] = v.w;
+    }
+}
+
+// Write a warp's box (lane = row y + lane, 128 bytes from column x: h) through its staging buffer
+// and a TMA store, which drops rows >= M and columns >= N.  TMA clips columns to 16-byte
+// granules only, so a box that straddles a ragged N is written with masked stores.
+template <int ELEM>
+__device__ __forceinline__ void store_rows(const uint32_t (&h)[32], int32_t x, int32_t y, int lane, uint32_t stg,
+                                           const CUtensorMap* tm, void* base, int64_t ld, int32_t M, int32_t N)
+{
+    constexpr int kPerChunk = 16 / ELEM;   // elements of 16 bytes
+    constexpr int kCols = 128 / ELEM;
+    if (N % kPerChunk != 0 && x + kCols > N) {
+        const int64_t row = static_cast<int64_t>(y) + lane;
+        if (row < M) {
+            uint8_t* dst = static_cast<uint8_t*>(base) + (row * ld + x) * ELEM;
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+                const int32_t col = x + ch * kPerChunk;
+                if (col + kPerChunk <= N) {
+                    *reinterpret_cast<uint4*>(dst + ch * 16) = make_uint4(h[4 * ch], h[4 * ch + 1], h[4 * ch + 2], h[4 * ch + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kPerChunk; ++e)
+                        if (col + e < N) {
+                            if constexpr (ELEM == 2)
+                                reinterpret_cast<uint16_t*>(dst)[8 * ch + e] = half_of(h, 8 * ch + e);
+                            else
+                                reinterpret_cast<uint32_t*>(dst)[4 * ch + e] = h[4 * ch + e];
+                        }
+                }
+            }
+        }
+        return;
+    }
+    if (lane == 0) ptx::bulk_wait_group_read<0>();  // the last store has read the buffer
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch)
+        ptx::st_shared_v4(stg + lane * 128 + ((ch ^ (lane & 7)) << 4), h[4 * ch], h[4 * ch + 1], h[4 * ch + 2], h[4 * ch + 3]);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        ptx::tma_store_2d(tm, stg, x, y);
+        ptx::bulk_commit_group();
+    }
+}
+
+// Sums over the warp's 32 rows of 64 columns held one row per lane: lane l ends with columns 2l, 2l + 1
+// in v[0], v[1].  Each step exchanges half of the columns still held with the lane `off` away.
+__device__ __forceinline__ void sum_rows(float* v, int lane)
+{
+#pragma unroll
+    for (int off = 16, n = 32; off > 0; off >>= 1, n >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = upper ? v[i] : v[i + n];
+            const float keep = upper ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
+        }
+    }
+}
+
+// IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward, kDgrad,
+// kWgrad; CLUSTER: 1 (one CTA) or 2 (a CTA pair).
+template <int BN, int STAGES, int IN, int OUT, int MODE, int CLUSTER>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ, const TileParams p)
+{
+    using T = Operand<IN>;
+    static_assert(IN <= 3 && (BN == 128 || BN == 256), "dense operands, 64 or 128 columns per epilogue warp");
+    static_assert(MODE == kForward || !T::kF8, "8-bit operands: forward only");
+    static_assert(OUT != kOutF32 || MODE == kWgrad, "fp32 output: weight gradients only");
+    constexpr bool PAIR = CLUSTER == 2;
+    constexpr bool AT = MODE == kWgrad;        // A is M-major
+    constexpr bool BT = MODE != kForward;      // B is N-major
+    constexpr int kRanks = PAIR ? 2 : 1;
+    constexpr int kTileM = kBM * kRanks;
+    constexpr int kBRows = BN / kRanks;
+    constexpr int CW = BN / 2;                 // columns per epilogue warp
+    constexpr uint32_t kTmemCols = 2 * BN;
+    using L = TileSmem<kBRows, STAGES>;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw_addr);
+    const uint32_t bar0 = base + L::kBarOff;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+    volatile int32_t* const abort_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 4);
+    volatile int32_t* const last_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 8);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;  // 0: the leader, which issues the pair's MMAs
+    const bool leader = rank == 0;
+    const int64_t unit = PAIR ? static_cast<int64_t>(ptx::cluster_id_x()) : static_cast<int64_t>(blockIdx.x);
+    const int64_t units = PAIR ? static_cast<int64_t>(ptx::num_clusters_x()) : static_cast<int64_t>(gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(accf_bar(b), 1);
+            ptx::mbar_init(acce_bar(b), kTileEpiWarps * kRanks);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        *last_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmA);
+        ptx::prefetch_tmap(&tmB);
+        ptx::prefetch_tmap(&tmC);
+    }
+    if (warp == kMmaWarp) {
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(tmem_slot), kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (PAIR)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    // Global memory waits for the stream's previous kernel.
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+
+    Watchdog wd{abort_flag, &p};
+    if constexpr (PAIR) wd.peer_abort = ptx::mapa_shared(ptx::smem_addr(const_cast<int32_t*>(abort_flag)), rank ^ 1u);
+
+    if (warp < kTileEpiWarp0) registers_down<kTileMainRegs>();
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            // ---------------------------------------------------------------- producer
+            uint32_t armed_mask = 0, armed_parity = 0;  // leader: stages armed, last parity
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t loaded = 0;
+            WorkIter it(p, unit, units);
+            int64_t tile;
+            int kb0, kb1;
+            while (it.next(p, tile, kb0, kb1)) {
+                int64_t tm, tn;
+                tile_coord(tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+                const int32_t y_a = static_cast<int32_t>(tm * kTileM + rank * kBM);
+                const int32_t n_b = static_cast<int32_t>(tn * BN + rank * kBRows);
+                const bool rev = it.reversed(p);
+                for (int i = 0; i < kb1 - kb0; ++i, ++loaded) {
+                    const int kb = rev ? kb1 - 1 - i : kb0 + i;
+                    if (!wd.wait(empty_bar(stage), phase ^ 1u, kRoleProducer, tile, kb)) goto producer_done;
+                    // Test hook: the first unit leaves one stage unloaded and unarmed.
+                    if (!(p.fault_inject && unit == 0 && loaded == 1)) {
+                        const uint32_t sa = base + stage * L::kStageBytes;
+                        const uint32_t sb = sa + L::kABytes;
+                        const int32_t k0 = kb * T::kStageK;
+                        const uint32_t fb = PAIR ? ptx::mapa_shared(full_bar(stage), 0u) : full_bar(stage);
+                        if (leader) {
+                            ptx::mbar_arrive_expect_tx(full_bar(stage), kRanks * L::kStageBytes);
+                            armed_mask |= 1u << stage;
+                            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                        }
+                        auto load = [&](uint32_t dst, const CUtensorMap* tm_, int32_t x, int32_t y) {
+                            if constexpr (PAIR)
+                                ptx::tma_load_2d_pair(dst, tm_, x, y, fb);
+                            else
+                                ptx::tma_load_2d(dst, tm_, x, y, fb);
+                        };
+                        if constexpr (AT) {
+                            // A stored contraction x rows: boxes of 64 rows (128 bytes) by kStageK contraction rows.
+#pragma unroll
+                            for (int q = 0; q < kBM / T::kNBlock; ++q)
+                                load(sa + q * (T::kStageK * 128), &tmA, y_a + q * T::kNBlock, k0);
+                        } else {
+                            load(sa, &tmA, k0, y_a);
+                        }
+                        if constexpr (BT) {
+#pragma unroll
+                            for (int q = 0; q < kBRows / T::kNBlock; ++q)
+                                load(sb + q * (T::kStageK * 128), &tmB, n_b + q * T::kNBlock, k0);
+                        } else {
+                            load(sb, &tmB, k0, n_b);
+                        }
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // Tail: every stage released, so no commit's arrival is still heading for this CTA.
+            for (int i = 0; i < STAGES; ++i) {
+                if (!wd.wait(empty_bar(stage), phase ^ 1u, kRoleProducer, -1, i)) goto producer_done;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        producer_done:
+            // The leader's full barriers count every load of the CTA (pair).
+            if (leader)
+                for (int s = 0; s < STAGES; ++s)
+                    if (armed_mask & (1u << s)) wd.drain(full_bar(s), (armed_parity >> s) & 1u);
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0 && leader) {
+            // ---------------------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc = idesc_mma<T::kFormat, BT, kTileM, BN>() | (AT ? 1u << 15 : 0u);
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool aborted = false;
+            WorkIter it(p, unit, units);
+            int64_t tile;
+            int kb0, kb1;
+            while (!aborted && it.next(p, tile, kb0, kb1)) {
+                int in_chunk = 0;
+                for (int i = 0; i < kb1 - kb0; ++i) {
+                    if (in_chunk == 0) {
+                        if (!wd.wait(acce_bar(acc), acc_phase ^ 1u, kRoleMma, tile, -1)) {
+                            aborted = true;
+                            break;
+                        }
+                    }
+                    if (!wd.wait(full_bar(stage), phase, kRoleMma, tile, kb0 + i)) {
+                        aborted = true;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                    const uint32_t sa = base + stage * L::kStageBytes;
+                    const uint32_t sb = sa + L::kABytes;
+#pragma unroll
+                    for (int k = 0; k < T::kStageK / T::kMmaK; ++k) {
+                        // K-major: the k-th slice starts 32 bytes further along each 128-byte row.  M- or N-major:
+                        // rows are the contraction, the k-th slice starts kMmaK rows of 128 bytes on, and 64-wide
+                        // blocks are kStageK rows apart.
+                        const uint64_t adesc = AT ? smem_desc_sw128(sa + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
+                                                  : smem_desc_sw128(sa + k * 32, 16, 1024);
+                        const uint64_t bdesc = BT ? smem_desc_sw128(sb + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
+                                                  : smem_desc_sw128(sb + k * 32, 16, 1024);
+                        const uint32_t accumulate = (in_chunk != 0 || k != 0) ? 1u : 0u;
+                        if constexpr (PAIR) {
+                            if constexpr (T::kF8)
+                                ptx::mma_f8_pair(d_tmem, adesc, bdesc, idesc, accumulate);
+                            else
+                                ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, accumulate);
+                        } else {
+                            if constexpr (T::kF8)
+                                ptx::mma_f8_cta1(d_tmem, adesc, bdesc, idesc, accumulate);
+                            else
+                                ptx::mma_f16_cta1(d_tmem, adesc, bdesc, idesc, accumulate);
+                        }
+                    }
+                    if constexpr (PAIR)
+                        ptx::mma_commit_pair(empty_bar(stage), 0x3);
+                    else
+                        ptx::mma_commit_cta1(empty_bar(stage));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++in_chunk == p.chunk_kb || i + 1 == kb1 - kb0) {
+                        if constexpr (PAIR)
+                            ptx::mma_commit_pair(accf_bar(acc), 0x3);
+                        else
+                            ptx::mma_commit_cta1(accf_bar(acc));
+                        in_chunk = 0;
+                        acc ^= 1;
+                        if (acc == 0) acc_phase ^= 1u;
+                    }
+                }
+            }
+            if (aborted) {
+                // Let every MMA issued so far finish before the TMEM is released.
+                if constexpr (PAIR)
+                    ptx::mma_commit_pair(drain_bar, static_cast<uint16_t>(1u << rank));
+                else
+                    ptx::mma_commit_cta1(drain_bar);
+                wd.drain(drain_bar, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kTileEpiWarp0) {
+        // -------------------------------------------------------------------- epilogue
+        registers_up<kTileEpiRegs>();
+        const int ew = warp - kTileEpiWarp0;     // 0..7
+        const int quad = warp & 3;               // TMEM lane quadrant this warp may read
+        const int half = ew >> 2;                // which BN/2 columns of the tile
+        const int row_in_cta = quad * 32 + lane;
+        const uint32_t stg = base + L::kStgOff + ew * kTileStgBytes;
+        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+        constexpr bool kBf16 = OUT == kOutBf16;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        WorkIter it(p, unit, units);
+        int64_t tile;
+        int kb0, kb1;
+        float s[CW];  // this thread's sums: row row_in_cta, columns half * CW ...
+
+        // The operator on the finished sums of the tile at (tm, tn), and its stores.
+        auto finish = [&](int64_t tm, int64_t tn) {
+            const int32_t y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
+            const int64_t row = static_cast<int64_t>(y) + lane;
+            const bool row_in = row < p.M;
+            if (y >= p.M) return;
+            if constexpr (OUT == kOutF32) {
+#pragma unroll
+                for (int b = 0; b < CW / 32; ++b) {
+                    const int32_t x = static_cast<int32_t>(tn * BN + half * CW + b * 32);
+                    if (x >= p.N) break;
+                    uint32_t h[32];
+                    float r[32];
+                    if (p.in && row_in) {
+                        load_row32(r, static_cast<const float*>(p.in) + row * p.ldin, x, p.N);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(fmaf(p.beta, r[i], p.alpha * s[b * 32 + i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(p.alpha * s[b * 32 + i]);
+                    }
+                    store_rows<4>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < CW / 64; ++b) {
+                    const int32_t x = static_cast<int32_t>(tn * BN + half * CW + b * 64);
+                    if (x >= p.N) break;
+                    float* const v = &s[b * 64];
+                    uint32_t r[32];
+                    const bool has_in = p.in != nullptr;
+                    if (has_in) {
+                        if (row_in)
+                            load_row16(r, static_cast<const uint16_t*>(p.in) + row * p.ldin, x, p.N);
+                        else
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[i] = 0;
+                    }
+                    if (MODE == kForward && p.bias) {
+                        // The box's 64 biases go through the staging buffer, from which all lanes read them.
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int32_t c = x + lane + 32 * e;
+                            float f = 0.0f;
+                            if (c < p.N)
+                                f = p.bias_f32 ? static_cast<const float*>(p.bias)[c]
+                                               : load16<kBf16>(static_cast<const uint16_t*>(p.bias) + c);
+                            st_shared_f32(stg + 4 * (lane + 32 * e), f);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 f = ld_shared_f4(stg + 16 * i);
+                            v[4 * i] = fmaf(p.alpha, v[4 * i], f.x);
+                            v[4 * i + 1] = fmaf(p.alpha, v[4 * i + 1], f.y);
+                            v[4 * i + 2] = fmaf(p.alpha, v[4 * i + 2], f.z);
+                            v[4 * i + 3] = fmaf(p.alpha, v[4 * i + 3], f.w);
+                        }
+                        __syncwarp();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i] *= p.alpha;
+                    }
+                    uint32_t h[32];
+                    if constexpr (MODE == kForward) {
+                        if (p.Z) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) h[i] = pack2<kBf16>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+                            store_rows<2>(h, x, y, lane, stg, &tmZ, p.Z, p.ldz, p.M, p.N);
+                        }
+                        DTG_ACT_SWITCH(p.act, {
+                            _Pragma("unroll") for (int i = 0; i < 64; ++i) v[i] = act_value<ACT>(v[i]);
+                        });
+                        if (has_in) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                v[2 * i] += unpack_lo<kBf16>(r[i]);
+                                v[2 * i + 1] += unpack_hi<kBf16>(r[i]);
+                            }
+                        }
+                    }
+                    if constexpr (MODE == kDgrad) {
+                        if (has_in) {
+                            DTG_ACT_SWITCH(p.act, {
+                                _Pragma("unroll") for (int i = 0; i < 32; ++i)
+                                {
+                                    v[2 * i] *= act_slope<ACT>(unpack_lo<kBf16>(r[i]));
+                                    v[2 * i + 1] *= act_slope<ACT>(unpack_hi<kBf16>(r[i]));
+                                }
+                            });
+                        }
+                    }
+                    if constexpr (MODE == kWgrad) {
+                        if (has_in) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                v[2 * i] = fmaf(p.beta, unpack_lo<kBf16>(r[i]), v[2 * i]);
+                                v[2 * i + 1] = fmaf(p.beta, unpack_hi<kBf16>(r[i]), v[2 * i + 1]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) h[i] = pack2<kBf16>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
+                    store_rows<2>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+                    if constexpr (MODE == kDgrad) {
+                        if (p.partials) {
+                            // Rows past M are not part of the sums (an infinite weight makes them NaN).
+                            if (!row_in) {
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                            }
+                            sum_rows(v, lane);
+                            *reinterpret_cast<float2*>(p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + 2 * lane) =
+                                make_float2(v[0], v[1]);
+                        }
+                    }
+                }
+            }
+        };
+
+        while (it.next(p, tile, kb0, kb1)) {
+            int64_t tm, tn;
+            tile_coord(tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+#pragma unroll
+            for (int i = 0; i < CW; ++i) s[i] = 0.0f;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
+                ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (ok) {
+                    ptx::tc_fence_after_sync();
+                    const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
+#pragma unroll
+                    for (int q = 0; q < CW / 32; ++q) {
+                        uint32_t v[32];
+                        ptx::tmem_ld_32x32b_x32(tacc + q * 32, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[q * 32 + i] += __uint_as_float(v[i]);
+                    }
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR)
+                            ptx::mbar_arrive_cluster(ptx::mapa_shared(acce_bar(acc), 0u));
+                        else
+                            ptx::mbar_arrive(acce_bar(acc));
+                    }
+                }
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!tile_epi_and(ok)) break;  // all eight epilogue warps leave together
+            if (kb0 == 0 && kb1 == p.num_kb) {
+                finish(tm, tn);
+                continue;
+            }
+            // Part of a stream-K tile: park the sums in this unit's slot and count the part in; the last part to
+            // arrive adds all of them in K order, whatever the order of arrival.
+            const int64_t tr = tile - p.dp_tiles;
+            constexpr size_t kSlotF4 = static_cast<size_t>(kBM) * BN / 4;
+            auto slot_f4 = [&](int64_t slot) {
+                return reinterpret_cast<float4*>(p.ws) + (static_cast<size_t>(slot) * CLUSTER + rank) * kSlotF4 +
+                       static_cast<size_t>(half * (CW / 4)) * kBM + row_in_cta;
+            };
+            int64_t first_unit, parts;
+            sk_parts(p, tr, first_unit, parts);
+            int32_t* const counter = p.counters + tr * CLUSTER + rank;
+            float4* const mine = slot_f4(sk_slot(p, unit, tr));
+#pragma unroll
+            for (int q = 0; q < CW / 4; ++q) mine[q * kBM] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+            __threadfence();
+            tile_epi_sync();
+            if (ew == 0 && lane == 0) {
+                const bool last = atomicAdd(counter, 1) == parts - 1;
+                if (last) {
+                    *counter = 0;  // ready for the next launch
+                    __threadfence();
+                }
+                *last_flag = last ? 1 : 0;
+            }
+            tile_epi_sync();
+            if (*last_flag) {
+#pragma unroll
+                for (int i = 0; i < CW; ++i) s[i] = 0.0f;
+                for (int64_t part = 0; part < parts; ++part) {
+                    const float4* f4 = slot_f4(sk_slot(p, first_unit + part, tr));
+#pragma unroll
+                    for (int q0 = 0; q0 < CW / 4; q0 += 8) {
+                        float4 f[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) f[q] = __ldcg(f4 + (q0 + q) * kBM);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            s[4 * (q0 + q)] += f[q].x;
+                            s[4 * (q0 + q) + 1] += f[q].y;
+                            s[4 * (q0 + q) + 2] += f[q].z;
+                            s[4 * (q0 + q) + 3] += f[q].w;
+                        }
+                    }
+                }
+                finish(tm, tn);
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (PAIR) ptx::cluster_sync();  // neither CTA exits or frees TMEM while the peer may use it
+    if (warp == kMmaWarp) {
+        ptx::tc_fence_after_sync();
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+        else
+            ptx::tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+}  // namespace linear
+}  // namespace dtg
