@@ -45,7 +45,7 @@ __device__ __forceinline__ void load8(uint32_t (&r)[4], const uint16_t* row, int
 }
 
 template <bool BF16, int ACT>
-__global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradParams p)
+__global__ void __launch_bounds__(kActWarps * 32, 3) act_grad_kernel(const ActGradParams p)
 {
     __shared__ float sums[kActWarps][kActCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -408,9 +408,9 @@ gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* arg
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Blocks of 128 rows, down to the 32 that the workspace has room for when they would not fill the GPU.
+    // Blocks of 64 rows, or the 32 that the workspace has room for when those would not fill the GPU.
     const int64_t strips = cdiv(a.N, dtg::linear::kActCols);
-    const int64_t block_rows = strips * cdiv(a.M, 128) >= 2 * h->dev.num_sms ? 128 : kSumRows;
+    const int64_t block_rows = strips * cdiv(a.M, 64) >= 6 * h->dev.num_sms ? 64 : kSumRows;
     const int64_t blocks = cdiv(a.M, block_rows);
     if (a.M > 0 && (a.dZ || a.dbias)) {
         dtg::linear::ActGradParams p;

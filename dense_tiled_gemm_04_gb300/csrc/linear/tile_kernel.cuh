@@ -135,46 +135,43 @@ __device__ __forceinline__ float unpack_hi(uint32_t w)
 }
 
 // Elements [col, col + 64) of a 16-bit row, two per word; zeros from column N on.
-__device__ __forceinline__ void load_row16(uint32_t (&r)[32], const uint16_t* row, int64_t col, int64_t N)
+__device__ __forceinline__ void load_row16(uint32_t (&r)[32], const uint16_t* row, int32_t col, int32_t N)
 {
+    row += col;
+    if (col + 64 <= N) {
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-        const int64_t c = col + ch * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c + 8 <= N) {
-            v = *reinterpret_cast<const uint4*>(row + c);
-        } else if (c < N) {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < N) w[e >> 1] |= static_cast<uint32_t>(row[c + e]) << ((e & 1) * 16);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int ch = 0; ch < 8; ++ch) {
+            const uint4 v = reinterpret_cast<const uint4*>(row)[ch];
+            r[4 * ch] = v.x;
+            r[4 * ch + 1] = v.y;
+            r[4 * ch + 2] = v.z;
+            r[4 * ch + 3] = v.w;
         }
-        r[4 * ch] = v.x;
-        r[4 * ch + 1] = v.y;
-        r[4 * ch + 2] = v.z;
-        r[4 * ch + 3] = v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            r[i] = col + 2 * i < N ? row[2 * i] : 0u;
+            if (col + 2 * i + 1 < N) r[i] |= static_cast<uint32_t>(row[2 * i + 1]) << 16;
+        }
     }
 }
 
 // Elements [col, col + 32) of an fp32 row; zeros from column N on.
-__device__ __forceinline__ void load_row32(float (&r)[32], const float* row, int64_t col, int64_t N)
+__device__ __forceinline__ void load_row32(float (&r)[32], const float* row, int32_t col, int32_t N)
 {
+    row += col;
+    if (col + 32 <= N) {
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-        const int64_t c = col + ch * 4;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (c + 4 <= N) {
-            v = *reinterpret_cast<const float4*>(row + c);
-        } else if (c < N) {
-            v.x = row[c];
-            if (c + 1 < N) v.y = row[c + 1];
-            if (c + 2 < N) v.z = row[c + 2];
+        for (int ch = 0; ch < 8; ++ch) {
+            const float4 v = reinterpret_cast<const float4*>(row)[ch];
+            r[4 * ch] = v.x;
+            r[4 * ch + 1] = v.y;
+            r[4 * ch + 2] = v.z;
+            r[4 * ch + 3] = v.w;
         }
-        r[4 * ch] = v.x;
-        r[4 * ch + 1] = v.y;
-        r[4 * ch + 2] = v.z;
-        r[4 * ch + 3] = v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = col + i < N ? row[i] : 0.0f;
     }
 }
 
@@ -613,7 +610,57 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
 
-        while (it.next(p, tile, kb0, kb1)) {
+        // Part of a stream-K tile: park the sums in this unit's slot and count the part in; the last part to
+        // arrive adds all of them in K order, whatever the order of arrival.  True for that one, which then holds the
+        // tile's sums.
+        auto join_parts = [&](int64_t tile) -> bool {
+            const int64_t tr = tile - p.dp_tiles;
+            constexpr size_t kSlotF4 = static_cast<size_t>(kBM) * BN / 4;
+            auto slot_f4 = [&](int64_t slot) {
+                return reinterpret_cast<float4*>(p.ws) + (static_cast<size_t>(slot) * CLUSTER + rank) * kSlotF4 +
+                       static_cast<size_t>(half * (CW / 4)) * kBM + row_in_cta;
+            };
+            int64_t first_unit, parts;
+            sk_parts(p, tr, first_unit, parts);
+            int32_t* const counter = p.counters + tr * CLUSTER + rank;
+            float4* const mine = slot_f4(sk_slot(p, unit, tr));
+#pragma unroll
+            for (int q = 0; q < CW / 4; ++q) mine[q * kBM] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+            __threadfence();
+            tile_epi_sync();
+            if (ew == 0 && lane == 0) {
+                const bool last = atomicAdd(counter, 1) == parts - 1;
+                if (last) {
+                    *counter = 0;  // ready for the next launch
+                    __threadfence();
+                }
+                *last_flag = last ? 1 : 0;
+            }
+            tile_epi_sync();
+            if (*last_flag == 0) return false;
+#pragma unroll
+            for (int i = 0; i < CW; ++i) s[i] = 0.0f;
+            for (int64_t part = 0; part < parts; ++part) {
+                    const float4* f4 = slot_f4(sk_slot(p, first_unit + part, tr));
+#pragma unroll
+                    for (int q0 = 0; q0 < CW / 4; q0 += 8) {
+                        float4 f[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) f[q] = __ldcg(f4 + (q0 + q) * kBM);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            s[4 * (q0 + q)] += f[q].x;
+                            s[4 * (q0 + q) + 1] += f[q].y;
+                            s[4 * (q0 + q) + 2] += f[q].z;
+                            s[4 * (q0 + q) + 3] += f[q].w;
+                        }
+                    }
+                }
+            return true;
+        };
+
+        // One work item; false when the launch is being abandoned.
+        auto one_item = [&](int64_t tile, int kb0, int kb1) -> bool {
             int64_t tm, tn;
             tile_coord(tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
 #pragma unroll
@@ -645,57 +692,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
-            if (!tile_epi_and(ok)) break;  // all eight epilogue warps leave together
-            if (kb0 == 0 && kb1 == p.num_kb) {
-                finish(tm, tn);
-                continue;
-            }
-            // Part of a stream-K tile: park the sums in this unit's slot and count the part in; the last part to
-            // arrive adds all of them in K order, whatever the order of arrival.
-            const int64_t tr = tile - p.dp_tiles;
-            constexpr size_t kSlotF4 = static_cast<size_t>(kBM) * BN / 4;
-            auto slot_f4 = [&](int64_t slot) {
-                return reinterpret_cast<float4*>(p.ws) + (static_cast<size_t>(slot) * CLUSTER + rank) * kSlotF4 +
-                       static_cast<size_t>(half * (CW / 4)) * kBM + row_in_cta;
-            };
-            int64_t first_unit, parts;
-            sk_parts(p, tr, first_unit, parts);
-            int32_t* const counter = p.counters + tr * CLUSTER + rank;
-            float4* const mine = slot_f4(sk_slot(p, unit, tr));
+            if (!tile_epi_and(ok)) return false;
+            const bool whole = kb0 == 0 && kb1 == p.num_kb;
+            if (whole || join_parts(tile)) finish(tm, tn);
+            return true;
+        };
+
+        // Bring the lines of `in` that this thread will read for a tile into L2.  An item ahead, so that
+        // the loads in finish() find them there even when the accumulators never wait.
+        auto prefetch_in = [&](int64_t t) {
+            if (!p.in) return;
+            int64_t tm, tn;
+            tile_coord(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+            const int64_t row = tm * kTileM + rank * kBM + row_in_cta;
+            if (row >= p.M) return;
+            constexpr int kElem = OUT == kOutF32 ? 4 : 2;
+            const uint8_t* line = static_cast<const uint8_t*>(p.in) + (row * p.ldin + tn * BN + half * CW) * kElem;
 #pragma unroll
-            for (int q = 0; q < CW / 4; ++q) mine[q * kBM] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
-            __threadfence();
-            tile_epi_sync();
-            if (ew == 0 && lane == 0) {
-                const bool last = atomicAdd(counter, 1) == parts - 1;
-                if (last) {
-                    *counter = 0;  // ready for the next launch
-                    __threadfence();
-                }
-                *last_flag = last ? 1 : 0;
-            }
-            tile_epi_sync();
-            if (*last_flag) {
-#pragma unroll
-                for (int i = 0; i < CW; ++i) s[i] = 0.0f;
-                for (int64_t part = 0; part < parts; ++part) {
-                    const float4* f4 = slot_f4(sk_slot(p, first_unit + part, tr));
-#pragma unroll
-                    for (int q0 = 0; q0 < CW / 4; q0 += 8) {
-                        float4 f[8];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) f[q] = __ldcg(f4 + (q0 + q) * kBM);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            s[4 * (q0 + q)] += f[q].x;
-                            s[4 * (q0 + q) + 1] += f[q].y;
-                            s[4 * (q0 + q) + 2] += f[q].z;
-                            s[4 * (q0 + q) + 3] += f[q].w;
-                        }
-                    }
-                }
-                finish(tm, tn);
-            }
+            for (int b = 0; b < CW * kElem / 128; ++b)
+                if (tn * BN + half * CW + b * (128 / kElem) < p.N)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
+        };
+        bool more = it.next(p, tile, kb0, kb1);
+        if (more) prefetch_in(tile);
+        while (more) {
+            const int64_t this_tile = tile;
+            const int this_kb0 = kb0, this_kb1 = kb1;
+            more = it.next(p, tile, kb0, kb1);
+            if (more) prefetch_in(tile);
+            if (!one_item(this_tile, this_kb0, this_kb1)) break;  // all eight epilogue warps leave together
         }
         if (lane == 0) ptx::bulk_wait_group_all();
         __syncwarp();

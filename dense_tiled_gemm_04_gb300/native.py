@@ -6,7 +6,6 @@ or the device is not an sm_103 GPU, the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -204,25 +203,36 @@ def empty_output(M: int, N: int, dtype: torch.dtype, device) -> torch.Tensor:
     return torch.empty((M, ldc), dtype=dtype, device=device)[:, :N]
 
 
-def _matrix(t: torch.Tensor, what: str, shape, dtype, device) -> int:
-    """Check a 2-D tensor argument and return its leading dimension."""
-    if t.dtype != dtype:
+# The checks of the linear-layer calls run for every call, also those of a few microseconds: they
+# touch each tensor's attributes as few times as they can.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(device).cuda_stream, without the wrapper
+
+
+def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dtype: torch.dtype, device: int) -> int:
+    """Check a 2-D tensor argument and return its leading dimension (one-row tensors: the padded row length)."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must have shape {(rows, cols)}, not {tuple(t.shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, not {t.device}")
-    return _ld(t)
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit stride along the last dimension (row-major)")
+    if rows <= 1:
+        align = 16 // t.element_size()
+        return max(-(-cols // align) * align, align)
+    return ld
 
 
-def _vector(t: torch.Tensor, what: str, n: int, dtypes, device) -> int:
-    """Check a dense 1-D tensor argument and return its element type's code."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != 1 or t.size(0) != n or (n > 1 and t.stride(0) != 1):
+def _vector(t: torch.Tensor, what: str, n: int, dtype: torch.dtype, device: int) -> int:
+    """Check a dense 1-D tensor argument, float32 or `dtype`, and return its element type's code."""
+    if t.dtype is not torch.float32 and t.dtype is not dtype:
+        raise TypeError(f"{what} must be float32 or {dtype}, not {t.dtype}")
+    if t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ValueError(f"{what} must be a dense vector of {n} elements")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
     return TORCH_TO_DTYPE_F32[t.dtype]
 
 
@@ -232,24 +242,23 @@ def _act(name) -> int:
     return ACTS[name]
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr() or None
-
-
-def _on_stream(stream, device):
-    """A context in which new tensors belong to `stream` (None: the current stream), so that their
-    memory is not handed out again while the stream still uses it."""
+def _new(rows: int, cols: int, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
+    """A new output that belongs to `stream` (None: the current stream), so that its memory is not
+    handed out again while the stream still uses it."""
     if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
-                             torch.cuda.ExternalStream(int(stream), device=device))
+        return _padded_output(rows, cols, dtype, device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return _padded_output(rows, cols, dtype, device)
 
 
 def _padded_output(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     """A rows x cols output whose row pitch is a multiple of 16 bytes."""
-    align = 4 if dtype == torch.float32 else 8
+    align = 4 if dtype is torch.float32 else 8
     ld = max(-(-cols // align) * align, align)
-    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
+    t = torch.empty((rows, ld), dtype=dtype, device=device)
+    return t if ld == cols else t[:, :cols]
 
 
 class Gemm:
@@ -260,6 +269,7 @@ class Gemm:
         if device is None:
             device = torch.cuda.current_device()
         self.device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+        self._index = self.device.index or 0
         h = ctypes.c_void_p()
         st = lib.gemm_create(ctypes.byref(h), self.device.index or 0)
         if st != OK:
@@ -491,14 +501,6 @@ class Gemm:
                                            _stream_ptr(stream) or None))
 
     # -------------------------------------------------------------- linear layers
-    def _device(self) -> torch.device:
-        return torch.device("cuda", self.device.index or 0)
-
-    def _stream(self, stream) -> int:
-        if stream is None:
-            return torch.cuda.current_stream(self._device()).cuda_stream
-        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-
     def linear(self, X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = None,
                residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
                preact: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, alpha: float = 1.0,
@@ -506,28 +508,32 @@ class Gemm:
         """Y = act(alpha * X·W^T + bias) + residual (gemm_run_linear): X (M x K) and W (N x K) 16-bit or
         8-bit floats, Y, residual and preact float16 or bfloat16, bias float32 or Y's type.  ``preact``, if
         given, receives alpha * X·W^T + bias; ``out`` may be ``residual`` itself.  Async on `stream`."""
-        if X.dtype != W.dtype or X.dtype not in TORCH_TO_DTYPE_EX:
+        dt, dev = X.dtype, self._index
+        in_code = TORCH_TO_DTYPE_EX.get(dt)
+        if in_code is None:
             raise TypeError("X and W must have the same 16-bit or 8-bit float type")
-        if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
-            raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
-        dev = self._device()
+        if X.dim() != 2 or W.dim() != 2:
+            raise ValueError("expected 2-D tensors")
         (M, K), N = X.shape, W.shape[0]
         if out_dtype is None:
-            out_dtype = out.dtype if out is not None else (X.dtype if X.dtype in TORCH_TO_DTYPE else torch.bfloat16)
-        if out_dtype not in TORCH_TO_DTYPE or (X.dtype in TORCH_TO_DTYPE and out_dtype != X.dtype):
+            out_dtype = out.dtype if out is not None else (dt if in_code <= DTYPE_BF16 else torch.bfloat16)
+        out_code = TORCH_TO_DTYPE.get(out_dtype)
+        if out_code is None or (in_code <= DTYPE_BF16 and out_code != in_code):
             raise TypeError("Y must be float16 or bfloat16, and of the operands' type if that is 16-bit")
-        ldx, ldw = _matrix(X, "X", (M, K), X.dtype, dev), _matrix(W, "W", (N, K), X.dtype, dev)
-        bias_dtype = 0 if bias is None else _vector(bias, "bias", N, (torch.float32, out_dtype), dev)
-        ldr = 0 if residual is None else _matrix(residual, "residual", (M, N), out_dtype, dev)
-        ldz = 0 if preact is None else _matrix(preact, "preact", (M, N), out_dtype, dev)
+        ldx, ldw = _matrix(X, "X", M, K, dt, dev), _matrix(W, "W", N, K, dt, dev)
+        bias_p = res_p = z_p = bias_code = ldr = ldz = 0
+        if bias is not None:
+            bias_code, bias_p = _vector(bias, "bias", N, out_dtype, dev), bias.data_ptr()
+        if residual is not None:
+            ldr, res_p = _matrix(residual, "residual", M, N, out_dtype, dev), residual.data_ptr()
+        if preact is not None:
+            ldz, z_p = _matrix(preact, "preact", M, N, out_dtype, dev), preact.data_ptr()
         if out is None:
-            with _on_stream(stream, dev):
-                out = _padded_output(M, N, out_dtype, dev)
-        ldy = _matrix(out, "out", (M, N), out_dtype, dev)
-        a = gemm_linear_args_t(_ptr(X), _ptr(W), _ptr(out), _ptr(bias), _ptr(residual), _ptr(preact), M, N, K, ldx, ldw,
-                               ldy, ldr, ldz, TORCH_TO_DTYPE_EX[X.dtype], TORCH_TO_DTYPE[out_dtype], bias_dtype,
-                               _act(act), alpha)
-        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), self._stream(stream) or None)
+            out = _new(M, N, out_dtype, dev, stream)
+        ldy = _matrix(out, "out", M, N, out_dtype, dev)
+        a = gemm_linear_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
+                               ldz, in_code, out_code, bias_code, _act(act), alpha)
+        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), self._stream(stream))
         if st != OK:
             raise GemmError(st, "gemm_run_linear")
         return out
@@ -538,25 +544,29 @@ class Gemm:
         """dX = (alpha * dY·W) * act'(Z) (gemm_run_linear_dgrad): dY (M x N), W (N x K), Z (M x K, what the
         layer below kept) of one 16-bit type.  ``dbias`` (K, float32 or that type), if given, becomes
         beta_bias * dbias + the column sums of dX.  Async on `stream`."""
-        if dY.dtype != W.dtype or dY.dtype not in TORCH_TO_DTYPE:
+        dt, dev, code = dY.dtype, self._index, _act(act)
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None:
             raise TypeError("dY and W must both be float16 or both bfloat16")
-        if dY.dim() != 2 or W.dim() != 2 or dY.shape[1] != W.shape[0]:
-            raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, W {tuple(W.shape)}")
-        code, dev, dt = _act(act), self._device(), dY.dtype
+        if dY.dim() != 2 or W.dim() != 2:
+            raise ValueError("expected 2-D tensors")
         (M, N), K = dY.shape, W.shape[1]
         if (Z is None) != (code == 0):
             raise ValueError("Z is the pre-activation of act: both or neither")
-        lddy, ldw = _matrix(dY, "dY", (M, N), dt, dev), _matrix(W, "W", (N, K), dt, dev)
-        ldz = 0 if Z is None else _matrix(Z, "Z", (M, K), dt, dev)
-        dbias_dtype = 0 if dbias is None else _vector(dbias, "dbias", K, (torch.float32, dt), dev)
-        with _on_stream(stream, dev):
-            if out is None:
-                out = _padded_output(M, K, dt, dev)
-            ws, ws_bytes = self._sums_workspace(dbias, M, K, dev)
-        lddx = _matrix(out, "out", (M, K), dt, dev)
-        a = gemm_dgrad_args_t(_ptr(dY), _ptr(W), _ptr(Z), _ptr(out), _ptr(dbias), _ptr(ws), ws_bytes, M, N, K, lddy, ldw,
-                              ldz, lddx, TORCH_TO_DTYPE[dt], dbias_dtype, code, alpha, beta_bias)
-        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), self._stream(stream) or None)
+        lddy, ldw = _matrix(dY, "dY", M, N, dt, dev), _matrix(W, "W", N, K, dt, dev)
+        z_p = db_p = ldz = db_code = ws_p = ws_bytes = 0
+        if Z is not None:
+            ldz, z_p = _matrix(Z, "Z", M, K, dt, dev), Z.data_ptr()
+        if out is None:
+            out = _new(M, K, dt, dev, stream)
+        lddx = _matrix(out, "out", M, K, dt, dev)
+        if dbias is not None:
+            db_code, db_p = _vector(dbias, "dbias", K, dt, dev), dbias.data_ptr()
+            ws = self._sums_workspace(M, K, stream)
+            ws_p, ws_bytes = ws.data_ptr(), ws.size(1) * 4
+        a = gemm_dgrad_args_t(dY.data_ptr(), W.data_ptr(), z_p, out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy, ldw,
+                              ldz, lddx, dt_code, db_code, code, alpha, beta_bias)
+        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), self._stream(stream))
         if st != OK:
             raise GemmError(st, "gemm_run_linear_dgrad")
         return out
@@ -566,26 +576,26 @@ class Gemm:
                      stream=None) -> torch.Tensor:
         """dW = alpha * dY^T·X + beta * dW (gemm_run_linear_wgrad): dY (M x N) and X (M x K) of one 16-bit
         type, dW (N x K) float32 (the default) or that type.  Async on `stream`."""
-        if dY.dtype != X.dtype or dY.dtype not in TORCH_TO_DTYPE:
+        dt, dev = dY.dtype, self._index
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None:
             raise TypeError("dY and X must both be float16 or both bfloat16")
-        if dY.dim() != 2 or X.dim() != 2 or dY.shape[0] != X.shape[0]:
-            raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, X {tuple(X.shape)}")
+        if dY.dim() != 2 or X.dim() != 2:
+            raise ValueError("expected 2-D tensors")
         if out is None and beta != 0.0:
             raise ValueError("beta adds to an existing dW: pass it as out")
-        dev, dt = self._device(), dY.dtype
         (M, N), K = dY.shape, X.shape[1]
         if out_dtype is None:
             out_dtype = out.dtype if out is not None else torch.float32
-        if out_dtype not in (torch.float32, dt):
+        if out_dtype is not torch.float32 and out_dtype is not dt:
             raise TypeError("dW must be float32 or of the operands' type")
-        lddy, ldx = _matrix(dY, "dY", (M, N), dt, dev), _matrix(X, "X", (M, K), dt, dev)
+        lddy, ldx = _matrix(dY, "dY", M, N, dt, dev), _matrix(X, "X", M, K, dt, dev)
         if out is None:
-            with _on_stream(stream, dev):
-                out = _padded_output(N, K, out_dtype, dev)
-        lddw = _matrix(out, "out", (N, K), out_dtype, dev)
-        a = gemm_wgrad_args_t(_ptr(dY), _ptr(X), _ptr(out), M, N, K, lddy, ldx, lddw, TORCH_TO_DTYPE[dt],
+            out = _new(N, K, out_dtype, dev, stream)
+        lddw = _matrix(out, "out", N, K, out_dtype, dev)
+        a = gemm_wgrad_args_t(dY.data_ptr(), X.data_ptr(), out.data_ptr(), M, N, K, lddy, ldx, lddw, dt_code,
                               TORCH_TO_DTYPE_F32[out_dtype], alpha, beta)
-        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), self._stream(stream) or None)
+        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), self._stream(stream))
         if st != OK:
             raise GemmError(st, "gemm_run_linear_wgrad")
         return out
@@ -596,33 +606,42 @@ class Gemm:
         """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N) of one 16-bit type; ``out`` may be dY itself.
         ``dbias`` as for linear_dgrad, with N columns.  With ``sums_only`` dZ is not written (and None is
         returned).  Async on `stream`."""
-        if dY.dtype not in TORCH_TO_DTYPE or dY.dim() != 2:
+        dt, dev, code = dY.dtype, self._index, _act(act)
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None or dY.dim() != 2:
             raise TypeError("dY must be a 2-D float16 or bfloat16 tensor")
-        code, dev, dt = _act(act), self._device(), dY.dtype
         M, N = dY.shape
         if (Z is None) != (code == 0):
             raise ValueError("Z is the pre-activation of act: both or neither")
         if sums_only and (out is not None or dbias is None):
             raise ValueError("sums_only writes dbias and no dZ")
-        lddy = _matrix(dY, "dY", (M, N), dt, dev)
-        ldz = 0 if Z is None else _matrix(Z, "Z", (M, N), dt, dev)
-        dbias_dtype = 0 if dbias is None else _vector(dbias, "dbias", N, (torch.float32, dt), dev)
-        with _on_stream(stream, dev):
-            if out is None and not sums_only:
-                out = _padded_output(M, N, dt, dev)
-            ws, ws_bytes = self._sums_workspace(dbias, M, N, dev)
-        lddz = 0 if out is None else _matrix(out, "out", (M, N), dt, dev)
-        a = gemm_act_grad_args_t(_ptr(dY), _ptr(Z), _ptr(out), _ptr(dbias), _ptr(ws), ws_bytes, M, N, lddy, ldz, lddz,
-                                 TORCH_TO_DTYPE[dt], dbias_dtype, code, beta_bias)
-        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), self._stream(stream) or None)
+        lddy = _matrix(dY, "dY", M, N, dt, dev)
+        z_p = dz_p = db_p = ldz = lddz = db_code = ws_p = ws_bytes = 0
+        if Z is not None:
+            ldz, z_p = _matrix(Z, "Z", M, N, dt, dev), Z.data_ptr()
+        if not sums_only:
+            if out is None:
+                out = _new(M, N, dt, dev, stream)
+            lddz, dz_p = _matrix(out, "out", M, N, dt, dev), out.data_ptr()
+        if dbias is not None:
+            db_code, db_p = _vector(dbias, "dbias", N, dt, dev), dbias.data_ptr()
+            ws = self._sums_workspace(M, N, stream)
+            ws_p, ws_bytes = ws.data_ptr(), ws.size(1) * 4
+        a = gemm_act_grad_args_t(dY.data_ptr(), z_p, dz_p, db_p, ws_p, ws_bytes, M, N, lddy, ldz, lddz, dt_code, db_code,
+                                 code, beta_bias)
+        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), self._stream(stream))
         if st != OK:
             raise GemmError(st, "gemm_run_act_grad")
         return out
 
-    def _sums_workspace(self, dbias, M: int, cols: int, device):
-        """(workspace, bytes) of a call that writes dbias, (None, 0) without."""
-        n = 0 if dbias is None else int(self._lib.gemm_bias_grad_workspace_bytes(M, cols))
-        return (torch.empty(n, dtype=torch.uint8, device=device), n) if n else (None, 0)
+    def _stream(self, stream):
+        if stream is None:
+            return _raw_stream(self._index)
+        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+    def _sums_workspace(self, M: int, cols: int, stream) -> torch.Tensor:
+        """A new workspace for the column sums of an M x cols matrix, one row of floats."""
+        return _new(1, self._lib.gemm_bias_grad_workspace_bytes(M, cols) // 4, torch.float32, self._index, stream)
 
     def sync_status(self, stream=None) -> int:
         return int(self._lib.gemm_sync_status(self._h, _stream_ptr(stream) or None))
@@ -631,35 +650,36 @@ class Gemm:
 _default: dict = {}
 
 
-def _default_handle(device: torch.device) -> Gemm:
+def _default_handle(device: int) -> Gemm:
     """The handle that matmul and the linear-layer functions use on a device."""
-    dev = device.index if device.index is not None else torch.cuda.current_device()
-    if dev not in _default:
-        _default[dev] = Gemm(dev)
-    return _default[dev]
+    h = _default.get(device)
+    if h is None:
+        h = _default[device] = Gemm(device)
+    return h
 
 
 def matmul(A: torch.Tensor, B: torch.Tensor, layout: str = "NN", out: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
     """C = A·B with the library's kernel, on a per-device default handle."""
-    return _default_handle(A.device).run(A, B, out, layout, stream)
+    dev = A.device.index if A.device.index is not None else torch.cuda.current_device()
+    return _default_handle(dev).run(A, B, out, layout, stream)
 
 
 def linear(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, **kw) -> torch.Tensor:
     """Gemm.linear on a per-device default handle."""
-    return _default_handle(X.device).linear(X, W, bias, **kw)
+    return _default_handle(X.get_device()).linear(X, W, bias, **kw)
 
 
 def linear_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, **kw) -> torch.Tensor:
     """Gemm.linear_dgrad on a per-device default handle."""
-    return _default_handle(dY.device).linear_dgrad(dY, W, Z, **kw)
+    return _default_handle(dY.get_device()).linear_dgrad(dY, W, Z, **kw)
 
 
 def linear_wgrad(dY: torch.Tensor, X: torch.Tensor, **kw) -> torch.Tensor:
     """Gemm.linear_wgrad on a per-device default handle."""
-    return _default_handle(dY.device).linear_wgrad(dY, X, **kw)
+    return _default_handle(dY.get_device()).linear_wgrad(dY, X, **kw)
 
 
 def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, **kw) -> torch.Tensor | None:
     """Gemm.act_grad on a per-device default handle."""
-    return _default_handle(dY.device).act_grad(dY, Z, **kw)
+    return _default_handle(dY.get_device()).act_grad(dY, Z, **kw)

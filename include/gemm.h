@@ -370,8 +370,7 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C,
  *   GELU       z Phi(z)                     Phi(z) + z phi(z)    (Phi, phi: normal distribution, density)
  *   GELU_TANH  z s(2u)                      s + z s (1 - s) 2u'  (u = sqrt(2/pi)(z + 0.044715 z^3), s = s(2u))
  *   SILU       z s(z)                       s (1 + z (1 - s))    (s(t) = 1 / (1 + exp(-t)))
- * NaN stays NaN.  The derivatives of +-infinity are their limits; GELU, GELU_TANH and SILU of
- * -infinity are NaN, as the formulas say.
+ * NaN stays NaN; values and derivatives at +-infinity are their limits.
  *
  * Sums run in fp32, in an order that depends on the sizes and the handle's options alone, so a
  * call's results do not change from one call to the next.  Every matrix is row-major, with the

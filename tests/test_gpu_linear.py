@@ -195,6 +195,9 @@ def test_linear_special_values(g):
         for act in ("gelu", "gelu_tanh", "silu"):
             assert bool((g.linear(-big, one, act=act) == 0).all()), act
             assert bool(g.linear(big, one, act=act).isfinite().all()), act
+            assert bool((g.linear(-big * 1e9, one, act=act) == 0).all()), act  # -infinity: the limit
+            assert bool((g.linear(big * 1e9, one, act=act) == float("inf")).all()), act
+            assert bool(g.linear(big * float("nan"), one, act=act).isnan().all()), act
 
 
 # ------------------------------------------------------------------ backward through the weights
