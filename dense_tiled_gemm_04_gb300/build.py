@@ -21,8 +21,8 @@ LIB = os.path.join(HERE, "libdtgemm.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("gemm_api.cu", "kernels_f16.cu", "kernels_bf16.cu", "kernels_e4m3.cu",
                                            "kernels_e5m2.cu", "kernels_mx.cu", "kernels_sparse.cu",
                                            "linear/linear_api.cu", "linear/forward_f16.cu", "linear/forward_bf16.cu",
-                                           "linear/forward_e4m3.cu", "linear/forward_e5m2.cu", "linear/dgrad.cu",
-                                           "linear/wgrad_f16.cu", "linear/wgrad_bf16.cu")]
+                                           "linear/forward_e4m3.cu", "linear/forward_e5m2.cu", "linear/dgrad_f16.cu",
+                                           "linear/dgrad_bf16.cu", "linear/wgrad_f16.cu", "linear/wgrad_bf16.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "sm103_ptx.cuh", "kernel_set.cuh",
                                                      "host/handle.cuh", "linear/activation.cuh",
                                                      "linear/elementwise.cuh", "linear/tile_kernel.cuh",

@@ -639,10 +639,12 @@ gemm_status_t gemm_create(gemm_handle_t* out, int device)
         cudaMemset(h->d_err, 0, 4 * sizeof(int32_t)) != cudaSuccess ||
         cudaMalloc(&h->ws.partials, h->ws.partial_floats * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&h->ws.counters, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) != cudaSuccess ||
-        cudaMemset(h->ws.counters, 0, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) != cudaSuccess) {
+        cudaMemset(h->ws.counters, 0, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) != cudaSuccess ||
+        cudaMalloc(&h->sums, GEMM_OWN_SUMS_BYTES) != cudaSuccess) {
         if (h->d_err) cudaFree(h->d_err);
         if (h->ws.partials) cudaFree(h->ws.partials);
         if (h->ws.counters) cudaFree(h->ws.counters);
+        if (h->sums) cudaFree(h->sums);
         delete h;
         return GEMM_ERR_CUDA;
     }
@@ -661,6 +663,7 @@ gemm_status_t gemm_destroy(gemm_handle_t h)
         if (h->d_stage && cudaFree(h->d_stage) != cudaSuccess) st = GEMM_ERR_CUDA;
         if (h->ws.partials && cudaFree(h->ws.partials) != cudaSuccess) st = GEMM_ERR_CUDA;
         if (h->ws.counters && cudaFree(h->ws.counters) != cudaSuccess) st = GEMM_ERR_CUDA;
+        if (h->sums && cudaFree(h->sums) != cudaSuccess) st = GEMM_ERR_CUDA;
         if (h->pipe.ready) {
             for (cudaStream_t q : {h->pipe.in, h->pipe.out}) cudaStreamDestroy(q);
             for (cudaEvent_t e : {h->pipe.start, h->pipe.done}) cudaEventDestroy(e);

@@ -136,6 +136,7 @@ struct gemm_handle_s {
     dtg::host::LaunchOptions opts;
     dtg::host::DeviceState dev;
     dtg::host::Workspace ws;
+    float* sums = nullptr;  // GEMM_OWN_SUMS_BYTES for column sums
     std::vector<dtg::host::TmapEntry> tmaps;
     // gemm_run_host staging and pipeline
     void* d_stage = nullptr;

@@ -17,32 +17,35 @@ constexpr int kActWarps = 8;
 constexpr int kActCols = 256;   // columns per block
 constexpr int kActUnroll = 4;   // rows in flight per warp
 
+// A bias gradient to be written: beta * dbias + sum, of type kOutF16, kOutBf16 or kOutF32.
+struct BiasGrad {
+    void* dbias;
+    int32_t type;
+    float beta;
+};
+
+__device__ __forceinline__ void write_bias_grad(const BiasGrad& b, int64_t n, float s)
+{
+    if (b.type == kOutF32) {
+        float* d = static_cast<float*>(b.dbias) + n;
+        *d = b.beta != 0.0f ? fmaf(b.beta, *d, s) : s;
+    } else {
+        uint16_t* d = static_cast<uint16_t*>(b.dbias) + n;
+        const bool bf16 = b.type == kOutBf16;
+        if (b.beta != 0.0f) s = fmaf(b.beta, bf16 ? load16<true>(d) : load16<false>(d), s);
+        *d = bf16 ? cvt16<true>(__float_as_uint(s)) : cvt16<false>(__float_as_uint(s));
+    }
+}
+
 struct ActGradParams {
     const uint16_t* dY;
     const uint16_t* Z;   // null: act is none
     uint16_t* dZ;        // null: sums only
-    float* partials;     // null: no sums; else a row of `pitch` columns per block of rows
+    float* partials;     // a row of `pitch` sums per block of rows; null: none, or one block of rows
+    BiasGrad bias;       // one block of rows: its sums are the whole columns' (dbias null: no sums)
     int64_t M, N, lddy, ldz, lddz, pitch;
-    int64_t block_rows;  // rows per block, a multiple of kActWarps
+    int64_t block_rows;  // rows per block
 };
-
-__device__ __forceinline__ void load8(uint32_t (&r)[4], const uint16_t* row, int64_t col, int64_t N)
-{
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (col + 8 <= N) {
-        v = *reinterpret_cast<const uint4*>(row + col);
-    } else if (col < N) {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (col + e < N) w[e >> 1] |= static_cast<uint32_t>(row[col + e]) << ((e & 1) * 16);
-        v = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    r[0] = v.x;
-    r[1] = v.y;
-    r[2] = v.z;
-    r[3] = v.w;
-}
 
 template <bool BF16, int ACT>
 __global__ void __launch_bounds__(kActWarps * 32, 3) act_grad_kernel(const ActGradParams p)
@@ -55,67 +58,82 @@ __global__ void __launch_bounds__(kActWarps * 32, 3) act_grad_kernel(const ActGr
     // Blocks of rows beyond the grid's second dimension are taken in turn.
     for (int64_t rb = blockIdx.y; rb * p.block_rows < p.M; rb += gridDim.y) {
         const int64_t r0 = rb * p.block_rows;
-        const int64_t r1 = r0 + p.block_rows < p.M ? r0 + p.block_rows : p.M;
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int64_t r = r0 + warp; r < r1; r += kActWarps * kActUnroll) {
-            uint32_t g[kActUnroll][4], z[kActUnroll][4];
+        const int64_t left = p.M - r0;
+        const int rows = static_cast<int>(left < p.block_rows ? left : p.block_rows);
+        const uint16_t* g_at = p.dY + r0 * p.lddy + col;
+        const uint16_t* z_at = ACT != kActNone ? p.Z + r0 * p.ldz + col : nullptr;
+        uint16_t* d_at = p.dZ ? p.dZ + r0 * p.lddz + col : nullptr;
+        f32x2 acc[4] = {0, 0, 0, 0};
+        if (col + 8 <= p.N) {
+            for (int r = warp; r < rows; r += kActWarps * kActUnroll) {
+                uint4 g[kActUnroll], z[kActUnroll];
 #pragma unroll
-            for (int u = 0; u < kActUnroll; ++u) {
-                const int64_t row = r + u * kActWarps;
-                const bool in = row < r1 && col < p.N;
-                if (in) load8(g[u], p.dY + row * p.lddy, col, p.N);
-                if (in && ACT != kActNone) load8(z[u], p.Z + row * p.ldz, col, p.N);
-            }
-#pragma unroll
-            for (int u = 0; u < kActUnroll; ++u) {
-                const int64_t row = r + u * kActWarps;
-                if (row >= r1 || col >= p.N) continue;
-                float d[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[2 * i] = unpack_lo<BF16>(g[u][i]);
-                    d[2 * i + 1] = unpack_hi<BF16>(g[u][i]);
-                    if constexpr (ACT != kActNone) {
-                        d[2 * i] *= act_slope<ACT>(unpack_lo<BF16>(z[u][i]));
-                        d[2 * i + 1] *= act_slope<ACT>(unpack_hi<BF16>(z[u][i]));
+                for (int u = 0; u < kActUnroll; ++u) {
+                    const int row = r + u * kActWarps;
+                    if (row < rows) {
+                        g[u] = *reinterpret_cast<const uint4*>(g_at + row * p.lddy);
+                        if constexpr (ACT != kActNone) z[u] = *reinterpret_cast<const uint4*>(z_at + row * p.ldz);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += d[i];
-                if (p.dZ) {
-                    uint32_t h[4];
+                for (int u = 0; u < kActUnroll; ++u) {
+                    const int row = r + u * kActWarps;
+                    if (row < rows) {
+                        const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+                        const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
+                        uint32_t h[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = pack2<BF16>(__float_as_uint(d[2 * i]), __float_as_uint(d[2 * i + 1]));
-                    uint16_t* dst = p.dZ + row * p.lddz + col;
-                    if (col + 8 <= p.N) {
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (col + e < p.N) dst[e] = static_cast<uint16_t>(h[e >> 1] >> ((e & 1) * 16));
+                        for (int i = 0; i < 4; ++i) {
+                            f32x2 v = unpack2<BF16>(gw[i]);
+                            if constexpr (ACT != kActNone) v = mul2(v, act_slope2<ACT>(unpack2<BF16>(zw[i])));
+                            acc[i] = add2(acc[i], v);
+                            h[i] = round2<BF16>(v);
+                        }
+                        if (d_at) *reinterpret_cast<uint4*>(d_at + row * p.lddz) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
             }
+        } else if (col < p.N) {  // the lane whose columns end inside its eight
+            const int n = static_cast<int>(p.N - col);
+            float tail[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int r = warp; r < rows; r += kActWarps) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) {
+                        f32x2 v = unpack2<BF16>(g_at[r * p.lddy + e]);
+                        if constexpr (ACT != kActNone) v = mul2(v, act_slope2<ACT>(unpack2<BF16>(z_at[r * p.ldz + e])));
+                        float d, unused;
+                        split(v, d, unused);
+                        tail[e] += d;
+                        if (d_at) d_at[r * p.lddz + e] = cvt16<BF16>(__float_as_uint(d));
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = pair(tail[2 * i], tail[2 * i + 1]);
         }
-        if (p.partials) {
+        if (p.partials || p.bias.dbias) {
             __syncthreads();  // the sums of the block of rows before have been read
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = acc[i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x2*>(&sums[warp][lane * 8 + 2 * i]) = acc[i];
             __syncthreads();
             const int64_t c = blockIdx.x * static_cast<int64_t>(kActCols) + threadIdx.x;
             float s = 0.0f;
 #pragma unroll
             for (int w = 0; w < kActWarps; ++w) s += sums[w][threadIdx.x];
-            if (c < p.N) p.partials[rb * p.pitch + c] = s;
+            if (c < p.N) {
+                if (p.partials)
+                    p.partials[rb * p.pitch + c] = s;
+                else
+                    write_bias_grad(p.bias, c, s);
+            }
         }
     }
 }
 
 // dbias[n] = beta * dbias[n] + the sum over `rows` partial sums of column n.  32 columns a block; warp w adds rows
 // w, w + 8, ..., and the eight warps' sums are added in warp order.
-template <int DB>  // kOutF16, kOutBf16, kOutF32: type of dbias
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* partials, int64_t rows, int64_t pitch, int64_t N,
-                                                         void* dbias, float beta)
+                                                         const BiasGrad b)
 {
     __shared__ float sums[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,14 +150,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partials, 
     if (warp == 0 && n < N) {
 #pragma unroll
         for (int w = 1; w < 8; ++w) s += sums[w][lane];
-        if constexpr (DB == kOutF32) {
-            float* d = static_cast<float*>(dbias) + n;
-            *d = beta != 0.0f ? fmaf(beta, *d, s) : s;
-        } else {
-            uint16_t* d = static_cast<uint16_t*>(dbias) + n;
-            if (beta != 0.0f) s = fmaf(beta, load16<DB == kOutBf16>(d), s);
-            *d = cvt16<DB == kOutBf16>(__float_as_uint(s));
-        }
+        write_bias_grad(b, n, s);
     }
 }
 

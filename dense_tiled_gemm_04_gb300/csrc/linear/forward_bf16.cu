@@ -3,6 +3,6 @@
 
 namespace dtg {
 namespace linear {
-KernelChoice forward_bf16(int config) { return tile_choice_for<1, kOutBf16, kForward>(config); }
+KernelChoice forward_bf16(int config) { return tile_choice_for<1, kOutBf16, kForward, false>(config); }
 }  // namespace linear
 }  // namespace dtg

@@ -5,7 +5,7 @@ namespace dtg {
 namespace linear {
 KernelChoice forward_e5m2(int config, bool out_bf16)
 {
-    return out_bf16 ? tile_choice_for<3, kOutBf16, kForward>(config) : tile_choice_for<3, kOutF16, kForward>(config);
+    return out_bf16 ? tile_choice_for<3, kOutBf16, kForward, false>(config) : tile_choice_for<3, kOutF16, kForward, false>(config);
 }
 }  // namespace linear
 }  // namespace dtg

@@ -52,8 +52,9 @@ void check_sums(Checks& c, const void* dbias, gemm_dtype_t t, const void* ws, in
 {
     if (!dbias) return;
     c.vector(dbias, t);
-    if (M == 0) return;
-    if (!ws || ws_bytes < gemm_bias_grad_workspace_bytes(M, cols))
+    const int64_t need = gemm_bias_grad_workspace_bytes(M, cols);
+    if (!ws && need <= GEMM_OWN_SUMS_BYTES) return;  // the handle's
+    if (!ws || ws_bytes < need)
         c.add(GEMM_ERR_INVALID_ARG);
     else if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0)
         c.add(GEMM_ERR_UNSUPPORTED);
@@ -79,15 +80,20 @@ gemm_status_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, size_t smem,
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// dbias = beta * dbias + the sums of `rows` rows of partial sums.
-gemm_status_t launch_sums(const void* partials, int64_t rows, int64_t cols, void* dbias, gemm_dtype_t t, float beta,
-                          cudaStream_t s)
+// Where a call's partial column sums go: the caller's workspace, or the handle's.
+float* sums_of(gemm_handle_t h, void* workspace) { return workspace ? static_cast<float*>(workspace) : h->sums; }
+
+dtg::linear::BiasGrad bias_grad(void* dbias, gemm_dtype_t t, float beta)
 {
-    const auto fn = t == GEMM_DTYPE_F32    ? &dtg::linear::column_sum_kernel<dtg::linear::kOutF32>
-                    : t == GEMM_DTYPE_BF16 ? &dtg::linear::column_sum_kernel<dtg::linear::kOutBf16>
-                                           : &dtg::linear::column_sum_kernel<dtg::linear::kOutF16>;
-    return launch_after(fn, dim3(static_cast<unsigned>(cdiv(cols, 32))), dim3(256), 0, s, static_cast<const float*>(partials),
-                        rows, sum_pitch(cols), cols, dbias, beta);
+    return {dbias, t == GEMM_DTYPE_F32 ? dtg::linear::kOutF32 : (t == GEMM_DTYPE_BF16 ? dtg::linear::kOutBf16 : dtg::linear::kOutF16),
+            beta};
+}
+
+// The bias gradient from `rows` rows of partial sums.
+gemm_status_t launch_sums(const float* partials, int64_t rows, int64_t cols, const dtg::linear::BiasGrad& b, cudaStream_t s)
+{
+    return launch_after(&dtg::linear::column_sum_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32))), dim3(256), 0, s, partials,
+                        rows, sum_pitch(cols), cols, b);
 }
 
 // One product: rows x cols over `depth`, as linear_tile_kernel names them.
@@ -113,7 +119,9 @@ struct Product {
 KernelChoice tile_kernel(const Product& q, int config)
 {
     const bool bf16 = q.out == GEMM_DTYPE_BF16, f32 = q.out == GEMM_DTYPE_F32;
-    if (q.mode == dtg::linear::kDgrad) return dtg::linear::dgrad_16(config, bf16);
+    if (q.mode == dtg::linear::kDgrad)
+        return bf16 ? dtg::linear::dgrad_bf16(config, q.partials != nullptr)
+                    : dtg::linear::dgrad_f16(config, q.partials != nullptr);
     if (q.mode == dtg::linear::kWgrad)
         return q.in == GEMM_DTYPE_BF16 ? dtg::linear::wgrad_bf16(config, f32) : dtg::linear::wgrad_f16(config, f32);
     switch (q.in) {
@@ -124,23 +132,22 @@ KernelChoice tile_kernel(const Product& q, int config)
     }
 }
 
-// Launch-state slot of a tile kernel: 12 operators and types x 3 configurations.
+// Launch-state slot of a tile kernel: 14 operators and types x 3 configurations.
 int tile_slot(const Product& q, int config)
 {
     int op;
     if (q.mode == dtg::linear::kForward)
         op = is_f8(q.in) ? 2 + 2 * (q.in - GEMM_DTYPE_E4M3) + (q.out == GEMM_DTYPE_BF16) : q.in;
     else if (q.mode == dtg::linear::kDgrad)
-        op = 6 + q.in;
+        op = 6 + 2 * q.in + (q.partials != nullptr);
     else
-        op = 8 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
+        op = 10 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
     return kLinearSlot0 + 3 * op + (config - 1);
 }
 
-// K blocks per chunk of the accumulation (see tile_kernel.cuh).  Where an fp32 result is wanted (a weight
-// gradient, or sums of the product's values) 8 blocks of 64 keep the truncation of the tensor core's
-// accumulator at 6e-7; a 16-bit result rounds at 2e-4 or more, and 32 blocks do.
-int chunk_blocks(const Product& q) { return q.out == GEMM_DTYPE_F32 || q.partials ? 8 : 32; }
+// K blocks per chunk of an accumulation in registers (see tile_kernel.cuh): 8 blocks of 64 keep the
+// truncation of the tensor core's accumulator at 6e-7 of the sum.
+constexpr int32_t kChunkBlocks = 8;
 
 gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t stream)
 {
@@ -202,7 +209,7 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t str
     p.counters = h->ws.counters;
     p.alpha = q.alpha;
     p.beta = q.beta;
-    p.chunk_kb = chunk_blocks(q);
+    p.chunk_kb = q.out == GEMM_DTYPE_F32 || q.partials ? kChunkBlocks : INT32_MAX;  // SUMS, or one chunk
     p.act = q.act;
     p.bias = q.bias;
     p.bias_f32 = q.bias_dtype == GEMM_DTYPE_F32;
@@ -342,12 +349,12 @@ gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* ar
         q.act = a.act;
         q.src = a.act != GEMM_ACT_NONE ? a.Z : nullptr;
         q.ldsrc = a.ldz;
-        q.partials = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
+        q.partials = a.dbias ? sums_of(h, a.workspace) : nullptr;
         const gemm_status_t st = launch_product(h, q, s);
         if (st != GEMM_OK) return st;
     }
     if (!a.dbias) return GEMM_OK;
-    return launch_sums(a.workspace, cdiv(a.M, kSumRows), a.K, a.dbias, a.dbias_dtype, a.beta_bias, s);
+    return launch_sums(sums_of(h, a.workspace), cdiv(a.M, kSumRows), a.K, bias_grad(a.dbias, a.dbias_dtype, a.beta_bias), s);
 }
 
 gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* args, void* stream)
@@ -408,30 +415,33 @@ gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* arg
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Blocks of 64 rows, or the 32 that the workspace has room for when those would not fill the GPU.
+    const dtg::linear::BiasGrad bias = bias_grad(a.dbias, a.dbias_dtype, a.beta_bias);
+    if (a.M == 0) return a.dbias ? launch_sums(nullptr, 0, a.N, bias, s) : GEMM_OK;
+    if (!a.dZ && !a.dbias) return GEMM_OK;
+    // Blocks of rows: 64, or 32 (what the workspace has room for) when those would not fill the GPU.  Up to 128
+    // rows are one block, which writes dbias itself and saves the second launch.
     const int64_t strips = cdiv(a.N, dtg::linear::kActCols);
-    const int64_t block_rows = strips * cdiv(a.M, 64) >= 6 * h->dev.num_sms ? 64 : kSumRows;
+    const int64_t block_rows = a.M <= 128 ? a.M : (strips * cdiv(a.M, 64) >= 6 * h->dev.num_sms ? 64 : kSumRows);
     const int64_t blocks = cdiv(a.M, block_rows);
-    if (a.M > 0 && (a.dZ || a.dbias)) {
-        dtg::linear::ActGradParams p;
-        p.dY = static_cast<const uint16_t*>(a.dY);
-        p.Z = static_cast<const uint16_t*>(a.Z);
-        p.dZ = static_cast<uint16_t*>(a.dZ);
-        p.partials = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
-        p.M = a.M;
-        p.N = a.N;
-        p.lddy = a.lddy;
-        p.ldz = a.ldz;
-        p.lddz = a.lddz;
-        p.pitch = sum_pitch(a.N);
-        p.block_rows = block_rows;
-        const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(std::min<int64_t>(blocks, 65535)));
-        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_act_grad<true>(p, a.act, grid, s)
-                                                            : launch_act_grad<false>(p, a.act, grid, s);
-        if (st != GEMM_OK) return st;
-    }
-    if (!a.dbias) return GEMM_OK;
-    return launch_sums(a.workspace, blocks, a.N, a.dbias, a.dbias_dtype, a.beta_bias, s);
+    const bool one_block = blocks == 1;
+    dtg::linear::ActGradParams p;
+    p.dY = static_cast<const uint16_t*>(a.dY);
+    p.Z = static_cast<const uint16_t*>(a.Z);
+    p.dZ = static_cast<uint16_t*>(a.dZ);
+    p.partials = a.dbias && !one_block ? sums_of(h, a.workspace) : nullptr;
+    p.bias = bias;
+    p.M = a.M;
+    p.N = a.N;
+    p.lddy = a.lddy;
+    p.ldz = a.ldz;
+    p.lddz = a.lddz;
+    p.pitch = sum_pitch(a.N);
+    p.block_rows = block_rows;
+    const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(std::min<int64_t>(blocks, 65535)));
+    const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_act_grad<true>(p, a.act, grid, s)
+                                                        : launch_act_grad<false>(p, a.act, grid, s);
+    if (st != GEMM_OK || !a.dbias || one_block) return st;
+    return launch_sums(p.partials, blocks, a.N, bias, s);
 }
 
 }  // extern "C"

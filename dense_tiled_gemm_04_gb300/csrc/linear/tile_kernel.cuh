@@ -17,10 +17,12 @@
 // chunk_kb; each chunk overwrites one of the two TMEM accumulators, and the epilogue warps
 // add it to a running sum in their registers, rounding to nearest.  The MMAs of the next chunk
 // run meanwhile, so the tensor pipe does not wait, and an item's accumulator is free as soon as its last
-// chunk has been read, before any of the epilogue's arithmetic.
+// chunk has been read, before any of the epilogue's arithmetic.  Only where an fp32 result is wanted (SUMS:
+// weight gradients, column sums); a result that is rounded to 16 bits alone takes the whole contraction as one
+// chunk, whose boxes go from TMEM straight through the epilogue.
 //
-// Epilogue.  Eight warps, two per TMEM lane quadrant, each holding 32 rows x BN/2 columns of sums
-// (128 registers at BN = 256).  Four warps would need 256 registers each for the sums alone.  Per box of 128 bytes of output columns: bias through the warp's staging
+// Epilogue.  Eight warps, two per TMEM lane quadrant, 32 rows x BN/2 columns each; with SUMS they hold
+// those sums (128 registers at BN = 256; four warps would need 256 each).  Per box of 128 bytes of output columns: bias through the warp's staging
 // buffer (every lane needs the same 64 values), residual or pre-activations straight from
 // global memory (16 bytes a load, a row's 128 bytes per lane), then the 128-byte-swizzled staging and TMA store.
 //
@@ -120,18 +122,22 @@ __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// The two 16-bit floats of a word, in fp32.
 template <bool BF16>
-__device__ __forceinline__ float unpack_lo(uint32_t w)
+__device__ __forceinline__ f32x2 unpack2(uint32_t w)
 {
-    if constexpr (BF16) return __uint_as_float(w << 16);
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xFFFFu)));
+    if constexpr (BF16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return pair(__half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xFFFFu))),
+                __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))));
 }
 
+// A pair of fp32 values rounded to a word of two 16-bit floats.
 template <bool BF16>
-__device__ __forceinline__ float unpack_hi(uint32_t w)
+__device__ __forceinline__ uint32_t round2(f32x2 v)
 {
-    if constexpr (BF16) return __uint_as_float(w & 0xFFFF0000u);
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+    float lo, hi;
+    split(v, lo, hi);
+    return pack2<BF16>(__float_as_uint(lo), __float_as_uint(hi));
 }
 
 // Elements [col, col + 64) of a 16-bit row, two per word; zeros from column N on.
@@ -237,8 +243,8 @@ __device__ __forceinline__ void sum_rows(float* v, int lane)
 }
 
 // IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward, kDgrad,
-// kWgrad; CLUSTER: 1 (one CTA) or 2 (a CTA pair).
-template <int BN, int STAGES, int IN, int OUT, int MODE, int CLUSTER>
+// kWgrad; SUMS: the contraction runs in chunks that are summed in registers; CLUSTER: 1 (one CTA) or 2 (a CTA pair).
+template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER>
 __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ, const TileParams p)
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     using T = Operand<IN>;
     static_assert(IN <= 3 && (BN == 128 || BN == 256), "dense operands, 64 or 128 columns per epilogue warp");
     static_assert(MODE == kForward || !T::kF8, "8-bit operands: forward only");
-    static_assert(OUT != kOutF32 || MODE == kWgrad, "fp32 output: weight gradients only");
+    static_assert(OUT != kOutF32 || (MODE == kWgrad && SUMS), "fp32 output: weight gradients only");
     constexpr bool PAIR = CLUSTER == 2;
     constexpr bool AT = MODE == kWgrad;        // A is M-major
     constexpr bool BT = MODE != kForward;      // B is N-major
@@ -486,149 +492,146 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         WorkIter it(p, unit, units);
         int64_t tile;
         int kb0, kb1;
-        float s[CW];  // this thread's sums: row row_in_cta, columns half * CW ...
-
-        // The operator on the finished sums of the tile at (tm, tn), and its stores.
-        auto finish = [&](int64_t tm, int64_t tn) {
-            const int32_t y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
+        // The operator on 64 columns (32 for an fp32 output) of this thread's row, from column x of C on: v holds
+        // the product's sums and is overwritten.  A warp's rows start at y < M, its columns at x < N.
+        auto finish_box = [&](float* v, int32_t x, int32_t y) {
             const int64_t row = static_cast<int64_t>(y) + lane;
             const bool row_in = row < p.M;
-            if (y >= p.M) return;
+            const f32x2 alpha = both(p.alpha);
             if constexpr (OUT == kOutF32) {
+                uint32_t h[32];
+                float r[32];
+                if (p.in && row_in) {
+                    load_row32(r, static_cast<const float*>(p.in) + row * p.ldin, x, p.N);
 #pragma unroll
-                for (int b = 0; b < CW / 32; ++b) {
-                    const int32_t x = static_cast<int32_t>(tn * BN + half * CW + b * 32);
-                    if (x >= p.N) break;
-                    uint32_t h[32];
-                    float r[32];
-                    if (p.in && row_in) {
-                        load_row32(r, static_cast<const float*>(p.in) + row * p.ldin, x, p.N);
+                    for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(fmaf(p.beta, r[i], p.alpha * v[i]));
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(fmaf(p.beta, r[i], p.alpha * s[b * 32 + i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(p.alpha * s[b * 32 + i]);
-                    }
-                    store_rows<4>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+                    for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(p.alpha * v[i]);
                 }
+                store_rows<4>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
             } else {
+                uint32_t r[32];
+                const bool has_in = p.in != nullptr;
+                if (has_in && row_in) {
+                    load_row16(r, static_cast<const uint16_t*>(p.in) + row * p.ldin, x, p.N);
+                } else {
 #pragma unroll
-                for (int b = 0; b < CW / 64; ++b) {
-                    const int32_t x = static_cast<int32_t>(tn * BN + half * CW + b * 64);
-                    if (x >= p.N) break;
-                    float* const v = &s[b * 64];
-                    uint32_t r[32];
-                    const bool has_in = p.in != nullptr;
+                    for (int i = 0; i < 32; ++i) r[i] = 0;
+                }
+                f32x2 w[32];
+                if (MODE == kForward && p.bias) {
+                    // The box's 64 biases go through the staging buffer, from which all lanes read them.
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int32_t c = x + lane + 32 * e;
+                        float f = 0.0f;
+                        if (c < p.N)
+                            f = p.bias_f32 ? static_cast<const float*>(p.bias)[c]
+                                           : load16<kBf16>(static_cast<const uint16_t*>(p.bias) + c);
+                        st_shared_f32(stg + 4 * (lane + 32 * e), f);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 f = ld_shared_f4(stg + 16 * i);
+                        w[2 * i] = fma2(alpha, pair(v[4 * i], v[4 * i + 1]), pair(f.x, f.y));
+                        w[2 * i + 1] = fma2(alpha, pair(v[4 * i + 2], v[4 * i + 3]), pair(f.z, f.w));
+                    }
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
+                }
+                uint32_t h[32];
+                if constexpr (MODE == kForward) {
+                    if (p.Z) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(w[i]);
+                        store_rows<2>(h, x, y, lane, stg, &tmZ, p.Z, p.ldz, p.M, p.N);
+                    }
+                    DTG_ACT_SWITCH(p.act, {
+                        _Pragma("unroll") for (int i = 0; i < 32; ++i) w[i] = act_value2<ACT>(w[i]);
+                    });
                     if (has_in) {
-                        if (row_in)
-                            load_row16(r, static_cast<const uint16_t*>(p.in) + row * p.ldin, x, p.N);
-                        else
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = 0;
+                        for (int i = 0; i < 32; ++i) w[i] = add2(w[i], unpack2<kBf16>(r[i]));
                     }
-                    if (MODE == kForward && p.bias) {
-                        // The box's 64 biases go through the staging buffer, from which all lanes read them.
-                        if (lane == 0) ptx::bulk_wait_group_read<0>();
-                        __syncwarp();
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int32_t c = x + lane + 32 * e;
-                            float f = 0.0f;
-                            if (c < p.N)
-                                f = p.bias_f32 ? static_cast<const float*>(p.bias)[c]
-                                               : load16<kBf16>(static_cast<const uint16_t*>(p.bias) + c);
-                            st_shared_f32(stg + 4 * (lane + 32 * e), f);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float4 f = ld_shared_f4(stg + 16 * i);
-                            v[4 * i] = fmaf(p.alpha, v[4 * i], f.x);
-                            v[4 * i + 1] = fmaf(p.alpha, v[4 * i + 1], f.y);
-                            v[4 * i + 2] = fmaf(p.alpha, v[4 * i + 2], f.z);
-                            v[4 * i + 3] = fmaf(p.alpha, v[4 * i + 3], f.w);
-                        }
-                        __syncwarp();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) v[i] *= p.alpha;
-                    }
-                    uint32_t h[32];
-                    if constexpr (MODE == kForward) {
-                        if (p.Z) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) h[i] = pack2<kBf16>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
-                            store_rows<2>(h, x, y, lane, stg, &tmZ, p.Z, p.ldz, p.M, p.N);
-                        }
+                }
+                if constexpr (MODE == kDgrad) {
+                    if (has_in) {
                         DTG_ACT_SWITCH(p.act, {
-                            _Pragma("unroll") for (int i = 0; i < 64; ++i) v[i] = act_value<ACT>(v[i]);
+                            _Pragma("unroll") for (int i = 0; i < 32; ++i) w[i] =
+                                mul2(w[i], act_slope2<ACT>(unpack2<kBf16>(r[i])));
                         });
-                        if (has_in) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                v[2 * i] += unpack_lo<kBf16>(r[i]);
-                                v[2 * i + 1] += unpack_hi<kBf16>(r[i]);
-                            }
-                        }
                     }
-                    if constexpr (MODE == kDgrad) {
-                        if (has_in) {
-                            DTG_ACT_SWITCH(p.act, {
-                                _Pragma("unroll") for (int i = 0; i < 32; ++i)
-                                {
-                                    v[2 * i] *= act_slope<ACT>(unpack_lo<kBf16>(r[i]));
-                                    v[2 * i + 1] *= act_slope<ACT>(unpack_hi<kBf16>(r[i]));
-                                }
-                            });
-                        }
+                }
+                if constexpr (MODE == kWgrad) {
+                    if (has_in) {
+                        const f32x2 beta = both(p.beta);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = fma2(beta, unpack2<kBf16>(r[i]), w[i]);
                     }
-                    if constexpr (MODE == kWgrad) {
-                        if (has_in) {
+                }
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                v[2 * i] = fmaf(p.beta, unpack_lo<kBf16>(r[i]), v[2 * i]);
-                                v[2 * i + 1] = fmaf(p.beta, unpack_hi<kBf16>(r[i]), v[2 * i + 1]);
-                            }
+                for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(w[i]);
+                store_rows<2>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+                if constexpr (MODE == kDgrad) {
+                    if (p.partials) {
+                        // Rows past M are not part of the sums (an infinite weight makes them NaN).
+                        if (!row_in) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) w[i] = 0;
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) h[i] = pack2<kBf16>(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]));
-                    store_rows<2>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
-                    if constexpr (MODE == kDgrad) {
-                        if (p.partials) {
-                            // Rows past M are not part of the sums (an infinite weight makes them NaN).
-                            if (!row_in) {
-#pragma unroll
-                                for (int i = 0; i < 64; ++i) v[i] = 0.0f;
-                            }
-                            sum_rows(v, lane);
-                            *reinterpret_cast<float2*>(p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + 2 * lane) =
-                                make_float2(v[0], v[1]);
-                        }
+                        for (int i = 0; i < 32; ++i) split(w[i], v[2 * i], v[2 * i + 1]);
+                        sum_rows(v, lane);
+                        *reinterpret_cast<float2*>(p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + 2 * lane) =
+                            make_float2(v[0], v[1]);
                     }
                 }
             }
         };
 
-        // Part of a stream-K tile: park the sums in this unit's slot and count the part in; the last part to
-        // arrive adds all of them in K order, whatever the order of arrival.  True for that one, which then holds the
-        // tile's sums.
-        auto join_parts = [&](int64_t tile) -> bool {
-            const int64_t tr = tile - p.dp_tiles;
-            constexpr size_t kSlotF4 = static_cast<size_t>(kBM) * BN / 4;
-            auto slot_f4 = [&](int64_t slot) {
-                return reinterpret_cast<float4*>(p.ws) + (static_cast<size_t>(slot) * CLUSTER + rank) * kSlotF4 +
-                       static_cast<size_t>(half * (CW / 4)) * kBM + row_in_cta;
-            };
-            int64_t first_unit, parts;
-            sk_parts(p, tr, first_unit, parts);
-            int32_t* const counter = p.counters + tr * CLUSTER + rank;
-            float4* const mine = slot_f4(sk_slot(p, unit, tr));
+        // 64 columns of the accumulator: TMEM -> v.
+        auto load_acc = [&](float* v, uint32_t taddr) {
+            uint32_t a[32];
+            uint32_t b[32];
+            ptx::tmem_ld_32x32b_x32(taddr, a);
+            ptx::tmem_ld_32x32b_x32(taddr + 32, b);
+            ptx::tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < CW / 4; ++q) mine[q * kBM] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+            for (int i = 0; i < 32; ++i) {
+                v[i] = __uint_as_float(a[i]);
+                v[32 + i] = __uint_as_float(b[i]);
+            }
+        };
+        auto release_acc = [&]() {
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(acce_bar(acc), 0u));
+                else
+                    ptx::mbar_arrive(acce_bar(acc));
+            }
+        };
+
+        // Stream-K bookkeeping (see gemm_tcgen05_kernel): slots of partial sums, float4 groups of four columns with
+        // the rows inner.  A part parks its sums and counts itself in; the last one to arrive adds all of them in K
+        // order, whatever the order of arrival.
+        constexpr size_t kSlotF4 = static_cast<size_t>(kBM) * BN / 4;
+        auto slot_f4 = [&](int64_t slot) {
+            return reinterpret_cast<float4*>(p.ws) + (static_cast<size_t>(slot) * CLUSTER + rank) * kSlotF4 +
+                   static_cast<size_t>(half * (CW / 4)) * kBM + row_in_cta;
+        };
+        auto count_in = [&](int64_t tr, int64_t parts) -> bool {  // true for the part that arrives last
             __threadfence();
             tile_epi_sync();
             if (ew == 0 && lane == 0) {
+                int32_t* const counter = p.counters + tr * CLUSTER + rank;
                 const bool last = atomicAdd(counter, 1) == parts - 1;
                 if (last) {
                     *counter = 0;  // ready for the next launch
@@ -637,64 +640,124 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 *last_flag = last ? 1 : 0;
             }
             tile_epi_sync();
-            if (*last_flag == 0) return false;
+            return *last_flag != 0;
+        };
+        auto add_part = [&](float* v, const float4* f4) {  // 64 columns of a slot
 #pragma unroll
-            for (int i = 0; i < CW; ++i) s[i] = 0.0f;
-            for (int64_t part = 0; part < parts; ++part) {
-                    const float4* f4 = slot_f4(sk_slot(p, first_unit + part, tr));
+            for (int q0 = 0; q0 < 16; q0 += 8) {
+                float4 f[8];
 #pragma unroll
-                    for (int q0 = 0; q0 < CW / 4; q0 += 8) {
-                        float4 f[8];
+                for (int q = 0; q < 8; ++q) f[q] = __ldcg(f4 + (q0 + q) * kBM);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) f[q] = __ldcg(f4 + (q0 + q) * kBM);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            s[4 * (q0 + q)] += f[q].x;
-                            s[4 * (q0 + q) + 1] += f[q].y;
-                            s[4 * (q0 + q) + 2] += f[q].z;
-                            s[4 * (q0 + q) + 3] += f[q].w;
-                        }
-                    }
+                for (int q = 0; q < 8; ++q) {
+                    v[4 * (q0 + q)] += f[q].x;
+                    v[4 * (q0 + q) + 1] += f[q].y;
+                    v[4 * (q0 + q) + 2] += f[q].z;
+                    v[4 * (q0 + q) + 3] += f[q].w;
                 }
-            return true;
+            }
         };
 
         // One work item; false when the launch is being abandoned.
         auto one_item = [&](int64_t tile, int kb0, int kb1) -> bool {
             int64_t tm, tn;
             tile_coord(tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+            const int32_t y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
+            const int32_t x0 = static_cast<int32_t>(tn * BN + half * CW);
+            const bool whole = kb0 == 0 && kb1 == p.num_kb;
+            const int64_t tr = tile - p.dp_tiles;
+            int64_t first_unit = 0, parts = 0;
+            if (!whole) sk_parts(p, tr, first_unit, parts);
+            if constexpr (SUMS) {
+                float s[CW];  // the running sums
 #pragma unroll
-            for (int i = 0; i < CW; ++i) s[i] = 0.0f;
-            bool ok = true;
-            for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
-                ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (ok) {
-                    ptx::tc_fence_after_sync();
-                    const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
+                for (int i = 0; i < CW; ++i) s[i] = 0.0f;
+                bool ok = true;
+                for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
+                    ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (ok) {
+                        ptx::tc_fence_after_sync();
+                        const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
 #pragma unroll
-                    for (int q = 0; q < CW / 32; ++q) {
-                        uint32_t v[32];
-                        ptx::tmem_ld_32x32b_x32(tacc + q * 32, v);
-                        ptx::tmem_wait_ld();
+                        for (int q = 0; q < CW / 32; ++q) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(tacc + q * 32, v);
+                            ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) s[q * 32 + i] += __uint_as_float(v[i]);
+                            for (int i = 0; i < 32; ++i) s[q * 32 + i] += __uint_as_float(v[i]);
+                        }
+                        release_acc();
                     }
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR)
-                            ptx::mbar_arrive_cluster(ptx::mapa_shared(acce_bar(acc), 0u));
-                        else
-                            ptx::mbar_arrive(acce_bar(acc));
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+                if (!tile_epi_and(ok)) return false;
+                if (!whole) {
+                    float4* const mine = slot_f4(sk_slot(p, unit, tr));
+#pragma unroll
+                    for (int q = 0; q < CW / 4; ++q)
+                        mine[q * kBM] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+                    if (!count_in(tr, parts)) return true;
+#pragma unroll
+                    for (int i = 0; i < CW; ++i) s[i] = 0.0f;
+                    for (int64_t part = 0; part < parts; ++part) {
+                        const float4* f4 = slot_f4(sk_slot(p, first_unit + part, tr));
+#pragma unroll
+                        for (int b = 0; b < CW / 64; ++b) add_part(&s[b * 64], f4 + b * 16 * kBM);
                     }
                 }
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
+                if (y < p.M) {
+                    constexpr int kBox = OUT == kOutF32 ? 32 : 64;
+#pragma unroll
+                    for (int b = 0; b < CW / kBox; ++b)
+                        if (x0 + b * kBox < p.N) finish_box(&s[b * kBox], x0 + b * kBox, y);
+                }
+            } else {
+                // One chunk: every box goes straight from the accumulator (or from the parts) to the output.
+                const bool ok = kb0 == kb1 || wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb0);
+                if (!tile_epi_and(ok)) return false;
+                ptx::tc_fence_after_sync();
+                const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
+                float v[64];
+                if (whole) {
+#pragma unroll 1
+                    for (int b = 0; b < CW / 64; ++b) {
+                        if (kb0 == kb1) {  // an empty contraction
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                        } else {
+                            load_acc(v, tacc + b * 64);
+                            if (b == CW / 64 - 1) release_acc();
+                        }
+                        if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
+                    }
+                } else {
+                    float4* const mine = slot_f4(sk_slot(p, unit, tr));
+#pragma unroll 1
+                    for (int b = 0; b < CW / 64; ++b) {
+                        load_acc(v, tacc + b * 64);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            mine[(b * 16 + q) * kBM] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    }
+                    release_acc();
+                    if (count_in(tr, parts)) {
+#pragma unroll 1
+                        for (int b = 0; b < CW / 64; ++b) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                            for (int64_t part = 0; part < parts; ++part)
+                                add_part(v, slot_f4(sk_slot(p, first_unit + part, tr)) + b * 16 * kBM);
+                            if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
+                        }
+                    }
+                }
+                if (kb0 < kb1) {
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
             }
-            if (!tile_epi_and(ok)) return false;
-            const bool whole = kb0 == 0 && kb1 == p.num_kb;
-            if (whole || join_parts(tile)) finish(tm, tn);
             return true;
         };
 

@@ -8,29 +8,30 @@
 namespace dtg {
 namespace linear {
 
-template <int BN, int STAGES, int IN, int OUT, int MODE, int CLUSTER>
+template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER>
 KernelChoice tile_choice(int config)
 {
     constexpr int kBRows = BN / CLUSTER;
     return {config, kBM * CLUSTER, BN, kBRows, Operand<IN>::kStageK, Operand<IN>::kNBlock, Operand<IN>::kAStageK,
-            STAGES, CLUSTER, reinterpret_cast<const void*>(&linear_tile_kernel<BN, STAGES, IN, OUT, MODE, CLUSTER>),
+            STAGES, CLUSTER, reinterpret_cast<const void*>(&linear_tile_kernel<BN, STAGES, IN, OUT, MODE, SUMS, CLUSTER>),
             TileSmem<kBRows, STAGES>::kAlloc, kTileThreads};
 }
 
 // config: GEMM_CONFIG_256x256 (3), _128x256 (1) or anything else (_128x128, 2).
-template <int IN, int OUT, int MODE>
+template <int IN, int OUT, int MODE, bool SUMS>
 KernelChoice tile_choice_for(int config)
 {
-    if (config == 3) return tile_choice<256, 6, IN, OUT, MODE, 2>(3);
-    if (config == 1) return tile_choice<256, 4, IN, OUT, MODE, 1>(1);
-    return tile_choice<128, 6, IN, OUT, MODE, 1>(2);
+    if (config == 3) return tile_choice<256, 6, IN, OUT, MODE, SUMS, 2>(3);
+    if (config == 1) return tile_choice<256, 4, IN, OUT, MODE, SUMS, 1>(1);
+    return tile_choice<128, 6, IN, OUT, MODE, SUMS, 1>(2);
 }
 
 KernelChoice forward_f16(int config);
 KernelChoice forward_bf16(int config);
 KernelChoice forward_e4m3(int config, bool out_bf16);
 KernelChoice forward_e5m2(int config, bool out_bf16);
-KernelChoice dgrad_16(int config, bool bf16);
+KernelChoice dgrad_f16(int config, bool sums);
+KernelChoice dgrad_bf16(int config, bool sums);
 KernelChoice wgrad_f16(int config, bool out_f32);
 KernelChoice wgrad_bf16(int config, bool out_f32);
 

@@ -24,6 +24,7 @@ TORCH_TO_DTYPE = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
 TORCH_TO_DTYPE_EX = {**TORCH_TO_DTYPE, torch.float8_e4m3fn: DTYPE_E4M3, torch.float8_e5m2: DTYPE_E5M2}
 # Biases, bias gradients and weight gradients (the linear-layer entry points).
 TORCH_TO_DTYPE_F32 = {**TORCH_TO_DTYPE, torch.float32: DTYPE_F32}
+OWN_SUMS_BYTES = 4 << 20  # GEMM_OWN_SUMS_BYTES: column sums that need no more use the handle's workspace
 ACTS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # gemm_act_t
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ARCH, ERR_CUDA, ERR_TIMEOUT = range(6)
@@ -562,8 +563,10 @@ class Gemm:
         lddx = _matrix(out, "out", M, K, dt, dev)
         if dbias is not None:
             db_code, db_p = _vector(dbias, "dbias", K, dt, dev), dbias.data_ptr()
-            ws = self._sums_workspace(M, K, stream)
-            ws_p, ws_bytes = ws.data_ptr(), ws.size(1) * 4
+            ws_bytes = self._lib.gemm_bias_grad_workspace_bytes(M, K)
+            if ws_bytes > OWN_SUMS_BYTES:
+                ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
+                ws_p = ws.data_ptr()
         a = gemm_dgrad_args_t(dY.data_ptr(), W.data_ptr(), z_p, out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy, ldw,
                               ldz, lddx, dt_code, db_code, code, alpha, beta_bias)
         st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), self._stream(stream))
@@ -625,8 +628,10 @@ class Gemm:
             lddz, dz_p = _matrix(out, "out", M, N, dt, dev), out.data_ptr()
         if dbias is not None:
             db_code, db_p = _vector(dbias, "dbias", N, dt, dev), dbias.data_ptr()
-            ws = self._sums_workspace(M, N, stream)
-            ws_p, ws_bytes = ws.data_ptr(), ws.size(1) * 4
+            ws_bytes = self._lib.gemm_bias_grad_workspace_bytes(M, N)
+            if ws_bytes > OWN_SUMS_BYTES:
+                ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
+                ws_p = ws.data_ptr()
         a = gemm_act_grad_args_t(dY.data_ptr(), z_p, dz_p, db_p, ws_p, ws_bytes, M, N, lddy, ldz, lddz, dt_code, db_code,
                                  code, beta_bias)
         st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), self._stream(stream))
@@ -638,10 +643,6 @@ class Gemm:
         if stream is None:
             return _raw_stream(self._index)
         return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-
-    def _sums_workspace(self, M: int, cols: int, stream) -> torch.Tensor:
-        """A new workspace for the column sums of an M x cols matrix, one row of floats."""
-        return _new(1, self._lib.gemm_bias_grad_workspace_bytes(M, cols) // 4, torch.float32, self._index, stream)
 
     def sync_status(self, stream=None) -> int:
         return int(self._lib.gemm_sync_status(self._h, _stream_ptr(stream) or None))

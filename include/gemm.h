@@ -25,7 +25,7 @@
  *
  * Ownership.  The caller owns A, B, C and the stream; the handle owns the watchdog's
  * 16-byte error word, a stream-K workspace (fp32 partial sums and arrival counters, about
- * 40 MB on a 152-SM GPU, allocated by gemm_create), a cache of tensor-map descriptors and,
+ * 40 MB on a 152-SM GPU, and 4 MiB for column sums, allocated by gemm_create), a cache of tensor-map descriptors and,
  * after the first gemm_run_host, device staging buffers plus that path's streams and
  * events.  A handle may be used from one host thread at a time, and its launches must not
  * overlap on the GPU (they share the workspace): enqueue them on one stream or order them.
@@ -414,9 +414,9 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, v
  *   - dY: M x N, W: N x K, Z: M x K (the pre-activations that the layer below saved; NULL when
  *     act is NONE, and not read then), dX: M x K, all of type dtype (F16 or BF16).
  *   - dbias: K values of dbias_dtype (F32, or dtype), or NULL.  With beta_bias == 0 it is not
- *     read.  workspace: gemm_bias_grad_workspace_bytes(M, K) bytes, 16-byte aligned, that the
- *     call may overwrite until its kernels are done; needed with dbias only (too small, or NULL:
- *     INVALID_ARG).
+ *     read.  workspace, used with dbias only: gemm_bias_grad_workspace_bytes(M, K) bytes, 16-byte
+ *     aligned, that the call may overwrite until its kernels are done (fewer: INVALID_ARG).  It
+ *     may be NULL if those are at most GEMM_OWN_SUMS_BYTES: the handle's own are used then.
  *   - K == 0 is a no-op; with M == 0 dbias becomes beta_bias * dbias; with N == 0 d is zero. */
 typedef struct {
     const void* dY;
@@ -477,6 +477,8 @@ typedef struct {
 } gemm_act_grad_args_t;
 
 gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* args, void* stream);
+
+#define GEMM_OWN_SUMS_BYTES (4 << 20) /* the handle's own workspace for column sums */
 
 /* Bytes of workspace for the column sums of an M x cols matrix: 4 * ceil(M / 32) * (cols rounded
  * up to 64); 0 when M or cols is 0. */

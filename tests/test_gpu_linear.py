@@ -553,7 +553,7 @@ def test_refusals(g):
     bwd = dict(dY=p, W=p, Z=p, dX=p, dbias=p, workspace=p, workspace_bytes=1 << 12, M=16, N=16, K=16, lddy=16, ldw=16,
                ldz=16, lddx=16, act=1, alpha=1.0, dbias_dtype=4)
     for bad, want in [(dict(Z=None), INV), (dict(dY=None), INV), (dict(dX=None), INV), (dict(dtype=2), INV),
-                      (dict(workspace=None), INV), (dict(workspace_bytes=255), INV), (dict(dbias_dtype=1), INV),
+                      (dict(workspace=None, M=1 << 20), INV), (dict(workspace_bytes=255), INV), (dict(dbias_dtype=1), INV),
                       (dict(beta_bias=float("nan")), INV), (dict(ldz=8), INV), (dict(act=7), INV), (dict(N=-1), INV),
                       (dict(workspace=p + 4), UNS), (dict(ldz=20), UNS), (dict(dbias=p + 2), UNS), (dict(dX=p + 2), UNS),
                       (dict(K=0, dX=None), native.OK)]:
@@ -567,7 +567,7 @@ def test_refusals(g):
         assert got == want, (bad, got)
     ag = dict(dY=p, Z=p, dZ=p, dbias=p, workspace=p, workspace_bytes=1 << 12, M=16, N=16, lddy=16, ldz=16, lddz=16, act=2,
               dbias_dtype=4)
-    for bad, want in [(dict(dY=None), INV), (dict(Z=None), INV), (dict(workspace=None), INV), (dict(lddz=8), INV),
+    for bad, want in [(dict(dY=None), INV), (dict(Z=None), INV), (dict(workspace=None, M=1 << 20), INV), (dict(lddz=8), INV),
                       (dict(dtype=4), INV), (dict(dZ=p + 2), UNS), (dict(lddy=20), UNS), (dict(N=0, dY=None), native.OK)]:
         got = lib.gemm_run_act_grad(h, struct(native.gemm_act_grad_args_t, ag, **bad), None)
         assert got == want, (bad, got)
