@@ -410,61 +410,64 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int64_t tile;
             int kb0, kb1;
             while (!aborted && it.next(p, tile, kb0, kb1)) {
-                int in_chunk = 0;
-                for (int i = 0; i < kb1 - kb0; ++i) {
-                    if (in_chunk == 0) {
-                        if (!wd.wait(acce_bar(acc), acc_phase ^ 1u, kRoleMma, tile, -1)) {
-                            aborted = true;
-                            break;
-                        }
-                    }
-                    if (!wd.wait(full_bar(stage), phase, kRoleMma, tile, kb0 + i)) {
+                // A loop over chunks around one over K blocks: with the chunk's wait and commit as conditions inside a
+                // single loop, each K block's issue took about 60 cycles longer (8192^3 bf16: 623 against 563 us).
+                const int n = kb1 - kb0;
+                for (int c0 = 0; c0 < n && !aborted;) {
+                    if (!wd.wait(acce_bar(acc), acc_phase ^ 1u, kRoleMma, tile, -1)) {
                         aborted = true;
                         break;
                     }
                     ptx::tc_fence_after_sync();
                     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                    const uint32_t sa = base + stage * L::kStageBytes;
-                    const uint32_t sb = sa + L::kABytes;
+                    const int c1 = n - c0 > p.chunk_kb ? c0 + p.chunk_kb : n;
+                    for (int i = c0; i < c1; ++i) {
+                        if (!wd.wait(full_bar(stage), phase, kRoleMma, tile, kb0 + i)) {
+                            aborted = true;
+                            break;
+                        }
+                        ptx::tc_fence_after_sync();
+                        const uint32_t sa = base + stage * L::kStageBytes;
+                        const uint32_t sb = sa + L::kABytes;
 #pragma unroll
-                    for (int k = 0; k < T::kStageK / T::kMmaK; ++k) {
-                        // K-major: the k-th slice starts 32 bytes further along each 128-byte row.  M- or N-major:
-                        // rows are the contraction, the k-th slice starts kMmaK rows of 128 bytes on, and 64-wide
-                        // blocks are kStageK rows apart.
-                        const uint64_t adesc = AT ? smem_desc_sw128(sa + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
-                                                  : smem_desc_sw128(sa + k * 32, 16, 1024);
-                        const uint64_t bdesc = BT ? smem_desc_sw128(sb + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
-                                                  : smem_desc_sw128(sb + k * 32, 16, 1024);
-                        const uint32_t accumulate = (in_chunk != 0 || k != 0) ? 1u : 0u;
-                        if constexpr (PAIR) {
-                            if constexpr (T::kF8)
-                                ptx::mma_f8_pair(d_tmem, adesc, bdesc, idesc, accumulate);
-                            else
-                                ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, accumulate);
-                        } else {
-                            if constexpr (T::kF8)
-                                ptx::mma_f8_cta1(d_tmem, adesc, bdesc, idesc, accumulate);
-                            else
-                                ptx::mma_f16_cta1(d_tmem, adesc, bdesc, idesc, accumulate);
+                        for (int k = 0; k < T::kStageK / T::kMmaK; ++k) {
+                            // K-major: the k-th slice starts 32 bytes further along each 128-byte row.  M- or
+                            // N-major: rows are the contraction, the k-th slice starts kMmaK rows of 128 bytes on, and
+                            // 64-wide blocks are kStageK rows apart.
+                            const uint64_t adesc = AT ? smem_desc_sw128(sa + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
+                                                      : smem_desc_sw128(sa + k * 32, 16, 1024);
+                            const uint64_t bdesc = BT ? smem_desc_sw128(sb + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
+                                                      : smem_desc_sw128(sb + k * 32, 16, 1024);
+                            const uint32_t accumulate = (i != c0 || k != 0) ? 1u : 0u;
+                            if constexpr (PAIR) {
+                                if constexpr (T::kF8)
+                                    ptx::mma_f8_pair(d_tmem, adesc, bdesc, idesc, accumulate);
+                                else
+                                    ptx::mma_f16_pair(d_tmem, adesc, bdesc, idesc, accumulate);
+                            } else {
+                                if constexpr (T::kF8)
+                                    ptx::mma_f8_cta1(d_tmem, adesc, bdesc, idesc, accumulate);
+                                else
+                                    ptx::mma_f16_cta1(d_tmem, adesc, bdesc, idesc, accumulate);
+                            }
+                        }
+                        if constexpr (PAIR)
+                            ptx::mma_commit_pair(empty_bar(stage), 0x3);
+                        else
+                            ptx::mma_commit_cta1(empty_bar(stage));
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
                         }
                     }
+                    if (aborted) break;
                     if constexpr (PAIR)
-                        ptx::mma_commit_pair(empty_bar(stage), 0x3);
+                        ptx::mma_commit_pair(accf_bar(acc), 0x3);
                     else
-                        ptx::mma_commit_cta1(empty_bar(stage));
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (++in_chunk == p.chunk_kb || i + 1 == kb1 - kb0) {
-                        if constexpr (PAIR)
-                            ptx::mma_commit_pair(accf_bar(acc), 0x3);
-                        else
-                            ptx::mma_commit_cta1(accf_bar(acc));
-                        in_chunk = 0;
-                        acc ^= 1;
-                        if (acc == 0) acc_phase ^= 1u;
-                    }
+                        ptx::mma_commit_cta1(accf_bar(acc));
+                    c0 = c1;
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
             }
             if (aborted) {
