@@ -145,9 +145,9 @@ int tile_slot(const Product& q, int config)
     return kLinearSlot0 + 3 * op + (config - 1);
 }
 
-// K blocks per chunk of an accumulation in registers (see tile_kernel.cuh): 8 blocks of 64 keep the
-// truncation of the tensor core's accumulator at 6e-7 of the sum.
-constexpr int32_t kChunkBlocks = 8;
+// K blocks per chunk of an accumulation in registers (see tile_kernel.cuh): 12 blocks of 64 keep the
+// truncation of the tensor core's accumulator under 1e-6 of the sum.
+constexpr int64_t kChunkBlocks = 12;
 
 gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t stream)
 {
@@ -176,6 +176,9 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t str
         return GEMM_ERR_CUDA;
     tA = tB = tZ = tC;  // those that are not used name a valid tensor
     if (q.Z && !get_tmap(nullptr, q.Z, q.cols, q.rows, q.ldz * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tZ))
+        return GEMM_ERR_CUDA;
+    if (q.mode == dtg::linear::kDgrad && q.src &&  // the boxes of pre-activations: those of the output
+        !get_tmap(nullptr, q.src, q.cols, q.rows, q.ldsrc * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tZ))
         return GEMM_ERR_CUDA;
     if (q.depth > 0) {
         const bool at = q.mode == dtg::linear::kWgrad, bt = q.mode != dtg::linear::kForward;
@@ -209,7 +212,10 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t str
     p.counters = h->ws.counters;
     p.alpha = q.alpha;
     p.beta = q.beta;
-    p.chunk_kb = q.out == GEMM_DTYPE_F32 || q.partials ? kChunkBlocks : INT32_MAX;  // SUMS, or one chunk
+    // SUMS kernels: chunks of equal length (within one); the others take a contraction as one chunk.
+    p.chunk_kb = INT32_MAX;
+    if ((q.out == GEMM_DTYPE_F32 || q.partials) && plan.k_blocks > 0)
+        p.chunk_kb = static_cast<int32_t>(cdiv(plan.k_blocks, cdiv(plan.k_blocks, kChunkBlocks)));
     p.act = q.act;
     p.bias = q.bias;
     p.bias_f32 = q.bias_dtype == GEMM_DTYPE_F32;

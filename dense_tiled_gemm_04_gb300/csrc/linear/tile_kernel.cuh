@@ -64,13 +64,16 @@ struct TileParams : KernelParams {
     int64_t pitch;
 };
 
-template <int B_ROWS, int STAGES>
+// STG_BUFS: staging buffers per epilogue warp.
+template <int B_ROWS, int STAGES, int STG_BUFS>
 struct TileSmem {
     static constexpr int kABytes = kBM * kRowBytes;
     static constexpr int kStageBytes = kABytes + B_ROWS * kRowBytes;
     static constexpr int kStgOff = STAGES * kStageBytes;
-    static constexpr int kBarOff = kStgOff + kTileEpiWarps * kTileStgBytes;
-    static constexpr int kNumBars = 2 * STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int kStgBufs = STG_BUFS;
+    static constexpr int kBarOff = kStgOff + kTileEpiWarps * STG_BUFS * kTileStgBytes;
+    // full, empty, acc_full[2], acc_empty[2], drain, pre-activation boxes per staging buffer
+    static constexpr int kNumBars = 2 * STAGES + 5 + kTileEpiWarps * 2;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kTotal = kMiscOff + 16;  // tmem slot, abort flag, stream-K "last" flag
     static constexpr int kAlloc = kTotal + 1024;  // slack for aligning the base to 1 KB
@@ -114,6 +117,13 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
 {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -181,6 +191,23 @@ __device__ __forceinline__ void load_row32(float (&r)[32], const float* row, int
     }
 }
 
+// Address of 16-byte chunk ch of row `lane` in a staging buffer (128-byte swizzle).
+__device__ __forceinline__ uint32_t box_chunk(uint32_t stg, int lane, int ch)
+{
+    return stg + lane * 128 + ((ch ^ (lane & 7)) << 4);
+}
+
+// TMA store of a staging buffer that the warp has just written.
+__device__ __forceinline__ void store_box_now(const CUtensorMap* tm, uint32_t stg, int32_t x, int32_t y, int lane)
+{
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        ptx::tma_store_2d(tm, stg, x, y);
+        ptx::bulk_commit_group();
+    }
+}
+
 // Write a warp's box (lane = row y + lane, 128 bytes from column x: h) through its staging buffer
 // and a TMA store, which drops rows >= M and columns >= N.  TMA clips columns to 16-byte
 // granules only, so a box that straddles a ragged N is written with masked stores.
@@ -217,13 +244,8 @@ __device__ __forceinline__ void store_rows(const uint32_t (&h)[32], int32_t x, i
     __syncwarp();
 #pragma unroll
     for (int ch = 0; ch < 8; ++ch)
-        ptx::st_shared_v4(stg + lane * 128 + ((ch ^ (lane & 7)) << 4), h[4 * ch], h[4 * ch + 1], h[4 * ch + 2], h[4 * ch + 3]);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        ptx::tma_store_2d(tm, stg, x, y);
-        ptx::bulk_commit_group();
-    }
+        ptx::st_shared_v4(box_chunk(stg, lane, ch), h[4 * ch], h[4 * ch + 1], h[4 * ch + 2], h[4 * ch + 3]);
+    store_box_now(tm, stg, x, y, lane);
 }
 
 // Sums over the warp's 32 rows of 64 columns held one row per lane: lane l ends with columns 2l, 2l + 1
@@ -261,7 +283,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kBRows = BN / kRanks;
     constexpr int CW = BN / 2;                 // columns per epilogue warp
     constexpr uint32_t kTmemCols = 2 * BN;
-    using L = TileSmem<kBRows, STAGES>;
+    using L = TileSmem<kBRows, STAGES, MODE == kDgrad ? 2 : 1>;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -273,6 +295,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 5 + 2 * w + b); };  // dgrad: box loaded
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int32_t* const abort_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 4);
     volatile int32_t* const last_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 8);
@@ -294,6 +317,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ptx::mbar_init(acce_bar(b), kTileEpiWarps * kRanks);
         }
         ptx::mbar_init(drain_bar, 1);
+        if constexpr (MODE == kDgrad)
+            for (int w = 0; w < kTileEpiWarps; ++w)
+                for (int b = 0; b < 2; ++b) ptx::mbar_init(in_bar(w, b), 1);
         *abort_flag = 0;
         *last_flag = 0;
         ptx::fence_mbar_init();
@@ -487,7 +513,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int quad = warp & 3;               // TMEM lane quadrant this warp may read
         const int half = ew >> 2;                // which BN/2 columns of the tile
         const int row_in_cta = quad * 32 + lane;
-        const uint32_t stg = base + L::kStgOff + ew * kTileStgBytes;
+        const uint32_t stg = base + L::kStgOff + ew * L::kStgBufs * kTileStgBytes;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         constexpr bool kBf16 = OUT == kOutBf16;
         int acc = 0;
@@ -495,9 +521,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         WorkIter it(p, unit, units);
         int64_t tile;
         int kb0, kb1;
+        // dgrad: pre-activations come by TMA, box by box, into the staging buffer that the box's result will leave
+        // from.  For whole tiles the loads run one box ahead, in the order in which finish_box takes the boxes; a tile
+        // that was shared out loads its boxes when its sums are ready.  (Loaded from global memory by the lanes, 16
+        // bytes of 32 rows at a time, they bound the kernel: 16384 x 1024 x 8192 relu 233 us against 176 without.)
+        int in_buf = 0;                        // buffer of the next box
+        uint32_t in_phase = 0, in_flight = 0;  // per buffer: parity its barrier completes next; a load is pending
+        int64_t in_tile = unit;                // the tile of the next box to load ahead
+        int in_box = 0;                        // and the box's place in it
+        auto load_in = [&](int buf, int32_t x, int32_t y) {
+            in_flight |= 1u << buf;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(in_bar(ew, buf), kTileStgBytes);
+                ptx::tma_load_2d(stg + buf * kTileStgBytes, &tmZ, x, y, in_bar(ew, buf));
+            }
+        };
+        auto load_ahead = [&](int buf) {
+            while (in_tile < p.dp_tiles) {
+                int64_t tm, tn;
+                tile_coord(in_tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+                const int32_t y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
+                const int32_t x = static_cast<int32_t>(tn * BN + half * CW + in_box * 64);
+                const bool inside = y < p.M && x < p.N;
+                if (++in_box == CW / 64) {
+                    in_box = 0;
+                    in_tile += units;
+                }
+                if (inside) {
+                    load_in(buf, x, y);
+                    return;
+                }
+            }
+        };
+
         // The operator on 64 columns (32 for an fp32 output) of this thread's row, from column x of C on: v holds
         // the product's sums and is overwritten.  A warp's rows start at y < M, its columns at x < N.
-        auto finish_box = [&](float* v, int32_t x, int32_t y) {
+        auto finish_box = [&](float* v, int32_t x, int32_t y, bool ahead) {
             const int64_t row = static_cast<int64_t>(y) + lane;
             const bool row_in = row < p.M;
             const f32x2 alpha = both(p.alpha);
@@ -513,6 +572,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(p.alpha * v[i]);
                 }
                 store_rows<4>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+            } else if constexpr (MODE == kDgrad) {
+                // The box's pre-activations are in (or on their way to) this box's staging buffer: each 16-byte chunk
+                // is read, its eight values of d rounded and written back in place, which keeps few registers alive.
+                const uint32_t buf = stg + in_buf * kTileStgBytes;
+                const bool has_in = p.in != nullptr;
+                f32x2 w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
+                if (has_in) {
+                    if (!ahead) {
+                        if (lane == 0) ptx::bulk_wait_group_read<0>();
+                        __syncwarp();
+                        load_in(in_buf, x, y);
+                    }
+                    const bool in = wd.wait(in_bar(ew, in_buf), (in_phase >> in_buf) & 1u, kRoleEpilogue, -1, 0);
+                    if (!__all_sync(0xFFFFFFFFu, in)) return;  // recorded: the launch is being abandoned
+                    in_phase ^= 1u << in_buf;
+                    in_flight &= ~(1u << in_buf);
+                    DTG_ACT_SWITCH(p.act, {
+                        _Pragma("unroll") for (int ch = 0; ch < 8; ++ch)
+                        {
+                            const uint4 z = ld_shared_u4(box_chunk(buf, lane, ch));
+                            w[4 * ch] = mul2(w[4 * ch], act_slope2<ACT>(unpack2<kBf16>(z.x)));
+                            w[4 * ch + 1] = mul2(w[4 * ch + 1], act_slope2<ACT>(unpack2<kBf16>(z.y)));
+                            w[4 * ch + 2] = mul2(w[4 * ch + 2], act_slope2<ACT>(unpack2<kBf16>(z.z)));
+                            w[4 * ch + 3] = mul2(w[4 * ch + 3], act_slope2<ACT>(unpack2<kBf16>(z.w)));
+                        }
+                    });
+                }
+                // The store issued one box ago has had this box's arithmetic to read its buffer, which the next box's
+                // pre-activations take (without any, the buffers alternate).
+                if (has_in && ahead) {
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+                    load_ahead(in_buf ^ 1);
+                } else {
+                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                    __syncwarp();
+                }
+                if ((p.N & 7) != 0 && x + 64 > p.N) {
+                    uint32_t h[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(w[i]);
+                    store_rows<2>(h, x, y, lane, buf, &tmC, p.C, p.ldc, p.M, p.N);  // its masked stores
+                } else {
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch)
+                        ptx::st_shared_v4(box_chunk(buf, lane, ch), round2<kBf16>(w[4 * ch]), round2<kBf16>(w[4 * ch + 1]),
+                                          round2<kBf16>(w[4 * ch + 2]), round2<kBf16>(w[4 * ch + 3]));
+                    store_box_now(&tmC, buf, x, y, lane);
+                }
+                in_buf ^= 1;
+                if (p.partials) {
+                    // Rows past M are not part of the sums (an infinite weight makes them NaN).
+                    if (!row_in) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) split(w[i], v[2 * i], v[2 * i + 1]);
+                    sum_rows(v, lane);
+                    *reinterpret_cast<float2*>(p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + 2 * lane) =
+                        make_float2(v[0], v[1]);
+                }
             } else {
                 uint32_t r[32];
                 const bool has_in = p.in != nullptr;
@@ -563,14 +686,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for (int i = 0; i < 32; ++i) w[i] = add2(w[i], unpack2<kBf16>(r[i]));
                     }
                 }
-                if constexpr (MODE == kDgrad) {
-                    if (has_in) {
-                        DTG_ACT_SWITCH(p.act, {
-                            _Pragma("unroll") for (int i = 0; i < 32; ++i) w[i] =
-                                mul2(w[i], act_slope2<ACT>(unpack2<kBf16>(r[i])));
-                        });
-                    }
-                }
                 if constexpr (MODE == kWgrad) {
                     if (has_in) {
                         const f32x2 beta = both(p.beta);
@@ -581,20 +696,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(w[i]);
                 store_rows<2>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
-                if constexpr (MODE == kDgrad) {
-                    if (p.partials) {
-                        // Rows past M are not part of the sums (an infinite weight makes them NaN).
-                        if (!row_in) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) w[i] = 0;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) split(w[i], v[2 * i], v[2 * i + 1]);
-                        sum_rows(v, lane);
-                        *reinterpret_cast<float2*>(p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + 2 * lane) =
-                            make_float2(v[0], v[1]);
-                    }
-                }
             }
         };
 
@@ -714,7 +815,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     constexpr int kBox = OUT == kOutF32 ? 32 : 64;
 #pragma unroll
                     for (int b = 0; b < CW / kBox; ++b)
-                        if (x0 + b * kBox < p.N) finish_box(&s[b * kBox], x0 + b * kBox, y);
+                        if (x0 + b * kBox < p.N) finish_box(&s[b * kBox], x0 + b * kBox, y, tile < p.dp_tiles);
                 }
             } else {
                 // One chunk: every box goes straight from the accumulator (or from the parts) to the output.
@@ -733,7 +834,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             load_acc(v, tacc + b * 64);
                             if (b == CW / 64 - 1) release_acc();
                         }
-                        if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
+                        if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y, tile < p.dp_tiles);
                     }
                 } else {
                     float4* const mine = slot_f4(sk_slot(p, unit, tr));
@@ -752,7 +853,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             for (int i = 0; i < 64; ++i) v[i] = 0.0f;
                             for (int64_t part = 0; part < parts; ++part)
                                 add_part(v, slot_f4(sk_slot(p, first_unit + part, tr)) + b * 16 * kBM);
-                            if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
+                            if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y, tile < p.dp_tiles);
                         }
                     }
                 }
@@ -779,6 +880,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (tn * BN + half * CW + b * (128 / kElem) < p.N)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
         };
+        if (MODE == kDgrad && p.in) load_ahead(0);
         bool more = it.next(p, tile, kb0, kb1);
         if (more) prefetch_in(tile);
         while (more) {
@@ -788,6 +890,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (more) prefetch_in(tile);
             if (!one_item(this_tile, this_kb0, this_kb1)) break;  // all eight epilogue warps leave together
         }
+        if constexpr (MODE == kDgrad)  // after an abandoned launch: a load may still be on its way
+            for (int b = 0; b < 2; ++b)
+                if (in_flight & (1u << b)) wd.drain(in_bar(ew, b), (in_phase >> b) & 1u);
         if (lane == 0) ptx::bulk_wait_group_all();
         __syncwarp();
     }
