@@ -22,11 +22,14 @@ SOURCES = [os.path.join(CSRC, f) for f in ("gemm_api.cu", "kernels_f16.cu", "ker
                                            "kernels_e5m2.cu", "kernels_mx.cu", "kernels_sparse.cu",
                                            "linear/linear_api.cu", "linear/forward_f16.cu", "linear/forward_bf16.cu",
                                            "linear/forward_e4m3.cu", "linear/forward_e5m2.cu", "linear/dgrad_f16.cu",
-                                           "linear/dgrad_bf16.cu", "linear/wgrad_f16.cu", "linear/wgrad_bf16.cu")]
+                                           "linear/dgrad_bf16.cu", "linear/wgrad_f16.cu", "linear/wgrad_bf16.cu",
+                                           "linear/cluster_forward.cu", "linear/cluster_forward_8bit.cu",
+                                           "linear/cluster_grad.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "sm103_ptx.cuh", "kernel_set.cuh",
                                                      "host/handle.cuh", "linear/activation.cuh",
                                                      "linear/elementwise.cuh", "linear/tile_kernel.cuh",
-                                                     "linear/tile_set.cuh")] + [
+                                                     "linear/tile_set.cuh", "linear/cluster_kernel.cuh",
+                                                     "linear/cluster_set.cuh")] + [
     os.path.join(INCLUDE, "gemm.h")]
 OBJ_DIR = os.path.join(HERE, "_build")
 

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "cluster_set.cuh"
 #include "elementwise.cuh"
 #include "gemm.h"
 #include "host/handle.cuh"
@@ -16,7 +17,7 @@ using dtg::KernelChoice;
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 512;  // the edges of the last tiles still fit 32 bits
 constexpr int64_t kSumRows = 32;   // rows of a partial column sum
 constexpr int64_t kSumAlign = 64;  // its row pitch is a multiple of this many columns
 
@@ -132,26 +133,122 @@ KernelChoice tile_kernel(const Product& q, int config)
     }
 }
 
-// Launch-state slot of a tile kernel: 14 operators and types x 3 configurations.
-int tile_slot(const Product& q, int config)
+// One of 14 operators and types, for the launch-state slots.
+int operator_index(const Product& q)
 {
-    int op;
     if (q.mode == dtg::linear::kForward)
-        op = is_f8(q.in) ? 2 + 2 * (q.in - GEMM_DTYPE_E4M3) + (q.out == GEMM_DTYPE_BF16) : q.in;
-    else if (q.mode == dtg::linear::kDgrad)
-        op = 6 + 2 * q.in + (q.partials != nullptr);
-    else
-        op = 10 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
-    return kLinearSlot0 + 3 * op + (config - 1);
+        return is_f8(q.in) ? 2 + 2 * (q.in - GEMM_DTYPE_E4M3) + (q.out == GEMM_DTYPE_BF16) : q.in;
+    if (q.mode == dtg::linear::kDgrad) return 6 + 2 * q.in + (q.partials != nullptr);
+    return 10 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
+}
+
+int tile_slot(const Product& q, int config) { return kLinearSlot0 + 3 * operator_index(q) + (config - 1); }
+
+int cluster_slot(const Product& q, int tokens)
+{
+    return kLinearSlot0 + 42 + 4 * operator_index(q) + (tokens == 16 ? 0 : tokens == 32 ? 1 : tokens == 64 ? 2 : 3);
 }
 
 // K blocks per chunk of an accumulation in registers (see tile_kernel.cuh): 12 blocks of 64 keep the
 // truncation of the tensor core's accumulator under 1e-6 of the sum.
 constexpr int64_t kChunkBlocks = 12;
 
-gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t stream)
+// Whether a product runs on linear_cluster_kernel, and how: tokens per tile and CTAs per cluster.
+struct ClusterPlan {
+    int tokens = 0;  // 0: the tile kernels
+    int ranks = 1;
+};
+
+ClusterPlan plan_cluster(const LaunchOptions& o, const DeviceState& dev, const Product& q)
+{
+    ClusterPlan c;
+    if (o.config != GEMM_CONFIG_AUTO || q.depth == 0) return c;
+    const int64_t kb = cdiv(q.depth, is_f8(q.in) ? 128 : 64);
+    int tokens = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
+    if (q.mode == dtg::linear::kDgrad && tokens < 64) tokens = 64;
+    if (q.mode == dtg::linear::kWgrad) tokens = 128;
+    const int64_t tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
+    const int64_t slots = 2 * dev.num_sms;
+    if (tiles > slots) return c;
+    int ranks = 1;
+    while (ranks < dtg::linear::kClusterMaxSplit && tiles * ranks * 2 <= slots && kb >= ranks * 4) ranks *= 2;
+    // fp32 results: a chain of products no longer than the tile kernels' chunks.
+    if ((q.out == GEMM_DTYPE_F32 || q.partials) && cdiv(kb, ranks) > kChunkBlocks) return c;
+    c.tokens = tokens;
+    c.ranks = ranks;
+    return c;
+}
+
+gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPlan& plan, int64_t* sum_rows, cudaStream_t stream)
+{
+    using namespace dtg::linear;
+    const bool bf16 = q.out == GEMM_DTYPE_BF16;
+    const KernelChoice kc = q.mode == kDgrad   ? cluster_dgrad(plan.tokens, bf16)
+                            : q.mode == kWgrad ? cluster_wgrad(q.in == GEMM_DTYPE_BF16, q.out == GEMM_DTYPE_F32)
+                            : is_f8(q.in)      ? cluster_forward_8(plan.tokens, q.in == GEMM_DTYPE_E5M2, bf16)
+                                               : cluster_forward_16(plan.tokens, bf16);
+    const gemm_status_t ready = ensure_kernel_ready(h->dev, kc, cluster_slot(q, plan.tokens));
+    if (ready != GEMM_OK) return ready;
+    const uint64_t eb = static_cast<uint64_t>(elem_bytes(q.in));
+    const uint32_t sk = static_cast<uint32_t>(kc.stage_k), nb = static_cast<uint32_t>(kc.n_block);
+    // The features' operand is B (its rows are the output's columns), the tokens' is A.
+    CUtensorMap tF, tT;
+    if (!(q.mode == kForward ? get_tmap(nullptr, q.B, q.depth, q.cols, q.ldb * eb, sk, dtg::kBM, q.in, &tF)
+                             : get_tmap(nullptr, q.B, q.cols, q.depth, q.ldb * eb, nb, sk, q.in, &tF)) ||
+        !(q.mode == kWgrad ? get_tmap(nullptr, q.A, q.rows, q.depth, q.lda * eb, nb, sk, q.in, &tT)
+                           : get_tmap(nullptr, q.A, q.depth, q.rows, q.lda * eb, sk, static_cast<uint32_t>(plan.tokens), q.in, &tT)))
+        return GEMM_ERR_CUDA;
+    const int64_t tiles_t = cdiv(q.rows, plan.tokens), tiles_f = cdiv(q.cols, dtg::kBM);
+    if (sum_rows) *sum_rows = tiles_t;
+    ClusterParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = static_cast<int32_t>(q.rows);
+    p.N = static_cast<int32_t>(q.cols);
+    p.K = static_cast<int32_t>(q.depth);
+    p.num_kb = static_cast<int32_t>(cdiv(q.depth, kc.stage_k));
+    p.fault_inject = static_cast<int32_t>(h->opts.fault_inject);
+    p.timeout_ns = static_cast<uint64_t>(h->opts.timeout_ns);
+    p.err = h->d_err;
+    p.C = q.C;
+    p.ldc = q.ldc;
+    p.alpha = q.alpha;
+    p.beta = q.beta;
+    p.tiles_t = static_cast<int32_t>(tiles_t);
+    p.act = q.act;
+    p.bias = q.bias;
+    p.bias_f32 = q.bias_dtype == GEMM_DTYPE_F32;
+    p.in = q.src;
+    p.ldin = q.ldsrc;
+    p.Z = q.Z;
+    p.ldz = q.ldz;
+    p.partials = q.partials;
+    p.pitch = sum_pitch(q.cols);
+    void* args[] = {&tF, &tT, &p};
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles_t * tiles_f * plan.ranks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(kc.threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(kc.smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(plan.ranks);
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, kc.fn, args) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// Enqueue a product.  sum_rows: receives the rows of partial column sums that it writes.
+gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_rows, cudaStream_t stream)
 {
     const LaunchOptions& o = h->opts;
+    const ClusterPlan few = plan_cluster(o, h->dev, q);
+    if (few.tokens) return launch_cluster(h, q, few, sum_rows, stream);
+    if (sum_rows) *sum_rows = cdiv(q.rows, kSumRows);
     int config = pick_config(o, h->dev, q.rows, q.cols, q.depth);
     if (config == GEMM_CONFIG_128x64) config = GEMM_CONFIG_128x128;
     const KernelChoice kc = tile_kernel(q, config);
@@ -167,6 +264,24 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, cudaStream_t str
     if (ready != GEMM_OK) return ready;
     gemm_plan_t plan;
     fill_plan(o, h->dev, h->dev.max_clusters[slot], &h->ws, q.rows, q.cols, q.depth, kc, kDense, &plan);
+    // Sharing out the K blocks of the last tiles (stream-K) pays when the units that a last wave of whole tiles would
+    // leave idle are worth more K blocks than the joins cost, about 56 blocks of a 256-wide 16-bit tile (16384 x 1024
+    // x 8192 forward, 81 blocks a tile: 166 us shared, 174 whole; dgrad of the same, 1 block: 311 and 294).  Without a
+    // whole wave before it every unit would start at another K, and the operands' L2 reuse is lost
+    // (wgrad 1024 x 8192 over 16384, 1.7 waves: 209 us shared, 190 whole).  Under one wave the planner's rule stands.
+    const int64_t tiles = plan.tiles_m * plan.tiles_n, units = plan.grid / kc.cluster;
+    if (plan.dp_tiles < tiles && tiles >= units) {
+        const int64_t idle = cdiv(tiles, units) * units - tiles;
+        const int64_t join = 56 * (256 / kc.bn) * (is_f8(q.in) ? 2 : 1);
+        if (plan.dp_tiles == 0 || idle * plan.k_blocks < join * units) {
+            LaunchOptions whole = o;
+            whole.stream_k = 0;
+            fill_plan(whole, h->dev, h->dev.max_clusters[slot], &h->ws, q.rows, q.cols, q.depth, kc, kDense, &plan);
+        }
+    }
+    // The kernel numbers tiles, and a raster group's, in 32 bits.
+    if (tiles > kMaxDim) return GEMM_ERR_UNSUPPORTED;
+    plan.raster_group = std::min(plan.raster_group, plan.tiles_m);
 
     const uint64_t eb = static_cast<uint64_t>(elem_bytes(q.in));
     const uint32_t sk = static_cast<uint32_t>(kc.stage_k), nb = static_cast<uint32_t>(kc.n_block);
@@ -311,7 +426,7 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, v
     q.ldsrc = a.ldr;
     q.Z = a.Z;
     q.ldz = a.ldz;
-    return launch_product(h, q, static_cast<cudaStream_t>(stream));
+    return launch_product(h, q, nullptr, static_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* args, void* stream)
@@ -338,6 +453,7 @@ gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* ar
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int64_t rows = 0;  // of partial sums
     if (a.M > 0) {
         Product q = {};
         q.mode = dtg::linear::kDgrad;
@@ -356,11 +472,11 @@ gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* ar
         q.src = a.act != GEMM_ACT_NONE ? a.Z : nullptr;
         q.ldsrc = a.ldz;
         q.partials = a.dbias ? sums_of(h, a.workspace) : nullptr;
-        const gemm_status_t st = launch_product(h, q, s);
+        const gemm_status_t st = launch_product(h, q, &rows, s);
         if (st != GEMM_OK) return st;
     }
     if (!a.dbias) return GEMM_OK;
-    return launch_sums(sums_of(h, a.workspace), cdiv(a.M, kSumRows), a.K, bias_grad(a.dbias, a.dbias_dtype, a.beta_bias), s);
+    return launch_sums(sums_of(h, a.workspace), rows, a.K, bias_grad(a.dbias, a.dbias_dtype, a.beta_bias), s);
 }
 
 gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* args, void* stream)
@@ -398,7 +514,7 @@ gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* ar
     q.beta = a.beta;
     q.src = a.beta != 0.0f ? a.dW : nullptr;
     q.ldsrc = a.lddw;
-    return launch_product(h, q, static_cast<cudaStream_t>(stream));
+    return launch_product(h, q, nullptr, static_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* args, void* stream)

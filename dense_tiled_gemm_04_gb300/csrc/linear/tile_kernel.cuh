@@ -264,6 +264,18 @@ __device__ __forceinline__ void sum_rows(float* v, int lane)
     }
 }
 
+// tile_coord in 32 bits (a launch has fewer than 2^31 tiles): 64-bit divisions for every item took the
+// epilogue warps more instructions than a relu.
+__device__ __forceinline__ void tile_coord32(uint32_t t, const KernelParams& p, uint32_t& tm, uint32_t& tn)
+{
+    const uint32_t group_m = p.group_m, per_group = group_m * p.tiles_n;
+    const uint32_t g = t / per_group, first_m = g * group_m, left = p.tiles_m - first_m;
+    const uint32_t rows = left < group_m ? left : group_m;
+    const uint32_t r = t - g * per_group;
+    tn = r / rows;
+    tm = first_m + (r - tn * rows);
+}
+
 // IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward, kDgrad,
 // kWgrad; SUMS: the contraction runs in chunks that are summed in registers; CLUSTER: 1 (one CTA) or 2 (a CTA pair).
 template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER>
@@ -362,8 +374,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int64_t tile;
             int kb0, kb1;
             while (it.next(p, tile, kb0, kb1)) {
-                int64_t tm, tn;
-                tile_coord(tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+                uint32_t tm, tn;
+                tile_coord32(static_cast<uint32_t>(tile), p, tm, tn);
                 const int32_t y_a = static_cast<int32_t>(tm * kTileM + rank * kBM);
                 const int32_t n_b = static_cast<int32_t>(tn * BN + rank * kBRows);
                 const bool rev = it.reversed(p);
@@ -519,16 +531,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         WorkIter it(p, unit, units);
-        int64_t tile;
-        int kb0, kb1;
+
         // dgrad: pre-activations come by TMA, box by box, into the staging buffer that the box's result will leave
         // from.  For whole tiles the loads run one box ahead, in the order in which finish_box takes the boxes; a tile
         // that was shared out loads its boxes when its sums are ready.  (Loaded from global memory by the lanes, 16
         // bytes of 32 rows at a time, they bound the kernel: 16384 x 1024 x 8192 relu 233 us against 176 without.)
         int in_buf = 0;                        // buffer of the next box
         uint32_t in_phase = 0, in_flight = 0;  // per buffer: parity its barrier completes next; a load is pending
-        int64_t in_tile = unit;                // the tile of the next box to load ahead
-        int in_box = 0;                        // and the box's place in it
         auto load_in = [&](int buf, int32_t x, int32_t y) {
             in_flight |= 1u << buf;
             if (lane == 0) {
@@ -536,27 +545,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ptx::tma_load_2d(stg + buf * kTileStgBytes, &tmZ, x, y, in_bar(ew, buf));
             }
         };
-        auto load_ahead = [&](int buf) {
-            while (in_tile < p.dp_tiles) {
-                int64_t tm, tn;
-                tile_coord(in_tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-                const int32_t y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
-                const int32_t x = static_cast<int32_t>(tn * BN + half * CW + in_box * 64);
-                const bool inside = y < p.M && x < p.N;
-                if (++in_box == CW / 64) {
-                    in_box = 0;
-                    in_tile += units;
-                }
-                if (inside) {
-                    load_in(buf, x, y);
-                    return;
-                }
-            }
+        // A work item as this warp sees it: columns from x, rows from y of C; inside: it has some of both.
+        struct Item {
+            int64_t tile;
+            int kb0, kb1;
+            int32_t x, y;
+            bool whole, inside;
         };
+        auto next_item = [&](Item& t) -> bool {
+            if (!it.next(p, t.tile, t.kb0, t.kb1)) return false;
+            uint32_t tm, tn;
+            tile_coord32(static_cast<uint32_t>(t.tile), p, tm, tn);
+            t.y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
+            t.x = static_cast<int32_t>(tn * BN + half * CW);
+            t.whole = t.kb0 == 0 && t.kb1 == p.num_kb;
+            t.inside = t.y < p.M && t.x < p.N;
+            return true;
+        };
+        Item cur = {}, nxt = {};
+        bool more_items = false;  // nxt is an item
 
         // The operator on 64 columns (32 for an fp32 output) of this thread's row, from column x of C on: v holds
         // the product's sums and is overwritten.  A warp's rows start at y < M, its columns at x < N.
-        auto finish_box = [&](float* v, int32_t x, int32_t y, bool ahead) {
+        auto finish_box = [&](float* v, int32_t x, int32_t y) {
             const int64_t row = static_cast<int64_t>(y) + lane;
             const bool row_in = row < p.M;
             const f32x2 alpha = both(p.alpha);
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
                 if (has_in) {
-                    if (!ahead) {
+                    if (!(in_flight & (1u << in_buf))) {
                         if (lane == 0) ptx::bulk_wait_group_read<0>();
                         __syncwarp();
                         load_in(in_buf, x, y);
@@ -602,11 +613,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     });
                 }
                 // The store issued one box ago has had this box's arithmetic to read its buffer, which the next box's
-                // pre-activations take (without any, the buffers alternate).
-                if (has_in && ahead) {
+                // pre-activations take: of this tile, or of the next item if that is a whole tile (without any, the
+                // buffers alternate).
+                const bool same_tile = x + 64 < p.N && x - cur.x + 64 < CW;
+                if (has_in && (same_tile || (more_items && nxt.whole && nxt.inside))) {
                     if (lane == 0) ptx::bulk_wait_group_read<0>();
                     __syncwarp();
-                    load_ahead(in_buf ^ 1);
+                    load_in(in_buf ^ 1, same_tile ? x + 64 : nxt.x, same_tile ? y : nxt.y);
                 } else {
                     if (lane == 0) ptx::bulk_wait_group_read<1>();
                     __syncwarp();
@@ -762,21 +775,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
 
-        // One work item; false when the launch is being abandoned.
-        auto one_item = [&](int64_t tile, int kb0, int kb1) -> bool {
-            int64_t tm, tn;
-            tile_coord(tile, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-            const int32_t y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
-            const int32_t x0 = static_cast<int32_t>(tn * BN + half * CW);
-            const bool whole = kb0 == 0 && kb1 == p.num_kb;
+        // The item `cur`; false when the launch is being abandoned.
+        auto one_item = [&]() -> bool {
+            const int64_t tile = cur.tile;
+            const int kb0 = cur.kb0, kb1 = cur.kb1;
+            const int32_t y = cur.y, x0 = cur.x;
+            const bool whole = cur.whole;
             const int64_t tr = tile - p.dp_tiles;
             int64_t first_unit = 0, parts = 0;
             if (!whole) sk_parts(p, tr, first_unit, parts);
             if constexpr (SUMS) {
                 float s[CW];  // the running sums
+                bool ok = true;
 #pragma unroll
                 for (int i = 0; i < CW; ++i) s[i] = 0.0f;
-                bool ok = true;
                 for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
                     ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -789,7 +801,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             ptx::tmem_ld_32x32b_x32(tacc + q * 32, v);
                             ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[q * 32 + i] += __uint_as_float(v[i]);
+                            for (int i = 0; i < 32; i += 2)
+                                split(add2(pair(s[q * 32 + i], s[q * 32 + i + 1]),
+                                           pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))),
+                                      s[q * 32 + i], s[q * 32 + i + 1]);
                         }
                         release_acc();
                     }
@@ -815,7 +830,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     constexpr int kBox = OUT == kOutF32 ? 32 : 64;
 #pragma unroll
                     for (int b = 0; b < CW / kBox; ++b)
-                        if (x0 + b * kBox < p.N) finish_box(&s[b * kBox], x0 + b * kBox, y, tile < p.dp_tiles);
+                        if (x0 + b * kBox < p.N) finish_box(&s[b * kBox], x0 + b * kBox, y);
                 }
             } else {
                 // One chunk: every box goes straight from the accumulator (or from the parts) to the output.
@@ -834,7 +849,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             load_acc(v, tacc + b * 64);
                             if (b == CW / 64 - 1) release_acc();
                         }
-                        if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y, tile < p.dp_tiles);
+                        if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
                     }
                 } else {
                     float4* const mine = slot_f4(sk_slot(p, unit, tr));
@@ -853,7 +868,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             for (int i = 0; i < 64; ++i) v[i] = 0.0f;
                             for (int64_t part = 0; part < parts; ++part)
                                 add_part(v, slot_f4(sk_slot(p, first_unit + part, tr)) + b * 16 * kBM);
-                            if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y, tile < p.dp_tiles);
+                            if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
                         }
                     }
                 }
@@ -865,30 +880,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             return true;
         };
 
-        // Bring the lines of `in` that this thread will read for a tile into L2.  An item ahead, so that
-        // the loads in finish() find them there even when the accumulators never wait.
-        auto prefetch_in = [&](int64_t t) {
-            if (!p.in) return;
-            int64_t tm, tn;
-            tile_coord(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-            const int64_t row = tm * kTileM + rank * kBM + row_in_cta;
-            if (row >= p.M) return;
+        // Bring the lines of `in` that this warp will read for `nxt` into L2, an item ahead.
+        auto prefetch_in = [&]() {
+            const int64_t row = static_cast<int64_t>(nxt.y) + lane;
+            if (!p.in || !nxt.inside || row >= p.M) return;
             constexpr int kElem = OUT == kOutF32 ? 4 : 2;
-            const uint8_t* line = static_cast<const uint8_t*>(p.in) + (row * p.ldin + tn * BN + half * CW) * kElem;
+            const uint8_t* line = static_cast<const uint8_t*>(p.in) + (row * p.ldin + nxt.x) * kElem;
 #pragma unroll
             for (int b = 0; b < CW * kElem / 128; ++b)
-                if (tn * BN + half * CW + b * (128 / kElem) < p.N)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
+                if (nxt.x + b * (128 / kElem) < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
         };
-        if (MODE == kDgrad && p.in) load_ahead(0);
-        bool more = it.next(p, tile, kb0, kb1);
-        if (more) prefetch_in(tile);
-        while (more) {
-            const int64_t this_tile = tile;
-            const int this_kb0 = kb0, this_kb1 = kb1;
-            more = it.next(p, tile, kb0, kb1);
-            if (more) prefetch_in(tile);
-            if (!one_item(this_tile, this_kb0, this_kb1)) break;  // all eight epilogue warps leave together
+        more_items = next_item(nxt);
+        while (more_items) {
+            cur = nxt;
+            more_items = next_item(nxt);
+            if (more_items) prefetch_in();
+            if (!one_item()) break;  // all eight epilogue warps leave together
         }
         if constexpr (MODE == kDgrad)  // after an abandoned launch: a load may still be on its way
             for (int b = 0; b < 2; ++b)

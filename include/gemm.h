@@ -375,7 +375,8 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C,
  * Sums run in fp32, in an order that depends on the sizes and the handle's options alone, so a
  * call's results do not change from one call to the next.  Every matrix is row-major, with the
  * alignment rules of gemm_run (bases of 16 bytes; row pitches that are multiples of 16 bytes);
- * bias and dbias are dense vectors of any alignment their type allows.  An output may not
+ * bias and dbias are dense vectors of any alignment their type allows; a dimension over
+ * 2^31 - 512 is UNSUPPORTED.  An output may not
  * overlap an input, except where it is said below.  Like gemm_run these calls enqueue on
  * `stream` and return; they share the handle's workspace, so the rule on overlapping launches
  * is the same, and so are the status codes and the watchdog (gemm_sync_status). */

@@ -154,6 +154,43 @@ def test_linear_every_tile(g, config, dtype, out):
             Y.check(), Z.check()
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (5, 2056, 8192), (20, 1000, 2050), (48, 520, 4104), (90, 300, 8192),
+                                   (256, 1030, 4100), (1000, 1000, 1000), (600, 136, 5000)])
+@pytest.mark.parametrize("dtype,out", [(F16, F16), (BF16, BF16), (E4M3, BF16), (E5M2, F16)])
+def test_linear_split_over_a_cluster(g, M, N, K, dtype, out):
+    # Few tiles and a long contraction: the K blocks are shared by the CTAs of a cluster.
+    r = gen(M + K)
+    X, W, bias, res = matrix(r, M, K, dtype), matrix(r, N, K, dtype), vector(r, N, out, offset=1), matrix(r, M, N, out)
+    Y, Z = Guarded(M, N, out), Guarded(M, N, out)
+    g.linear(X, W, bias, act="silu", residual=res, out=Y.t, preact=Z.t, alpha=K ** -0.5)
+    y, z = ref.linear(X, W, bias, "silu", res, out, K ** -0.5)
+    ref.assert_within(Y.t, y, "Y")
+    ref.assert_within(Z.t, z, "Z")
+    Y.check(), Z.check()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 520), (70, 4100, 300), (130, 1000, 1030), (300, 2048, 136), (1003, 520, 1000)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gradients_split_over_a_cluster(g, M, N, K, dtype):
+    r = gen(M + K)
+    dY, W, Z, X = matrix(r, M, N, dtype), matrix(r, N, K, dtype, scale=N ** -0.5), matrix(r, M, K, dtype), matrix(r, M, K, dtype)
+    for sums in (True, False):
+        dX, db = Guarded(M, K, dtype), Guarded(1, K, F32)
+        g.linear_dgrad(dY, W, Z, act="gelu_tanh", out=dX.t, dbias=db.t[0] if sums else None)
+        d, b = ref.through_act(*ref.product(dY, W), Z, "gelu_tanh", dtype, F32)
+        ref.assert_within(dX.t, d, "dX")
+        dX.check()
+        if sums:
+            ref.assert_within(db.t[0], b, "dbias")
+            db.check()
+    for out in (F32, dtype):
+        dW0 = matrix(r, N, K, out)
+        dW = Guarded(N, K, out, init=dW0)
+        g.linear_wgrad(dY, X, out=dW.t, beta=0.5)
+        ref.assert_within(dW.t, ref.wgrad(dY, X, out, 1.0, 0.5, dW0), f"dW {out}")
+        dW.check()
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_linear_in_place_residual(g, M):
     r = gen(1)
@@ -589,3 +626,32 @@ def test_binding_refusals(g):
             call()
     with pytest.raises(native.GemmError):
         g.linear(torch.zeros((8, 12), dtype=F16, device="cuda"), torch.zeros((8, 12), dtype=F16, device="cuda"))
+
+
+# ------------------------------------------------------------------ the watchdog
+
+@pytest.mark.parametrize("M,config", [(4, native.CONFIG_AUTO), (100, native.CONFIG_AUTO), (600, native.CONFIG_128x128),
+                                      (600, native.CONFIG_128x256), (600, native.CONFIG_256x256)])
+def test_a_wait_that_runs_out_is_reported(g, M, config):
+    # A stage that never arrives (the library's own test hook): each wait gives up after its limit, the kernel
+    # leaves, the host reads the status, and the next call is right.
+    r = gen(14)
+    X, W, Z = matrix(r, M, 1024, BF16), matrix(r, 520, 1024, BF16, scale=0.03), matrix(r, M, 1024, BF16)
+    dY, db = matrix(r, M, 520, BF16), torch.empty(1024, device="cuda")
+    calls = [lambda: g.linear(X, W, act="gelu"), lambda: g.linear_dgrad(dY, W, Z, act="gelu", dbias=db),
+             lambda: g.linear_wgrad(dY, X)]
+    g.set_option(native.OPT_CONFIG, config)
+    want = [c().clone() for c in calls]
+    assert g.sync_status() == native.OK
+    for call, w in zip(calls, want):
+        g.set_option(native.OPT_TIMEOUT_NS, 50_000_000)
+        g.set_option(native.OPT_FAULT_INJECT, 1)
+        try:
+            call()
+            assert g.sync_status() == native.ERR_TIMEOUT
+            assert g.error_info()[0] == 1
+        finally:
+            g.set_option(native.OPT_FAULT_INJECT, 0)
+            g.set_option(native.OPT_TIMEOUT_NS, 2_000_000_000)
+        same(call(), w)
+        assert g.sync_status() == native.OK
