@@ -61,6 +61,7 @@ struct DeviceState {
     std::mutex mu;
     bool attrs_set[kNumSlots] = {};
     int max_clusters[kNumSlots] = {};  // pair kernels: co-resident clusters (0 = not yet queried)
+    int fits[kNumSlots][5] = {};       // kernels of any cluster size: those of 1, 2, 4, 8, 16 CTAs, likewise
 };
 
 // Streams and events of gemm_run_host's copy/compute pipeline (created on first use).

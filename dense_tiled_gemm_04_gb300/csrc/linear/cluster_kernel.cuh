@@ -8,7 +8,7 @@
 //        forward  features N from W (K-major),    tokens M from X (K-major)
 //        dgrad    features K from W (M-major),    tokens M from dY (K-major)
 //        wgrad    features K from X (M-major),    "tokens" N from dY (N-major)
-//  * A tile's contraction is split over the CTAs of a cluster, up to 8, so that there are one or two CTAs per
+//  * A tile's contraction is split over the CTAs of a cluster, up to 16, so that there are one or two CTAs per
 //    SM even when there are 32 tiles.  Two fit per SM (under 113 KB of ring each), so their waits overlap.
 //  * The partial sums meet through distributed shared memory: each CTA puts its 128 x BN block in its own shared memory
 //    (the ring's, done with), and after a cluster barrier adds its share of the outputs over all ranks in rank
@@ -24,7 +24,7 @@ namespace linear {
 
 constexpr int kClusterThreads = 256;  // producer, MMA, four TMEM warps, two more for the joining
 constexpr int kClusterTmemWarp0 = 2;
-constexpr int kClusterMaxSplit = 8;
+constexpr int kClusterMaxSplit = 16;
 
 struct ClusterParams : KernelParams {  // M: tokens, N: features of the output; K: the contraction
     int32_t tiles_t;     // token tiles
@@ -323,23 +323,22 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     ptx::cluster_sync();  // every rank's sums are in its shared memory
 
     // ---------------------------------------------------------------- join, operator, store
-    uint32_t at[kClusterMaxSplit];
-#pragma unroll
-    for (int r = 0; r < kClusterMaxSplit; ++r) at[r] = r < static_cast<int>(ranks) ? ptx::mapa_shared(base, r) : 0u;
     f32x2 col[2] = {0, 0};  // dgrad: sums of this thread's units; a thread's features never change (32 divides 256)
     if (*abort_flag == 0) {
         for (int i = u; i < u1; i += kClusterThreads) {
-            float4 v[kClusterMaxSplit];
+            f32x2 s[2] = {0, 0};
+            for (uint32_t r0 = 0; r0 < ranks; r0 += 8) {  // eight reads of other CTAs' memory in flight
+                float4 v[8];
 #pragma unroll
-            for (int r = 0; r < kClusterMaxSplit; ++r)
-                if (r < static_cast<int>(ranks)) v[r] = ld_cluster_f4(at[r] + 16u * static_cast<uint32_t>(i));
-            f32x2 s[2] = {pair(v[0].x, v[0].y), pair(v[0].z, v[0].w)};
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < ranks) v[r] = ld_cluster_f4(ptx::mapa_shared(base, r0 + r) + 16u * static_cast<uint32_t>(i));
 #pragma unroll
-            for (int r = 1; r < kClusterMaxSplit; ++r)
-                if (r < static_cast<int>(ranks)) {
-                    s[0] = add2(s[0], pair(v[r].x, v[r].y));
-                    s[1] = add2(s[1], pair(v[r].z, v[r].w));
-                }
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < ranks) {
+                        s[0] = add2(s[0], pair(v[r].x, v[r].y));
+                        s[1] = add2(s[1], pair(v[r].z, v[r].w));
+                    }
+            }
             Extra x = first;
             if (i != u) fetch(i, x);
             const int32_t f = f0 + 4 * (i & 31);
@@ -415,16 +414,14 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     ptx::cluster_sync();  // no rank's shared memory is read any more (dgrad: the sums of every rank are ready)
     if constexpr (MODE == kDgrad) {
         if (rank == 0 && p.partials && threadIdx.x < 32) {
-            float4 s = ld_cluster_f4(at[0] + L::kColOff + 16u * threadIdx.x);
-#pragma unroll
-            for (int r = 1; r < kClusterMaxSplit; ++r)
-                if (r < static_cast<int>(ranks)) {
-                    const float4 v = ld_cluster_f4(at[r] + L::kColOff + 16u * threadIdx.x);
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
+            float4 s = ld_cluster_f4(base + L::kColOff + 16u * threadIdx.x);
+            for (uint32_t r = 1; r < ranks; ++r) {
+                const float4 v = ld_cluster_f4(ptx::mapa_shared(base, r) + L::kColOff + 16u * threadIdx.x);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
             float* row = p.partials + static_cast<int64_t>(tt) * p.pitch + f0;
             const float o[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll

@@ -153,42 +153,89 @@ int cluster_slot(const Product& q, int tokens)
 // truncation of the tensor core's accumulator under 1e-6 of the sum.
 constexpr int64_t kChunkBlocks = 12;
 
-// Whether a product runs on linear_cluster_kernel, and how: tokens per tile and CTAs per cluster.
+// Whether a product runs on linear_cluster_kernel, and how.
 struct ClusterPlan {
-    int tokens = 0;  // 0: the tile kernels
-    int ranks = 1;
+    int tokens = 0;  // per tile; 0: the tile kernels
+    int ranks = 1;   // CTAs per cluster
+    KernelChoice kc;
 };
 
-ClusterPlan plan_cluster(const LaunchOptions& o, const DeviceState& dev, const Product& q)
+KernelChoice cluster_kernel(const Product& q, int tokens)
 {
-    ClusterPlan c;
-    if (o.config != GEMM_CONFIG_AUTO || q.depth == 0) return c;
+    using namespace dtg::linear;
+    const bool bf16 = q.out == GEMM_DTYPE_BF16;
+    if (q.mode == kDgrad) return cluster_dgrad(tokens, bf16);
+    if (q.mode == kWgrad) return cluster_wgrad(q.in == GEMM_DTYPE_BF16, q.out == GEMM_DTYPE_F32);
+    return is_f8(q.in) ? cluster_forward_8(tokens, q.in == GEMM_DTYPE_E5M2, bf16) : cluster_forward_16(tokens, bf16);
+}
+
+// Clusters of 2^log CTAs of a kernel that the GPU runs at once.  Its GPCs differ in size, so that is fewer than the
+// SMs alone would say: clusters of 16 for 16 tiles took a second round, 21.3 us for 256 x 1024 x 8192 against 13.6
+// with 8.  The runtime counts one CTA of these kernels per SM (76, 36, 15, 7 clusters of 2, 4, 8, 16); two run, as
+// their shared memory allows: 128 x 8192 x 8192 on 64 clusters of 4 takes 28.7 us, on 64 of 2 36.2.
+gemm_status_t clusters_that_fit(DeviceState& dev, const KernelChoice& kc, int slot, int log, int* n)
+{
+    std::lock_guard<std::mutex> lock(dev.mu);
+    if (dev.fits[slot][log] == 0) {
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3(1u << log, 1, 1);
+        cfg.blockDim = dim3(static_cast<unsigned>(kc.threads), 1, 1);
+        cfg.dynamicSmemBytes = static_cast<size_t>(kc.smem);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1u << log;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&dev.fits[slot][log], kc.fn, &cfg) != cudaSuccess) return GEMM_ERR_CUDA;
+        if (dev.fits[slot][log] == 0) dev.fits[slot][log] = -1;
+    }
+    *n = 2 * dev.fits[slot][log];
+    return GEMM_OK;
+}
+
+gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Product& q, ClusterPlan* c)
+{
+    if (o.config != GEMM_CONFIG_AUTO || q.depth == 0) return GEMM_OK;
     const int64_t kb = cdiv(q.depth, is_f8(q.in) ? 128 : 64);
     int tokens = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
     if (q.mode == dtg::linear::kDgrad && tokens < 64) tokens = 64;
     if (q.mode == dtg::linear::kWgrad) tokens = 128;
+    // Where the tile kernels would leave SMs idle.  Tiles of 128 tokens are as large as theirs, and only a split
+    // gains: with a short K their whole tiles are as fast or faster (2048 x 1024 x 1024: 12.3 us split in two, 10.0
+    // whole; 1000^3: 10.9 and 11.4; 256 x 8192 x 8192: 37.8 and 40.8), and more tiles than SMs are not split
+    // (512 x 8192 x 8192: 65 us, 47 on CTA pairs).  Fewer tokens take narrower tiles (8 x 8192 x 1024: 7.1 and 10.6).
     const int64_t tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
     const int64_t slots = 2 * dev.num_sms;
-    if (tiles > slots) return c;
-    int ranks = 1;
-    while (ranks < dtg::linear::kClusterMaxSplit && tiles * ranks * 2 <= slots && kb >= ranks * 4) ranks *= 2;
+    if (tokens == 128 ? (tiles > dev.num_sms || kb <= 16) : tiles > slots) return GEMM_OK;
+    c->kc = cluster_kernel(q, tokens);
+    const int slot = cluster_slot(q, tokens);
+    // Clusters of 16 are beyond the portable size.
+    if (!dev.attrs_set[slot] && cudaFuncSetAttribute(c->kc.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    gemm_status_t st = ensure_kernel_ready(dev, c->kc, slot);
+    // Double the ranks while every cluster still runs at once and each rank keeps two K blocks.
+    int log = 0;
+    while (st == GEMM_OK && (1 << log) < dtg::linear::kClusterMaxSplit && tiles * (2 << log) <= slots && kb >= (4 << log)) {
+        int n = 0;
+        st = clusters_that_fit(dev, c->kc, slot, log + 1, &n);
+        if (n < tiles) break;
+        ++log;
+    }
+    if (st != GEMM_OK) return st;
     // fp32 results: a chain of products no longer than the tile kernels' chunks.
-    if ((q.out == GEMM_DTYPE_F32 || q.partials) && cdiv(kb, ranks) > kChunkBlocks) return c;
-    c.tokens = tokens;
-    c.ranks = ranks;
-    return c;
+    if ((q.out == GEMM_DTYPE_F32 || q.partials) && cdiv(kb, 1 << log) > kChunkBlocks) return GEMM_OK;
+    c->tokens = tokens;
+    c->ranks = 1 << log;
+    return GEMM_OK;
 }
 
 gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPlan& plan, int64_t* sum_rows, cudaStream_t stream)
 {
     using namespace dtg::linear;
-    const bool bf16 = q.out == GEMM_DTYPE_BF16;
-    const KernelChoice kc = q.mode == kDgrad   ? cluster_dgrad(plan.tokens, bf16)
-                            : q.mode == kWgrad ? cluster_wgrad(q.in == GEMM_DTYPE_BF16, q.out == GEMM_DTYPE_F32)
-                            : is_f8(q.in)      ? cluster_forward_8(plan.tokens, q.in == GEMM_DTYPE_E5M2, bf16)
-                                               : cluster_forward_16(plan.tokens, bf16);
-    const gemm_status_t ready = ensure_kernel_ready(h->dev, kc, cluster_slot(q, plan.tokens));
-    if (ready != GEMM_OK) return ready;
+    const KernelChoice& kc = plan.kc;
     const uint64_t eb = static_cast<uint64_t>(elem_bytes(q.in));
     const uint32_t sk = static_cast<uint32_t>(kc.stage_k), nb = static_cast<uint32_t>(kc.n_block);
     // The features' operand is B (its rows are the output's columns), the tokens' is A.
@@ -199,6 +246,7 @@ gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPla
                            : get_tmap(nullptr, q.A, q.depth, q.rows, q.lda * eb, sk, static_cast<uint32_t>(plan.tokens), q.in, &tT)))
         return GEMM_ERR_CUDA;
     const int64_t tiles_t = cdiv(q.rows, plan.tokens), tiles_f = cdiv(q.cols, dtg::kBM);
+    const int64_t grid = tiles_t * tiles_f * plan.ranks;
     if (sum_rows) *sum_rows = tiles_t;
     ClusterParams p;
     std::memset(&p, 0, sizeof(p));
@@ -226,7 +274,7 @@ gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPla
     void* args[] = {&tF, &tT, &p};
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles_t * tiles_f * plan.ranks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(kc.threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(kc.smem);
     cfg.stream = stream;
@@ -246,7 +294,9 @@ gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPla
 gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_rows, cudaStream_t stream)
 {
     const LaunchOptions& o = h->opts;
-    const ClusterPlan few = plan_cluster(o, h->dev, q);
+    ClusterPlan few;
+    const gemm_status_t planned = plan_cluster(o, h->dev, q, &few);
+    if (planned != GEMM_OK) return planned;
     if (few.tokens) return launch_cluster(h, q, few, sum_rows, stream);
     if (sum_rows) *sum_rows = cdiv(q.rows, kSumRows);
     int config = pick_config(o, h->dev, q.rows, q.cols, q.depth);

@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int i = 0; i < kb1 - kb0; ++i, ++loaded) {
                     const int kb = rev ? kb1 - 1 - i : kb0 + i;
                     if (!wd.wait(empty_bar(stage), phase ^ 1u, kRoleProducer, tile, kb)) goto producer_done;
-                    // Test hook: the first unit leaves one stage unloaded and unarmed.
-                    if (!(p.fault_inject && unit == 0 && loaded == 1)) {
+                    // Test hook: the first unit leaves its first stage unloaded and unarmed.
+                    if (!(p.fault_inject && unit == 0 && loaded == 0)) {
                         const uint32_t sa = base + stage * L::kStageBytes;
                         const uint32_t sb = sa + L::kABytes;
                         const int32_t k0 = kb * T::kStageK;
