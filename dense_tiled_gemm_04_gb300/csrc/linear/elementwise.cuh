@@ -10,12 +10,13 @@ namespace linear {
 // dZ = dY * act'(Z) and its column sums over blocks of rows.
 //
 // Floor: 2 + 2 bytes read and 2 written per element.  A warp covers 256 columns of a row (16 bytes a lane), the
-// eight warps of a block rows r, r + 8, ... of its block of rows, four of them in flight per warp.
+// eight warps of a block rows r, r + 8, ... of its block of rows, two of them in flight per warp and four blocks per SM
+// (8192 x 8192 bf16 gelu with sums: 75.8 us; four rows and three blocks 82.0, one row and six blocks 86.0).
 // Each lane adds its eight columns in registers over all its rows; the eight warps' sums meet in shared memory in
 // warp order, so a row of partial sums is written per block of rows (not per 32 rows).
 constexpr int kActWarps = 8;
 constexpr int kActCols = 256;   // columns per block
-constexpr int kActUnroll = 4;   // rows in flight per warp
+constexpr int kActUnroll = 2;   // rows in flight per warp
 
 // A bias gradient to be written: beta * dbias + sum, of type kOutF16, kOutBf16 or kOutF32.
 struct BiasGrad {
@@ -48,7 +49,7 @@ struct ActGradParams {
 };
 
 template <bool BF16, int ACT>
-__global__ void __launch_bounds__(kActWarps * 32, 3) act_grad_kernel(const ActGradParams p)
+__global__ void __launch_bounds__(kActWarps * 32, 4) act_grad_kernel(const ActGradParams p)
 {
     __shared__ float sums[kActWarps][kActCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
