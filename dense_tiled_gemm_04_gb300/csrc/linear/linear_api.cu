@@ -203,13 +203,23 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
     int tokens = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
     if (q.mode == dtg::linear::kDgrad && tokens < 64) tokens = 64;
     if (q.mode == dtg::linear::kWgrad) tokens = 128;
-    // Where the tile kernels would leave SMs idle.  Tiles of 128 tokens are as large as theirs, and only a split
-    // gains: with a short K their whole tiles are as fast or faster (2048 x 1024 x 1024: 12.3 us split in two, 10.0
-    // whole; 1000^3: 10.9 and 11.4; 256 x 8192 x 8192: 37.8 and 40.8), and more tiles than SMs are not split
-    // (512 x 8192 x 8192: 65 us, 47 on CTA pairs).  Fewer tokens take narrower tiles (8 x 8192 x 1024: 7.1 and 10.6).
-    const int64_t tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
+    // Where the tile kernels would leave SMs idle: on fewer than 128 tokens, whose narrower tiles are the cheaper ones
+    // (8 x 8192 x 1024: 7.1 us, 10.6 on 128 x 128 tiles); and, in tiles of 128 tokens as large as theirs, where a
+    // split gains.  On a quarter of a tile per SM or less it always does, and 64 tokens a tile do it better (256 x
+    // 1024 x 1024: 5.8 us, 9.5 whole; 128 x 4096 x 4096: 12.1, 14.1 in 128).  Up to a tile per SM it does with more
+    // than 16 K blocks (256 x 8192 x 8192: 37.8 us, 40.8 whole; but 2048 x 1024 x 1024: 12.3, 10.0 whole).  More
+    // tiles are not split (512 x 8192 x 8192: 65 us, 47 on CTA pairs).
+    int64_t tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
     const int64_t slots = 2 * dev.num_sms;
-    if (tokens == 128 ? (tiles > dev.num_sms || kb <= 16) : tiles > slots) return GEMM_OK;
+    if (tokens == 128) {
+        const bool few = 4 * tiles <= dev.num_sms;
+        if (!few && (tiles > dev.num_sms || kb <= 16)) return GEMM_OK;
+        if (few && q.mode != dtg::linear::kWgrad) {
+            tokens = 64;
+            tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
+        }
+    }
+    if (tiles > slots) return GEMM_OK;
     c->kc = cluster_kernel(q, tokens);
     const int slot = cluster_slot(q, tokens);
     // Clusters of 16 are beyond the portable size.
