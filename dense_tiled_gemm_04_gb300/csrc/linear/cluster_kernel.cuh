@@ -181,27 +181,16 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     const int units = tokens * (kBM / 4);
     const int u0 = static_cast<int>(static_cast<int64_t>(units) * rank / ranks);
     const int u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / ranks);
-    // The operator's other inputs for one unit.
-    struct Extra {
-        f32x2 bias[2], in[2];
-    };
-    auto fetch = [&](int u, Extra& x) {
-        const int32_t f = f0 + 4 * (u & 31);
+    const int32_t f = f0 + 4 * ((u0 + static_cast<int>(threadIdx.x)) & 31);  // the features of all of its units (32 divides 256)
+    // Residual, pre-activations or dW of one unit.
+    auto fetch_in = [&](int u, f32x2 (&x)[2]) {
+        x[0] = x[1] = 0;
+        if (!p.in || f >= p.N) return;
         const int64_t t = t0 + (u >> 5);
-        x.bias[0] = x.bias[1] = x.in[0] = x.in[1] = 0;
-        if (f >= p.N) return;
-        if (MODE == kForward && p.bias) {
-            if (p.bias_f32)
-                load4f(x.bias, static_cast<const float*>(p.bias), f, p.N);
-            else
-                load4<kBf16>(x.bias, static_cast<const uint16_t*>(p.bias), f, p.N);
-        }
-        if (p.in) {
-            if constexpr (OUT == kOutF32)
-                load4f(x.in, static_cast<const float*>(p.in) + t * p.ldin, f, p.N);
-            else
-                load4<kBf16>(x.in, static_cast<const uint16_t*>(p.in) + t * p.ldin, f, p.N);
-        }
+        if constexpr (OUT == kOutF32)
+            load4f(x, static_cast<const float*>(p.in) + t * p.ldin, f, p.N);
+        else
+            load4<kBf16>(x, static_cast<const uint16_t*>(p.in) + t * p.ldin, f, p.N);
     };
 
     if (warp == kProducerWarp) {
@@ -282,10 +271,17 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
         __syncwarp();
     }
 
-    // Every thread fetches what its first unit needs beside the sums while the product runs.
-    Extra first;
-    int u = u0 + static_cast<int>(threadIdx.x);
-    if (u < u1) fetch(u, first);
+    // Every thread fetches what its first two units need beside the sums while the product runs.
+    const int u = u0 + static_cast<int>(threadIdx.x);
+    f32x2 bias[2] = {0, 0}, in0[2] = {0, 0}, in1[2] = {0, 0};
+    if (MODE == kForward && p.bias && u < u1 && f < p.N) {
+        if (p.bias_f32)
+            load4f(bias, static_cast<const float*>(p.bias), f, p.N);
+        else
+            load4<kBf16>(bias, static_cast<const uint16_t*>(p.bias), f, p.N);
+    }
+    if (u < u1) fetch_in(u, in0);
+    if (u + kClusterThreads < u1) fetch_in(u + kClusterThreads, in1);
 
     if (warp >= kClusterTmemWarp0 && warp < kClusterTmemWarp0 + 4) {
         // ---------------------------------------------------------------- accumulator -> shared memory
@@ -323,81 +319,100 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     ptx::cluster_sync();  // every rank's sums are in its shared memory
 
     // ---------------------------------------------------------------- join, operator, store
-    f32x2 col[2] = {0, 0};  // dgrad: sums of this thread's units; a thread's features never change (32 divides 256)
-    if (*abort_flag == 0) {
-        for (int i = u; i < u1; i += kClusterThreads) {
-            f32x2 s[2] = {0, 0};
-            for (uint32_t r0 = 0; r0 < ranks; r0 += 8) {  // eight reads of other CTAs' memory in flight
-                float4 v[8];
+    f32x2 col[2] = {0, 0};  // dgrad: sums of this thread's units
+    // Unit i, whose sums are s.
+    auto finish = [&](int i, f32x2 (&s)[2], const f32x2 (&in)[2]) {
+        if (f >= p.N) return;
+        const int64_t t = t0 + (i >> 5);
+        const f32x2 alpha = both(p.alpha);
+        if constexpr (MODE == kForward) {
+            s[0] = fma2(alpha, s[0], bias[0]);
+            s[1] = fma2(alpha, s[1], bias[1]);
+            if (p.Z) store4<kBf16>(static_cast<uint16_t*>(p.Z) + t * p.ldz, f, p.N, s);
+            DTG_ACT_SWITCH(p.act, {
+                s[0] = act_value2<ACT>(s[0]);
+                s[1] = act_value2<ACT>(s[1]);
+            });
+            if (p.in) {
+                s[0] = add2(s[0], in[0]);
+                s[1] = add2(s[1], in[1]);
+            }
+        } else if constexpr (MODE == kDgrad) {
+            s[0] = mul2(alpha, s[0]);
+            s[1] = mul2(alpha, s[1]);
+            if (p.in) {
+                DTG_ACT_SWITCH(p.act, {
+                    s[0] = mul2(s[0], act_slope2<ACT>(in[0]));
+                    s[1] = mul2(s[1], act_slope2<ACT>(in[1]));
+                });
+            }
+            col[0] = add2(col[0], s[0]);
+            col[1] = add2(col[1], s[1]);
+        } else {
+            s[0] = mul2(alpha, s[0]);
+            s[1] = mul2(alpha, s[1]);
+            if (p.in) {
+                s[0] = fma2(both(p.beta), in[0], s[0]);
+                s[1] = fma2(both(p.beta), in[1], s[1]);
+            }
+        }
+        if constexpr (OUT == kOutF32) {
+            float o[4];
+            split(s[0], o[0], o[1]);
+            split(s[1], o[2], o[3]);
+            float* row = static_cast<float*>(p.C) + t * p.ldc;
+            if (f + 4 <= p.N) {
+                *reinterpret_cast<float4*>(row + f) = make_float4(o[0], o[1], o[2], o[3]);
+            } else {
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r0 + r < ranks) v[r] = ld_cluster_f4(ptx::mapa_shared(base, r0 + r) + 16u * static_cast<uint32_t>(i));
+                for (int e = 0; e < 4; ++e)
+                    if (f + e < p.N) row[f + e] = o[e];
+            }
+        } else {
+            store4<kBf16>(static_cast<uint16_t*>(p.C) + t * p.ldc, f, p.N, s);
+        }
+    };
+    if (*abort_flag == 0) {
+        // Two units at a time, eight ranks' sums of each in flight, the inputs of the next two on their way.
+        for (int i = u; i < u1; i += 2 * kClusterThreads) {
+            const int j = i + kClusterThreads;
+            f32x2 s0[2] = {0, 0}, s1[2] = {0, 0};
+            for (uint32_t r0 = 0; r0 < ranks; r0 += 8) {
+                float4 v[8], w[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
                     if (r0 + r < ranks) {
-                        s[0] = add2(s[0], pair(v[r].x, v[r].y));
-                        s[1] = add2(s[1], pair(v[r].z, v[r].w));
+                        const uint32_t at = ptx::mapa_shared(base, r0 + r);
+                        v[r] = ld_cluster_f4(at + 16u * static_cast<uint32_t>(i));
+                        if (j < u1) w[r] = ld_cluster_f4(at + 16u * static_cast<uint32_t>(j));
+                    }
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < ranks) {
+                        s0[0] = add2(s0[0], pair(v[r].x, v[r].y));
+                        s0[1] = add2(s0[1], pair(v[r].z, v[r].w));
+                        if (j < u1) {
+                            s1[0] = add2(s1[0], pair(w[r].x, w[r].y));
+                            s1[1] = add2(s1[1], pair(w[r].z, w[r].w));
+                        }
                     }
             }
-            Extra x = first;
-            if (i != u) fetch(i, x);
-            const int32_t f = f0 + 4 * (i & 31);
-            const int64_t t = t0 + (i >> 5);
-            if (f >= p.N) continue;
-            const f32x2 alpha = both(p.alpha);
-            if constexpr (MODE == kForward) {
-                s[0] = fma2(alpha, s[0], x.bias[0]);
-                s[1] = fma2(alpha, s[1], x.bias[1]);
-                if (p.Z) store4<kBf16>(static_cast<uint16_t*>(p.Z) + t * p.ldz, f, p.N, s);
-                DTG_ACT_SWITCH(p.act, {
-                    s[0] = act_value2<ACT>(s[0]);
-                    s[1] = act_value2<ACT>(s[1]);
-                });
-                if (p.in) {
-                    s[0] = add2(s[0], x.in[0]);
-                    s[1] = add2(s[1], x.in[1]);
-                }
-            } else if constexpr (MODE == kDgrad) {
-                s[0] = mul2(alpha, s[0]);
-                s[1] = mul2(alpha, s[1]);
-                if (p.in) {
-                    DTG_ACT_SWITCH(p.act, {
-                        s[0] = mul2(s[0], act_slope2<ACT>(x.in[0]));
-                        s[1] = mul2(s[1], act_slope2<ACT>(x.in[1]));
-                    });
-                }
-                col[0] = add2(col[0], s[0]);
-                col[1] = add2(col[1], s[1]);
-            } else {
-                s[0] = mul2(alpha, s[0]);
-                s[1] = mul2(alpha, s[1]);
-                if (p.in) {
-                    s[0] = fma2(both(p.beta), x.in[0], s[0]);
-                    s[1] = fma2(both(p.beta), x.in[1], s[1]);
-                }
-            }
-            if constexpr (OUT == kOutF32) {
-                float o[4];
-                split(s[0], o[0], o[1]);
-                split(s[1], o[2], o[3]);
-                float* row = static_cast<float*>(p.C) + t * p.ldc;
-                if (f + 4 <= p.N) {
-                    *reinterpret_cast<float4*>(row + f) = make_float4(o[0], o[1], o[2], o[3]);
-                } else {
+            f32x2 next0[2] = {0, 0}, next1[2] = {0, 0};
+            if (i + 2 * kClusterThreads < u1) fetch_in(i + 2 * kClusterThreads, next0);
+            if (j + 2 * kClusterThreads < u1) fetch_in(j + 2 * kClusterThreads, next1);
+            finish(i, s0, in0);
+            if (j < u1) finish(j, s1, in1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (f + e < p.N) row[f + e] = o[e];
-                }
-            } else {
-                store4<kBf16>(static_cast<uint16_t*>(p.C) + t * p.ldc, f, p.N, s);
+            for (int e = 0; e < 2; ++e) {
+                in0[e] = next0[e];
+                in1[e] = next1[e];
             }
         }
     }
     __syncwarp();
     if constexpr (MODE == kDgrad) {
         // Column sums of the tile: per thread over its units, then over the CTA's warps, then over the ranks, each in a
-        // fixed order.  A thread's units are those of one feature group only if the rank's first unit is a multiple of
-        // 32; the group a thread adds to is that of its own units.
+        // fixed order.
         float* const cols = reinterpret_cast<float*>(smem + L::kColOff);
         const int group = (u0 + static_cast<int>(threadIdx.x)) & 31;
         *reinterpret_cast<f32x2*>(&cols[warp * kBM + 4 * group]) = col[0];
