@@ -543,7 +543,7 @@ class Gemm:
                      out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
                      beta_bias: float = 0.0, stream=None) -> torch.Tensor:
         """dX = (alpha * dY·W) * act'(Z) (gemm_run_linear_dgrad): dY (M x N), W (N x K), Z (M x K, what the
-        layer below kept) of one 16-bit type.  ``dbias`` (K, float32 or that type), if given, becomes
+        layer below kept; not read without an activation) of one 16-bit type.  ``dbias`` (K, float32 or that type), if given, becomes
         beta_bias * dbias + the column sums of dX.  Async on `stream`."""
         dt, dev, code = dY.dtype, self._index, _act(act)
         dt_code = TORCH_TO_DTYPE.get(dt)
@@ -552,8 +552,10 @@ class Gemm:
         if dY.dim() != 2 or W.dim() != 2:
             raise ValueError("expected 2-D tensors")
         (M, N), K = dY.shape, W.shape[1]
-        if (Z is None) != (code == 0):
-            raise ValueError("Z is the pre-activation of act: both or neither")
+        if code == 0:
+            Z = None  # not read
+        elif Z is None:
+            raise ValueError("act needs its pre-activation Z")
         lddy, ldw = _matrix(dY, "dY", M, N, dt, dev), _matrix(W, "W", N, K, dt, dev)
         z_p = db_p = ldz = db_code = ws_p = ws_bytes = 0
         if Z is not None:
@@ -606,7 +608,8 @@ class Gemm:
     def act_grad(self, dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
                  out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, beta_bias: float = 0.0,
                  sums_only: bool = False, stream=None) -> torch.Tensor | None:
-        """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N) of one 16-bit type; ``out`` may be dY itself.
+        """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N; not read without an activation) of one 16-bit type; ``out`` may be
+        dY itself.
         ``dbias`` as for linear_dgrad, with N columns.  With ``sums_only`` dZ is not written (and None is
         returned).  Async on `stream`."""
         dt, dev, code = dY.dtype, self._index, _act(act)
@@ -614,8 +617,10 @@ class Gemm:
         if dt_code is None or dY.dim() != 2:
             raise TypeError("dY must be a 2-D float16 or bfloat16 tensor")
         M, N = dY.shape
-        if (Z is None) != (code == 0):
-            raise ValueError("Z is the pre-activation of act: both or neither")
+        if code == 0:
+            Z = None  # not read
+        elif Z is None:
+            raise ValueError("act needs its pre-activation Z")
         if sums_only and (out is not None or dbias is None):
             raise ValueError("sums_only writes dbias and no dZ")
         lddy = _matrix(dY, "dY", M, N, dt, dev)

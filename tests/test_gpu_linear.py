@@ -417,6 +417,13 @@ def test_act_grad_sums_only_in_place_and_empty(g):
     assert bool((db == 0.5).all())
 
 
+def test_z_is_not_read_without_an_activation(g):
+    r = gen(15)
+    dY, W, Z = matrix(r, 40, 64, F16, ints=True), matrix(r, 64, 72, F16, ints=True), matrix(r, 40, 72, F16) * float("nan")
+    same(g.linear_dgrad(dY, W, Z, act="none"), (dY.double() @ W.double()).half())
+    same(g.act_grad(dY, matrix(r, 40, 64, F16) * float("nan")), dY)
+
+
 def test_act_grad_special_values(g):
     inf, nan = float("inf"), float("nan")
     Z = torch.tensor([[inf, -inf, nan, 0.0, -0.0, 3e4, -3e4, 1e-7]], dtype=F16, device="cuda")
