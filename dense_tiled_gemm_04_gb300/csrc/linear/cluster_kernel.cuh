@@ -28,6 +28,7 @@ constexpr int kClusterMaxSplit = 16;
 
 struct ClusterParams : KernelParams {  // M: tokens, N: features of the output; K: the contraction
     int32_t tiles_t;     // token tiles
+    int32_t chunk_kb;    // K blocks per accumulator (at most ClusterAccs of them per CTA)
     int32_t act;
     const void* bias;
     int32_t bias_f32;
@@ -38,6 +39,12 @@ struct ClusterParams : KernelParams {  // M: tokens, N: features of the output; 
     float* partials;     // dgrad: a row of `pitch` column sums per token tile; null: none
     int64_t pitch;
 };
+
+// Accumulators of a CTA.  Where an fp32 result is wanted, a chain of products on one accumulator is no longer than the
+// tile kernels' chunks (see there); a longer share of K goes to further accumulators, which are added when they
+// leave TMEM.  256 of its columns per CTA, as two CTAs share an SM.
+template <int BN, int MODE>
+constexpr int kClusterAccs = MODE == kForward ? 1 : 256 / BN;
 
 template <int BN>
 struct ClusterSmem {
@@ -126,7 +133,8 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     constexpr bool BT = MODE == kWgrad;    // tokens' operand is N-major
     constexpr bool kBf16 = OUT == kOutBf16;
     static_assert(!BT || BN % T::kNBlock == 0, "an N-major box is one 128-byte row");
-    constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
+    constexpr int kAccs = kClusterAccs<BN, MODE>;
+    constexpr uint32_t kTmemCols = BN * kAccs < 32 ? 32 : BN * kAccs;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -239,12 +247,18 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
             int stage = 0;
             uint32_t phase = 0;
             bool aborted = false;
+            int in_chunk = 0;
+            uint32_t acc = tmem_base;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wd.wait(full_bar(stage), phase, kRoleMma, tile, kb)) {
                     aborted = true;
                     break;
                 }
                 ptx::tc_fence_after_sync();
+                if (kAccs > 1 && in_chunk == p.chunk_kb) {
+                    in_chunk = 0;
+                    acc += BN;
+                }
                 const uint32_t sa = base + stage * L::kStageBytes, sb = sa + L::kABytes;
 #pragma unroll
                 for (int k = 0; k < T::kStageK / T::kMmaK; ++k) {
@@ -252,12 +266,13 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
                                               : smem_desc_sw128(sa + k * 32, 16, 1024);
                     const uint64_t bdesc = BT ? smem_desc_sw128(sb + k * (T::kMmaK * 128), T::kStageK * 128, 1024)
                                               : smem_desc_sw128(sb + k * 32, 16, 1024);
-                    const uint32_t accumulate = (kb != kb0 || k != 0) ? 1u : 0u;
+                    const uint32_t accumulate = (in_chunk != 0 || k != 0) ? 1u : 0u;
                     if constexpr (T::kF8)
-                        ptx::mma_f8_cta1(tmem_base, adesc, bdesc, idesc, accumulate);
+                        ptx::mma_f8_cta1(acc, adesc, bdesc, idesc, accumulate);
                     else
-                        ptx::mma_f16_cta1(tmem_base, adesc, bdesc, idesc, accumulate);
+                        ptx::mma_f16_cta1(acc, adesc, bdesc, idesc, accumulate);
                 }
+                ++in_chunk;
                 ptx::mma_commit_cta1(empty_bar(stage));
                 if (++stage == STAGES) {
                     stage = 0;
@@ -307,6 +322,16 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
                     ptx::tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
                 }
                 ptx::tmem_wait_ld();
+                if constexpr (kAccs > 1) {
+                    // The further accumulators (chunk_kb may be the largest int: no sum with a K block's number).
+                    for (int done = p.chunk_kb, a = 1; done < kb1 - kb0; done += p.chunk_kb, ++a) {
+                        uint32_t w[32];
+                        ptx::tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + a * BN + c, w);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) st_shared_f32(sum + (c + i) * (kBM * 4), __uint_as_float(v[i]));
             } else if (c < tokens) {  // no K block of its own

@@ -132,25 +132,27 @@ __global__ void __launch_bounds__(kActWarps * 32, 4) act_grad_kernel(const ActGr
 }
 
 // dbias[n] = beta * dbias[n] + the sum over `rows` partial sums of column n.  32 columns a block; warp w adds rows
-// w, w + 8, ..., and the eight warps' sums are added in warp order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* partials, int64_t rows, int64_t pitch, int64_t N,
-                                                         const BiasGrad b)
+// w, w + 16, ..., sixteen of them in flight, and the warps' sums are added in warp order.
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float* partials, int64_t rows, int64_t pitch,
+                                                                    int64_t N, const BiasGrad b)
 {
-    __shared__ float sums[8][32];
+    __shared__ float sums[kSumWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n = blockIdx.x * int64_t(32) + lane;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     float s = 0.0f;
     if (n < N) {
-#pragma unroll 8
-        for (int64_t r = warp; r < rows; r += 8) s += partials[r * pitch + n];
+#pragma unroll 16
+        for (int64_t r = warp; r < rows; r += kSumWarps) s += partials[r * pitch + n];
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && n < N) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += sums[w][lane];
+        for (int w = 1; w < kSumWarps; ++w) s += sums[w][lane];
         write_bias_grad(b, n, s);
     }
 }

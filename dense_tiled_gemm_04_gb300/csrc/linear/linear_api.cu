@@ -93,7 +93,7 @@ dtg::linear::BiasGrad bias_grad(void* dbias, gemm_dtype_t t, float beta)
 // The bias gradient from `rows` rows of partial sums.
 gemm_status_t launch_sums(const float* partials, int64_t rows, int64_t cols, const dtg::linear::BiasGrad& b, cudaStream_t s)
 {
-    return launch_after(&dtg::linear::column_sum_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32))), dim3(256), 0, s, partials,
+    return launch_after(&dtg::linear::column_sum_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32))), dim3(32 * dtg::linear::kSumWarps), 0, s, partials,
                         rows, sum_pitch(cols), cols, b);
 }
 
@@ -157,6 +157,7 @@ constexpr int64_t kChunkBlocks = 12;
 struct ClusterPlan {
     int tokens = 0;  // per tile; 0: the tile kernels
     int ranks = 1;   // CTAs per cluster
+    int32_t chunk_kb = INT32_MAX;  // K blocks per accumulator
     KernelChoice kc;
 };
 
@@ -235,8 +236,12 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
         ++log;
     }
     if (st != GEMM_OK) return st;
-    // fp32 results: a chain of products no longer than the tile kernels' chunks.
-    if ((q.out == GEMM_DTYPE_F32 || q.partials) && cdiv(kb, 1 << log) > kChunkBlocks) return GEMM_OK;
+    // fp32 results: chains of products no longer than the tile kernels' chunks, on as many accumulators as there are.
+    if (q.out == GEMM_DTYPE_F32 || q.partials) {
+        const int64_t blocks = cdiv(kb, 1 << log), chunks = cdiv(blocks, kChunkBlocks);
+        if (chunks > 256 / tokens) return GEMM_OK;
+        c->chunk_kb = static_cast<int32_t>(cdiv(blocks, chunks));
+    }
     c->tokens = tokens;
     c->ranks = 1 << log;
     return GEMM_OK;
@@ -272,6 +277,7 @@ gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPla
     p.alpha = q.alpha;
     p.beta = q.beta;
     p.tiles_t = static_cast<int32_t>(tiles_t);
+    p.chunk_kb = plan.chunk_kb;
     p.act = q.act;
     p.bias = q.bias;
     p.bias_f32 = q.bias_dtype == GEMM_DTYPE_F32;
