@@ -22,9 +22,17 @@
 // chunk, whose boxes go from TMEM straight through the epilogue.
 //
 // Epilogue.  Eight warps, two per TMEM lane quadrant, 32 rows x BN/2 columns each; with SUMS they hold
-// those sums (128 registers at BN = 256; four warps would need 256 each).  Per box of 128 bytes of output columns: bias through the warp's staging
-// buffer (every lane needs the same 64 values), residual or pre-activations straight from
-// global memory (16 bytes a load, a row's 128 bytes per lane), then the 128-byte-swizzled staging and TMA store.
+// those sums (128 registers at BN = 256; four warps would need 256 each).  Per box of 128 bytes of output
+// columns: bias through the warp's staging buffer (every lane needs the same 64 values); the residual straight from
+// global memory (16 bytes a load, a row's 128 bytes per lane, brought into L2 an item ahead) or, in dgrad, the
+// pre-activations by TMA; then the 128-byte-swizzled staging buffer and a TMA store.
+//
+// What bounds it (one GB300, short bursts): 8192^3 bf16 forward with bias, gelu_tanh and z kept 577-588 us, as
+// gemm_run's product alone (559-575).  16384 x 1024 x 8192: forward with residual 174-182 us (gemm_run 163-168), wgrad fp32
+// accumulated 180-186 us; dgrad with gelu 223 us, with sums 266 us, against 178 without either: there a tile's MMAs
+// (8192 cycles) leave the epilogue 32 issue slots an element, of which it takes 23, or 29 with the sums, at 0.4
+// instructions a cycle -- two warps per scheduler waiting on fixed latencies, TMEM and shared memory.  Sixteen warps,
+// loads a tile ahead, coalesced plain stores without the proxy fence, and rolled loops were slower.
 //
 // Column sums (kDgrad): the 32 lanes' rows are summed by five exchange steps that halve the columns
 // a lane holds each time, which leaves two finished columns per lane and a fixed order of additions.

@@ -377,9 +377,14 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C,
  * alignment rules of gemm_run (bases of 16 bytes; row pitches that are multiples of 16 bytes);
  * bias and dbias are dense vectors of any alignment their type allows; a dimension over
  * 2^31 - 512 is UNSUPPORTED.  An output may not
- * overlap an input, except where it is said below.  Like gemm_run these calls enqueue on
+ * overlap an input or another output, except where it is said below.  Like gemm_run these calls enqueue on
  * `stream` and return; they share the handle's workspace, so the rule on overlapping launches
- * is the same, and so are the status codes and the watchdog (gemm_sync_status). */
+ * is the same, and so are the status codes and the watchdog (gemm_sync_status).
+ *
+ * Options: a GEMM_OPT_CONFIG other than AUTO asks for that tile (128x64 runs as 128x128); AUTO
+ * also takes kernels that split a product of few tiles over a cluster of CTAs, to which MAX_CTAS, RASTER_GROUP and the
+ * stream-K options do not apply.  The others act as in gemm_run, except that sharing out the last
+ * tiles' K blocks is also left out where it would not pay. */
 typedef int32_t gemm_act_t;
 enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_GELU_TANH = 3, GEMM_ACT_SILU = 4 };
 

@@ -458,9 +458,9 @@ def test_slopes_against_differences(g, act):
 
 def test_layer_gradients_against_differences(g):
     # L = sum(G * act(X W^T + b)): dL along a direction of each parameter, from the kernels' gradients, against
-    # central differences of L in fp64.  The kernels round dZ and dX to bf16 (2^-9 each, relative to the terms of
-    # the sums): the bound is 2^-8 of the sum of the terms' magnitudes, plus h^2 times third derivatives (under 6
-    # per element) of a direction of unit entries.
+    # central differences of L in fp64.  The kernels round dZ and Z to bf16 (2^-8 of a value at most, 2^-9 on
+    # average): the bound is 2^-8 of the sum of the terms' magnitudes for dZ, the average for the other roundings, and
+    # h^2 times third derivatives (under 6 per element) of a direction of unit entries.
     r = gen(9)
     M, N, K, act = 70, 200, 96, "gelu_tanh"
     X, W, b = matrix(r, M, K, BF16), matrix(r, N, K, BF16, scale=0.1), vector(r, N, BF16)
@@ -482,8 +482,8 @@ def test_layer_gradients_against_differences(g):
             plus[at], minus[at] = plus[at] + h * v, minus[at] - h * v
             want = ((loss(*plus) - loss(*minus)) / (2 * h)).item()
             terms = grad.double() * v
-            # dZ's own rounding (Z is rounded to bf16 before its slope is taken: 2^-9 |Z| times a second derivative
-            # under 1.2) enters every gradient through magnitudes, not signed sums.
+            # dZ's own rounding (Z is rounded to bf16 before its slope is taken: 2^-9 |Z| on average times a second
+            # derivative under 1.2) enters every gradient through magnitudes, not signed sums.
             dz = (G.double().abs() * (2.0 ** -8 + 2.0 ** -9 * 1.2 * Z.double().abs()))
             mags = {0: dz @ w.abs(), 1: dz.t() @ x.abs(), 2: dz.sum(0)}[at]
             bound = (mags * v.abs()).sum().item() + 2.0 ** -9 * terms.abs().sum().item() + 1e-3
@@ -685,7 +685,7 @@ def test_feed_forward_example(g):
 
 def test_feed_forward_gradients_against_autograd(g):
     # The block's gradients in bf16 against autograd's in fp64 on the same (bf16) weights: each bf16 rounding on the way
-    # (H, Z, dZ) is 2^-9 of its value at random, so the norms agree within 1 %.
+    # (H, Z, dZ) is 2^-9 of its value on average, so the norms agree within 1 %.
     import importlib.util
     import os
 
