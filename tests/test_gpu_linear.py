@@ -357,6 +357,37 @@ def test_wgrad_every_tile(g, config, dtype, out):
             dW.check()
 
 
+@pytest.mark.parametrize("rows", [1100, 890, 1500])
+def test_last_tiles_shared_after_whole_ones(g, rows):
+    # Four CTAs, a long contraction, and tiles that do not divide by four (9 and 12; 7, so less than two waves): whole tiles,
+    # then the K blocks of the rest shared out and joined.
+    L = 12288
+    r = gen(rows)
+    g.set_option(native.OPT_CONFIG, native.CONFIG_128x128)
+    g.set_option(native.OPT_MAX_CTAS, 4)
+    for dtype in (F16, BF16):
+        X, W, res = matrix(r, rows, L, dtype), matrix(r, 100, L, dtype, scale=L ** -0.5), matrix(r, rows, 100, dtype)
+        Y = Guarded(rows, 100, dtype)
+        g.linear(X, W, act="gelu", residual=res, out=Y.t)
+        ref.assert_within(Y.t, ref.linear(X, W, None, "gelu", res, dtype)[0], "forward")
+        Y.check()
+        dY, Wd, Z = X, matrix(r, L, 100, dtype, scale=L ** -0.5), matrix(r, rows, 100, dtype)
+        for sums in (True, False):
+            dX, db = Guarded(rows, 100, dtype), Guarded(1, 100, F32)
+            g.linear_dgrad(dY, Wd, Z, act="silu", out=dX.t, dbias=db.t[0] if sums else None)
+            d, b = ref.through_act(*ref.product(dY, Wd), Z, "silu", dtype, F32)
+            ref.assert_within(dX.t, d, "dgrad")
+            dX.check()
+            if sums:
+                ref.assert_within(db.t[0], b, "dbias")
+        A, B = matrix(r, L, rows, dtype), matrix(r, L, 100, dtype)
+        for out in (F32, dtype):
+            dW = Guarded(rows, 100, out)
+            g.linear_wgrad(A, B, out=dW.t)
+            ref.assert_within(dW.t, ref.wgrad(A, B, out), f"wgrad {out}")
+            dW.check()
+
+
 @pytest.mark.parametrize("out", [F16, F32])
 def test_wgrad_no_tokens(g, out):
     dY, X = torch.zeros((0, 40), dtype=F16, device="cuda"), torch.zeros((0, 56), dtype=F16, device="cuda")
