@@ -338,19 +338,13 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     // leave idle are worth more K blocks than the joins cost, about 56 blocks of a 256-wide 16-bit tile (16384 x 1024
     // x 8192 forward, 81 blocks a tile: 166 us shared, 174 whole; dgrad of the same, 1 block: 311 and 294).  Between
     // one and two waves the planner would share every tile, with each unit starting at another K, and the operands'
-    // reuse in L2 is lost: there a wave of whole tiles goes first, and the rest, if it is half a wave or more, is
-    // shared (wgrad 1024 x 8192 over 16384 tokens, 1.7 waves: all shared 209 us, all whole 184, one wave whole 173).
-    // Under one wave the planner's rule stands.
+    // reuse in L2 is lost (wgrad 1024 x 8192 over 16384 tokens, 1.7 waves: 209 us shared, 190 whole; a wave of whole
+    // tiles and the rest shared, under the power limit: 191).  Under one wave the planner's rule stands.
     const int64_t tiles = plan.tiles_m * plan.tiles_n, units = plan.grid / kc.cluster;
     if (plan.dp_tiles < tiles && tiles >= units) {
         const int64_t idle = cdiv(tiles, units) * units - tiles;
         const int64_t join = 56 * (256 / kc.bn) * (is_f8(q.in) ? 2 : 1);
-        const int64_t rest = tiles - units;
-        if (plan.dp_tiles == 0 && 2 * rest >= units && idle * plan.k_blocks >= join * units) {
-            plan.dp_tiles = units;
-            plan.sk_base = rest * plan.k_blocks / units;
-            plan.sk_extra = rest * plan.k_blocks % units;
-        } else if (plan.dp_tiles == 0 || idle * plan.k_blocks < join * units) {
+        if (plan.dp_tiles == 0 || idle * plan.k_blocks < join * units) {
             LaunchOptions whole = o;
             whole.stream_k = 0;
             fill_plan(whole, h->dev, h->dev.max_clusters[slot], &h->ws, q.rows, q.cols, q.depth, kc, kDense, &plan);

@@ -767,6 +767,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tile_epi_sync();
             return *last_flag != 0;
         };
+        // Has the other part of a tile of two come in already?  Then this one need not be parked: two parts give
+        // the same sum in either order (v + 0 first, as a join of parked parts starts from 0: the sign of a zero).
+        auto other_is_in = [&](int64_t tr, int64_t parts) -> bool {
+            if (ew == 0 && lane == 0) {
+                int32_t* const counter = p.counters + tr * CLUSTER + rank;
+                const bool in = parts == 2 && atomicAdd(counter, 0) == 1;
+                if (in) {
+                    *counter = 0;
+                    __threadfence();
+                }
+                *last_flag = in ? 1 : 0;
+            }
+            tile_epi_sync();
+            return *last_flag != 0;
+        };
         auto add_part = [&](float* v, const float4* f4) {  // 64 columns of a slot
 #pragma unroll
             for (int q0 = 0; q0 < 16; q0 += 8) {
@@ -820,7 +835,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (acc == 0) acc_phase ^= 1u;
                 }
                 if (!tile_epi_and(ok)) return false;
-                if (!whole) {
+                if (!whole && other_is_in(tr, parts)) {
+                    const float4* f4 = slot_f4(sk_slot(p, first_unit + (unit == first_unit ? 1 : 0), tr));
+#pragma unroll
+                    for (int i = 0; i < CW; ++i) s[i] += 0.0f;
+#pragma unroll
+                    for (int b = 0; b < CW / 64; ++b) add_part(&s[b * 64], f4 + b * 16 * kBM);
+                } else if (!whole) {
                     float4* const mine = slot_f4(sk_slot(p, unit, tr));
 #pragma unroll
                     for (int q = 0; q < CW / 4; ++q)
@@ -857,6 +878,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             load_acc(v, tacc + b * 64);
                             if (b == CW / 64 - 1) release_acc();
                         }
+                        if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
+                    }
+                } else if (other_is_in(tr, parts)) {
+                    const float4* f4 = slot_f4(sk_slot(p, first_unit + (unit == first_unit ? 1 : 0), tr));
+#pragma unroll 1
+                    for (int b = 0; b < CW / 64; ++b) {
+                        load_acc(v, tacc + b * 64);
+                        if (b == CW / 64 - 1) release_acc();
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i] += 0.0f;
+                        add_part(v, f4 + b * 16 * kBM);
                         if (y < p.M && x0 + b * 64 < p.N) finish_box(v, x0 + b * 64, y);
                     }
                 } else {

@@ -359,8 +359,8 @@ def test_wgrad_every_tile(g, config, dtype, out):
 
 @pytest.mark.parametrize("rows", [1100, 890, 1500])
 def test_last_tiles_shared_after_whole_ones(g, rows):
-    # Four CTAs, a long contraction, and tiles that do not divide by four (9 and 12; 7, so less than two waves): whole tiles,
-    # then the K blocks of the rest shared out and joined.
+    # Four CTAs, a long contraction, and tiles that do not divide by four (9, 7): whole tiles, then, where it pays, the K
+    # blocks of the rest shared out and joined.
     L = 12288
     r = gen(rows)
     g.set_option(native.OPT_CONFIG, native.CONFIG_128x128)
