@@ -209,6 +209,12 @@ def empty_output(M: int, N: int, dtype: torch.dtype, device) -> torch.Tensor:
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(device).cuda_stream, without the wrapper
 
 
+def _stream_of(stream, device: int) -> int:
+    if stream is None:
+        return _raw_stream(device)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dtype: torch.dtype, device: int) -> int:
     """Check a 2-D tensor argument and return its leading dimension (one-row tensors: the padded row length)."""
     if t.shape != (rows, cols):
@@ -534,7 +540,7 @@ class Gemm:
         ldy = _matrix(out, "out", M, N, out_dtype, dev)
         a = gemm_linear_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
                                ldz, in_code, out_code, bias_code, _act(act), alpha)
-        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), self._stream(stream))
+        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), _stream_of(stream, dev))
         if st != OK:
             raise GemmError(st, "gemm_run_linear")
         return out
@@ -571,7 +577,7 @@ class Gemm:
                 ws_p = ws.data_ptr()
         a = gemm_dgrad_args_t(dY.data_ptr(), W.data_ptr(), z_p, out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy, ldw,
                               ldz, lddx, dt_code, db_code, code, alpha, beta_bias)
-        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), self._stream(stream))
+        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), _stream_of(stream, dev))
         if st != OK:
             raise GemmError(st, "gemm_run_linear_dgrad")
         return out
@@ -600,7 +606,7 @@ class Gemm:
         lddw = _matrix(out, "out", N, K, out_dtype, dev)
         a = gemm_wgrad_args_t(dY.data_ptr(), X.data_ptr(), out.data_ptr(), M, N, K, lddy, ldx, lddw, dt_code,
                               TORCH_TO_DTYPE_F32[out_dtype], alpha, beta)
-        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), self._stream(stream))
+        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), _stream_of(stream, dev))
         if st != OK:
             raise GemmError(st, "gemm_run_linear_wgrad")
         return out
@@ -608,9 +614,8 @@ class Gemm:
     def act_grad(self, dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
                  out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, beta_bias: float = 0.0,
                  sums_only: bool = False, stream=None) -> torch.Tensor | None:
-        """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N; not read without an activation) of one 16-bit type; ``out`` may be
-        dY itself.
-        ``dbias`` as for linear_dgrad, with N columns.  With ``sums_only`` dZ is not written (and None is
+        """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N; not read without an activation) of one 16-bit
+        type; ``out`` may be dY itself.  ``dbias`` as for linear_dgrad, with N columns.  With ``sums_only`` dZ is not written (and None is
         returned).  Async on `stream`."""
         dt, dev, code = dY.dtype, self._index, _act(act)
         dt_code = TORCH_TO_DTYPE.get(dt)
@@ -639,15 +644,10 @@ class Gemm:
                 ws_p = ws.data_ptr()
         a = gemm_act_grad_args_t(dY.data_ptr(), z_p, dz_p, db_p, ws_p, ws_bytes, M, N, lddy, ldz, lddz, dt_code, db_code,
                                  code, beta_bias)
-        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), self._stream(stream))
+        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), _stream_of(stream, dev))
         if st != OK:
             raise GemmError(st, "gemm_run_act_grad")
         return out
-
-    def _stream(self, stream):
-        if stream is None:
-            return _raw_stream(self._index)
-        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
     def sync_status(self, stream=None) -> int:
         return int(self._lib.gemm_sync_status(self._h, _stream_ptr(stream) or None))
@@ -671,21 +671,28 @@ def matmul(A: torch.Tensor, B: torch.Tensor, layout: str = "NN", out: torch.Tens
     return _default_handle(dev).run(A, B, out, layout, stream)
 
 
-def linear(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, **kw) -> torch.Tensor:
+def linear(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = None,
+           residual: torch.Tensor | None = None, out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+           out_dtype: torch.dtype | None = None, alpha: float = 1.0, stream=None) -> torch.Tensor:
     """Gemm.linear on a per-device default handle."""
-    return _default_handle(X.get_device()).linear(X, W, bias, **kw)
+    return _default_handle(X.get_device()).linear(X, W, bias, act, residual, out, preact, out_dtype, alpha, stream)
 
 
-def linear_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, **kw) -> torch.Tensor:
+def linear_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
+                 out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
+                 beta_bias: float = 0.0, stream=None) -> torch.Tensor:
     """Gemm.linear_dgrad on a per-device default handle."""
-    return _default_handle(dY.get_device()).linear_dgrad(dY, W, Z, **kw)
+    return _default_handle(dY.get_device()).linear_dgrad(dY, W, Z, act, out, dbias, alpha, beta_bias, stream)
 
 
-def linear_wgrad(dY: torch.Tensor, X: torch.Tensor, **kw) -> torch.Tensor:
+def linear_wgrad(dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, alpha: float = 1.0, beta: float = 0.0, stream=None) -> torch.Tensor:
     """Gemm.linear_wgrad on a per-device default handle."""
-    return _default_handle(dY.get_device()).linear_wgrad(dY, X, **kw)
+    return _default_handle(dY.get_device()).linear_wgrad(dY, X, out, out_dtype, alpha, beta, stream)
 
 
-def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, **kw) -> torch.Tensor | None:
+def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None, out: torch.Tensor | None = None,
+             dbias: torch.Tensor | None = None, beta_bias: float = 0.0, sums_only: bool = False,
+             stream=None) -> torch.Tensor | None:
     """Gemm.act_grad on a per-device default handle."""
-    return _default_handle(dY.get_device()).act_grad(dY, Z, **kw)
+    return _default_handle(dY.get_device()).act_grad(dY, Z, act, out, dbias, beta_bias, sums_only, stream)
