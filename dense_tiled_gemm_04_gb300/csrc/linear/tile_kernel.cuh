@@ -931,6 +931,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (nxt.x + b * (128 / kElem) < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
         };
         more_items = next_item(nxt);
+        if (more_items) prefetch_in();
         while (more_items) {
             cur = nxt;
             more_items = next_item(nxt);
