@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     });
                 }
                 // The store issued one box ago has had this box's arithmetic to read its buffer, which the next box's
-                // pre-activations take: of this tile, or of the next item if that is a whole tile (without any, the
-                // buffers alternate).
+                // pre-activations take: of this tile, or of the next item if that is a whole tile.  Without any, the
+                // buffers alternate from TMA store to TMA store: the newest group has read the other buffer.
                 const bool same_tile = x + 64 < p.N && x - cur.x + 64 < CW;
                 if (has_in && (same_tile || (more_items && nxt.whole && nxt.inside))) {
                     if (lane == 0) ptx::bulk_wait_group_read<0>();
@@ -632,7 +632,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (lane == 0) ptx::bulk_wait_group_read<1>();
                     __syncwarp();
                 }
-                if ((p.N & 7) != 0 && x + 64 > p.N) {
+                const bool masked = (p.N & 7) != 0 && x + 64 > p.N;
+                if (masked) {
                     uint32_t h[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(w[i]);
@@ -644,7 +645,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                           round2<kBf16>(w[4 * ch + 2]), round2<kBf16>(w[4 * ch + 3]));
                     store_box_now(&tmC, buf, x, y, lane);
                 }
-                in_buf ^= 1;
+                // A masked box leaves its buffer as it was and commits no group: without pre-activations the next box takes
+                // the same buffer, so that waiting for all groups but the newest keeps covering it.
+                if (has_in || !masked) in_buf ^= 1;
                 if (p.partials) {
                     // Rows past M are not part of the sums (an infinite weight makes them NaN).
                     if (!row_in) {
