@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
         ptx::prefetch_tmap(&tmA);
         ptx::prefetch_tmap(&tmB);
     }
+    __syncwarp();
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(ptx::smem_addr(tmem_slot), kTmemCols);
         ptx::tmem_relinquish();
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     }
     if (u < u1) fetch_in(u, in0);
     if (u + kClusterThreads < u1) fetch_in(u + kClusterThreads, in1);
+    __syncwarp();  // the lanes' shares end at different units; TMEM loads and the cluster's barrier take whole warps
 
     if (warp >= kClusterTmemWarp0 && warp < kClusterTmemWarp0 + 4) {
         // ---------------------------------------------------------------- accumulator -> shared memory
@@ -340,6 +342,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
             }
         }
     }
+    __syncwarp();
     ptx::tc_fence_before_sync();
     ptx::cluster_sync();  // every rank's sums are in its shared memory
 

@@ -101,8 +101,11 @@ __device__ __forceinline__ void registers_up()
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Barriers, TMEM loads and cluster barriers are .aligned: a warp's threads execute them together, so code that its
+// lanes leave at different points ends in __syncwarp() before one of them.
 __device__ __forceinline__ void tile_epi_sync()
 {
+    __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"n"(kTileEpiBarrier), "n"(kTileEpiWarps * 32) : "memory");
 }
 
@@ -110,6 +113,7 @@ __device__ __forceinline__ void tile_epi_sync()
 __device__ __forceinline__ bool tile_epi_and(bool v)
 {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred pi, po;\n\t"
         "setp.ne.u32 pi, %1, 0;\n\t"
@@ -347,6 +351,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ptx::prefetch_tmap(&tmB);
         ptx::prefetch_tmap(&tmC);
     }
+    __syncwarp();
     if (warp == kMmaWarp) {
         if constexpr (PAIR) {
             ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), kTmemCols);
@@ -443,6 +448,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int s = 0; s < STAGES; ++s)
                     if (armed_mask & (1u << s)) wd.drain(full_bar(s), (armed_parity >> s) & 1u);
         }
+        __syncwarp();
     } else if (warp == kMmaWarp) {
         if (lane == 0 && leader) {
             // ---------------------------------------------------------------- MMA issuer
@@ -727,6 +733,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         auto load_acc = [&](float* v, uint32_t taddr) {
             uint32_t a[32];
             uint32_t b[32];
+            __syncwarp();
             ptx::tmem_ld_32x32b_x32(taddr, a);
             ptx::tmem_ld_32x32b_x32(taddr + 32, b);
             ptx::tmem_wait_ld();

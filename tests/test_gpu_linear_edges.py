@@ -39,3 +39,31 @@ def test_dgrad_ragged_columns_without_an_activation(g, config, M, N, K, ctas):  
                 if with_sums:
                     same(db.t[0], sums, "dbias")
                     db.check("dbias")
+
+
+# ------------------------------------------------------------------ shares that end inside a warp
+
+# The lanes of a warp take different paths before the cluster's barriers: features and tokens that end inside a
+# warp's units, a bias and a residual whose last groups of four are read one by one, ranks with fewer units than threads.
+@pytest.mark.parametrize("M,N,K", [(1, 5, 4096), (3, 131, 2048), (17, 1003, 4100), (61, 130, 1024), (127, 2047, 1000)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_cluster_shares_that_end_inside_a_warp(g, M, N, K, dtype):  # noqa: F811
+    r = gen(M + N + K)
+    X, W = matrix(r, M, K, dtype, ints=True), matrix(r, N, K, dtype, ints=True)
+    z = X.double() @ W.double().t()
+    for bias in (vector(r, N, F32, ints=True, offset=1), vector(r, N, dtype, ints=True, offset=3), None):
+        res = matrix(r, M, N, dtype, ints=True)
+        y = z + (0 if bias is None else bias.double())
+        y = ref.act_value(y, "relu") + res.double()
+        for _ in range(3):
+            Y = Guarded(M, N, dtype)
+            g.linear(X, W, bias, act="relu", residual=res, out=Y.t)
+            same(Y.t, y.to(dtype), "Y")
+            Y.check("Y")
+    dY = matrix(r, M, N, dtype, ints=True)
+    d = dY.double() @ W.double()
+    dX, db = Guarded(M, K, dtype), Guarded(1, K, F32)
+    g.linear_dgrad(dY, W, out=dX.t, dbias=db.t[0])
+    same(dX.t, d.to(dtype), "dX")
+    same(db.t[0], d.sum(0).float(), "dbias")
+    dX.check("dX"), db.check("dbias")
