@@ -48,10 +48,16 @@ struct ActGradParams {
     int64_t block_rows;  // rows per block
 };
 
+// A warp's column sums in shared memory, written two at a time.
+struct __align__(16) WarpSums {
+    float col[kActCols];
+};
+static_assert(alignof(WarpSums) >= sizeof(f32x2), "pairs of sums are stored at once");
+
 template <bool BF16, int ACT>
 __global__ void __launch_bounds__(kActWarps * 32, 4) act_grad_kernel(const ActGradParams p)
 {
-    __shared__ float sums[kActWarps][kActCols];
+    __shared__ WarpSums sums[kActWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t col = blockIdx.x * static_cast<int64_t>(kActCols) + lane * 8;
     ptx::grid_dependency_wait();
@@ -115,12 +121,12 @@ __global__ void __launch_bounds__(kActWarps * 32, 4) act_grad_kernel(const ActGr
         if (p.partials || p.bias.dbias) {
             __syncthreads();  // the sums of the block of rows before have been read
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x2*>(&sums[warp][lane * 8 + 2 * i]) = acc[i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x2*>(&sums[warp].col[lane * 8 + 2 * i]) = acc[i];
             __syncthreads();
             const int64_t c = blockIdx.x * static_cast<int64_t>(kActCols) + threadIdx.x;
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kActWarps; ++w) s += sums[w][threadIdx.x];
+            for (int w = 0; w < kActWarps; ++w) s += sums[w].col[threadIdx.x];
             if (c < p.N) {
                 if (p.partials)
                     p.partials[rb * p.pitch + c] = s;
