@@ -8,7 +8,8 @@ memory and streams only.
 from .native import (CONFIG_128x64, CONFIG_128x128, CONFIG_128x256, CONFIG_256x256, CONFIG_AUTO, Gemm, GemmError,
                      LAYOUT_NN, LAYOUT_TN, OPT_CONFIG, OPT_FAULT_INJECT, OPT_HOST_COL_CHUNKS, OPT_HOST_ROW_CHUNKS,
                      OPT_K_SNAKE, OPT_MAX_CTAS, OPT_RASTER_GROUP, OPT_SK_MIN_BLOCKS, OPT_SPLIT_MIN_BLOCKS,
-                     OPT_STREAM_K, OPT_TIMEOUT_NS, empty_output, load, matmul)
+                     OPT_STREAM_K, OPT_TIMEOUT_NS, act_grad, empty_output, linear, linear_dgrad, linear_wgrad, load,
+                     matmul)
 
 __all__ = ["Gemm", "GemmError", "matmul", "linear", "linear_dgrad", "linear_wgrad", "act_grad", "load",
            "empty_output", "LAYOUT_NN", "LAYOUT_TN",

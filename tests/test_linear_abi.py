@@ -55,3 +55,12 @@ def test_activation_codes_match_the_header(lib):
     for name, code in lib.ACTS.items():
         if name:
             assert f"GEMM_ACT_{name.upper()} = {code}" in text
+
+
+def test_every_name_that_the_package_lists_resolves():
+    import dense_tiled_gemm_04_gb300 as package
+
+    assert [n for n in package.__all__ if not hasattr(package, n)] == []
+    names = {}
+    exec("from dense_tiled_gemm_04_gb300 import *", names)
+    assert set(package.__all__) <= set(names)
