@@ -607,6 +607,17 @@ int host_chunks(int64_t extent, int64_t wanted, int64_t min_size, int64_t* bound
     return n;
 }
 
+// Lets this thread make calls that a capture in progress would forbid, until the end of the scope.
+struct CaptureRelaxed {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    bool swapped;
+    CaptureRelaxed() : swapped(cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess) {}
+    ~CaptureRelaxed()
+    {
+        if (swapped) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -635,12 +646,20 @@ gemm_status_t gemm_create(gemm_handle_t* out, int device)
     // stream-K tile (at most two waves of tiles) and CTA.
     h->ws.partial_floats = static_cast<size_t>(2 * sms) * dtg::kBM * 256;
     h->ws.counter_count = 4 * static_cast<int64_t>(sms);
-    if (cudaMalloc(&h->d_err, 4 * sizeof(int32_t)) != cudaSuccess ||
-        cudaMemset(h->d_err, 0, 4 * sizeof(int32_t)) != cudaSuccess ||
-        cudaMalloc(&h->ws.partials, h->ws.partial_floats * sizeof(float)) != cudaSuccess ||
-        cudaMalloc(&h->ws.counters, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) != cudaSuccess ||
-        cudaMemset(h->ws.counters, 0, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) != cudaSuccess ||
-        cudaMalloc(&h->sums, GEMM_OWN_SUMS_BYTES) != cudaSuccess) {
+    // Allocating and clearing are allowed while a stream is being captured (by this thread or another): the calls below
+    // touch no stream but their own.
+    CaptureRelaxed relaxed;
+    cudaStream_t s = nullptr;
+    const bool ok =
+        cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess &&
+        cudaMalloc(&h->d_err, 4 * sizeof(int32_t)) == cudaSuccess &&
+        cudaMemsetAsync(h->d_err, 0, 4 * sizeof(int32_t), s) == cudaSuccess &&
+        cudaMalloc(&h->ws.partials, h->ws.partial_floats * sizeof(float)) == cudaSuccess &&
+        cudaMalloc(&h->ws.counters, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) == cudaSuccess &&
+        cudaMemsetAsync(h->ws.counters, 0, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t), s) == cudaSuccess &&
+        cudaMalloc(&h->sums, GEMM_OWN_SUMS_BYTES) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+    if (s) cudaStreamDestroy(s);
+    if (!ok) {
         if (h->d_err) cudaFree(h->d_err);
         if (h->ws.partials) cudaFree(h->ws.partials);
         if (h->ws.counters) cudaFree(h->ws.counters);

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -269,7 +270,10 @@ def _padded_output(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Te
 
 
 class Gemm:
-    """A library handle bound to one CUDA device."""
+    """A library handle bound to one CUDA device.
+
+    Its calls share a workspace: make them from one host thread at a time, on one stream or on streams that are ordered.
+    A captured graph uses it too: keep the handle open, and its other calls ordered with the replays."""
 
     def __init__(self, device=None):
         lib = load()
@@ -653,46 +657,72 @@ class Gemm:
         return int(self._lib.gemm_sync_status(self._h, _stream_ptr(stream) or None))
 
 
+# The handles of the module functions, one per (device, stream): a handle's workspace (stream-K parts and counters, column
+# sums) serves one call at a time, so calls on streams that are not ordered need one each, and a captured graph keeps
+# that of the stream it was captured on.  A call may be two launches: the lock keeps those of two host threads apart.
 _default: dict = {}
+_default_lock = threading.Lock()
 
 
-def _default_handle(device: int) -> Gemm:
-    """The handle that matmul and the linear-layer functions use on a device."""
-    h = _default.get(device)
+def _default_handle(device: int, stream: int):
+    """The (handle, lock) of a device's stream."""
+    if device < 0:
+        raise ValueError("expected CUDA tensors")
+    h = _default.get((device, stream))
     if h is None:
-        h = _default[device] = Gemm(device)
+        with _default_lock:
+            h = _default.get((device, stream))
+            if h is None:
+                h = _default[device, stream] = (Gemm(device), threading.RLock())
     return h
+
+
+def _default_of(t: torch.Tensor, stream):
+    device = t.get_device()
+    return _default_handle(device, _stream_of(stream, device) if device >= 0 else 0)
 
 
 def matmul(A: torch.Tensor, B: torch.Tensor, layout: str = "NN", out: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
-    """C = A·B with the library's kernel, on a per-device default handle."""
+    """C = A·B with the library's kernel, on a default handle of the stream (so calls on several streams and from
+    several threads do not disturb one another).  A captured graph keeps that of its capture stream: replays of
+    graphs captured on one stream must not overlap."""
     dev = A.device.index if A.device.index is not None else torch.cuda.current_device()
-    return _default_handle(dev).run(A, B, out, layout, stream)
+    h, lock = _default_handle(dev, _stream_ptr(stream))
+    with lock:
+        return h.run(A, B, out, layout, stream)
 
 
 def linear(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = None,
            residual: torch.Tensor | None = None, out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
            out_dtype: torch.dtype | None = None, alpha: float = 1.0, stream=None) -> torch.Tensor:
-    """Gemm.linear on a per-device default handle."""
-    return _default_handle(X.get_device()).linear(X, W, bias, act, residual, out, preact, out_dtype, alpha, stream)
+    """Gemm.linear on a default handle of the stream (see matmul)."""
+    h, lock = _default_of(X, stream)
+    with lock:
+        return h.linear(X, W, bias, act, residual, out, preact, out_dtype, alpha, stream)
 
 
 def linear_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
                  out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
                  beta_bias: float = 0.0, stream=None) -> torch.Tensor:
-    """Gemm.linear_dgrad on a per-device default handle."""
-    return _default_handle(dY.get_device()).linear_dgrad(dY, W, Z, act, out, dbias, alpha, beta_bias, stream)
+    """Gemm.linear_dgrad on a default handle of the stream (see matmul)."""
+    h, lock = _default_of(dY, stream)
+    with lock:
+        return h.linear_dgrad(dY, W, Z, act, out, dbias, alpha, beta_bias, stream)
 
 
 def linear_wgrad(dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype | None = None, alpha: float = 1.0, beta: float = 0.0, stream=None) -> torch.Tensor:
-    """Gemm.linear_wgrad on a per-device default handle."""
-    return _default_handle(dY.get_device()).linear_wgrad(dY, X, out, out_dtype, alpha, beta, stream)
+    """Gemm.linear_wgrad on a default handle of the stream (see matmul)."""
+    h, lock = _default_of(dY, stream)
+    with lock:
+        return h.linear_wgrad(dY, X, out, out_dtype, alpha, beta, stream)
 
 
 def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None, out: torch.Tensor | None = None,
              dbias: torch.Tensor | None = None, beta_bias: float = 0.0, sums_only: bool = False,
              stream=None) -> torch.Tensor | None:
-    """Gemm.act_grad on a per-device default handle."""
-    return _default_handle(dY.get_device()).act_grad(dY, Z, act, out, dbias, beta_bias, sums_only, stream)
+    """Gemm.act_grad on a default handle of the stream (see matmul)."""
+    h, lock = _default_of(dY, stream)
+    with lock:
+        return h.act_grad(dY, Z, act, out, dbias, beta_bias, sums_only, stream)

@@ -29,6 +29,8 @@
  * after the first gemm_run_host, device staging buffers plus that path's streams and
  * events.  A handle may be used from one host thread at a time, and its launches must not
  * overlap on the GPU (they share the workspace): enqueue them on one stream or order them.
+ * A captured graph holds the handle's addresses: its replays count as launches of the handle,
+ * which must outlive it.
  * Aliasing C with A or B is undefined.
  *
  * Errors.  Every entry point returns a status; nothing throws across the ABI.
@@ -140,7 +142,8 @@ typedef struct {
 } gemm_plan_t;
 
 /* Create a handle bound to CUDA device `device`.  Checks that the device is sm_103,
- * reads its SM count and allocates the device error word and the stream-K workspace.
+ * reads its SM count and allocates the device error word and the workspaces.  A stream may be
+ * under capture meanwhile (nothing of this is captured).
  * Returns INVALID_ARG (out == NULL or no such device), ARCH, or CUDA. */
 gemm_status_t gemm_create(gemm_handle_t* out, int device);
 

@@ -67,3 +67,69 @@ def test_cluster_shares_that_end_inside_a_warp(g, M, N, K, dtype):  # noqa: F811
     same(dX.t, d.to(dtype), "dX")
     same(db.t[0], d.sum(0).float(), "dbias")
     dX.check("dX"), db.check("dbias")
+
+
+# ------------------------------------------------------------------ several streams at once
+
+def test_module_functions_on_two_streams_at_once(g):  # noqa: F811
+    # Column sums, stream-K parts and counters of unordered calls must not meet.
+    r = gen(40)
+    cases = []
+    for seed, (M, N, K) in enumerate([(1000, 136, 520), (2000, 72, 264)]):
+        dY, W, Z = matrix(r, M, N, BF16, ints=True), matrix(r, N, K, BF16, ints=True), matrix(r, M, K, BF16, ints=True)
+        G, Zn = matrix(r, M, K, BF16, ints=True), matrix(r, M, K, BF16, ints=True)
+        slope = ref.act_slope(Z.double(), "relu")
+        cases.append((dY, W, Z, G, Zn, ((dY.double() @ W.double()) * slope).sum(0).float(),
+                      (G.double() * ref.act_slope(Zn.double(), "relu")).sum(0).float()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    rounds = 40
+    out = [[(torch.empty(c[5].shape, device="cuda"), torch.empty(c[6].shape, device="cuda")) for _ in range(rounds)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        for s, c, o in zip(streams, cases, out):
+            native.linear_dgrad(c[0], c[1], c[2], act="relu", dbias=o[i][0], stream=s)
+            native.act_grad(c[3], c[4], act="relu", dbias=o[i][1], sums_only=True, stream=s)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, out):
+        for db, dz in o:
+            same(db, c[5], "dgrad's sums")
+            same(dz, c[6], "act_grad's sums")
+
+
+def test_module_functions_captured_on_a_stream_of_their_own(g):  # noqa: F811
+    # The capture stream's handle is made during the capture; the graph's replays and eager calls do not share a workspace.
+    r = gen(41)
+    dY, W, Z = matrix(r, 1000, 136, BF16, ints=True), matrix(r, 136, 520, BF16, ints=True), matrix(r, 1000, 520, BF16, ints=True)
+    db, db2 = torch.zeros(520, device="cuda"), torch.zeros(520, device="cuda")
+    want = ((dY.double() @ W.double()) * ref.act_slope(Z.double(), "relu")).sum(0).float()
+    native.linear_dgrad(dY, W, Z, act="relu", dbias=db)
+    same(db, want, "eager")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    db.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        dX = native.linear_dgrad(dY, W, Z, act="relu", dbias=db)
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            graph.replay()
+        native.linear_dgrad(dY, W, Z, act="relu", dbias=db2)
+        native.linear_wgrad(dY, Z)
+    torch.cuda.synchronize()
+    same(db, want, "replayed")
+    same(db2, want, "beside the replays")
+    same(dX, ((dY.double() @ W.double()) * ref.act_slope(Z.double(), "relu")).bfloat16(), "dX")
+
+
+def test_a_handle_made_during_a_capture(g):  # noqa: F811
+    x = matrix(gen(42), 64, 64, BF16, ints=True)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        h = native.Gemm(0)
+        y = h.linear(x, x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert h.sync_status() == native.OK
+    same(y, (x.double() @ x.double().t()).bfloat16())
+    del graph
+    h.close()

@@ -2,8 +2,11 @@
 import ctypes
 import os
 import subprocess
+import threading
+import time
 
 import pytest
+import torch
 
 from conftest import ROOT
 
@@ -64,3 +67,63 @@ def test_every_name_that_the_package_lists_resolves():
     names = {}
     exec("from dense_tiled_gemm_04_gb300 import *", names)
     assert set(package.__all__) <= set(names)
+
+
+class FakeGemm:
+    """A handle that records its calls, as native.Gemm's stand-in; creating one takes a while."""
+
+    made = []
+
+    def __init__(self, device):
+        time.sleep(0.02)
+        self.device, self.inside, self.overlaps, self.calls = device, 0, 0, 0
+        FakeGemm.made.append(self)
+
+    def linear_dgrad(self, *args):
+        self.overlaps += self.inside
+        self.inside += 1
+        time.sleep(0.002)
+        self.inside -= 1
+        self.calls += 1
+        return self
+
+
+class FakeTensor:
+    def get_device(self):
+        return 0
+
+
+@pytest.fixture
+def fake(lib, monkeypatch):
+    monkeypatch.setattr(lib, "Gemm", FakeGemm)
+    monkeypatch.setattr(lib, "_default", {})
+    FakeGemm.made = []
+    return lib
+
+
+def test_module_functions_use_a_handle_per_stream(fake):
+    # Calls on streams that are not ordered share no workspace.
+    t = FakeTensor()
+    a, b = fake.linear_dgrad(t, None, stream=64), fake.linear_dgrad(t, None, stream=128)
+    assert a is not b and fake.linear_dgrad(t, None, stream=64) is a
+    assert len(FakeGemm.made) == 2
+
+
+def test_module_functions_from_several_threads(fake):
+    # One handle per stream is made however many threads ask first, and its calls (two launches each) do not interleave.
+    t = FakeTensor()
+    threads = [threading.Thread(target=lambda s=s: [fake.linear_dgrad(t, None, stream=s) for _ in range(5)])
+               for s in (64, 128) for _ in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert len(FakeGemm.made) == 2
+    assert [h.calls for h in FakeGemm.made] == [20, 20] and [h.overlaps for h in FakeGemm.made] == [0, 0]
+
+
+def test_module_functions_refuse_host_tensors(lib):
+    x = torch.zeros((8, 8), dtype=torch.float16)
+    for call in (lambda: lib.linear(x, x), lambda: lib.linear_dgrad(x, x), lambda: lib.linear_wgrad(x, x), lambda: lib.act_grad(x)):
+        with pytest.raises(ValueError):
+            call()
