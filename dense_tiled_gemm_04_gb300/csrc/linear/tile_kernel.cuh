@@ -448,7 +448,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int s = 0; s < STAGES; ++s)
                     if (armed_mask & (1u << s)) wd.drain(full_bar(s), (armed_parity >> s) & 1u);
         }
-        __syncwarp();
     } else if (warp == kMmaWarp) {
         if (lane == 0 && leader) {
             // ---------------------------------------------------------------- MMA issuer
@@ -957,6 +956,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     ptx::tc_fence_before_sync();
     __syncthreads();
+    __syncwarp();
     if constexpr (PAIR) ptx::cluster_sync();  // neither CTA exits or frees TMEM while the peer may use it
     if (warp == kMmaWarp) {
         ptx::tc_fence_after_sync();
