@@ -23,6 +23,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("gemm_api.cu", "kernels_f16.cu", "ker
                                            "linear/linear_api.cu", "linear/forward_f16.cu", "linear/forward_bf16.cu",
                                            "linear/forward_e4m3.cu", "linear/forward_e5m2.cu", "linear/dgrad_f16.cu",
                                            "linear/dgrad_bf16.cu", "linear/wgrad_f16.cu", "linear/wgrad_bf16.cu",
+                                           "linear/forward_long_f16.cu", "linear/forward_long_bf16.cu",
+                                           "linear/forward_long_e4m3.cu", "linear/forward_long_e5m2.cu",
+                                           "linear/wgrad_long_f16.cu", "linear/wgrad_long_bf16.cu",
                                            "linear/cluster_forward.cu", "linear/cluster_forward_8bit.cu",
                                            "linear/cluster_grad.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "sm103_ptx.cuh", "kernel_set.cuh",

@@ -18,7 +18,9 @@ constexpr int64_t kTimeoutDefaultNs = 2000000000LL;  // 2 s per wait
 // Kernels whose launch state is kept: gemm_run and its relatives (4 configurations x 12 operand /
 // output types x 2 layouts), then those of the linear-layer entry points.
 constexpr int kLinearSlot0 = 96;
-constexpr int kNumSlots = kLinearSlot0 + 42 + 56;  // 14 operators and types x (3 tile + 4 token sizes)
+constexpr int kLinearTileSlots = 3 * 22;     // tile kernels: operators, types and sums x tiles
+constexpr int kLinearClusterSlots = 4 * 14;  // cluster kernels: operators and types x token sizes
+constexpr int kNumSlots = kLinearSlot0 + kLinearTileSlots + kLinearClusterSlots;
 constexpr int64_t kMinStreamKBlocks = 8;   // default shortest stream-K share (GEMM_OPT_SK_MIN_BLOCKS)
 constexpr int64_t kMinSplitBlocks = 32;    // default shortest share of a split under one wave (GEMM_OPT_SPLIT_MIN_BLOCKS)
 

@@ -117,19 +117,34 @@ struct Product {
     float* partials;
 };
 
+// K blocks per accumulation on one tensor-core accumulator, which truncates: a chain of K blocks loses about 1.2e-9 of
+// its sum per product (see tile_kernel.cuh).  Where an fp32 result is wanted, 12 blocks of 64 keep that under 1e-6.  A
+// result that is rounded to 16 bits takes up to 128 blocks as one chain, whose 1e-5 is 1/25 of fp16's half spacing where
+// that is smallest; a longer contraction is cut into chains of at most that.
+constexpr int64_t kChunkBlocks = 12, kLongChunkBlocks = 128;
+
+bool fp32_result(const Product& q) { return q.out == GEMM_DTYPE_F32 || q.partials; }
+int64_t k_blocks(const Product& q) { return cdiv(q.depth, is_f8(q.in) ? 128 : 64); }
+int64_t chunk_limit(const Product& q) { return fp32_result(q) ? kChunkBlocks : kLongChunkBlocks; }
+
+// Whether a product takes the tile kernel that sums chunks in registers.
+bool summed(const Product& q) { return fp32_result(q) || k_blocks(q) > kLongChunkBlocks; }
+
 KernelChoice tile_kernel(const Product& q, int config)
 {
-    const bool bf16 = q.out == GEMM_DTYPE_BF16, f32 = q.out == GEMM_DTYPE_F32;
-    if (q.mode == dtg::linear::kDgrad)
-        return bf16 ? dtg::linear::dgrad_bf16(config, q.partials != nullptr)
-                    : dtg::linear::dgrad_f16(config, q.partials != nullptr);
-    if (q.mode == dtg::linear::kWgrad)
-        return q.in == GEMM_DTYPE_BF16 ? dtg::linear::wgrad_bf16(config, f32) : dtg::linear::wgrad_f16(config, f32);
+    using namespace dtg::linear;
+    const bool bf16 = q.out == GEMM_DTYPE_BF16, sums = summed(q);
+    if (q.mode == kDgrad) return bf16 ? dgrad_bf16(config, sums) : dgrad_f16(config, sums);
+    if (q.mode == kWgrad) {
+        const bool f32 = q.out == GEMM_DTYPE_F32;
+        if (sums && !f32) return bf16 ? wgrad_long_bf16(config) : wgrad_long_f16(config);
+        return q.in == GEMM_DTYPE_BF16 ? wgrad_bf16(config, f32) : wgrad_f16(config, f32);
+    }
     switch (q.in) {
-    case GEMM_DTYPE_BF16: return dtg::linear::forward_bf16(config);
-    case GEMM_DTYPE_E4M3: return dtg::linear::forward_e4m3(config, bf16);
-    case GEMM_DTYPE_E5M2: return dtg::linear::forward_e5m2(config, bf16);
-    default: return dtg::linear::forward_f16(config);
+    case GEMM_DTYPE_BF16: return sums ? forward_long_bf16(config) : forward_bf16(config);
+    case GEMM_DTYPE_E4M3: return sums ? forward_long_e4m3(config, bf16) : forward_e4m3(config, bf16);
+    case GEMM_DTYPE_E5M2: return sums ? forward_long_e5m2(config, bf16) : forward_e5m2(config, bf16);
+    default: return sums ? forward_long_f16(config) : forward_f16(config);
     }
 }
 
@@ -142,22 +157,27 @@ int operator_index(const Product& q)
     return 10 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
 }
 
-int tile_slot(const Product& q, int config) { return kLinearSlot0 + 3 * operator_index(q) + (config - 1); }
+// One of 22 tile kernels of a configuration: forward 6 types x summed or not, dgrad 2 x 2, wgrad 2 x (16-bit, fp32, 16-bit
+// summed).
+int tile_slot(const Product& q, int config)
+{
+    const int sums = summed(q);
+    const int kernel = q.mode == dtg::linear::kForward  ? 2 * operator_index(q) + sums
+                       : q.mode == dtg::linear::kDgrad ? 12 + 2 * q.in + sums
+                                                       : 16 + 3 * q.in + (q.out == GEMM_DTYPE_F32 ? 1 : 2 * sums);
+    return kLinearSlot0 + 3 * kernel + (config - 1);
+}
 
 int cluster_slot(const Product& q, int tokens)
 {
-    return kLinearSlot0 + 42 + 4 * operator_index(q) + (tokens == 16 ? 0 : tokens == 32 ? 1 : tokens == 64 ? 2 : 3);
+    return kLinearSlot0 + kLinearTileSlots + 4 * operator_index(q) + (tokens == 16 ? 0 : tokens == 32 ? 1 : tokens == 64 ? 2 : 3);
 }
-
-// K blocks per chunk of an accumulation in registers (see tile_kernel.cuh): 12 blocks of 64 keep the
-// truncation of the tensor core's accumulator under 1e-6 of the sum.
-constexpr int64_t kChunkBlocks = 12;
 
 // Whether a product runs on linear_cluster_kernel, and how.
 struct ClusterPlan {
     int tokens = 0;  // per tile; 0: the tile kernels
     int ranks = 1;   // CTAs per cluster
-    int32_t chunk_kb = INT32_MAX;  // K blocks per accumulator
+    int32_t chunk_kb = 0;  // K blocks per accumulator
     KernelChoice kc;
 };
 
@@ -200,7 +220,7 @@ gemm_status_t clusters_that_fit(DeviceState& dev, const KernelChoice& kc, int sl
 gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Product& q, ClusterPlan* c)
 {
     if (o.config != GEMM_CONFIG_AUTO || q.depth == 0) return GEMM_OK;
-    const int64_t kb = cdiv(q.depth, is_f8(q.in) ? 128 : 64);
+    const int64_t kb = k_blocks(q);
     int tokens = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
     if (q.mode == dtg::linear::kDgrad && tokens < 64) tokens = 64;
     if (q.mode == dtg::linear::kWgrad) tokens = 128;
@@ -236,12 +256,10 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
         ++log;
     }
     if (st != GEMM_OK) return st;
-    // fp32 results: chains of products no longer than the tile kernels' chunks, on as many accumulators as there are.
-    if (q.out == GEMM_DTYPE_F32 || q.partials) {
-        const int64_t blocks = cdiv(kb, 1 << log), chunks = cdiv(blocks, kChunkBlocks);
-        if (chunks > 256 / tokens) return GEMM_OK;
-        c->chunk_kb = static_cast<int32_t>(cdiv(blocks, chunks));
-    }
+    // Chains of products no longer than the tile kernels', on as many accumulators as there are.
+    const int64_t blocks = cdiv(kb, 1 << log), chunks = cdiv(blocks, chunk_limit(q));
+    if (chunks > 256 / tokens) return GEMM_OK;
+    c->chunk_kb = static_cast<int32_t>(cdiv(blocks, chunks));
     c->tokens = tokens;
     c->ranks = 1 << log;
     return GEMM_OK;
@@ -400,8 +418,8 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     p.beta = q.beta;
     // SUMS kernels: chunks of equal length (within one); the others take a contraction as one chunk.
     p.chunk_kb = INT32_MAX;
-    if ((q.out == GEMM_DTYPE_F32 || q.partials) && plan.k_blocks > 0)
-        p.chunk_kb = static_cast<int32_t>(cdiv(plan.k_blocks, cdiv(plan.k_blocks, kChunkBlocks)));
+    if (summed(q) && plan.k_blocks > 0)
+        p.chunk_kb = static_cast<int32_t>(cdiv(plan.k_blocks, cdiv(plan.k_blocks, chunk_limit(q))));
     p.act = q.act;
     p.bias = q.bias;
     p.bias_f32 = q.bias_dtype == GEMM_DTYPE_F32;

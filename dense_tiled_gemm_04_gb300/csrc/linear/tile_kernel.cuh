@@ -17,9 +17,9 @@
 // chunk_kb; each chunk overwrites one of the two TMEM accumulators, and the epilogue warps
 // add it to a running sum in their registers, rounding to nearest.  The MMAs of the next chunk
 // run meanwhile, so the tensor pipe does not wait, and an item's accumulator is free as soon as its last
-// chunk has been read, before any of the epilogue's arithmetic.  Only where an fp32 result is wanted (SUMS:
-// weight gradients, column sums); a result that is rounded to 16 bits alone takes the whole contraction as one
-// chunk, whose boxes go from TMEM straight through the epilogue.
+// chunk has been read, before any of the epilogue's arithmetic.  That is SUMS: where an fp32 result is wanted (weight
+// gradients, column sums; chunks of 12 blocks), and contractions of more than 128 blocks.  A result that is rounded to 16
+// bits alone takes a shorter contraction as one chunk, whose boxes go from TMEM straight through the epilogue.
 //
 // Epilogue.  Eight warps, two per TMEM lane quadrant, 32 rows x BN/2 columns each; with SUMS they hold
 // those sums (128 registers at BN = 256; four warps would need 256 each).  Per box of 128 bytes of output

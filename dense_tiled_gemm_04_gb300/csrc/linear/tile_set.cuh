@@ -36,6 +36,13 @@ KernelChoice dgrad_f16(int config, bool sums);
 KernelChoice dgrad_bf16(int config, bool sums);
 KernelChoice wgrad_f16(int config, bool out_f32);
 KernelChoice wgrad_bf16(int config, bool out_f32);
+// 16-bit results of contractions that are summed in chunks for their length alone.
+KernelChoice forward_long_f16(int config);
+KernelChoice forward_long_bf16(int config);
+KernelChoice forward_long_e4m3(int config, bool out_bf16);
+KernelChoice forward_long_e5m2(int config, bool out_bf16);
+KernelChoice wgrad_long_f16(int config);
+KernelChoice wgrad_long_bf16(int config);
 
 }  // namespace linear
 }  // namespace dtg

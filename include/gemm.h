@@ -376,7 +376,10 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C,
  * NaN stays NaN; values and derivatives at +-infinity are their limits.
  *
  * Sums run in fp32, in an order that depends on the sizes and the handle's options alone, so a
- * call's results do not change from one call to the next.  Every matrix is row-major, with the
+ * call's results do not change from one call to the next.  The tensor core truncates as it adds: a
+ * chain of n 16-bit products is short by about 1.2e-9 n of its value.  Chains end after 768 products
+ * where a result or a column sum is fp32, after 8192 (8-bit operands: 16384) where it is rounded
+ * to 16 bits; longer contractions add chains in fp32, rounding to nearest.  Every matrix is row-major, with the
  * alignment rules of gemm_run (bases of 16 bytes; row pitches that are multiples of 16 bytes);
  * bias and dbias are dense vectors of any alignment their type allows; a dimension over
  * 2^31 - 512 is UNSUPPORTED.  An output may not

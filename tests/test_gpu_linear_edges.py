@@ -133,3 +133,73 @@ def test_a_handle_made_during_a_capture(g):  # noqa: F811
     same(y, (x.double() @ x.double().t()).bfloat16())
     del graph
     h.close()
+
+
+# ------------------------------------------------------------------ contractions longer than one accumulator keeps
+
+# The tensor core's fp32 accumulator truncates: a chain of K products ends about 1.2e-9 K of its value nearer to zero.
+# Chains stop at 8192 products of 16 bits (16384 of 8 bits, which are added two at a time), so whatever the length, the
+# results' projection on the exact ones is short by no more than 1e-5 and what the fp32 additions of the chains add;
+# the rounding to fp16 is unbiased, 2^-11 / sqrt(3) at most on average, over 1e5 results or more 1e-6.
+def shrink(got, want):
+    return ((got.double() - want) * want).sum().item() / (want * want).sum().item()
+
+
+LONG = 2e-5
+
+
+@pytest.mark.parametrize("config", [native.CONFIG_AUTO] + TILES)
+@pytest.mark.parametrize("dtype", [F16, BF16, torch.float8_e4m3fn, torch.float8_e5m2])
+def test_long_contractions_forward(g, config, dtype):  # noqa: F811
+    g.set_option(native.OPT_CONFIG, config)
+    r = gen(50)
+    M, N, K = 300, 400, 100000
+    out = BF16 if dtype == BF16 else F16
+    X, W = matrix(r, M, K, dtype), matrix(r, N, K, dtype)
+    bias, res = vector(r, N, F32), matrix(r, M, N, out)
+    Y, Z = Guarded(M, N, out), Guarded(M, N, out)
+    g.linear(X, W, bias, act="gelu", residual=res, out=Y.t, preact=Z.t, alpha=K ** -0.5)
+    y, z = ref.linear(X, W, bias, "gelu", res, out, K ** -0.5)
+    ref.assert_within(Y.t, y, "Y")
+    ref.assert_within(Z.t, z, "Z")
+    Y.check(), Z.check()
+    if out == F16:
+        assert abs(shrink(Z.t, z[0])) < LONG
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 128 * 160, 16400), (16, 2048, 262144), (20, 6000, 40000), (64, 20000, 12300), (120, 19000, 12400)])
+@pytest.mark.parametrize("dtype", [F16, torch.float8_e4m3fn])
+def test_long_contractions_of_few_tokens(g, M, N, K, dtype):  # noqa: F811
+    # Shares of a rank longer than one accumulator keeps: further accumulators, or the tile kernels.
+    r = gen(51)
+    X, W = matrix(r, M, K, dtype), matrix(r, N, K, dtype)
+    Y = Guarded(M, N, F16)
+    g.linear(X, W, out=Y.t, alpha=K ** -0.5)
+    y, _ = ref.linear(X, W, None, "none", None, F16, K ** -0.5)
+    ref.assert_within(Y.t, y, "Y")
+    assert abs(shrink(Y.t, y[0])) < LONG
+    Y.check()
+
+
+@pytest.mark.parametrize("config", [native.CONFIG_AUTO] + TILES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_long_contractions_backward(g, config, dtype):  # noqa: F811
+    g.set_option(native.OPT_CONFIG, config)
+    r = gen(52)
+    L = 100000
+    dY, W, Z = matrix(r, 300, L, dtype, scale=L ** -0.5), matrix(r, L, 392, dtype), matrix(r, 300, 392, dtype)
+    dX = Guarded(300, 392, dtype)
+    g.linear_dgrad(dY, W, Z, act="silu", out=dX.t)
+    d, _ = ref.through_act(*ref.product(dY, W), Z, "silu", dtype, F32)
+    ref.assert_within(dX.t, d, "dX")
+    dX.check()
+    A, B = matrix(r, L, 300, dtype, scale=L ** -0.5), matrix(r, L, 392, dtype)
+    dW0 = matrix(r, 300, 392, dtype)
+    dW = Guarded(300, 392, dtype, init=dW0)
+    g.linear_wgrad(A, B, out=dW.t, beta=0.5)
+    w = ref.wgrad(A, B, dtype, 1.0, 0.5, dW0)
+    ref.assert_within(dW.t, w, "dW")
+    dW.check()
+    if dtype == F16:
+        assert abs(shrink(dX.t, d[0])) < LONG
+        assert abs(shrink(dW.t, w[0])) < LONG
