@@ -256,7 +256,8 @@ def _new(rows: int, cols: int, dtype: torch.dtype, device: int, stream) -> torch
     if stream is None:
         return _padded_output(rows, cols, dtype, device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # (ExternalStream(0) would be a stream of the pool.)
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return _padded_output(rows, cols, dtype, device)
 

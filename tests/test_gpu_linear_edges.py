@@ -203,3 +203,21 @@ def test_long_contractions_backward(g, config, dtype):  # noqa: F811
     if dtype == F16:
         assert abs(shrink(dX.t, d[0])) < LONG
         assert abs(shrink(dW.t, w[0])) < LONG
+
+
+# ------------------------------------------------------------------ streams by their numbers
+
+def test_outputs_belong_to_the_stream_that_a_number_names(g, monkeypatch):  # noqa: F811
+    # A new output's memory goes back to its stream's pool: it must be the stream that the call runs on.  0 is the
+    # default stream.
+    r = gen(60)
+    X, W = matrix(r, 40, 64, F16, ints=True), matrix(r, 72, 64, F16, ints=True)
+    side, real, seen = torch.cuda.Stream(), torch.cuda.stream, []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: seen.append(s.cuda_stream) or real(s))
+    torch.cuda.synchronize()
+    want = (X.double() @ W.double().t()).half()
+    for number in (0, side.cuda_stream):
+        Y = g.linear(X, W, stream=number)
+        torch.cuda.synchronize()
+        same(Y, want)
+        assert seen.pop() == number and not seen
