@@ -221,3 +221,20 @@ def test_outputs_belong_to_the_stream_that_a_number_names(g, monkeypatch):  # no
         torch.cuda.synchronize()
         same(Y, want)
         assert seen.pop() == number and not seen
+
+
+# ------------------------------------------------------------------ wide layers
+
+@pytest.mark.parametrize("M,N,K", [(1, 28672, 264), (1, 128256, 520), (3, 39001, 1000), (33, 64000, 136)])
+@pytest.mark.parametrize("dtype", [F16, BF16, torch.float8_e4m3fn])
+def test_few_tokens_through_wide_layers(g, M, N, K, dtype):  # noqa: F811
+    # More tiles of 128 features than the GPU runs at once in clusters: those products take the tile kernels.
+    r = gen(70)
+    out = F16 if dtype == F16 else BF16
+    X, W = matrix(r, M, K, dtype, ints=True), matrix(r, N, K, dtype, ints=True)
+    bias, res = vector(r, N, F32, ints=True), matrix(r, M, N, out, ints=True)
+    Y = Guarded(M, N, out)
+    g.linear(X, W, bias, act="relu", residual=res, out=Y.t)
+    want = ref.act_value(X.double() @ W.double().t() + bias.double(), "relu") + res.double()
+    same(Y.t, want.to(out), "Y")
+    Y.check("Y")
