@@ -11,7 +11,8 @@ namespace linear {
 //
 // Floor: 2 + 2 bytes read and 2 written per element.  A warp covers 256 columns of a row (16 bytes a lane), the
 // eight warps of a block rows r, r + 8, ... of its block of rows, two of them in flight per warp and four blocks per SM
-// (8192 x 8192 bf16 gelu with sums: 75.8 us; four rows and three blocks 82.0, one row and six blocks 86.0).
+// (8192 x 8192 bf16 gelu with sums, when those took eight warps a block: 75.8 us; four rows and three blocks 82.0, one row
+// and six blocks 86.0.  Now, with gelu_tanh: 69.5, 85 % of the copy rate).
 // Each lane adds its eight columns in registers over all its rows; the eight warps' sums meet in shared memory in
 // warp order, so a row of partial sums is written per block of rows (not per 32 rows).
 constexpr int kActWarps = 8;

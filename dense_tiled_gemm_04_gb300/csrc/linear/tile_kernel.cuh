@@ -28,9 +28,11 @@
 // pre-activations by TMA; then the 128-byte-swizzled staging buffer and a TMA store.
 //
 // What bounds it (one GB300, short bursts): 8192^3 bf16 forward with bias, gelu_tanh and z kept 577-588 us, as
-// gemm_run's product alone (559-575).  16384 x 1024 x 8192: forward with residual 174-182 us (gemm_run 163-168), wgrad fp32
-// accumulated 180-186 us; dgrad with gelu 223 us, with sums 266 us, against 178 without either: there a tile's MMAs
-// (8192 cycles) leave the epilogue 32 issue slots an element, of which it takes 23, or 29 with the sums, at 0.4
+// gemm_run's product alone (559-575).  16384 x 1024 x 8192: forward with residual 168-182 us (gemm_run 163-168), wgrad fp32
+// accumulated 180-186 us; back to back, under the power limit, the three take 670-689, 197-203 and 189-193 us (gemm_run
+// 8192^3 654-666).  dgrad of the tall layer with gelu takes 223 us, with sums 266 us (back to back 275-282), against 178
+// without either: there a tile's MMAs (8192 cycles) leave the epilogue 32 issue slots an element, of which it takes 23, or
+// 29 with the sums, at 0.4
 // instructions a cycle -- two warps per scheduler waiting on fixed latencies, TMEM and shared memory.  Sixteen warps,
 // loads a tile ahead, coalesced plain stores without the proxy fence, and rolled loops were slower.
 //
