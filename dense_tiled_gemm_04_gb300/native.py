@@ -173,6 +173,11 @@ def bias_grad_workspace_bytes(M: int, cols: int) -> int:
     return int(load().gemm_bias_grad_workspace_bytes(M, cols))
 
 
+def _sums_bytes(M: int, cols: int) -> int:
+    """bias_grad_workspace_bytes without a call into the library, which a small call would notice."""
+    return 4 * -(-M // 32) * (-(-cols // 64) * 64)
+
+
 def tile_coord(tile: int, tiles_m: int, tiles_n: int, group_m: int):
     tm, tn = ctypes.c_int64(), ctypes.c_int64()
     st = load().gemm_tile_coord(tile, tiles_m, tiles_n, group_m, ctypes.byref(tm), ctypes.byref(tn))
@@ -513,10 +518,11 @@ class Gemm:
                                            _stream_ptr(stream) or None))
 
     # -------------------------------------------------------------- linear layers
+    # (_ptr: the stream's address, where the caller has looked it up)
     def linear(self, X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = None,
                residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
                preact: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, alpha: float = 1.0,
-               stream=None) -> torch.Tensor:
+               stream=None, _ptr=None) -> torch.Tensor:
         """Y = act(alpha * X·W^T + bias) + residual (gemm_run_linear): X (M x K) and W (N x K) 16-bit or
         8-bit floats, Y, residual and preact float16 or bfloat16, bias float32 or Y's type.  ``preact``, if
         given, receives alpha * X·W^T + bias; ``out`` may be ``residual`` itself.  Async on `stream`."""
@@ -545,14 +551,14 @@ class Gemm:
         ldy = _matrix(out, "out", M, N, out_dtype, dev)
         a = gemm_linear_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
                                ldz, in_code, out_code, bias_code, _act(act), alpha)
-        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), _stream_of(stream, dev))
+        st = self._lib.gemm_run_linear(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_linear")
         return out
 
     def linear_dgrad(self, dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
                      out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
-                     beta_bias: float = 0.0, stream=None) -> torch.Tensor:
+                     beta_bias: float = 0.0, stream=None, _ptr=None) -> torch.Tensor:
         """dX = (alpha * dY·W) * act'(Z) (gemm_run_linear_dgrad): dY (M x N), W (N x K), Z (M x K, what the
         layer below kept; not read without an activation) of one 16-bit type.  ``dbias`` (K, float32 or that type), if given, becomes
         beta_bias * dbias + the column sums of dX.  Async on `stream`."""
@@ -576,20 +582,20 @@ class Gemm:
         lddx = _matrix(out, "out", M, K, dt, dev)
         if dbias is not None:
             db_code, db_p = _vector(dbias, "dbias", K, dt, dev), dbias.data_ptr()
-            ws_bytes = self._lib.gemm_bias_grad_workspace_bytes(M, K)
+            ws_bytes = _sums_bytes(M, K)
             if ws_bytes > OWN_SUMS_BYTES:
                 ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
                 ws_p = ws.data_ptr()
         a = gemm_dgrad_args_t(dY.data_ptr(), W.data_ptr(), z_p, out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy, ldw,
                               ldz, lddx, dt_code, db_code, code, alpha, beta_bias)
-        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), _stream_of(stream, dev))
+        st = self._lib.gemm_run_linear_dgrad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_linear_dgrad")
         return out
 
     def linear_wgrad(self, dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = None,
                      out_dtype: torch.dtype | None = None, alpha: float = 1.0, beta: float = 0.0,
-                     stream=None) -> torch.Tensor:
+                     stream=None, _ptr=None) -> torch.Tensor:
         """dW = alpha * dY^T·X + beta * dW (gemm_run_linear_wgrad): dY (M x N) and X (M x K) of one 16-bit
         type, dW (N x K) float32 (the default) or that type.  Async on `stream`."""
         dt, dev = dY.dtype, self._index
@@ -611,14 +617,14 @@ class Gemm:
         lddw = _matrix(out, "out", N, K, out_dtype, dev)
         a = gemm_wgrad_args_t(dY.data_ptr(), X.data_ptr(), out.data_ptr(), M, N, K, lddy, ldx, lddw, dt_code,
                               TORCH_TO_DTYPE_F32[out_dtype], alpha, beta)
-        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), _stream_of(stream, dev))
+        st = self._lib.gemm_run_linear_wgrad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_linear_wgrad")
         return out
 
     def act_grad(self, dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
                  out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, beta_bias: float = 0.0,
-                 sums_only: bool = False, stream=None) -> torch.Tensor | None:
+                 sums_only: bool = False, stream=None, _ptr=None) -> torch.Tensor | None:
         """dZ = dY * act'(Z) (gemm_run_act_grad): dY and Z (M x N; not read without an activation) of one 16-bit
         type; ``out`` may be dY itself.  ``dbias`` as for linear_dgrad, with N columns.  With ``sums_only`` dZ is not written (and None is
         returned).  Async on `stream`."""
@@ -643,13 +649,13 @@ class Gemm:
             lddz, dz_p = _matrix(out, "out", M, N, dt, dev), out.data_ptr()
         if dbias is not None:
             db_code, db_p = _vector(dbias, "dbias", N, dt, dev), dbias.data_ptr()
-            ws_bytes = self._lib.gemm_bias_grad_workspace_bytes(M, N)
+            ws_bytes = _sums_bytes(M, N)
             if ws_bytes > OWN_SUMS_BYTES:
                 ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
                 ws_p = ws.data_ptr()
         a = gemm_act_grad_args_t(dY.data_ptr(), z_p, dz_p, db_p, ws_p, ws_bytes, M, N, lddy, ldz, lddz, dt_code, db_code,
                                  code, beta_bias)
-        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), _stream_of(stream, dev))
+        st = self._lib.gemm_run_act_grad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_act_grad")
         return out
@@ -667,8 +673,6 @@ _default_lock = threading.Lock()
 
 def _default_handle(device: int, stream: int):
     """The (handle, lock) of a device's stream."""
-    if device < 0:
-        raise ValueError("expected CUDA tensors")
     h = _default.get((device, stream))
     if h is None:
         with _default_lock:
@@ -679,8 +683,13 @@ def _default_handle(device: int, stream: int):
 
 
 def _default_of(t: torch.Tensor, stream):
+    """The (handle, lock) of a tensor's device and a stream, and the stream's address."""
     device = t.get_device()
-    return _default_handle(device, _stream_of(stream, device) if device >= 0 else 0)
+    if device < 0:
+        raise ValueError("expected CUDA tensors")
+    ptr = _raw_stream(device) if stream is None else _stream_of(stream, device)
+    h, lock = _default.get((device, ptr)) or _default_handle(device, ptr)
+    return h, lock, ptr
 
 
 def matmul(A: torch.Tensor, B: torch.Tensor, layout: str = "NN", out: torch.Tensor | None = None,
@@ -698,32 +707,32 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, a
            residual: torch.Tensor | None = None, out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
            out_dtype: torch.dtype | None = None, alpha: float = 1.0, stream=None) -> torch.Tensor:
     """Gemm.linear on a default handle of the stream (see matmul)."""
-    h, lock = _default_of(X, stream)
+    h, lock, ptr = _default_of(X, stream)
     with lock:
-        return h.linear(X, W, bias, act, residual, out, preact, out_dtype, alpha, stream)
+        return h.linear(X, W, bias, act, residual, out, preact, out_dtype, alpha, stream, ptr)
 
 
 def linear_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None,
                  out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
                  beta_bias: float = 0.0, stream=None) -> torch.Tensor:
     """Gemm.linear_dgrad on a default handle of the stream (see matmul)."""
-    h, lock = _default_of(dY, stream)
+    h, lock, ptr = _default_of(dY, stream)
     with lock:
-        return h.linear_dgrad(dY, W, Z, act, out, dbias, alpha, beta_bias, stream)
+        return h.linear_dgrad(dY, W, Z, act, out, dbias, alpha, beta_bias, stream, ptr)
 
 
 def linear_wgrad(dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype | None = None, alpha: float = 1.0, beta: float = 0.0, stream=None) -> torch.Tensor:
     """Gemm.linear_wgrad on a default handle of the stream (see matmul)."""
-    h, lock = _default_of(dY, stream)
+    h, lock, ptr = _default_of(dY, stream)
     with lock:
-        return h.linear_wgrad(dY, X, out, out_dtype, alpha, beta, stream)
+        return h.linear_wgrad(dY, X, out, out_dtype, alpha, beta, stream, ptr)
 
 
 def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = None, out: torch.Tensor | None = None,
              dbias: torch.Tensor | None = None, beta_bias: float = 0.0, sums_only: bool = False,
              stream=None) -> torch.Tensor | None:
     """Gemm.act_grad on a default handle of the stream (see matmul)."""
-    h, lock = _default_of(dY, stream)
+    h, lock, ptr = _default_of(dY, stream)
     with lock:
-        return h.act_grad(dY, Z, act, out, dbias, beta_bias, sums_only, stream)
+        return h.act_grad(dY, Z, act, out, dbias, beta_bias, sums_only, stream, ptr)

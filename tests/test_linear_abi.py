@@ -45,6 +45,11 @@ def test_workspace_bytes(lib, M, cols, want):
     assert lib.bias_grad_workspace_bytes(M, cols) == want
 
 
+@pytest.mark.parametrize("M,cols", [(0, 5), (5, 0), (1, 1), (31, 63), (32, 64), (33, 65), (4097, 40), (16384, 8192), (1 << 30, 1000)])
+def test_workspace_bytes_in_the_binding(lib, M, cols):
+    assert lib._sums_bytes(M, cols) == lib.bias_grad_workspace_bytes(M, cols)
+
+
 def test_null_handles_and_arguments(lib):
     so = lib.load()
     for name, cls in (("gemm_run_linear", lib.gemm_linear_args_t), ("gemm_run_linear_dgrad", lib.gemm_dgrad_args_t),
