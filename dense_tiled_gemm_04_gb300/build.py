@@ -27,12 +27,14 @@ SOURCES = [os.path.join(CSRC, f) for f in ("gemm_api.cu", "kernels_f16.cu", "ker
                                            "linear/forward_long_e4m3.cu", "linear/forward_long_e5m2.cu",
                                            "linear/wgrad_long_f16.cu", "linear/wgrad_long_bf16.cu",
                                            "linear/cluster_forward.cu", "linear/cluster_forward_8bit.cu",
-                                           "linear/cluster_grad.cu")]
+                                           "linear/cluster_grad.cu", "linear/forward_scaled.cu", "linear/glu_16.cu",
+                                           "linear/glu_scaled.cu", "linear/glu_dgrad_f16.cu", "linear/glu_dgrad_bf16.cu",
+                                           "linear/cluster_scaled.cu", "linear/cluster_glu.cu", "linear/norm_api.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "sm103_ptx.cuh", "kernel_set.cuh",
                                                      "host/handle.cuh", "linear/activation.cuh",
                                                      "linear/elementwise.cuh", "linear/tile_kernel.cuh",
                                                      "linear/tile_set.cuh", "linear/cluster_kernel.cuh",
-                                                     "linear/cluster_set.cuh")] + [
+                                                     "linear/cluster_set.cuh", "linear/api_common.cuh", "linear/norm.cuh")] + [
     os.path.join(INCLUDE, "gemm.h")]
 OBJ_DIR = os.path.join(HERE, "_build")
 

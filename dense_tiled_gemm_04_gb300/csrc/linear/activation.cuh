@@ -190,14 +190,47 @@ __device__ __forceinline__ f32x2 act_slope2(f32x2 z)
     return both(1.0f);
 }
 
+// Value and slope together, sharing the logistic function or the exponential and polynomial.
+template <int ACT>
+__device__ __forceinline__ void act_both2(f32x2 z, f32x2& value, f32x2& slope)
+{
+    if constexpr (ACT == kGelu) {
+        const f32x2 na = minus_abs14(z), e = gauss2(z), h = half_erfcx2(na);
+        value = fma2(mul2(na, e), h, each(z, [](float x) { return fmaxf(x, 0.0f); }));
+        float z0, z1, u0, u1, w0, w1;
+        const f32x2 u = mul2(e, fma2(na, both(kInvSqrt2Pi), h));
+        split(z, z0, z1);
+        split(u, u0, u1);
+        split(fma2(u, both(-1.0f), both(1.0f)), w0, w1);
+        slope = pair(z0 < 0.0f ? u0 : w0, z1 < 0.0f ? u1 : w1);
+    } else if constexpr (ACT == kGeluTanh) {
+        // Above the clamp the logistic function is 1 in fp32: the value is z.
+        const f32x2 low = each(z, [](float x) { return max_nan(x, -12.0f); });
+        const f32x2 c = each(low, [](float x) { return min_nan(x, 12.0f); });
+        const f32x2 q = mul2(c, c);
+        const f32x2 s = logistic2(mul2(c, fma2(q, both(-kTanhC1 * kLog2e), both(-kTanhC0 * kLog2e))));
+        value = mul2(low, s);
+        slope = fma2(mul2(mul2(c, s), fma2(s, both(-1.0f), both(1.0f))), fma2(q, both(3.0f * kTanhC1), both(kTanhC0)), s);
+    } else if constexpr (ACT == kSilu) {
+        const f32x2 low = each(z, [](float x) { return max_nan(x, -100.0f); });
+        const f32x2 c = each(low, [](float x) { return min_nan(x, 100.0f); });
+        const f32x2 s = logistic2(mul2(c, both(-kLog2e)));
+        value = mul2(low, s);
+        slope = mul2(s, fma2(c, fma2(s, both(-1.0f), both(1.0f)), both(1.0f)));
+    } else {
+        value = act_value2<ACT>(z);
+        slope = act_slope2<ACT>(z);
+    }
+}
+
 // Runs f<ACT>() for the activation of a launch (uniform over the grid).
-#define DTG_ACT_SWITCH(act, STATEMENT)                              \
+#define DTG_ACT_SWITCH(act, ...)                                    \
     switch (act) {                                                  \
-    case kRelu: { constexpr int ACT = kRelu; STATEMENT; } break;          \
-    case kGelu: { constexpr int ACT = kGelu; STATEMENT; } break;          \
-    case kGeluTanh: { constexpr int ACT = kGeluTanh; STATEMENT; } break;  \
-    case kSilu: { constexpr int ACT = kSilu; STATEMENT; } break;          \
-    default: { constexpr int ACT = kActNone; STATEMENT; } break;          \
+    case kRelu: { constexpr int ACT = kRelu; __VA_ARGS__; } break;          \
+    case kGelu: { constexpr int ACT = kGelu; __VA_ARGS__; } break;          \
+    case kGeluTanh: { constexpr int ACT = kGeluTanh; __VA_ARGS__; } break;  \
+    case kSilu: { constexpr int ACT = kSilu; __VA_ARGS__; } break;          \
+    default: { constexpr int ACT = kActNone; __VA_ARGS__; } break;          \
     }
 
 }  // namespace linear

@@ -8,12 +8,16 @@
 //        forward  features N from W (K-major),    tokens M from X (K-major)
 //        dgrad    features K from W (M-major),    tokens M from dY (K-major)
 //        wgrad    features K from X (M-major),    "tokens" N from dY (N-major)
+//    A gated layer's tile is 64 features: rows 0-63 are those of Wg, rows 64-127 the same ones of Wu, so the thread that
+//    joins a feature's sums finds both halves in the same shared memory.
 //  * A tile's contraction is split over the CTAs of a cluster, up to 16, so that there are one or two CTAs per
 //    SM even when there are 32 tiles.  Two fit per SM (under 113 KB of ring each), so their waits overlap.
 //  * The partial sums meet through distributed shared memory: each CTA puts its 128 x BN block in its own shared memory
 //    (the ring's, done with), and after a cluster barrier adds its share of the outputs over all ranks in rank
 //    order -- no workspace, no atomics, the same result every time.  Adding in the same place the operator is
 //    applied: four features of a token per thread, 8 or 16 bytes stored, bias and residual fetched before the barrier.
+//  * With block scales every K block is a product of its own: its accumulator, one of a ring that fills half of the
+//    TMEM, is scaled and added to the running sums by the four TMEM warps while the next blocks arrive.
 // Measured, cold L2, against the tile kernels: see the launch rule in linear_api.cu.
 #pragma once
 
@@ -38,6 +42,13 @@ struct ClusterParams : KernelParams {  // M: tokens, N: features of the output; 
     int64_t ldz;
     float* partials;     // dgrad: a row of `pitch` column sums per token tile; null: none
     int64_t pitch;
+    // As in TileParams.
+    const void* bias_up;
+    const float* x_scales;
+    const float* w_scales;
+    int64_t ld_xs, ld_ws;
+    int64_t up_scales;
+    uint32_t format_bits;
 };
 
 // Accumulators of a CTA.  A chain of products on one accumulator is no longer than the tile kernels' chunks (see there); a
@@ -46,7 +57,8 @@ struct ClusterParams : KernelParams {  // M: tokens, N: features of the output; 
 template <int BN>
 constexpr int kClusterAccs = 256 / BN;
 
-template <int BN>
+// SCALED: barriers for a ring of accumulators; COL_SETS: column sums per feature (gated dgrad: 2).
+template <int BN, bool SCALED = false, int COL_SETS = 1>
 struct ClusterSmem {
     static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 4 : 3;
     static constexpr int kABytes = kBM * kRowBytes;
@@ -55,8 +67,9 @@ struct ClusterSmem {
     static constexpr int kSumBytes = BN * kBM * 4;   // the partial sums, [token][feature], in the ring's place
     static constexpr int kColOff = kRing;            // dgrad: column sums, kColRows rows of 128 floats
     static constexpr int kColRows = BN >= 64 ? kClusterThreads / 32 : 0;
-    static constexpr int kBarOff = kColOff + kColRows * kBM * 4;
-    static constexpr int kNumBars = 2 * kStages + 2;  // full, empty, accumulator full, drain
+    static constexpr int kBarOff = kColOff + COL_SETS * kColRows * kBM * 4;
+    static constexpr int kAccBars = SCALED ? kClusterAccs<BN> : 1;
+    static constexpr int kNumBars = 2 * kStages + 2 * kAccBars + 1;  // full, empty, accumulators full and empty, drain
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kAlloc = kMiscOff + 16 + 1024;
     static_assert(kSumBytes <= kRing, "the sums fit the ring");
@@ -139,15 +152,30 @@ __device__ __forceinline__ void store4(uint16_t* row, int32_t c, int32_t n, cons
     }
 }
 
-// IN, OUT, MODE as linear_tile_kernel; BN: tokens per tile.  The cluster's size is the launch's.
-template <int BN, int IN, int OUT, int MODE>
+// Tensor maps of a launch: A the features' operand, B the tokens'; gated forward: A_up that of u.
+template <int MODE>
+struct ClusterMaps {
+    CUtensorMap A, B;
+};
+template <>
+struct ClusterMaps<kGlu> {
+    CUtensorMap A, B, A_up;
+};
+
+// IN, OUT, MODE, SCALED as linear_tile_kernel; BN: tokens per tile.  The cluster's size is the launch's.
+template <int BN, int IN, int OUT, int MODE, bool SCALED = false>
 __global__ void __launch_bounds__(kClusterThreads, 2)
-    linear_cluster_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const ClusterParams p)
+    linear_cluster_kernel(const __grid_constant__ ClusterMaps<MODE> maps, const ClusterParams p)
 {
     using T = Operand<IN>;
-    using L = ClusterSmem<BN>;
+    constexpr bool GLU = MODE == kGlu, GLU_DGRAD = MODE == kGluDgrad;
+    using L = ClusterSmem<BN, SCALED, GLU_DGRAD ? 2 : 1>;
     constexpr int STAGES = L::kStages;
-    constexpr bool AT = MODE != kForward;  // features' operand is M-major
+    constexpr bool AT = MODE != kForward && !GLU;  // features' operand is M-major
+    constexpr int kFeatures = GLU ? kBM / 2 : kBM;  // output features of a tile
+    constexpr int kGroups = kFeatures / 4;          // ... in groups of four
+    const CUtensorMap &tmA = maps.A, &tmB = maps.B;
+    static_assert(!SCALED || (IN == 2 && BN <= 64), "8-bit operands; the running sums are in registers");
     constexpr bool BT = MODE == kWgrad;    // tokens' operand is N-major
     constexpr bool kBf16 = OUT == kOutBf16;
     static_assert(!BT || BN % T::kNBlock == 0, "an N-major box is one 128-byte row");
@@ -160,7 +188,9 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     const uint32_t bar0 = base + L::kBarOff;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    const uint32_t acc_bar = bar0 + 8u * (2 * STAGES), drain_bar = acc_bar + 8u;
+    const uint32_t acc_bar = bar0 + 8u * (2 * STAGES);  // of the first accumulator
+    auto acce_bar = [&](int a) { return acc_bar + 8u * (L::kAccBars + a); };
+    const uint32_t drain_bar = acc_bar + 8u * (2 * L::kAccBars);
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int32_t* const abort_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 4);
 
@@ -171,7 +201,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     const uint32_t rank = ptx::cluster_ctarank();
     const uint32_t tile = blockIdx.x / ranks;
     const int32_t tf = static_cast<int32_t>(tile / p.tiles_t), tt = static_cast<int32_t>(tile - tf * p.tiles_t);
-    const int32_t f0 = tf * kBM, t0 = tt * BN;
+    const int32_t f0 = tf * kFeatures, t0 = tt * BN;
     // This CTA's K blocks.
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / ranks);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / ranks);
@@ -181,7 +211,10 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
             ptx::mbar_init(full_bar(s), 1);
             ptx::mbar_init(empty_bar(s), 1);
         }
-        ptx::mbar_init(acc_bar, 1);
+        for (int a = 0; a < L::kAccBars; ++a) {
+            ptx::mbar_init(acc_bar + 8u * a, 1);
+            ptx::mbar_init(acce_bar(a), 4);
+        }
         ptx::mbar_init(drain_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -204,19 +237,29 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     // This thread's share of the outputs: units of four features of a token, numbered token by token; this rank's are
     // [u0, u1), thread by thread.
     const int tokens = p.M - t0 < BN ? p.M - t0 : BN;
-    const int units = tokens * (kBM / 4);
+    const int units = tokens * kGroups;
     const int u0 = static_cast<int>(static_cast<int64_t>(units) * rank / ranks);
     const int u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / ranks);
-    const int32_t f = f0 + 4 * ((u0 + static_cast<int>(threadIdx.x)) & 31);  // the features of all of its units (32 divides 256)
-    // Residual, pre-activations or dW of one unit.
-    auto fetch_in = [&](int u, f32x2 (&x)[2]) {
-        x[0] = x[1] = 0;
+    const int32_t f = f0 + 4 * ((u0 + static_cast<int>(threadIdx.x)) & (kGroups - 1));  // the features of all of its units (kGroups divides 256)
+    // Residual, pre-activations or dW of one unit.  A gated layer's g is in x, its u in x[2], x[3].
+    constexpr int kIn = GLU_DGRAD ? 4 : 2;
+    auto fetch_in = [&](int u, f32x2 (&x)[kIn]) {
+#pragma unroll
+        for (int e = 0; e < kIn; ++e) x[e] = 0;
         if (!p.in || f >= p.N) return;
-        const int64_t t = t0 + (u >> 5);
+        const int64_t t = t0 + u / kGroups;
+        f32x2 four[2];
         if constexpr (OUT == kOutF32)
-            load4f(x, static_cast<const float*>(p.in) + t * p.ldin, f, p.N);
+            load4f(four, static_cast<const float*>(p.in) + t * p.ldin, f, p.N);
         else
-            load4<kBf16>(x, static_cast<const uint16_t*>(p.in) + t * p.ldin, f, p.N);
+            load4<kBf16>(four, static_cast<const uint16_t*>(p.in) + t * p.ldin, f, p.N);
+        x[0] = four[0];
+        x[1] = four[1];
+        if constexpr (GLU_DGRAD) {
+            load4<kBf16>(four, static_cast<const uint16_t*>(p.in) + t * p.ldin + p.N, f, p.N);
+            x[2] = four[0];
+            x[3] = four[1];
+        }
     };
 
     if (warp == kProducerWarp) {
@@ -240,6 +283,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
                             ptx::tma_load_2d(sa + q * (T::kStageK * 128), &tmA, f0 + q * T::kNBlock, k0, full_bar(stage));
                     } else {
                         ptx::tma_load_2d(sa, &tmA, k0, f0, full_bar(stage));
+                        if constexpr (GLU) ptx::tma_load_2d(sa + kFeatures * kRowBytes, &maps.A_up, k0, f0, full_bar(stage));
                     }
                     if constexpr (BT) {
 #pragma unroll
@@ -261,7 +305,8 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     } else if (warp == kMmaWarp) {
         if (lane == 0) {
             // ---------------------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc = idesc_mma<T::kFormat, BT, kBM, BN>() | (AT ? 1u << 15 : 0u);
+            uint32_t idesc = idesc_mma<T::kFormat, BT, kBM, BN>() | (AT ? 1u << 15 : 0u);
+            if constexpr (SCALED) idesc |= p.format_bits;
             int stage = 0;
             uint32_t phase = 0;
             bool aborted = false;
@@ -294,7 +339,18 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
             };
             // Mostly one chunk, in a loop of its own: a chunk's end as a condition in the K loop cost one token through
             // 4096 x 4096 0.17 us of 8.74, an outer loop over chunks alone 0.06, this 0.04.
-            if (__builtin_expect(kb1 - kb0 <= p.chunk_kb, 1)) {
+            if constexpr (SCALED) {
+                for (int kb = kb0; kb < kb1 && !aborted; ++kb) {
+                    const int i = kb - kb0, a = i % L::kAccBars;
+                    if (!wd.wait(acce_bar(a), ((i / L::kAccBars) & 1) ^ 1u, kRoleMma, tile, kb)) {
+                        aborted = true;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    chunk(kb, kb + 1, tmem_base + a * BN);
+                    if (!aborted) ptx::mma_commit_cta1(acc_bar + 8u * a);
+                }
+            } else if (__builtin_expect(kb1 - kb0 <= p.chunk_kb, 1)) {
                 chunk(kb0, kb1, tmem_base);
             } else {
                 uint32_t acc = tmem_base;
@@ -302,7 +358,7 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
                     chunk(c0, kb1 - c0 > p.chunk_kb ? c0 + p.chunk_kb : kb1, acc);
             }
             // The accumulator is complete -- or, after a wait that ran out, every MMA issued has finished.
-            ptx::mma_commit_cta1(aborted ? drain_bar : acc_bar);
+            if (aborted || !SCALED) ptx::mma_commit_cta1(aborted ? drain_bar : acc_bar);
             if (aborted) wd.drain(drain_bar, 0);
         }
         __syncwarp();
@@ -310,21 +366,29 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
 
     // Every thread fetches what its first two units need beside the sums while the product runs.
     const int u = u0 + static_cast<int>(threadIdx.x);
-    f32x2 bias[2] = {0, 0}, in0[2] = {0, 0}, in1[2] = {0, 0};
-    if (MODE == kForward && p.bias && u < u1 && f < p.N) {
+    f32x2 bias[2] = {0, 0}, in0[kIn] = {}, in1[kIn] = {};
+    [[maybe_unused]] f32x2 bias_up[2] = {0, 0};
+    auto fetch_bias = [&](f32x2 (&b)[2], const void* from) {
         if (p.bias_f32)
-            load4f(bias, static_cast<const float*>(p.bias), f, p.N);
+            load4f(b, static_cast<const float*>(from), f, p.N);
         else
-            load4<kBf16>(bias, static_cast<const uint16_t*>(p.bias), f, p.N);
+            load4<kBf16>(b, static_cast<const uint16_t*>(from), f, p.N);
+    };
+    if ((MODE == kForward || GLU) && p.bias && u < u1 && f < p.N) {
+        fetch_bias(bias, p.bias);
+        if constexpr (GLU) fetch_bias(bias_up, p.bias_up);
     }
-    if (u < u1) fetch_in(u, in0);
-    if (u + kClusterThreads < u1) fetch_in(u + kClusterThreads, in1);
+    if constexpr (!GLU) {
+        if (u < u1) fetch_in(u, in0);
+        if (u + kClusterThreads < u1) fetch_in(u + kClusterThreads, in1);
+    }
     __syncwarp();  // the lanes' shares end at different units; TMEM loads and the cluster's barrier take whole warps
 
     if (warp >= kClusterTmemWarp0 && warp < kClusterTmemWarp0 + 4) {
         // ---------------------------------------------------------------- accumulator -> shared memory
         const int quad = warp & 3;
-        const bool ok = __all_sync(0xFFFFFFFFu, kb0 == kb1 || wd.wait(acc_bar, 0, kRoleEpilogue, tile, -1));
+        bool ok = true;
+        if constexpr (!SCALED) ok = __all_sync(0xFFFFFFFFu, kb0 == kb1 || wd.wait(acc_bar, 0, kRoleEpilogue, tile, -1));
         ptx::tc_fence_after_sync();
         // All loads and MMAs of this CTA are done: the ring is free.
         const uint32_t sum = base + 4u * (quad * 32 + lane);
@@ -334,7 +398,59 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
 #pragma unroll
             for (int i = 0; i < kStep; ++i) st_shared_f32(sum + (c + i) * (kBM * 4), __uint_as_float(v[i]));
         };
-        if (__builtin_expect(kb1 - kb0 <= p.chunk_kb, 1)) {
+        if constexpr (SCALED) {
+            // Running sums of this lane's feature, for BN tokens.  The tokens' scales of a K block, each times the scale of
+            // the warp's weights, are held a token (or two) a lane and loaded a block ahead.
+            float s[BN];
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = 0.0f;
+            constexpr int kHeld = BN > 32 ? BN / 32 : 1;
+            // Rows of a tile lie inside one block of 128 (gated: of Wg in quadrants 0 and 1, of Wu in 2 and 3).
+            const float* const w_at =
+                p.w_scales ? p.w_scales + (f0 >> 7) * p.ld_ws + (GLU && quad >= 2 ? p.up_scales : 0) : nullptr;
+            float held[kHeld], next[kHeld];
+            auto load_scales = [&](int kb) {
+                const float w = w_at ? w_at[kb] : 1.0f;
+#pragma unroll
+                for (int e = 0; e < kHeld; ++e) {
+                    const int c = lane + 32 * e;
+                    next[e] = w * (p.x_scales && c < tokens ? p.x_scales[(t0 + static_cast<int64_t>(c)) * p.ld_xs + kb] : 1.0f);
+                }
+            };
+            if (kb0 < kb1) load_scales(kb0);
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                const int i = kb - kb0, a = i % L::kAccBars;
+#pragma unroll
+                for (int e = 0; e < kHeld; ++e) held[e] = next[e];
+                if (kb + 1 < kb1) load_scales(kb + 1);
+                ok = __all_sync(0xFFFFFFFFu, wd.wait(acc_bar + 8u * a, (i / L::kAccBars) & 1, kRoleEpilogue, tile, kb));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < BN; c += kStep) {
+                    uint32_t v[32];
+                    load_columns<kStep>(v, lanes + a * BN + c);
+                    if (c + kStep == BN) {
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(acce_bar(a));
+                    }
+#pragma unroll
+                    for (int e = 0; e < kStep; ++e)
+                        s[c + e] = fmaf(__uint_as_float(v[e]), __shfl_sync(0xFFFFFFFFu, held[(c + e) / 32], (c + e) & 31), s[c + e]);
+                }
+            }
+            if (ok) {
+#pragma unroll
+                for (int c = 0; c < BN; c += kStep)
+                    if (c < tokens) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int e = 0; e < kStep; ++e) v[e] = __float_as_uint(s[c + e]);
+                        leave(c, v);
+                    }
+            }
+        } else if (__builtin_expect(kb1 - kb0 <= p.chunk_kb, 1)) {
 #pragma unroll
             for (int c = 0; c < BN; c += kStep) {
                 uint32_t v[32];
@@ -367,11 +483,11 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
     ptx::cluster_sync();  // every rank's sums are in its shared memory
 
     // ---------------------------------------------------------------- join, operator, store
-    f32x2 col[2] = {0, 0};  // dgrad: sums of this thread's units
+    f32x2 col[kIn] = {};  // dgrad: sums of this thread's units
     // Unit i, whose sums are s.
-    auto finish = [&](int i, f32x2 (&s)[2], const f32x2 (&in)[2]) {
+    auto finish = [&](int i, f32x2 (&s)[2], const f32x2 (&in)[kIn]) {
         if (f >= p.N) return;
-        const int64_t t = t0 + (i >> 5);
+        const int64_t t = t0 + i / kGroups;
         const f32x2 alpha = both(p.alpha);
         if constexpr (MODE == kForward) {
             s[0] = fma2(alpha, s[0], bias[0]);
@@ -396,6 +512,24 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
             }
             col[0] = add2(col[0], s[0]);
             col[1] = add2(col[1], s[1]);
+        } else if constexpr (GLU_DGRAD) {
+            f32x2 du[2];
+            DTG_ACT_SWITCH(p.act, {
+                _Pragma("unroll") for (int e = 0; e < 2; ++e)
+                {
+                    const f32x2 d = mul2(alpha, s[e]);
+                    f32x2 value, slope;
+                    act_both2<ACT>(in[e], value, slope);
+                    s[e] = mul2(mul2(d, in[2 + e]), slope);
+                    du[e] = mul2(d, value);
+                }
+            });
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                col[e] = add2(col[e], s[e]);
+                col[2 + e] = add2(col[2 + e], du[e]);
+            }
+            store4<kBf16>(static_cast<uint16_t*>(p.C) + t * p.ldc + p.N, f, p.N, du);
         } else {
             s[0] = mul2(alpha, s[0]);
             s[1] = mul2(alpha, s[1]);
@@ -420,7 +554,51 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
             store4<kBf16>(static_cast<uint16_t*>(p.C) + t * p.ldc, f, p.N, s);
         }
     };
-    if (*abort_flag == 0) {
+    if constexpr (GLU) {
+        if (*abort_flag == 0) {
+            // One unit at a time: a token's sums are 32 groups of four, 16 of g and the same features' 16 of u.
+            for (int i = u; i < u1; i += kClusterThreads) {
+                f32x2 g[2] = {0, 0}, h[2] = {0, 0};
+                const uint32_t off = 16u * static_cast<uint32_t>((i / kGroups) * 2 * kGroups + i % kGroups);
+                for (uint32_t r0 = 0; r0 < ranks; r0 += 8) {
+                    float4 v[8], w[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r0 + r < ranks) {
+                            const uint32_t at = ptx::mapa_shared(base, r0 + r) + off;
+                            v[r] = ld_cluster_f4(at);
+                            w[r] = ld_cluster_f4(at + 16u * kGroups);
+                        }
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r0 + r < ranks) {
+                            g[0] = add2(g[0], pair(v[r].x, v[r].y));
+                            g[1] = add2(g[1], pair(v[r].z, v[r].w));
+                            h[0] = add2(h[0], pair(w[r].x, w[r].y));
+                            h[1] = add2(h[1], pair(w[r].z, w[r].w));
+                        }
+                }
+                if (f >= p.N) continue;
+                const int64_t t = t0 + i / kGroups;
+                const f32x2 alpha = both(p.alpha);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    g[e] = fma2(alpha, g[e], bias[e]);
+                    h[e] = fma2(alpha, h[e], bias_up[e]);
+                }
+                if (p.Z) {
+                    uint16_t* const z = static_cast<uint16_t*>(p.Z) + t * p.ldz;
+                    store4<kBf16>(z, f, p.N, g);
+                    store4<kBf16>(z + p.N, f, p.N, h);
+                }
+                DTG_ACT_SWITCH(p.act, {
+                    g[0] = mul2(act_value2<ACT>(g[0]), h[0]);
+                    g[1] = mul2(act_value2<ACT>(g[1]), h[1]);
+                });
+                store4<kBf16>(static_cast<uint16_t*>(p.C) + t * p.ldc, f, p.N, g);
+            }
+        }
+    } else if (*abort_flag == 0) {
         // Two units at a time, eight ranks' sums of each in flight, the inputs of the next two on their way.
         for (int i = u; i < u1; i += 2 * kClusterThreads) {
             const int j = i + kClusterThreads;
@@ -445,51 +623,64 @@ __global__ void __launch_bounds__(kClusterThreads, 2)
                         }
                     }
             }
-            f32x2 next0[2] = {0, 0}, next1[2] = {0, 0};
+            f32x2 next0[kIn] = {}, next1[kIn] = {};
             if (i + 2 * kClusterThreads < u1) fetch_in(i + 2 * kClusterThreads, next0);
             if (j + 2 * kClusterThreads < u1) fetch_in(j + 2 * kClusterThreads, next1);
             finish(i, s0, in0);
             if (j < u1) finish(j, s1, in1);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < kIn; ++e) {
                 in0[e] = next0[e];
                 in1[e] = next1[e];
             }
         }
     }
     __syncwarp();
-    if constexpr (MODE == kDgrad) {
+    constexpr int kColSets = MODE == kDgrad ? 1 : GLU_DGRAD ? 2 : 0;
+    if constexpr (kColSets > 0) {
         // Column sums of the tile: per thread over its units, then over the CTA's warps, then over the ranks, each in a
         // fixed order.
         float* const cols = reinterpret_cast<float*>(smem + L::kColOff);
         const int group = (u0 + static_cast<int>(threadIdx.x)) & 31;
-        *reinterpret_cast<f32x2*>(&cols[warp * kBM + 4 * group]) = col[0];
-        *reinterpret_cast<f32x2*>(&cols[warp * kBM + 4 * group + 2]) = col[1];
+#pragma unroll
+        for (int e = 0; e < kColSets; ++e) {
+            float* const set = cols + e * (L::kColRows * kBM);
+            *reinterpret_cast<f32x2*>(&set[warp * kBM + 4 * group]) = col[2 * e];
+            *reinterpret_cast<f32x2*>(&set[warp * kBM + 4 * group + 2]) = col[2 * e + 1];
+        }
         __syncthreads();
         if (threadIdx.x < kBM) {
-            float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < L::kColRows; ++w) s += cols[w * kBM + threadIdx.x];
-            cols[threadIdx.x] = s;  // read above by this thread alone
+            for (int e = 0; e < kColSets; ++e) {
+                float* const set = cols + e * (L::kColRows * kBM);
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < L::kColRows; ++w) s += set[w * kBM + threadIdx.x];
+                set[threadIdx.x] = s;  // read above by this thread alone
+            }
         }
     }
     __syncwarp();
     ptx::cluster_sync();  // no rank's shared memory is read any more (dgrad: the sums of every rank are ready)
-    if constexpr (MODE == kDgrad) {
+    if constexpr (kColSets > 0) {
         if (rank == 0 && p.partials && threadIdx.x < 32) {
-            float4 s = ld_cluster_f4(base + L::kColOff + 16u * threadIdx.x);
-            for (uint32_t r = 1; r < ranks; ++r) {
-                const float4 v = ld_cluster_f4(ptx::mapa_shared(base, r) + L::kColOff + 16u * threadIdx.x);
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
-            }
-            float* row = p.partials + static_cast<int64_t>(tt) * p.pitch + f0;
-            const float o[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (f0 + 4 * static_cast<int>(threadIdx.x) + e < p.N) row[4 * threadIdx.x + e] = o[e];
+            for (int e = 0; e < kColSets; ++e) {
+                const uint32_t at = L::kColOff + e * (L::kColRows * kBM * 4) + 16u * threadIdx.x;
+                float4 s = ld_cluster_f4(base + at);
+                for (uint32_t r = 1; r < ranks; ++r) {
+                    const float4 v = ld_cluster_f4(ptx::mapa_shared(base, r) + at);
+                    s.x += v.x;
+                    s.y += v.y;
+                    s.z += v.z;
+                    s.w += v.w;
+                }
+                float* row = p.partials + static_cast<int64_t>(tt) * p.pitch + e * static_cast<int64_t>(p.N) + f0;
+                const float o[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (f0 + 4 * static_cast<int>(threadIdx.x) + k < p.N) row[4 * threadIdx.x + k] = o[k];
+            }
         }
         __syncwarp();
         ptx::cluster_sync();

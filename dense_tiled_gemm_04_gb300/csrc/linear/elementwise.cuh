@@ -139,15 +139,19 @@ __global__ void __launch_bounds__(kActWarps * 32, 4) act_grad_kernel(const ActGr
 }
 
 // dbias[n] = beta * dbias[n] + the sum over `rows` partial sums of column n.  32 columns a block; warp w adds rows
-// w, w + 16, ..., sixteen of them in flight, and the warps' sums are added in warp order.
+// w, w + 16, ..., sixteen of them in flight, and the warps' sums are added in warp order.  Two vectors of one matrix of
+// partial sums go in one launch: the grid's second row takes `second`, whose sums start `offset` floats on.
 constexpr int kSumWarps = 16;
 
 __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float* partials, int64_t rows, int64_t pitch,
-                                                                    int64_t N, const BiasGrad b)
+                                                                    int64_t N, const BiasGrad first, const BiasGrad second,
+                                                                    int64_t offset)
 {
     __shared__ float sums[kSumWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n = blockIdx.x * int64_t(32) + lane;
+    const BiasGrad& b = blockIdx.y ? second : first;
+    partials += blockIdx.y * offset;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     float s = 0.0f;

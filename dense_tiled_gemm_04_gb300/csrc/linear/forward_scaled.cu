@@ -1,0 +1,11 @@
+// Forward products of 8-bit operands with block scales.
+#include "tile_set.cuh"
+
+namespace dtg {
+namespace linear {
+KernelChoice forward_scaled(int config, bool out_bf16)
+{
+    return out_bf16 ? scaled_choice<kOutBf16>(config) : scaled_choice<kOutF16>(config);
+}
+}  // namespace linear
+}  // namespace dtg

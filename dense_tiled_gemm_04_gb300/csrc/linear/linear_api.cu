@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "api_common.cuh"
 #include "cluster_set.cuh"
 #include "elementwise.cuh"
 #include "gemm.h"
@@ -15,86 +16,36 @@
 using namespace dtg::host;
 using dtg::KernelChoice;
 
+namespace dtg {
+namespace host {
+
+static linear::BiasGrad bias_grad(const SumVector& v)
+{
+    return {v.to, v.type == GEMM_DTYPE_F32 ? linear::kOutF32 : (v.type == GEMM_DTYPE_BF16 ? linear::kOutBf16 : linear::kOutF16), v.beta};
+}
+
+gemm_status_t launch_sums(const float* partials, int64_t rows, int64_t cols, const SumVector& first, const SumVector& second,
+                          int64_t offset, cudaStream_t s)
+{
+    const bool both = first.to && second.to;
+    if (!first.to && !second.to) return GEMM_OK;
+    if (!first.to) partials += offset;
+    return launch_after(&linear::column_sum_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32)), both ? 2 : 1), dim3(32 * linear::kSumWarps),
+                        0, s, partials, rows, sum_pitch(cols), cols, bias_grad(first.to ? first : second), bias_grad(second), offset);
+}
+
+}  // namespace host
+}  // namespace dtg
+
 namespace {
-
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 512;  // the edges of the last tiles still fit 32 bits
-constexpr int64_t kSumRows = 32;   // rows of a partial column sum
-constexpr int64_t kSumAlign = 64;  // its row pitch is a multiple of this many columns
-
-bool is_16bit(gemm_dtype_t t) { return t == GEMM_DTYPE_F16 || t == GEMM_DTYPE_BF16; }
-bool is_act(gemm_act_t a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_SILU; }
-int bytes_of(gemm_dtype_t t) { return t == GEMM_DTYPE_F32 ? 4 : elem_bytes(t); }
-
-// A matrix argument of `cols` > 0 elements per row: null or too small a pitch is INVALID_ARG, a
-// base or pitch that is not a multiple of 16 bytes UNSUPPORTED.
-gemm_status_t check_matrix(const void* p, int64_t cols, int64_t ld, gemm_dtype_t t)
-{
-    if (!p || ld < cols) return GEMM_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0 || (ld & (16 / bytes_of(t) - 1)) != 0) return GEMM_ERR_UNSUPPORTED;
-    return GEMM_OK;
-}
-
-// INVALID_ARG outranks UNSUPPORTED, whatever the order of the arguments.
-struct Checks {
-    gemm_status_t st = GEMM_OK;
-    void add(gemm_status_t s)
-    {
-        if (s == GEMM_ERR_INVALID_ARG || st == GEMM_OK) st = s;
-    }
-    void matrix(const void* p, int64_t cols, int64_t ld, gemm_dtype_t t) { add(check_matrix(p, cols, ld, t)); }
-    void vector(const void* p, gemm_dtype_t t)
-    {
-        if ((reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes_of(t) - 1)) != 0) add(GEMM_ERR_UNSUPPORTED);
-    }
-};
-
-// Column sums: dbias's type and address, and the workspace for M x cols.
-void check_sums(Checks& c, const void* dbias, gemm_dtype_t t, const void* ws, int64_t ws_bytes, int64_t M, int64_t cols)
-{
-    if (!dbias) return;
-    c.vector(dbias, t);
-    const int64_t need = gemm_bias_grad_workspace_bytes(M, cols);
-    if (!ws && need <= GEMM_OWN_SUMS_BYTES) return;  // the handle's
-    if (!ws || ws_bytes < need)
-        c.add(GEMM_ERR_INVALID_ARG);
-    else if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0)
-        c.add(GEMM_ERR_UNSUPPORTED);
-}
-
-int64_t sum_pitch(int64_t cols) { return cdiv(cols, kSumAlign) * kSumAlign; }
-
-// Kernels that start while the stream's previous kernel finishes (they wait for it themselves).
-template <class... P, class... A>
-gemm_status_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args)
-{
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
-}
 
 // Where a call's partial column sums go: the caller's workspace, or the handle's.
 float* sums_of(gemm_handle_t h, void* workspace) { return workspace ? static_cast<float*>(workspace) : h->sums; }
 
-dtg::linear::BiasGrad bias_grad(void* dbias, gemm_dtype_t t, float beta)
-{
-    return {dbias, t == GEMM_DTYPE_F32 ? dtg::linear::kOutF32 : (t == GEMM_DTYPE_BF16 ? dtg::linear::kOutBf16 : dtg::linear::kOutF16),
-            beta};
-}
-
 // The bias gradient from `rows` rows of partial sums.
-gemm_status_t launch_sums(const float* partials, int64_t rows, int64_t cols, const dtg::linear::BiasGrad& b, cudaStream_t s)
+gemm_status_t bias_sums(const float* partials, int64_t rows, int64_t cols, void* dbias, gemm_dtype_t t, float beta, cudaStream_t s)
 {
-    return launch_after(&dtg::linear::column_sum_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32))), dim3(32 * dtg::linear::kSumWarps), 0, s, partials,
-                        rows, sum_pitch(cols), cols, b);
+    return launch_sums(partials, rows, cols, {dbias, t, beta}, {nullptr, t, beta}, 0, s);
 }
 
 // One product: rows x cols over `depth`, as linear_tile_kernel names them.
@@ -115,7 +66,14 @@ struct Product {
     void* Z;
     int64_t ldz;
     float* partials;
+    // Gated layers: the weights of u and their biases.  8-bit operands with block scales: scaled, and the scales (null: 1).
+    const void *B_up, *bias_up;
+    bool scaled;
+    const float *x_scales, *w_scales;
+    int64_t ld_xs, ld_ws, up_scales;
 };
+
+bool gated(const Product& q) { return q.mode == dtg::linear::kGlu || q.mode == dtg::linear::kGluDgrad; }
 
 // K blocks per accumulation on one tensor-core accumulator, which truncates: a chain of K blocks loses about 1.2e-9 of
 // its sum per product (see tile_kernel.cuh).  Where an fp32 result is wanted, 12 blocks of 64 keep that under 1e-6.  A
@@ -125,15 +83,18 @@ constexpr int64_t kChunkBlocks = 12, kLongChunkBlocks = 128;
 
 bool fp32_result(const Product& q) { return q.out == GEMM_DTYPE_F32 || q.partials; }
 int64_t k_blocks(const Product& q) { return cdiv(q.depth, is_f8(q.in) ? 128 : 64); }
-int64_t chunk_limit(const Product& q) { return fp32_result(q) ? kChunkBlocks : kLongChunkBlocks; }
+int64_t chunk_limit(const Product& q) { return q.scaled ? 1 : fp32_result(q) ? kChunkBlocks : kLongChunkBlocks; }
 
 // Whether a product takes the tile kernel that sums chunks in registers.
-bool summed(const Product& q) { return fp32_result(q) || k_blocks(q) > kLongChunkBlocks; }
+bool summed(const Product& q) { return fp32_result(q) || q.scaled || k_blocks(q) > kLongChunkBlocks; }
 
 KernelChoice tile_kernel(const Product& q, int config)
 {
     using namespace dtg::linear;
     const bool bf16 = q.out == GEMM_DTYPE_BF16, sums = summed(q);
+    if (q.mode == kGlu) return q.scaled ? glu_scaled(config, bf16) : glu_16(config, bf16, sums);
+    if (q.mode == kGluDgrad) return bf16 ? glu_dgrad_bf16(config, sums) : glu_dgrad_f16(config, sums);
+    if (q.scaled) return forward_scaled(config, bf16);
     if (q.mode == kDgrad) return bf16 ? dgrad_bf16(config, sums) : dgrad_f16(config, sums);
     if (q.mode == kWgrad) {
         const bool f32 = q.out == GEMM_DTYPE_F32;
@@ -148,23 +109,30 @@ KernelChoice tile_kernel(const Product& q, int config)
     }
 }
 
-// One of 14 operators and types, for the launch-state slots.
+// One of kLinearOperators operators and types, for the launch-state slots.
 int operator_index(const Product& q)
 {
+    const int bf16 = q.out == GEMM_DTYPE_BF16;
+    if (q.mode == dtg::linear::kGlu) return 14 + 2 * q.scaled + bf16;
+    if (q.mode == dtg::linear::kGluDgrad) return 18 + 2 * q.in + (q.partials != nullptr);
+    if (q.scaled) return 22 + bf16;
     if (q.mode == dtg::linear::kForward)
-        return is_f8(q.in) ? 2 + 2 * (q.in - GEMM_DTYPE_E4M3) + (q.out == GEMM_DTYPE_BF16) : q.in;
+        return is_f8(q.in) ? 2 + 2 * (q.in - GEMM_DTYPE_E4M3) + bf16 : q.in;
     if (q.mode == dtg::linear::kDgrad) return 6 + 2 * q.in + (q.partials != nullptr);
     return 10 + 2 * q.in + (q.out == GEMM_DTYPE_F32);
 }
 
-// One of 22 tile kernels of a configuration: forward 6 types x summed or not, dgrad 2 x 2, wgrad 2 x (16-bit, fp32, 16-bit
-// summed).
+// One of kLinearTileKernels tile kernels of a configuration: forward 6 types x summed or not, dgrad 2 x 2, wgrad 2 x (16-bit,
+// fp32, 16-bit summed), gated 2 x 2 and two with scales, gated dgrad 2 x 2, two forward with scales.
 int tile_slot(const Product& q, int config)
 {
-    const int sums = summed(q);
-    const int kernel = q.mode == dtg::linear::kForward  ? 2 * operator_index(q) + sums
-                       : q.mode == dtg::linear::kDgrad ? 12 + 2 * q.in + sums
-                                                       : 16 + 3 * q.in + (q.out == GEMM_DTYPE_F32 ? 1 : 2 * sums);
+    const int sums = summed(q), bf16 = q.out == GEMM_DTYPE_BF16;
+    const int kernel = q.mode == dtg::linear::kGlu       ? (q.scaled ? 26 + bf16 : 22 + 2 * q.in + sums)
+                       : q.mode == dtg::linear::kGluDgrad ? 28 + 2 * q.in + sums
+                       : q.scaled                        ? 32 + bf16
+                       : q.mode == dtg::linear::kForward ? 2 * operator_index(q) + sums
+                       : q.mode == dtg::linear::kDgrad   ? 12 + 2 * q.in + sums
+                                                         : 16 + 3 * q.in + (q.out == GEMM_DTYPE_F32 ? 1 : 2 * sums);
     return kLinearSlot0 + 3 * kernel + (config - 1);
 }
 
@@ -185,6 +153,9 @@ KernelChoice cluster_kernel(const Product& q, int tokens)
 {
     using namespace dtg::linear;
     const bool bf16 = q.out == GEMM_DTYPE_BF16;
+    if (q.mode == kGlu) return q.scaled ? cluster_glu_scaled(tokens, bf16) : cluster_glu_16(tokens, bf16);
+    if (q.mode == kGluDgrad) return cluster_glu_dgrad(bf16);
+    if (q.scaled) return cluster_scaled(tokens, bf16);
     if (q.mode == kDgrad) return cluster_dgrad(tokens, bf16);
     if (q.mode == kWgrad) return cluster_wgrad(q.in == GEMM_DTYPE_BF16, q.out == GEMM_DTYPE_F32);
     return is_f8(q.in) ? cluster_forward_8(tokens, q.in == GEMM_DTYPE_E5M2, bf16) : cluster_forward_16(tokens, bf16);
@@ -222,7 +193,7 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
     if (o.config != GEMM_CONFIG_AUTO || q.depth == 0) return GEMM_OK;
     const int64_t kb = k_blocks(q);
     int tokens = q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : q.rows <= 64 ? 64 : 128;
-    if (q.mode == dtg::linear::kDgrad && tokens < 64) tokens = 64;
+    if ((q.mode == dtg::linear::kDgrad || q.mode == dtg::linear::kGluDgrad) && tokens < 64) tokens = 64;
     if (q.mode == dtg::linear::kWgrad) tokens = 128;
     // Where the tile kernels would leave SMs idle: on fewer than 128 tokens, whose narrower tiles are the cheaper ones
     // (8 x 8192 x 1024: 7.1 us, 10.6 on 128 x 128 tiles); and, in tiles of 128 tokens as large as theirs, where a
@@ -230,14 +201,16 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
     // 1024 x 1024: 5.8 us, 9.5 whole; 128 x 4096 x 4096: 12.1, 14.1 in 128).  Up to a tile per SM it does with more
     // than 16 K blocks (256 x 8192 x 8192: 37.8 us, 40.8 whole; but 2048 x 1024 x 1024: 12.3, 10.0 whole).  More
     // tiles are not split (512 x 8192 x 8192: 65 us, 47 on CTA pairs).
-    int64_t tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
+    const int64_t features = q.mode == dtg::linear::kGlu ? dtg::kBM / 2 : dtg::kBM;
+    int64_t tiles = cdiv(q.cols, features) * cdiv(q.rows, tokens);
     const int64_t slots = 2 * dev.num_sms;
     if (tokens == 128) {
         const bool few = 4 * tiles <= dev.num_sms;
         if (!few && (tiles > dev.num_sms || kb <= 16)) return GEMM_OK;
-        if (few && q.mode != dtg::linear::kWgrad) {
+        // (Gated and scaled kernels have 64 tokens at most.)
+        if ((few && q.mode != dtg::linear::kWgrad) || gated(q) || q.scaled) {
             tokens = 64;
-            tiles = cdiv(q.cols, dtg::kBM) * cdiv(q.rows, tokens);
+            tiles = cdiv(q.cols, features) * cdiv(q.rows, tokens);
         }
     }
     if (tiles > slots) return GEMM_OK;
@@ -258,11 +231,26 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
     if (st != GEMM_OK) return st;
     // Chains of products no longer than the tile kernels', on as many accumulators as there are.
     const int64_t blocks = cdiv(kb, 1 << log), chunks = cdiv(blocks, chunk_limit(q));
-    if (chunks > 256 / tokens) return GEMM_OK;
+    if (chunks > 256 / tokens && !q.scaled) return GEMM_OK;  // (scaled: a ring of accumulators)
     c->chunk_kb = static_cast<int32_t>(cdiv(blocks, chunks));
     c->tokens = tokens;
     c->ranks = 1 << log;
     return GEMM_OK;
+}
+
+// The row pitch of a product's partial column sums (gated dgrad: of both halves).
+int64_t sum_columns(const Product& q) { return sum_pitch(q.mode == dtg::linear::kGluDgrad ? 2 * q.cols : q.cols); }
+
+template <class P>
+void set_gated_and_scaled(P& p, const Product& q)
+{
+    p.bias_up = q.bias_up;
+    p.x_scales = q.x_scales;
+    p.w_scales = q.w_scales;
+    p.ld_xs = q.ld_xs;
+    p.ld_ws = q.ld_ws;
+    p.up_scales = q.up_scales;
+    p.format_bits = q.in == GEMM_DTYPE_E5M2 ? (1u << 7) | (1u << 10) : 0u;  // of A and of B
 }
 
 gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPlan& plan, int64_t* sum_rows, cudaStream_t stream)
@@ -272,13 +260,16 @@ gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPla
     const uint64_t eb = static_cast<uint64_t>(elem_bytes(q.in));
     const uint32_t sk = static_cast<uint32_t>(kc.stage_k), nb = static_cast<uint32_t>(kc.n_block);
     // The features' operand is B (its rows are the output's columns), the tokens' is A.
-    CUtensorMap tF, tT;
-    if (!(q.mode == kForward ? get_tmap(nullptr, q.B, q.depth, q.cols, q.ldb * eb, sk, dtg::kBM, q.in, &tF)
-                             : get_tmap(nullptr, q.B, q.cols, q.depth, q.ldb * eb, nb, sk, q.in, &tF)) ||
+    ClusterMaps<kGlu> maps;  // (the others' begins alike)
+    CUtensorMap &tF = maps.A, &tT = maps.B;
+    const uint32_t features = static_cast<uint32_t>(kc.bn);
+    if (!(q.mode == kForward || q.mode == kGlu ? get_tmap(nullptr, q.B, q.depth, q.cols, q.ldb * eb, sk, features, q.in, &tF)
+                                               : get_tmap(nullptr, q.B, q.cols, q.depth, q.ldb * eb, nb, sk, q.in, &tF)) ||
+        (q.mode == kGlu && !get_tmap(nullptr, q.B_up, q.depth, q.cols, q.ldb * eb, sk, features, q.in, &maps.A_up)) ||
         !(q.mode == kWgrad ? get_tmap(nullptr, q.A, q.rows, q.depth, q.lda * eb, nb, sk, q.in, &tT)
                            : get_tmap(nullptr, q.A, q.depth, q.rows, q.lda * eb, sk, static_cast<uint32_t>(plan.tokens), q.in, &tT)))
         return GEMM_ERR_CUDA;
-    const int64_t tiles_t = cdiv(q.rows, plan.tokens), tiles_f = cdiv(q.cols, dtg::kBM);
+    const int64_t tiles_t = cdiv(q.rows, plan.tokens), tiles_f = cdiv(q.cols, kc.bn);
     const int64_t grid = tiles_t * tiles_f * plan.ranks;
     if (sum_rows) *sum_rows = tiles_t;
     ClusterParams p;
@@ -304,8 +295,9 @@ gemm_status_t launch_cluster(gemm_handle_t h, const Product& q, const ClusterPla
     p.Z = q.Z;
     p.ldz = q.ldz;
     p.partials = q.partials;
-    p.pitch = sum_pitch(q.cols);
-    void* args[] = {&tF, &tT, &p};
+    p.pitch = sum_columns(q);
+    set_gated_and_scaled(p, q);
+    void* args[] = {&maps, &p};
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -333,11 +325,14 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     if (planned != GEMM_OK) return planned;
     if (few.tokens) return launch_cluster(h, q, few, sum_rows, stream);
     if (sum_rows) *sum_rows = cdiv(q.rows, kSumRows);
-    int config = pick_config(o, h->dev, q.rows, q.cols, q.depth);
+    // Columns of accumulators: a gated tile has 128 of each half, however few of them the output has.
+    const int64_t cols = q.mode == dtg::linear::kGlu ? 256 * cdiv(q.cols, 128) : q.cols;
+    int config = pick_config(o, h->dev, q.rows, cols, q.depth);
     if (config == GEMM_CONFIG_128x64) config = GEMM_CONFIG_128x128;
+    if (gated(q) && config == GEMM_CONFIG_128x128) config = GEMM_CONFIG_128x256;
     // CTA pairs from 2/5 of a tile per SM on, where gemm_run asks for 1/2: on 64 pair tiles 512 x 8192 x 8192 takes 46.8
     // us against 57.7 in 128 x 256 tiles, 1024 x 4096 x 4096 27.0 and 30.7; on 32 256 x 8192 x 8192 46.2 and 40.8.
-    if (o.config == GEMM_CONFIG_AUTO && cdiv(q.rows, 256) * cdiv(q.cols, 256) * 5 >= 2 * h->dev.num_sms)
+    if (o.config == GEMM_CONFIG_AUTO && cdiv(q.rows, 256) * cdiv(cols, 256) * 5 >= 2 * h->dev.num_sms)
         config = GEMM_CONFIG_256x256;
     const KernelChoice kc = tile_kernel(q, config);
     const int slot = tile_slot(q, kc.config);
@@ -351,7 +346,8 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     const gemm_status_t ready = ensure_kernel_ready(h->dev, kc, slot);
     if (ready != GEMM_OK) return ready;
     gemm_plan_t plan;
-    fill_plan(o, h->dev, h->dev.max_clusters[slot], &h->ws, q.rows, q.cols, q.depth, kc, kDense, &plan);
+    // (Gated kernels take whole tiles only.)
+    fill_plan(o, h->dev, h->dev.max_clusters[slot], gated(q) ? nullptr : &h->ws, q.rows, cols, q.depth, kc, kDense, &plan);
     // Sharing out the K blocks of the last tiles (stream-K) pays when the units that a last wave of whole tiles would
     // leave idle are worth more K blocks than the joins cost, about 56 blocks of a 256-wide 16-bit tile (16384 x 1024
     // x 8192 forward, 81 blocks a tile: 166 us shared, 174 whole; dgrad of the same, 1 block: 311 and 294).  Between
@@ -375,21 +371,32 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     const uint64_t eb = static_cast<uint64_t>(elem_bytes(q.in));
     const uint32_t sk = static_cast<uint32_t>(kc.stage_k), nb = static_cast<uint32_t>(kc.n_block);
     const uint64_t oe = static_cast<uint64_t>(bytes_of(q.out));
-    CUtensorMap tA, tB, tC, tZ;
-    if (!get_tmap(nullptr, q.C, q.cols, q.rows, q.ldc * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tC))
-        return GEMM_ERR_CUDA;
-    tA = tB = tZ = tC;  // those that are not used name a valid tensor
-    if (q.Z && !get_tmap(nullptr, q.Z, q.cols, q.rows, q.ldz * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tZ))
-        return GEMM_ERR_CUDA;
-    if (q.mode == dtg::linear::kDgrad && q.src &&  // the boxes of pre-activations: those of the output
-        !get_tmap(nullptr, q.src, q.cols, q.rows, q.ldsrc * oe, static_cast<uint32_t>(128 / oe), 32, q.out, &tZ))
+    dtg::linear::TileMaps<dtg::linear::kGlu> maps;  // (the others' begin alike; gated dgrad's has the same six)
+    CUtensorMap &tA = maps.A, &tB = maps.B, &tC = maps.C, &tZ = maps.Z, &t5 = maps.B_up, &t6 = maps.Z_up;
+    const auto out_map = [&](const void* at, int64_t ld, CUtensorMap* map) {
+        // Boxes of the output and of what is read or kept beside it; gated dgrad's are half as wide.
+        const bool half = q.mode == dtg::linear::kGluDgrad;
+        return get_tmap(nullptr, at, q.cols, q.rows, ld * oe, static_cast<uint32_t>((half ? 64 : 128) / oe), 32, q.out, map,
+                        half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    const auto up = [&](const void* at) { return static_cast<const uint16_t*>(at) + q.cols; };  // the other half of g, u
+    if (!out_map(q.C, q.ldc, &tC)) return GEMM_ERR_CUDA;
+    tA = tB = tZ = t5 = t6 = tC;  // those that are not used name a valid tensor
+    if (q.Z && !out_map(q.Z, q.ldz, &tZ)) return GEMM_ERR_CUDA;
+    if (q.mode == dtg::linear::kGlu && q.Z && !out_map(up(q.Z), q.ldz, &t6)) return GEMM_ERR_CUDA;
+    if (q.mode == dtg::linear::kDgrad && q.src && !out_map(q.src, q.ldsrc, &tZ)) return GEMM_ERR_CUDA;  // pre-activations
+    if (q.mode == dtg::linear::kGluDgrad &&
+        (!out_map(q.src, q.ldsrc, &tZ) || !out_map(up(q.src), q.ldsrc, &t6) || !out_map(up(q.C), q.ldc, &t5)))
         return GEMM_ERR_CUDA;
     if (q.depth > 0) {
-        const bool at = q.mode == dtg::linear::kWgrad, bt = q.mode != dtg::linear::kForward;
+        const bool at = q.mode == dtg::linear::kWgrad, bt = q.mode != dtg::linear::kForward && q.mode != dtg::linear::kGlu;
+        const uint32_t b_box = q.mode == dtg::linear::kGlu ? 128u : static_cast<uint32_t>(kc.b_box);
         if (!(at ? get_tmap(nullptr, q.A, q.rows, q.depth, q.lda * eb, nb, sk, q.in, &tA)
                  : get_tmap(nullptr, q.A, q.depth, q.rows, q.lda * eb, sk, dtg::kBM, q.in, &tA)) ||
             !(bt ? get_tmap(nullptr, q.B, q.cols, q.depth, q.ldb * eb, nb, sk, q.in, &tB)
-                 : get_tmap(nullptr, q.B, q.depth, q.cols, q.ldb * eb, sk, static_cast<uint32_t>(kc.b_box), q.in, &tB)))
+                 : get_tmap(nullptr, q.B, q.depth, q.cols, q.ldb * eb, sk, b_box, q.in, &tB)))
+            return GEMM_ERR_CUDA;
+        if (q.mode == dtg::linear::kGlu && !get_tmap(nullptr, q.B_up, q.depth, q.cols, q.ldb * eb, sk, b_box, q.in, &t5))
             return GEMM_ERR_CUDA;
     }
 
@@ -428,9 +435,10 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     p.Z = q.Z;
     p.ldz = q.ldz;
     p.partials = q.partials;
-    p.pitch = sum_pitch(q.cols);
+    p.pitch = sum_columns(q);
+    set_gated_and_scaled(p, q);
 
-    void* args[] = {&tA, &tB, &tC, &tZ, &p};
+    void* args[] = {&maps, &p};
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(plan.grid), 1, 1);
@@ -461,21 +469,22 @@ gemm_status_t launch_act_grad(const dtg::linear::ActGradParams& p, gemm_act_t ac
     return launch_after(fn, grid, dim3(kActWarps * 32), 0, s, p);
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t gemm_bias_grad_workspace_bytes(int64_t M, int64_t cols)
+// Block scales of a contraction of K > 0: fp32, at least ceil(K / 128) a row; null: 1.
+void check_scales(Checks& c, int64_t K, const float* xs, int64_t ld_xs, const float* ws, int64_t ld_ws)
 {
-    if (M <= 0 || cols <= 0) return 0;
-    return 4 * cdiv(M, kSumRows) * sum_pitch(cols);
+    const int64_t blocks = cdiv(K, kScaleBlock);
+    if ((xs && ld_xs < blocks) || (ws && ld_ws < blocks)) c.add(GEMM_ERR_INVALID_ARG);
+    if (xs) c.vector(xs, GEMM_DTYPE_F32);
+    if (ws) c.vector(ws, GEMM_DTYPE_F32);
 }
 
-gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, void* stream)
+// gemm_run_linear, and with `scaled` gemm_run_linear_scaled.
+gemm_status_t run_forward(gemm_handle_t h, const gemm_linear_args_t* args, bool scaled, const float* x_scales, int64_t ld_xs,
+                          const float* w_scales, int64_t ld_ws, void* stream)
 {
     if (!h || !args) return GEMM_ERR_INVALID_ARG;
     const gemm_linear_args_t& a = *args;
-    if (!is_16bit(a.dtype) && !is_f8(a.dtype)) return GEMM_ERR_INVALID_ARG;
+    if ((scaled || !is_16bit(a.dtype)) && !is_f8(a.dtype)) return GEMM_ERR_INVALID_ARG;
     if (!is_16bit(a.out_dtype) || (is_16bit(a.dtype) && a.out_dtype != a.dtype)) return GEMM_ERR_INVALID_ARG;
     if (!is_act(a.act) || !std::isfinite(a.alpha)) return GEMM_ERR_INVALID_ARG;
     if (a.M < 0 || a.N < 0 || a.K < 0) return GEMM_ERR_INVALID_ARG;
@@ -491,6 +500,7 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, v
     if (a.bias) c.vector(a.bias, a.bias_dtype);
     if (a.residual) c.matrix(a.residual, a.N, a.ldr, a.out_dtype);
     if (a.Z) c.matrix(a.Z, a.N, a.ldz, a.out_dtype);
+    if (scaled && a.K > 0) check_scales(c, a.K, x_scales, ld_xs, w_scales, ld_ws);
     if (c.st != GEMM_OK) return c.st;
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
@@ -515,7 +525,143 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, v
     q.ldsrc = a.ldr;
     q.Z = a.Z;
     q.ldz = a.ldz;
+    if (scaled) {
+        q.scaled = true;
+        q.x_scales = x_scales;
+        q.ld_xs = ld_xs;
+        q.w_scales = w_scales;
+        q.ld_ws = ld_ws;
+    }
     return launch_product(h, q, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_bias_grad_workspace_bytes(int64_t M, int64_t cols)
+{
+    if (M <= 0 || cols <= 0) return 0;
+    return 4 * cdiv(M, kSumRows) * sum_pitch(cols);
+}
+
+gemm_status_t gemm_run_linear(gemm_handle_t h, const gemm_linear_args_t* args, void* stream)
+{
+    return run_forward(h, args, false, nullptr, 0, nullptr, 0, stream);
+}
+
+gemm_status_t gemm_run_linear_scaled(gemm_handle_t h, const gemm_linear_args_t* args, const float* x_scales, int64_t ld_xs,
+                                     const float* w_scales, int64_t ld_ws, void* stream)
+{
+    return run_forward(h, args, true, x_scales, ld_xs, w_scales, ld_ws, stream);
+}
+
+gemm_status_t gemm_run_linear_glu(gemm_handle_t h, const gemm_glu_args_t* args, void* stream)
+{
+    if (!h || !args) return GEMM_ERR_INVALID_ARG;
+    const gemm_glu_args_t& a = *args;
+    if (!is_16bit(a.dtype) && !is_f8(a.dtype)) return GEMM_ERR_INVALID_ARG;
+    if (!is_16bit(a.out_dtype) || (is_16bit(a.dtype) && a.out_dtype != a.dtype)) return GEMM_ERR_INVALID_ARG;
+    if (!is_act(a.act) || !std::isfinite(a.alpha)) return GEMM_ERR_INVALID_ARG;
+    if (a.M < 0 || a.N < 0 || a.K < 0) return GEMM_ERR_INVALID_ARG;
+    if (a.bias && a.bias_dtype != GEMM_DTYPE_F32 && a.bias_dtype != a.out_dtype) return GEMM_ERR_INVALID_ARG;
+    if (is_16bit(a.dtype) && (a.x_scales || a.w_scales)) return GEMM_ERR_INVALID_ARG;
+    if (a.M == 0 || a.N == 0) return GEMM_OK;
+    Checks c;
+    if (a.M > kMaxDim || a.N > kMaxDim / 2 || a.K > kMaxDim) c.add(GEMM_ERR_UNSUPPORTED);
+    if (a.K > 0) {
+        c.matrix(a.X, a.K, a.ldx, a.dtype);
+        c.matrix(a.W, a.K, a.ldw, a.dtype);
+        check_scales(c, a.K, a.x_scales, a.ld_xs, a.w_scales, a.ld_ws);
+    }
+    c.matrix(a.H, a.N, a.ldh, a.out_dtype);
+    if (a.bias) c.vector(a.bias, a.bias_dtype);
+    if (a.Z) {
+        c.matrix(a.Z, 2 * a.N, a.ldz, a.out_dtype);
+        if (a.N % 8 != 0) c.add(GEMM_ERR_UNSUPPORTED);
+    }
+    if (c.st != GEMM_OK) return c.st;
+    DeviceGuard g(h->device);
+    if (!g.ok) return GEMM_ERR_CUDA;
+    Product q = {};
+    q.mode = dtg::linear::kGlu;
+    q.in = a.dtype;
+    q.out = a.out_dtype;
+    q.rows = a.M;
+    q.cols = a.N;
+    q.depth = a.K;
+    q.A = a.X;
+    q.lda = a.ldx;
+    q.B = a.W;
+    q.B_up = static_cast<const uint8_t*>(a.W) + a.N * a.ldw * elem_bytes(a.dtype);
+    q.ldb = a.ldw;
+    q.C = a.H;
+    q.ldc = a.ldh;
+    q.alpha = a.alpha;
+    q.act = a.act;
+    q.bias = a.bias;
+    q.bias_dtype = a.bias_dtype;
+    if (a.bias) q.bias_up = static_cast<const uint8_t*>(a.bias) + a.N * bytes_of(a.bias_dtype);
+    q.Z = a.Z;
+    q.ldz = a.ldz;
+    q.scaled = is_f8(a.dtype);  // (absent scales are 1)
+    q.x_scales = a.x_scales;
+    q.ld_xs = a.ld_xs;
+    q.w_scales = a.w_scales;
+    q.ld_ws = a.ld_ws;
+    q.up_scales = cdiv(a.N, kScaleBlock) * a.ld_ws;
+    return launch_product(h, q, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_run_linear_glu_dgrad(gemm_handle_t h, const gemm_glu_dgrad_args_t* args, void* stream)
+{
+    if (!h || !args) return GEMM_ERR_INVALID_ARG;
+    const gemm_glu_dgrad_args_t& a = *args;
+    if (!is_16bit(a.dtype) || !is_act(a.act) || !std::isfinite(a.alpha) || !std::isfinite(a.beta_bias))
+        return GEMM_ERR_INVALID_ARG;
+    if (a.M < 0 || a.N < 0 || a.K < 0) return GEMM_ERR_INVALID_ARG;
+    if (a.dbias && a.dbias_dtype != GEMM_DTYPE_F32 && a.dbias_dtype != a.dtype) return GEMM_ERR_INVALID_ARG;
+    if (a.N == 0) return GEMM_OK;
+    Checks c;
+    if (a.M > kMaxDim || a.N > kMaxDim / 2 || a.K > kMaxDim) c.add(GEMM_ERR_UNSUPPORTED);
+    if (a.N % 8 != 0) c.add(GEMM_ERR_UNSUPPORTED);
+    if (a.M > 0) {
+        if (a.K > 0) {
+            c.matrix(a.dY, a.K, a.lddy, a.dtype);
+            c.matrix(a.W, a.N, a.ldw, a.dtype);
+        }
+        c.matrix(a.Z, 2 * a.N, a.ldz, a.dtype);
+        c.matrix(a.dZ, 2 * a.N, a.lddz, a.dtype);
+    }
+    check_sums(c, a.dbias, a.dbias_dtype, a.workspace, a.workspace_bytes, a.M, 2 * a.N);
+    if (c.st != GEMM_OK) return c.st;
+    DeviceGuard g(h->device);
+    if (!g.ok) return GEMM_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int64_t rows = 0;  // of partial sums
+    if (a.M > 0) {
+        Product q = {};
+        q.mode = dtg::linear::kGluDgrad;
+        q.in = q.out = a.dtype;
+        q.rows = a.M;
+        q.cols = a.N;
+        q.depth = a.K;
+        q.A = a.dY;
+        q.lda = a.lddy;
+        q.B = a.W;
+        q.ldb = a.ldw;
+        q.C = a.dZ;
+        q.ldc = a.lddz;
+        q.alpha = a.alpha;
+        q.act = a.act;
+        q.src = a.Z;
+        q.ldsrc = a.ldz;
+        q.partials = a.dbias ? sums_of(h, a.workspace) : nullptr;
+        const gemm_status_t st = launch_product(h, q, &rows, s);
+        if (st != GEMM_OK) return st;
+    }
+    if (!a.dbias) return GEMM_OK;
+    return bias_sums(sums_of(h, a.workspace), rows, 2 * a.N, a.dbias, a.dbias_dtype, a.beta_bias, s);
 }
 
 gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* args, void* stream)
@@ -565,7 +711,7 @@ gemm_status_t gemm_run_linear_dgrad(gemm_handle_t h, const gemm_dgrad_args_t* ar
         if (st != GEMM_OK) return st;
     }
     if (!a.dbias) return GEMM_OK;
-    return launch_sums(sums_of(h, a.workspace), rows, a.K, bias_grad(a.dbias, a.dbias_dtype, a.beta_bias), s);
+    return bias_sums(sums_of(h, a.workspace), rows, a.K, a.dbias, a.dbias_dtype, a.beta_bias, s);
 }
 
 gemm_status_t gemm_run_linear_wgrad(gemm_handle_t h, const gemm_wgrad_args_t* args, void* stream)
@@ -626,8 +772,8 @@ gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* arg
     DeviceGuard g(h->device);
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dtg::linear::BiasGrad bias = bias_grad(a.dbias, a.dbias_dtype, a.beta_bias);
-    if (a.M == 0) return a.dbias ? launch_sums(nullptr, 0, a.N, bias, s) : GEMM_OK;
+    const dtg::linear::BiasGrad bias = bias_grad({a.dbias, a.dbias_dtype, a.beta_bias});
+    if (a.M == 0) return a.dbias ? bias_sums(nullptr, 0, a.N, a.dbias, a.dbias_dtype, a.beta_bias, s) : GEMM_OK;
     if (!a.dZ && !a.dbias) return GEMM_OK;
     // Blocks of rows: 64, or 32 (what the workspace has room for) when those would not fill the GPU.  Up to 128
     // rows are one block, which writes dbias itself and saves the second launch.
@@ -652,7 +798,7 @@ gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* arg
     const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_act_grad<true>(p, a.act, grid, s)
                                                         : launch_act_grad<false>(p, a.act, grid, s);
     if (st != GEMM_OK || !a.dbias || one_block) return st;
-    return launch_sums(p.partials, blocks, a.N, bias, s);
+    return bias_sums(p.partials, blocks, a.N, a.dbias, a.dbias_dtype, a.beta_bias, s);
 }
 
 }  // extern "C"

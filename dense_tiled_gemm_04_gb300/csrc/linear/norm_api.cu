@@ -1,0 +1,219 @@
+// Host side of gemm_run_layer_norm, gemm_run_layer_norm_grad and gemm_run_quantize: argument checks and launches.
+#include <algorithm>
+#include <cmath>
+
+#include "api_common.cuh"
+#include "norm.cuh"
+
+using namespace dtg::host;
+using namespace dtg::linear;
+
+namespace {
+
+void check_param(Checks& c, const void* at, gemm_dtype_t t, gemm_dtype_t matrix)
+{
+    if (!at) return;
+    if (t != GEMM_DTYPE_F32 && t != matrix)
+        c.add(GEMM_ERR_INVALID_ARG);
+    else
+        c.vector(at, t);
+}
+
+void check_stat(Checks& c, const float* at)
+{
+    c.vector(at, GEMM_DTYPE_F32);
+}
+
+NormVector vector_of(const void* at, gemm_dtype_t t) { return {at, t == GEMM_DTYPE_F32}; }
+
+unsigned blocks_for(int64_t rows, int64_t per_block) { return static_cast<unsigned>(cdiv(rows, per_block)); }
+
+template <bool BF16>
+gemm_status_t launch_norm(const NormParams& p, cudaStream_t s)
+{
+    // Warps, 16-byte chunks a lane, and rows a block, by the row's length: short rows are a warp each.
+    if (p.N <= 256) return launch_after(&layer_norm_kernel<BF16, 1, 1, 8>, blocks_for(p.M, 8), 256, 0, s, p);
+    if (p.N <= 512) return launch_after(&layer_norm_kernel<BF16, 1, 2, 8>, blocks_for(p.M, 8), 256, 0, s, p);
+    if (p.N <= 1024) return launch_after(&layer_norm_kernel<BF16, 4, 1, 1>, blocks_for(p.M, 1), 128, 0, s, p);
+    if (p.N <= 2048) return launch_after(&layer_norm_kernel<BF16, 4, 2, 1>, blocks_for(p.M, 1), 128, 0, s, p);
+    if (p.N <= 4096) return launch_after(&layer_norm_kernel<BF16, 8, 2, 1>, blocks_for(p.M, 1), 256, 0, s, p);
+    if (p.N <= 8192) return launch_after(&layer_norm_kernel<BF16, 16, 2, 1>, blocks_for(p.M, 1), 512, 0, s, p);
+    if (p.N <= kNormMaxHeld) return launch_after(&layer_norm_kernel<BF16, 32, 2, 1>, blocks_for(p.M, 1), 1024, 0, s, p);
+    return launch_after(&layer_norm_wide_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
+}
+
+// Rows of partial sums of dw and db.
+int64_t norm_grad_blocks(int64_t M) { return std::min<int64_t>(M, kNormMaxBlocks); }
+
+template <bool BF16>
+gemm_status_t launch_norm_grad(const NormGradParams& q, int64_t* blocks, cudaStream_t s)
+{
+    NormGradParams p = q;
+    if (p.N > kNormMaxHeld) {
+        const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
+        if (st != GEMM_OK) return st;
+        p.block_rows = cdiv(p.M, norm_grad_blocks(cdiv(p.M, 32)));
+        *blocks = cdiv(p.M, p.block_rows);
+        return launch_after(&layer_norm_grad_wide_kernel<BF16>, dim3(blocks_for(p.N, kStripCols), static_cast<unsigned>(*blocks)),
+                            kStripWarps * 32, 0, s, p);
+    }
+    const int64_t rows = p.N <= 512 ? 8 : 1;  // of a block at once
+    *blocks = norm_grad_blocks(cdiv(p.M, rows));
+    const unsigned n = static_cast<unsigned>(*blocks);
+    if (p.N <= 256) return launch_after(&layer_norm_grad_kernel<BF16, 1, 1, 8>, n, 256, 0, s, p);
+    if (p.N <= 512) return launch_after(&layer_norm_grad_kernel<BF16, 1, 2, 8>, n, 256, 0, s, p);
+    if (p.N <= 1024) return launch_after(&layer_norm_grad_kernel<BF16, 4, 1, 1>, n, 128, 0, s, p);
+    if (p.N <= 2048) return launch_after(&layer_norm_grad_kernel<BF16, 4, 2, 1>, n, 128, 0, s, p);
+    if (p.N <= 4096) return launch_after(&layer_norm_grad_kernel<BF16, 8, 2, 1>, n, 256, 0, s, p);
+    if (p.N <= 8192) return launch_after(&layer_norm_grad_kernel<BF16, 16, 2, 1>, n, 512, 0, s, p);
+    return launch_after(&layer_norm_grad_kernel<BF16, 16, 4, 1>, n, 512, 0, s, p);
+}
+
+template <bool BF16, bool E5M2>
+gemm_status_t launch_quantize(const QuantizeParams& p, bool square, cudaStream_t s)
+{
+    const int64_t rows = square ? kScaleBlock : kQuantWarps * kQuantRows;
+    const dim3 grid(blocks_for(p.K, square ? kScaleBlock : 256), static_cast<unsigned>(std::min<int64_t>(cdiv(p.M, rows), 65535)));
+    return square ? launch_after(&quantize_blocks_kernel<BF16, E5M2>, grid, 256, 0, s, p)
+                  : launch_after(&quantize_rows_kernel<BF16, E5M2>, grid, kQuantWarps * 32, 0, s, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_run_layer_norm(gemm_handle_t h, const gemm_layer_norm_args_t* args, void* stream)
+{
+    if (!h || !args) return GEMM_ERR_INVALID_ARG;
+    const gemm_layer_norm_args_t& a = *args;
+    if (!is_16bit(a.dtype) || !std::isfinite(a.eps) || a.eps < 0.0f) return GEMM_ERR_INVALID_ARG;
+    if (a.M < 0 || a.N < 0) return GEMM_ERR_INVALID_ARG;
+    if (a.M == 0 || a.N == 0) return GEMM_OK;
+    Checks c;
+    if (a.M > kMaxDim || a.N > kMaxDim) c.add(GEMM_ERR_UNSUPPORTED);
+    c.matrix(a.X, a.N, a.ldx, a.dtype);
+    c.matrix(a.Y, a.N, a.ldy, a.dtype);
+    check_param(c, a.weight, a.weight_dtype, a.dtype);
+    check_param(c, a.bias, a.bias_dtype, a.dtype);
+    check_stat(c, a.mean);
+    check_stat(c, a.rstd);
+    if (c.st != GEMM_OK) return c.st;
+    DeviceGuard g(h->device);
+    if (!g.ok) return GEMM_ERR_CUDA;
+    NormParams p;
+    p.X = static_cast<const uint16_t*>(a.X);
+    p.Y = static_cast<uint16_t*>(a.Y);
+    p.mean = a.mean;
+    p.rstd = a.rstd;
+    p.w = vector_of(a.weight, a.weight_dtype);
+    p.b = vector_of(a.bias, a.bias_dtype);
+    p.M = a.M;
+    p.N = a.N;
+    p.ldx = a.ldx;
+    p.ldy = a.ldy;
+    p.eps = a.eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return a.dtype == GEMM_DTYPE_BF16 ? launch_norm<true>(p, s) : launch_norm<false>(p, s);
+}
+
+int64_t gemm_layer_norm_grad_workspace_bytes(int64_t M, int64_t N)
+{
+    if (M <= 0 || N <= 0) return 0;
+    return 8 * norm_grad_blocks(M) * sum_pitch(N) + (N > kNormMaxHeld ? 8 * M : 0);
+}
+
+gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_grad_args_t* args, void* stream)
+{
+    if (!h || !args) return GEMM_ERR_INVALID_ARG;
+    const gemm_layer_norm_grad_args_t& a = *args;
+    if (!is_16bit(a.dtype) || !std::isfinite(a.beta)) return GEMM_ERR_INVALID_ARG;
+    if (a.M < 0 || a.N < 0) return GEMM_ERR_INVALID_ARG;
+    if (a.N == 0) return GEMM_OK;
+    Checks c;
+    if (a.M > kMaxDim || a.N > kMaxDim) c.add(GEMM_ERR_UNSUPPORTED);
+    check_param(c, a.weight, a.weight_dtype, a.dtype);
+    check_param(c, a.dweight, a.dweight_dtype, a.dtype);
+    check_param(c, a.dbias, a.dbias_dtype, a.dtype);
+    const bool sums = a.dweight || a.dbias;
+    if (a.M > 0) {
+        c.matrix(a.dY, a.N, a.lddy, a.dtype);
+        c.matrix(a.X, a.N, a.ldx, a.dtype);
+        c.matrix(a.dX, a.N, a.lddx, a.dtype);
+        if (a.residual) c.matrix(a.residual, a.N, a.ldr, a.dtype);
+        if (!a.mean || !a.rstd) c.add(GEMM_ERR_INVALID_ARG);
+        check_stat(c, a.mean);
+        check_stat(c, a.rstd);
+        const int64_t need = gemm_layer_norm_grad_workspace_bytes(a.M, a.N);
+        if ((sums || a.N > kNormMaxHeld) && (a.workspace || need > GEMM_OWN_SUMS_BYTES)) {
+            if (!a.workspace || a.workspace_bytes < need)
+                c.add(GEMM_ERR_INVALID_ARG);
+            else if ((reinterpret_cast<uintptr_t>(a.workspace) & 15u) != 0)
+                c.add(GEMM_ERR_UNSUPPORTED);
+        }
+    }
+    if (c.st != GEMM_OK) return c.st;
+    DeviceGuard g(h->device);
+    if (!g.ok) return GEMM_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* const partials = a.workspace ? static_cast<float*>(a.workspace) : h->sums;
+    const int64_t pitch = sum_pitch(a.N), half = norm_grad_blocks(a.M) * pitch;
+    int64_t blocks = 0;
+    if (a.M > 0) {
+        NormGradParams p;
+        p.dY = static_cast<const uint16_t*>(a.dY);
+        p.X = static_cast<const uint16_t*>(a.X);
+        p.residual = static_cast<const uint16_t*>(a.residual);
+        p.mean = a.mean;
+        p.rstd = a.rstd;
+        p.w = vector_of(a.weight, a.weight_dtype);
+        p.dX = static_cast<uint16_t*>(a.dX);
+        p.dw = a.dweight ? partials : nullptr;
+        p.db = a.dbias ? partials + half : nullptr;
+        p.row_means = reinterpret_cast<float2*>(partials + 2 * half);
+        p.M = a.M;
+        p.N = a.N;
+        p.lddy = a.lddy;
+        p.ldx = a.ldx;
+        p.ldr = a.ldr;
+        p.lddx = a.lddx;
+        p.pitch = pitch;
+        p.block_rows = 0;
+        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_norm_grad<true>(p, &blocks, s) : launch_norm_grad<false>(p, &blocks, s);
+        if (st != GEMM_OK) return st;
+    }
+    return launch_sums(partials, blocks, a.N, {a.dweight, a.dweight_dtype, a.beta}, {a.dbias, a.dbias_dtype, a.beta}, half, s);
+}
+
+gemm_status_t gemm_run_quantize(gemm_handle_t h, const gemm_quantize_args_t* args, void* stream)
+{
+    if (!h || !args) return GEMM_ERR_INVALID_ARG;
+    const gemm_quantize_args_t& a = *args;
+    if (!is_16bit(a.dtype) || !is_f8(a.q_dtype) || (a.block_rows != 1 && a.block_rows != kScaleBlock)) return GEMM_ERR_INVALID_ARG;
+    if (a.M < 0 || a.K < 0) return GEMM_ERR_INVALID_ARG;
+    if (a.M == 0 || a.K == 0) return GEMM_OK;
+    Checks c;
+    if (a.M > kMaxDim || a.K > kMaxDim) c.add(GEMM_ERR_UNSUPPORTED);
+    c.matrix(a.X, a.K, a.ldx, a.dtype);
+    c.matrix(a.Q, a.K, a.ldq, a.q_dtype);
+    if (!a.scales || a.lds < cdiv(a.K, kScaleBlock)) c.add(GEMM_ERR_INVALID_ARG);
+    c.vector(a.scales, GEMM_DTYPE_F32);
+    if (c.st != GEMM_OK) return c.st;
+    DeviceGuard g(h->device);
+    if (!g.ok) return GEMM_ERR_CUDA;
+    QuantizeParams p;
+    p.X = static_cast<const uint16_t*>(a.X);
+    p.Q = static_cast<uint8_t*>(a.Q);
+    p.S = a.scales;
+    p.M = a.M;
+    p.K = a.K;
+    p.ldx = a.ldx;
+    p.ldq = a.ldq;
+    p.lds = a.lds;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool square = a.block_rows != 1;
+    if (a.dtype == GEMM_DTYPE_BF16)
+        return a.q_dtype == GEMM_DTYPE_E5M2 ? launch_quantize<true, true>(p, square, s) : launch_quantize<true, false>(p, square, s);
+    return a.q_dtype == GEMM_DTYPE_E5M2 ? launch_quantize<false, true>(p, square, s) : launch_quantize<false, false>(p, square, s);
+}
+
+}  // extern "C"

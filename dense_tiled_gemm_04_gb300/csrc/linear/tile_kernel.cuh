@@ -7,6 +7,9 @@
 //             and the sums of d over each warp's 32 rows.  dY is K-major, W N-major (its rows are the contraction).
 //   kWgrad    rows = outputs N, columns = inputs K, contraction M:   dW = alpha dY^T X + beta dW.
 //             Both operands have the contraction as rows: A is M-major, B N-major.
+//   kGlu      a gated layer: g = alpha X Wg^T + bg, u = alpha X Wu^T + bu (kept on request), H = act(g) u.  A tile is 128
+//             columns of H; its accumulator holds the same columns of g, then of u, so that one epilogue warp has both.
+//   kGluDgrad backward through the weights above H: d = alpha dY W, dG = d u act'(g), dU = d act(g) and their column sums.
 //
 // The work schedule (tile raster, stream-K shares, backwards K walks, CTA pairs), the operand
 // ring and the bounded waits are those of gemm_tcgen05_kernel.  What differs:
@@ -46,7 +49,7 @@
 namespace dtg {
 namespace linear {
 
-constexpr int kForward = 0, kDgrad = 1, kWgrad = 2;
+constexpr int kForward = 0, kDgrad = 1, kWgrad = 2, kGlu = 3, kGluDgrad = 4;
 constexpr int kOutF16 = 0, kOutBf16 = 1, kOutF32 = 2;
 // Warps 0-3: producer, MMA and two idle ones; warps 4-11: epilogue.  setmaxnreg moves registers
 // between them by warpgroup: the block starts with 384 x 168 = 64512, the first four warps go down
@@ -72,6 +75,30 @@ struct TileParams : KernelParams {
     int64_t ldz;
     float* partials;      // dgrad: sums of 32-row blocks, `pitch` columns a row; null: none
     int64_t pitch;
+    const void* bias_up;  // gated: the biases of u
+    // SCALED: a scale for every 128 of a row of A, and for every 128 x 128 of B; null: 1
+    const float* x_scales;
+    const float* w_scales;
+    int64_t ld_xs, ld_ws;
+    int64_t up_scales;     // gated: offset of the scales of Wu
+    uint32_t format_bits;  // SCALED: what E5M2 operands add to the MMA's descriptor
+};
+
+// Tensor maps of a launch.  C: output; Z: forward z, dgrad pre-activations.
+template <int MODE>
+struct TileMaps {
+    CUtensorMap A, B, C, Z;
+};
+
+// Gated layers.  kGlu: B, B_up the weights of g and u, Z, Z_up where g and u are kept.  kGluDgrad: Z, Z_up the g and u
+// that the forward pass kept, C, C_up the gradients of both.
+template <>
+struct TileMaps<kGlu> {
+    CUtensorMap A, B, C, Z, B_up, Z_up;
+};
+template <>
+struct TileMaps<kGluDgrad> {
+    CUtensorMap A, B, C, Z, C_up, Z_up;
 };
 
 // STG_BUFS: staging buffers per epilogue warp.
@@ -83,7 +110,7 @@ struct TileSmem {
     static constexpr int kStgBufs = STG_BUFS;
     static constexpr int kBarOff = kStgOff + kTileEpiWarps * STG_BUFS * kTileStgBytes;
     // full, empty, acc_full[2], acc_empty[2], drain, pre-activation boxes per staging buffer
-    static constexpr int kNumBars = 2 * STAGES + 5 + kTileEpiWarps * 2;
+    static constexpr int kNumBars = 2 * STAGES + 5 + kTileEpiWarps * (STG_BUFS < 2 ? 2 : STG_BUFS);
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kTotal = kMiscOff + 16;  // tmem slot, abort flag, stream-K "last" flag
     static constexpr int kAlloc = kTotal + 1024;  // slack for aligning the base to 1 KB
@@ -211,6 +238,12 @@ __device__ __forceinline__ uint32_t box_chunk(uint32_t stg, int lane, int ch)
     return stg + lane * 128 + ((ch ^ (lane & 7)) << 4);
 }
 
+// The same for a buffer of 32 rows of 64 bytes (64-byte swizzle).
+__device__ __forceinline__ uint32_t half_box_chunk(uint32_t stg, int lane, int ch)
+{
+    return stg + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4);
+}
+
 // TMA store of a staging buffer that the warp has just written.
 __device__ __forceinline__ void store_box_now(const CUtensorMap* tm, uint32_t stg, int32_t x, int32_t y, int lane)
 {
@@ -278,6 +311,21 @@ __device__ __forceinline__ void sum_rows(float* v, int lane)
     }
 }
 
+// The same for 32 columns in v[0..31]: lane l ends with column l in v[0].
+__device__ __forceinline__ void sum_rows32(float* v, int lane)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float give = upper ? v[i] : v[i + off];
+            const float keep = upper ? v[i + off] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
+        }
+    }
+}
+
 // tile_coord in 32 bits (a launch has fewer than 2^31 tiles): 64-bit divisions for every item took the
 // epilogue warps more instructions than a relu.
 __device__ __forceinline__ void tile_coord32(uint32_t t, const KernelParams& p, uint32_t& tm, uint32_t& tn)
@@ -290,26 +338,34 @@ __device__ __forceinline__ void tile_coord32(uint32_t t, const KernelParams& p, 
     tm = first_m + (r - tn * rows);
 }
 
-// IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward, kDgrad,
-// kWgrad; SUMS: the contraction runs in chunks that are summed in registers; CLUSTER: 1 (one CTA) or 2 (a CTA pair).
-template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER>
+// IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward ... kGluDgrad;
+// SUMS: the contraction runs in chunks that are summed in registers; CLUSTER: 1 (one CTA) or 2 (a CTA pair); SCALED:
+// 8-bit operands with a scale for each block of 128: every K block is a chunk, multiplied by its scales as it is
+// added (IN is 2, and format_bits makes the operands E5M2: one kernel serves both); STG_BUFS: staging buffers per warp.
+template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER, bool SCALED, int STG_BUFS>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ, const TileParams p)
+    linear_tile_kernel(const __grid_constant__ TileMaps<MODE> maps, const TileParams p)
 {
     using T = Operand<IN>;
     static_assert(IN <= 3 && (BN == 128 || BN == 256), "dense operands, 64 or 128 columns per epilogue warp");
-    static_assert(MODE == kForward || !T::kF8, "8-bit operands: forward only");
+    static_assert(MODE == kForward || MODE == kGlu || !T::kF8, "8-bit operands: forward only");
     static_assert(OUT != kOutF32 || (MODE == kWgrad && SUMS), "fp32 output: weight gradients only");
+    static_assert(!SCALED || (IN == 2 && SUMS), "scales meet the products in the registers' sums");
+    static_assert((MODE != kGlu && MODE != kGluDgrad) || BN == 256, "gated: a box of 64 columns of both halves per warp");
+    static_assert(MODE != kDgrad || STG_BUFS == 2, "dgrad alternates between two buffers");
+    const CUtensorMap &tmA = maps.A, &tmB = maps.B, &tmC = maps.C, &tmZ = maps.Z;
+    constexpr bool GLU = MODE == kGlu;
     constexpr bool PAIR = CLUSTER == 2;
     constexpr bool AT = MODE == kWgrad;        // A is M-major
-    constexpr bool BT = MODE != kForward;      // B is N-major
+    constexpr bool BT = MODE != kForward && !GLU;  // B is N-major
     constexpr int kRanks = PAIR ? 2 : 1;
     constexpr int kTileM = kBM * kRanks;
     constexpr int kBRows = BN / kRanks;
-    constexpr int CW = BN / 2;                 // columns per epilogue warp
+    constexpr int CW = BN / 2;                 // accumulator columns per epilogue warp
+    constexpr int kTileN = GLU ? BN / 2 : BN;  // output columns of a tile
+    constexpr int kWarpN = kTileN / 2;         // ... and of an epilogue warp
     constexpr uint32_t kTmemCols = 2 * BN;
-    using L = TileSmem<kBRows, STAGES, MODE == kDgrad ? 2 : 1>;
+    using L = TileSmem<kBRows, STAGES, STG_BUFS>;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -321,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 5 + 2 * w + b); };  // dgrad: box loaded
+    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 5 + STG_BUFS * w + b); };  // dgrad: box loaded
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int32_t* const abort_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 4);
     volatile int32_t* const last_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 8);
@@ -343,9 +399,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ptx::mbar_init(acce_bar(b), kTileEpiWarps * kRanks);
         }
         ptx::mbar_init(drain_bar, 1);
-        if constexpr (MODE == kDgrad)
+        if constexpr (MODE == kDgrad || MODE == kGluDgrad)
             for (int w = 0; w < kTileEpiWarps; ++w)
-                for (int b = 0; b < 2; ++b) ptx::mbar_init(in_bar(w, b), 1);
+                for (int b = 0; b < STG_BUFS; ++b) ptx::mbar_init(in_bar(w, b), 1);
         *abort_flag = 0;
         *last_flag = 0;
         ptx::fence_mbar_init();
@@ -392,7 +448,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 uint32_t tm, tn;
                 tile_coord32(static_cast<uint32_t>(tile), p, tm, tn);
                 const int32_t y_a = static_cast<int32_t>(tm * kTileM + rank * kBM);
-                const int32_t n_b = static_cast<int32_t>(tn * BN + rank * kBRows);
+                // Gated: the same rows of Wg and Wu; in a pair the leader loads those of Wg, its peer those of Wu.
+                const int32_t n_b = static_cast<int32_t>(GLU ? tn * kTileN : tn * BN + rank * kBRows);
                 const bool rev = it.reversed(p);
                 for (int i = 0; i < kb1 - kb0; ++i, ++loaded) {
                     const int kb = rev ? kb1 - 1 - i : kb0 + i;
@@ -426,6 +483,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                             for (int q = 0; q < kBRows / T::kNBlock; ++q)
                                 load(sb + q * (T::kStageK * 128), &tmB, n_b + q * T::kNBlock, k0);
+                        } else if constexpr (GLU) {
+                            if (leader) load(sb, &tmB, k0, n_b);
+                            if (!PAIR || !leader) load(sb + (PAIR ? 0 : kTileN * kRowBytes), &maps.B_up, k0, n_b);
                         } else {
                             load(sb, &tmB, k0, n_b);
                         }
@@ -453,7 +513,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp == kMmaWarp) {
         if (lane == 0 && leader) {
             // ---------------------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc = idesc_mma<T::kFormat, BT, kTileM, BN>() | (AT ? 1u << 15 : 0u);
+            uint32_t idesc = idesc_mma<T::kFormat, BT, kTileM, BN>() | (AT ? 1u << 15 : 0u);
+            if constexpr (SCALED) idesc |= p.format_bits;
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
@@ -553,11 +614,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // bytes of 32 rows at a time, they bound the kernel: 16384 x 1024 x 8192 relu 233 us against 176 without.)
         int in_buf = 0;                        // buffer of the next box
         uint32_t in_phase = 0, in_flight = 0;  // per buffer: parity its barrier completes next; a load is pending
+        // A gated layer's boxes are 32 columns wide: g in the first half of a buffer, u in the second.
         auto load_in = [&](int buf, int32_t x, int32_t y) {
             in_flight |= 1u << buf;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(in_bar(ew, buf), kTileStgBytes);
                 ptx::tma_load_2d(stg + buf * kTileStgBytes, &tmZ, x, y, in_bar(ew, buf));
+                if constexpr (MODE == kGluDgrad)
+                    ptx::tma_load_2d(stg + buf * kTileStgBytes + kTileStgBytes / 2, &maps.Z_up, x, y, in_bar(ew, buf));
             }
         };
         // A work item as this warp sees it: columns from x, rows from y of C; inside: it has some of both.
@@ -565,20 +629,149 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int64_t tile;
             int kb0, kb1;
             int32_t x, y;
-            bool whole, inside;
+            bool whole, inside, rev;
         };
         auto next_item = [&](Item& t) -> bool {
             if (!it.next(p, t.tile, t.kb0, t.kb1)) return false;
             uint32_t tm, tn;
             tile_coord32(static_cast<uint32_t>(t.tile), p, tm, tn);
             t.y = static_cast<int32_t>(tm * kTileM + rank * kBM + quad * 32);
-            t.x = static_cast<int32_t>(tn * BN + half * CW);
+            t.x = static_cast<int32_t>(tn * kTileN + half * kWarpN);
+            t.rev = it.reversed(p);
             t.whole = t.kb0 == 0 && t.kb1 == p.num_kb;
             t.inside = t.y < p.M && t.x < p.N;
             return true;
         };
         Item cur = {}, nxt = {};
         bool more_items = false;  // nxt is an item
+
+        // w = alpha v + bias over 64 columns from column x of C on.
+        auto with_bias = [&](f32x2 (&w)[32], const float* v, const void* bias, int32_t x) {
+            const f32x2 alpha = both(p.alpha);
+            if (bias) {
+                // The box's 64 biases go through the staging buffer, from which all lanes read them.
+                if (lane == 0) ptx::bulk_wait_group_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int32_t c = x + lane + 32 * e;
+                    float f = 0.0f;
+                    if (c < p.N)
+                        f = p.bias_f32 ? static_cast<const float*>(bias)[c] : load16<kBf16>(static_cast<const uint16_t*>(bias) + c);
+                    st_shared_f32(stg + 4 * (lane + 32 * e), f);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 f = ld_shared_f4(stg + 16 * i);
+                    w[2 * i] = fma2(alpha, pair(v[4 * i], v[4 * i + 1]), pair(f.x, f.y));
+                    w[2 * i + 1] = fma2(alpha, pair(v[4 * i + 2], v[4 * i + 3]), pair(f.z, f.w));
+                }
+                __syncwarp();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
+            }
+        };
+
+        // Gated forward on 64 columns of this thread's row: vg, vu hold the products' sums.
+        auto finish_glu = [&](const float* vg, const float* vu, int32_t x, int32_t y) {
+            f32x2 g[32], u[32];
+            uint32_t h[32];
+            with_bias(g, vg, p.bias, x);
+            with_bias(u, vu, p.bias_up, x);
+            if constexpr (GLU) {
+                if (p.Z) {  // (N is a multiple of 8 then: no masked stores)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(g[i]);
+                    store_rows<2>(h, x, y, lane, stg, &tmZ, p.Z, p.ldz, p.M, p.N);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(u[i]);
+                    store_rows<2>(h, x, y, lane, stg, &maps.Z_up, p.Z, p.ldz, p.M, p.N);
+                }
+                DTG_ACT_SWITCH(p.act, {
+                    _Pragma("unroll") for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(mul2(act_value2<ACT>(g[i]), u[i]));
+                });
+                store_rows<2>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+            }
+        };
+
+        // Gated dgrad on 32 columns of this thread's row: v holds d's sums.  g and u come by TMA (see load_in), the next box's
+        // while this one is worked on; their gradients are written over them and leave from there.  N is a multiple of 8:
+        // TMA clips every box exactly.
+        auto finish_glu_dgrad = [&](float* v, int32_t x, int32_t y) {
+            if constexpr (MODE == kGluDgrad) {
+                const uint32_t buf = stg + in_buf * kTileStgBytes;
+                auto free_for = [&](int b, int32_t lx, int32_t ly) {  // the store that left from buffer b has read it; load it
+                    if (lane == 0) ptx::bulk_wait_group_read<STG_BUFS - 2>();
+                    __syncwarp();
+                    load_in(b, lx, ly);
+                };
+                if (!(in_flight & (1u << in_buf))) {
+                    if (lane == 0) ptx::bulk_wait_group_read<STG_BUFS - 1>();
+                    __syncwarp();
+                    load_in(in_buf, x, y);
+                }
+                const int next = in_buf + 1 == STG_BUFS ? 0 : in_buf + 1;
+                const bool same_tile = x + 32 < p.N && x - cur.x + 32 < CW;
+                if (same_tile)
+                    free_for(next, x + 32, y);
+                else if (more_items && nxt.inside)
+                    free_for(next, nxt.x, nxt.y);
+                const bool in = wd.wait(in_bar(ew, in_buf), (in_phase >> in_buf) & 1u, kRoleEpilogue, -1, 0);
+                if (!__all_sync(0xFFFFFFFFu, in)) return;  // recorded: the launch is being abandoned
+                in_phase ^= 1u << in_buf;
+                in_flight &= ~(1u << in_buf);
+                const f32x2 alpha = both(p.alpha);
+                const bool row_in = y + lane < p.M;
+                float du[32];  // v becomes dG
+                DTG_ACT_SWITCH(p.act, {
+                    _Pragma("unroll") for (int ch = 0; ch < 4; ++ch)
+                    {
+                        const uint32_t at_g = half_box_chunk(buf, lane, ch), at_u = at_g + kTileStgBytes / 2;
+                        const uint4 gw = ld_shared_u4(at_g), uw = ld_shared_u4(at_u);
+                        const uint32_t gi[4] = {gw.x, gw.y, gw.z, gw.w}, ui[4] = {uw.x, uw.y, uw.z, uw.w};
+                        uint32_t hg[4], hu[4];
+                        _Pragma("unroll") for (int i = 0; i < 4; ++i)
+                        {
+                            const int c = 8 * ch + 2 * i;
+                            const f32x2 d = mul2(alpha, pair(v[c], v[c + 1]));
+                            f32x2 value, slope;
+                            act_both2<ACT>(unpack2<kBf16>(gi[i]), value, slope);
+                            const f32x2 a = mul2(mul2(d, unpack2<kBf16>(ui[i])), slope), b = mul2(d, value);
+                            hg[i] = round2<kBf16>(a);
+                            hu[i] = round2<kBf16>(b);
+                            split(a, v[c], v[c + 1]);
+                            split(b, du[c], du[c + 1]);
+                        }
+                        ptx::st_shared_v4(at_g, hg[0], hg[1], hg[2], hg[3]);
+                        ptx::st_shared_v4(at_u, hu[0], hu[1], hu[2], hu[3]);
+                    }
+                });
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_2d(&tmC, buf, x, y);
+                    ptx::tma_store_2d(&maps.C_up, buf + kTileStgBytes / 2, x, y);
+                    ptx::bulk_commit_group();
+                }
+                in_buf = next;
+                if (p.partials) {
+                    // Rows past M are not part of the sums (an infinite weight makes them NaN).
+                    if (!row_in) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = du[i] = 0.0f;
+                    }
+                    sum_rows32(v, lane);
+                    sum_rows32(du, lane);
+                    if (x + lane < p.N) {
+                        float* const sums = p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + lane;
+                        sums[0] = v[0];
+                        sums[p.N] = du[0];
+                    }
+                }
+            }
+        };
 
         // The operator on 64 columns (32 for an fp32 output) of this thread's row, from column x of C on: v holds
         // the product's sums and is overwritten.  A warp's rows start at y < M, its columns at x < N.
@@ -677,31 +870,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int i = 0; i < 32; ++i) r[i] = 0;
                 }
                 f32x2 w[32];
-                if (MODE == kForward && p.bias) {
-                    // The box's 64 biases go through the staging buffer, from which all lanes read them.
-                    if (lane == 0) ptx::bulk_wait_group_read<0>();
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int32_t c = x + lane + 32 * e;
-                        float f = 0.0f;
-                        if (c < p.N)
-                            f = p.bias_f32 ? static_cast<const float*>(p.bias)[c]
-                                           : load16<kBf16>(static_cast<const uint16_t*>(p.bias) + c);
-                        st_shared_f32(stg + 4 * (lane + 32 * e), f);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float4 f = ld_shared_f4(stg + 16 * i);
-                        w[2 * i] = fma2(alpha, pair(v[4 * i], v[4 * i + 1]), pair(f.x, f.y));
-                        w[2 * i + 1] = fma2(alpha, pair(v[4 * i + 2], v[4 * i + 3]), pair(f.z, f.w));
-                    }
-                    __syncwarp();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
-                }
+                with_bias(w, v, MODE == kForward ? p.bias : nullptr, x);
                 uint32_t h[32];
                 if constexpr (MODE == kForward) {
                     if (p.Z) {
@@ -730,6 +899,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
 
+        // Where the warp's q-th 32 accumulator columns are (gated: those of g, then those of u).
+        auto acc_col = [&](int q) -> uint32_t {
+            if constexpr (GLU) return static_cast<uint32_t>((q * 32 / kWarpN) * kTileN + half * kWarpN + q * 32 % kWarpN);
+            return static_cast<uint32_t>(half * CW + q * 32);
+        };
+        // SCALED: the factors of K block kb for this thread's row, of the warp's columns (of g and of u).
+        auto load_scales = [&](int kb, float& fg, float& fu) {
+            const int64_t row = static_cast<int64_t>(cur.y) + lane;
+            const int64_t block = cur.x >> 7;  // 128 columns of a weight's block: a warp's lie inside one
+            const float xs = p.x_scales && row < p.M ? p.x_scales[row * p.ld_xs + kb] : 1.0f;
+            const bool w = p.w_scales && cur.x < p.N;
+            fg = xs * (w ? p.w_scales[block * p.ld_ws + kb] : 1.0f);
+            if constexpr (GLU) fu = xs * (w ? p.w_scales[p.up_scales + block * p.ld_ws + kb] : 1.0f);
+        };
         // 64 columns of the accumulator: TMEM -> v.
         auto load_acc = [&](float* v, uint32_t taddr) {
             uint32_t a[32];
@@ -823,22 +1006,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 bool ok = true;
 #pragma unroll
                 for (int i = 0; i < CW; ++i) s[i] = 0.0f;
+                [[maybe_unused]] float next_g = 1.0f, next_u = 1.0f;  // SCALED: loaded a K block ahead
+                auto block_at = [&](int i) { return cur.rev ? kb1 - 1 - (i - kb0) : i; };
+                if constexpr (SCALED) {
+                    if (kb0 < kb1) load_scales(block_at(kb0), next_g, next_u);
+                }
                 for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
+                    [[maybe_unused]] const f32x2 fg = both(next_g), fu = both(next_u);
+                    if constexpr (SCALED) {
+                        if (kb + 1 < kb1) load_scales(block_at(kb + 1), next_g, next_u);
+                    }
                     ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (ok) {
                         ptx::tc_fence_after_sync();
-                        const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
+                        const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN);
 #pragma unroll
                         for (int q = 0; q < CW / 32; ++q) {
                             uint32_t v[32];
-                            ptx::tmem_ld_32x32b_x32(tacc + q * 32, v);
+                            ptx::tmem_ld_32x32b_x32(tacc + acc_col(q), v);
                             ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2)
-                                split(add2(pair(s[q * 32 + i], s[q * 32 + i + 1]),
-                                           pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))),
-                                      s[q * 32 + i], s[q * 32 + i + 1]);
+                            for (int i = 0; i < 32; i += 2) {
+                                const f32x2 sum = pair(s[q * 32 + i], s[q * 32 + i + 1]);
+                                const f32x2 add = pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                                if constexpr (SCALED)
+                                    split(fma2(GLU && q * 32 >= CW / 2 ? fu : fg, add, sum), s[q * 32 + i], s[q * 32 + i + 1]);
+                                else
+                                    split(add2(sum, add), s[q * 32 + i], s[q * 32 + i + 1]);
+                            }
                         }
                         release_acc();
                     }
@@ -866,7 +1062,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for (int b = 0; b < CW / 64; ++b) add_part(&s[b * 64], f4 + b * 16 * kBM);
                     }
                 }
-                if (y < p.M) {
+                if constexpr (GLU) {
+                    if (y < p.M && x0 < p.N) finish_glu(&s[0], &s[CW / 2], x0, y);
+                } else if constexpr (MODE == kGluDgrad) {
+                    if (y < p.M) {
+#pragma unroll
+                        for (int b = 0; b < CW / 32; ++b)
+                            if (x0 + b * 32 < p.N) finish_glu_dgrad(&s[b * 32], x0 + b * 32, y);
+                    }
+                } else if (y < p.M) {
                     constexpr int kBox = OUT == kOutF32 ? 32 : 64;
 #pragma unroll
                     for (int b = 0; b < CW / kBox; ++b)
@@ -879,7 +1083,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ptx::tc_fence_after_sync();
                 const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
                 float v[64];
-                if (whole) {
+                if constexpr (GLU) {  // (always a whole tile)
+                    float u[64];
+                    if (kb0 == kb1) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i] = u[i] = 0.0f;
+                    } else {
+                        const uint32_t at = tmem_base + lane_off + static_cast<uint32_t>(acc * BN) + acc_col(0);
+                        load_acc(v, at);
+                        load_acc(u, at + kTileN);
+                        release_acc();
+                    }
+                    if (y < p.M && x0 < p.N) finish_glu(v, u, x0, y);
+                } else if constexpr (MODE == kGluDgrad) {  // (always a whole tile)
+#pragma unroll 1
+                    for (int b = 0; b < CW / 32; ++b) {
+                        if (kb0 == kb1) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                        } else {
+                            uint32_t a[32];
+                            __syncwarp();
+                            ptx::tmem_ld_32x32b_x32(tacc + b * 32, a);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
+                            if (b == CW / 32 - 1) release_acc();
+                        }
+                        if (y < p.M && x0 + b * 32 < p.N) finish_glu_dgrad(v, x0 + b * 32, y);
+                    }
+                } else if (whole) {
 #pragma unroll 1
                     for (int b = 0; b < CW / 64; ++b) {
                         if (kb0 == kb1) {  // an empty contraction
@@ -939,7 +1172,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const uint8_t* line = static_cast<const uint8_t*>(p.in) + (row * p.ldin + nxt.x) * kElem;
 #pragma unroll
             for (int b = 0; b < CW * kElem / 128; ++b)
-                if (nxt.x + b * (128 / kElem) < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
+                if (nxt.x + b * (128 / kElem) < p.N) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
+                    if constexpr (MODE == kGluDgrad)  // u, N columns after g
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128 + static_cast<int64_t>(p.N) * kElem));
+                }
         };
         more_items = next_item(nxt);
         if (more_items) prefetch_in();
@@ -949,8 +1186,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (more_items) prefetch_in();
             if (!one_item()) break;  // all eight epilogue warps leave together
         }
-        if constexpr (MODE == kDgrad)  // after an abandoned launch: a load may still be on its way
-            for (int b = 0; b < 2; ++b)
+        if constexpr (MODE == kDgrad || MODE == kGluDgrad)  // after an abandoned launch: a load may still be on its way
+            for (int b = 0; b < STG_BUFS; ++b)
                 if (in_flight & (1u << b)) wd.drain(in_bar(ew, b), (in_phase >> b) & 1u);
         if (lane == 0) ptx::bulk_wait_group_all();
         __syncwarp();

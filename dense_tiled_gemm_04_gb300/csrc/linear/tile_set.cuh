@@ -8,13 +8,15 @@
 namespace dtg {
 namespace linear {
 
-template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER>
+template <int BN, int STAGES, int IN, int OUT, int MODE, bool SUMS, int CLUSTER, bool SCALED = false,
+          int STG_BUFS = MODE == kDgrad ? 2 : 1>
 KernelChoice tile_choice(int config)
 {
     constexpr int kBRows = BN / CLUSTER;
     return {config, kBM * CLUSTER, BN, kBRows, Operand<IN>::kStageK, Operand<IN>::kNBlock, Operand<IN>::kAStageK,
-            STAGES, CLUSTER, reinterpret_cast<const void*>(&linear_tile_kernel<BN, STAGES, IN, OUT, MODE, SUMS, CLUSTER>),
-            TileSmem<kBRows, STAGES, MODE == kDgrad ? 2 : 1>::kAlloc, kTileThreads};
+            STAGES, CLUSTER,
+            reinterpret_cast<const void*>(&linear_tile_kernel<BN, STAGES, IN, OUT, MODE, SUMS, CLUSTER, SCALED, STG_BUFS>),
+            TileSmem<kBRows, STAGES, STG_BUFS>::kAlloc, kTileThreads};
 }
 
 // config: GEMM_CONFIG_256x256 (3), _128x256 (1) or anything else (_128x128, 2).  dgrad gives a ring stage for its second
@@ -26,6 +28,31 @@ KernelChoice tile_choice_for(int config)
     if (config == 3) return tile_choice<256, 6 - kLess, IN, OUT, MODE, SUMS, 2>(3);
     if (config == 1) return tile_choice<256, 4 - kLess, IN, OUT, MODE, SUMS, 1>(1);
     return tile_choice<128, 6 - kLess, IN, OUT, MODE, SUMS, 1>(2);
+}
+
+// 8-bit operands with block scales.
+template <int OUT>
+KernelChoice scaled_choice(int config)
+{
+    if (config == 3) return tile_choice<256, 6, 2, OUT, kForward, true, 2, true>(3);
+    if (config == 1) return tile_choice<256, 4, 2, OUT, kForward, true, 1, true>(1);
+    return tile_choice<128, 6, 2, OUT, kForward, true, 1, true>(2);
+}
+
+// Gated forward: a pair or (any other config) one CTA with 256 accumulator columns, 128 of each half.
+template <int IN, int OUT, bool SUMS, bool SCALED>
+KernelChoice glu_choice(int config)
+{
+    if (config == 3) return tile_choice<256, 6, IN, OUT, kGlu, SUMS, 2, SCALED>(3);
+    return tile_choice<256, 4, IN, OUT, kGlu, SUMS, 1, SCALED>(1);
+}
+
+// Gated dgrad: three staging buffers per warp in a pair, two beside one CTA's wider stages.
+template <int IN, int OUT, bool SUMS>
+KernelChoice glu_dgrad_choice(int config)
+{
+    if (config == 3) return tile_choice<256, 4, IN, OUT, kGluDgrad, SUMS, 2, false, 3>(3);
+    return tile_choice<256, 3, IN, OUT, kGluDgrad, SUMS, 1, false, 2>(1);
 }
 
 KernelChoice forward_f16(int config);
@@ -43,6 +70,12 @@ KernelChoice forward_long_e4m3(int config, bool out_bf16);
 KernelChoice forward_long_e5m2(int config, bool out_bf16);
 KernelChoice wgrad_long_f16(int config);
 KernelChoice wgrad_long_bf16(int config);
+// Block scales (E4M3 and E5M2), and gated layers.
+KernelChoice forward_scaled(int config, bool out_bf16);
+KernelChoice glu_16(int config, bool bf16, bool sums);
+KernelChoice glu_scaled(int config, bool out_bf16);
+KernelChoice glu_dgrad_f16(int config, bool sums);
+KernelChoice glu_dgrad_bf16(int config, bool sums);
 
 }  // namespace linear
 }  // namespace dtg

@@ -87,6 +87,48 @@ class gemm_act_grad_args_t(ctypes.Structure):
                 ("beta_bias", ctypes.c_float)]
 
 
+class gemm_glu_args_t(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("W", ctypes.c_void_p), ("H", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("Z", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldh", ctypes.c_int64), ("ldz", ctypes.c_int64),
+                ("ld_xs", ctypes.c_int64), ("ld_ws", ctypes.c_int64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("bias_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("alpha", ctypes.c_float)]
+
+
+class gemm_glu_dgrad_args_t(ctypes.Structure):
+    _fields_ = [("dY", ctypes.c_void_p), ("W", ctypes.c_void_p), ("Z", ctypes.c_void_p), ("dZ", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("lddy", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldz", ctypes.c_int64), ("lddz", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("dbias_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta_bias", ctypes.c_float)]
+
+
+class gemm_quantize_args_t(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("Q", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldq", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("dtype", ctypes.c_int32), ("q_dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32)]
+
+
+class gemm_layer_norm_args_t(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("bias_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class gemm_layer_norm_grad_args_t(ctypes.Structure):
+    _fields_ = [("dY", ctypes.c_void_p), ("X", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dX", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("lddy", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("lddx", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("dweight_dtype", ctypes.c_int32),
+                ("dbias_dtype", ctypes.c_int32), ("beta", ctypes.c_float)]
+
+
 class GemmError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -135,6 +177,13 @@ def load() -> ctypes.CDLL:
         "gemm_run_linear_wgrad": ([p, ctypes.POINTER(gemm_wgrad_args_t), p], i32),
         "gemm_run_act_grad": ([p, ctypes.POINTER(gemm_act_grad_args_t), p], i32),
         "gemm_bias_grad_workspace_bytes": ([i64, i64], i64),
+        "gemm_run_linear_glu": ([p, ctypes.POINTER(gemm_glu_args_t), p], i32),
+        "gemm_run_linear_glu_dgrad": ([p, ctypes.POINTER(gemm_glu_dgrad_args_t), p], i32),
+        "gemm_run_linear_scaled": ([p, ctypes.POINTER(gemm_linear_args_t), p, i64, p, i64, p], i32),
+        "gemm_run_quantize": ([p, ctypes.POINTER(gemm_quantize_args_t), p], i32),
+        "gemm_run_layer_norm": ([p, ctypes.POINTER(gemm_layer_norm_args_t), p], i32),
+        "gemm_run_layer_norm_grad": ([p, ctypes.POINTER(gemm_layer_norm_grad_args_t), p], i32),
+        "gemm_layer_norm_grad_workspace_bytes": ([i64, i64], i64),
         "gemm_status_string": ([i32], ctypes.c_char_p),
         "gemm_api_version": ([], i32),
     }
@@ -176,6 +225,16 @@ def bias_grad_workspace_bytes(M: int, cols: int) -> int:
 def _sums_bytes(M: int, cols: int) -> int:
     """bias_grad_workspace_bytes without a call into the library, which a small call would notice."""
     return 4 * -(-M // 32) * (-(-cols // 64) * 64)
+
+
+def layer_norm_grad_workspace_bytes(M: int, N: int) -> int:
+    """Bytes of workspace for layer_norm_grad's sums over an M x N matrix."""
+    return int(load().gemm_layer_norm_grad_workspace_bytes(M, N))
+
+
+def _norm_bytes(M: int, N: int) -> int:
+    """layer_norm_grad_workspace_bytes without a call into the library."""
+    return (8 * min(M, 304) * (-(-N // 64) * 64) + (8 * M if N > 16384 else 0)) if M and N else 0
 
 
 def tile_coord(tile: int, tiles_m: int, tiles_n: int, group_m: int):
@@ -249,6 +308,31 @@ def _vector(t: torch.Tensor, what: str, n: int, dtype: torch.dtype, device: int)
     return TORCH_TO_DTYPE_F32[t.dtype]
 
 
+def _scales(t: torch.Tensor, what: str, rows: int, cols: int, device: int) -> int:
+    """Check a float32 matrix of block scales and return its leading dimension."""
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{what} must be float32, not {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must have shape {(rows, cols)}, not {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit stride along the last dimension (row-major)")
+    return max(ld, cols) if rows <= 1 else ld
+
+
+def _stat(t: torch.Tensor, what: str, n: int, device: int) -> int:
+    """Check a dense float32 vector and return its address."""
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{what} must be float32, not {t.dtype}")
+    if t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+        raise ValueError(f"{what} must be a dense vector of {n} elements")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
+    return t.data_ptr()
+
+
 def _act(name) -> int:
     if name not in ACTS:
         raise ValueError(f"unknown activation {name!r}: one of {sorted(k for k in ACTS if k)}")
@@ -269,7 +353,7 @@ def _new(rows: int, cols: int, dtype: torch.dtype, device: int, stream) -> torch
 
 def _padded_output(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     """A rows x cols output whose row pitch is a multiple of 16 bytes."""
-    align = 4 if dtype is torch.float32 else 8
+    align = 16 // dtype.itemsize
     ld = max(-(-cols // align) * align, align)
     t = torch.empty((rows, ld), dtype=dtype, device=device)
     return t if ld == cols else t[:, :cols]
@@ -660,6 +744,228 @@ class Gemm:
             raise GemmError(st, "gemm_run_act_grad")
         return out
 
+    # -------------------------------------------------------------- gated feed-forward blocks
+    def linear_scaled(self, X: torch.Tensor, W: torch.Tensor, x_scales: torch.Tensor | None, w_scales: torch.Tensor | None,
+                      bias: torch.Tensor | None = None, act: str | None = None, residual: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                      out_dtype: torch.dtype | None = None, alpha: float = 1.0, stream=None, _ptr=None) -> torch.Tensor:
+        """linear with 8-bit operands and a float32 scale for each block of 128 (gemm_run_linear_scaled): x_scales
+        (M x ceil(K/128)) for every 128 of a row of X, w_scales (ceil(N/128) x ceil(K/128)) for every 128 x 128 of W, as
+        quantize makes them; None: 1.  The other arguments as for linear.  Async on `stream`."""
+        dt, dev = X.dtype, self._index
+        in_code = TORCH_TO_DTYPE_EX.get(dt)
+        if in_code is None or in_code <= DTYPE_BF16:
+            raise TypeError("X and W must have the same 8-bit float type")
+        if X.dim() != 2 or W.dim() != 2:
+            raise ValueError("expected 2-D tensors")
+        (M, K), N = X.shape, W.shape[0]
+        if out_dtype is None:
+            out_dtype = out.dtype if out is not None else torch.bfloat16
+        out_code = TORCH_TO_DTYPE.get(out_dtype)
+        if out_code is None:
+            raise TypeError("Y must be float16 or bfloat16")
+        ldx, ldw = _matrix(X, "X", M, K, dt, dev), _matrix(W, "W", N, K, dt, dev)
+        xs_p = ws_p = ld_xs = ld_ws = 0
+        if x_scales is not None:
+            ld_xs, xs_p = _scales(x_scales, "x_scales", M, -(-K // 128), dev), x_scales.data_ptr()
+        if w_scales is not None:
+            ld_ws, ws_p = _scales(w_scales, "w_scales", -(-N // 128), -(-K // 128), dev), w_scales.data_ptr()
+        bias_p = res_p = z_p = bias_code = ldr = ldz = 0
+        if bias is not None:
+            bias_code, bias_p = _vector(bias, "bias", N, out_dtype, dev), bias.data_ptr()
+        if residual is not None:
+            ldr, res_p = _matrix(residual, "residual", M, N, out_dtype, dev), residual.data_ptr()
+        if preact is not None:
+            ldz, z_p = _matrix(preact, "preact", M, N, out_dtype, dev), preact.data_ptr()
+        if out is None:
+            out = _new(M, N, out_dtype, dev, stream)
+        ldy = _matrix(out, "out", M, N, out_dtype, dev)
+        a = gemm_linear_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
+                               ldz, in_code, out_code, bias_code, _act(act), alpha)
+        st = self._lib.gemm_run_linear_scaled(self._h, ctypes.byref(a), xs_p, ld_xs, ws_p, ld_ws,
+                                              _stream_of(stream, dev) if _ptr is None else _ptr)
+        if st != OK:
+            raise GemmError(st, "gemm_run_linear_scaled")
+        return out
+
+    def linear_glu(self, X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = "silu",
+                   out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, alpha: float = 1.0, x_scales: torch.Tensor | None = None,
+                   w_scales: torch.Tensor | None = None, stream=None, _ptr=None) -> torch.Tensor:
+        """H = act(G) * U with [G | U] = alpha * X·W^T + bias (gemm_run_linear_glu): X (M x K) and W (2N x K: the gate's N rows
+        above the up projection's) 16-bit or 8-bit floats, H (M x N) float16 or bfloat16, bias (2N) float32 or H's type.
+        ``preact`` (M x 2N, N a multiple of 8), if given, receives [G | U].  8-bit operands may have block scales: x_scales as
+        for linear_scaled, w_scales (2 ceil(N/128) x ceil(K/128)) those of the gate's blocks above those of the up
+        projection's.  Async on `stream`."""
+        dt, dev = X.dtype, self._index
+        in_code = TORCH_TO_DTYPE_EX.get(dt)
+        if in_code is None:
+            raise TypeError("X and W must have the same 16-bit or 8-bit float type")
+        if X.dim() != 2 or W.dim() != 2:
+            raise ValueError("expected 2-D tensors")
+        (M, K), N2 = X.shape, W.shape[0]
+        if N2 & 1:
+            raise ValueError(f"W stacks two halves: an even number of rows, not {N2}")
+        N = N2 >> 1
+        if out_dtype is None:
+            out_dtype = out.dtype if out is not None else (dt if in_code <= DTYPE_BF16 else torch.bfloat16)
+        out_code = TORCH_TO_DTYPE.get(out_dtype)
+        if out_code is None or (in_code <= DTYPE_BF16 and out_code != in_code):
+            raise TypeError("H must be float16 or bfloat16, and of the operands' type if that is 16-bit")
+        if in_code <= DTYPE_BF16 and (x_scales is not None or w_scales is not None):
+            raise TypeError("block scales go with 8-bit operands")
+        ldx, ldw = _matrix(X, "X", M, K, dt, dev), _matrix(W, "W", N2, K, dt, dev)
+        bias_p = z_p = xs_p = ws_p = bias_code = ldz = ld_xs = ld_ws = 0
+        if bias is not None:
+            bias_code, bias_p = _vector(bias, "bias", N2, out_dtype, dev), bias.data_ptr()
+        if preact is not None:
+            ldz, z_p = _matrix(preact, "preact", M, N2, out_dtype, dev), preact.data_ptr()
+        if x_scales is not None:
+            ld_xs, xs_p = _scales(x_scales, "x_scales", M, -(-K // 128), dev), x_scales.data_ptr()
+        if w_scales is not None:
+            ld_ws, ws_p = _scales(w_scales, "w_scales", 2 * -(-N // 128), -(-K // 128), dev), w_scales.data_ptr()
+        if out is None:
+            out = _new(M, N, out_dtype, dev, stream)
+        ldh = _matrix(out, "out", M, N, out_dtype, dev)
+        a = gemm_glu_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, z_p, xs_p, ws_p, M, N, K, ldx, ldw, ldh, ldz, ld_xs,
+                            ld_ws, in_code, out_code, bias_code, _act(act), alpha)
+        st = self._lib.gemm_run_linear_glu(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        if st != OK:
+            raise GemmError(st, "gemm_run_linear_glu")
+        return out
+
+    def linear_glu_dgrad(self, dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor, act: str | None = "silu",
+                         out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
+                         beta_bias: float = 0.0, stream=None, _ptr=None) -> torch.Tensor:
+        """dZ = [d * U * act'(G) | d * act(G)] with d = alpha * dY·W (gemm_run_linear_glu_dgrad): dY (M x K), W (K x N, the layer
+        that takes H), Z = [G | U] (M x 2N, what linear_glu kept, N a multiple of 8) of one 16-bit type.  ``dbias`` (2N,
+        float32 or that type), if given, becomes beta_bias * dbias + the column sums of dZ.  linear_dgrad(dZ, W_glu) and
+        linear_wgrad(dZ, X) give the rest of the gated layer's gradients.  Async on `stream`."""
+        dt, dev, code = dY.dtype, self._index, _act(act)
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None:
+            raise TypeError("dY, W and Z must all be float16 or all bfloat16")
+        if dY.dim() != 2 or W.dim() != 2:
+            raise ValueError("expected 2-D tensors")
+        (M, K), N = dY.shape, W.shape[1]
+        lddy, ldw = _matrix(dY, "dY", M, K, dt, dev), _matrix(W, "W", K, N, dt, dev)
+        ldz = _matrix(Z, "Z", M, 2 * N, dt, dev)
+        if out is None:
+            out = _new(M, 2 * N, dt, dev, stream)
+        lddz = _matrix(out, "out", M, 2 * N, dt, dev)
+        db_p = db_code = ws_p = ws_bytes = 0
+        if dbias is not None:
+            db_code, db_p = _vector(dbias, "dbias", 2 * N, dt, dev), dbias.data_ptr()
+            ws_bytes = _sums_bytes(M, 2 * N)
+            if ws_bytes > OWN_SUMS_BYTES:
+                ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
+                ws_p = ws.data_ptr()
+        a = gemm_glu_dgrad_args_t(dY.data_ptr(), W.data_ptr(), Z.data_ptr(), out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy,
+                                  ldw, ldz, lddz, dt_code, db_code, code, alpha, beta_bias)
+        st = self._lib.gemm_run_linear_glu_dgrad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        if st != OK:
+            raise GemmError(st, "gemm_run_linear_glu_dgrad")
+        return out
+
+    def quantize(self, X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, stream=None, _ptr=None):
+        """8-bit values of a float16 or bfloat16 matrix with a float32 scale for each block of block_rows (1 or 128) x 128
+        (gemm_run_quantize): returns (Q, scales), X about Q times its scale.  ``dtype``: float8_e4m3fn (the default) or
+        float8_e5m2.  Async on `stream`."""
+        dt, dev = X.dtype, self._index
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None or X.dim() != 2:
+            raise TypeError("X must be a 2-D float16 or bfloat16 tensor")
+        if block_rows != 1 and block_rows != 128:
+            raise ValueError("block_rows is 1 or 128")
+        M, K = X.shape
+        if dtype is None:
+            dtype = out.dtype if out is not None else torch.float8_e4m3fn
+        q_code = TORCH_TO_DTYPE_EX.get(dtype)
+        if q_code is None or q_code <= DTYPE_BF16:
+            raise TypeError("Q must be float8_e4m3fn or float8_e5m2")
+        ldx, rows, cols = _matrix(X, "X", M, K, dt, dev), -(-M // block_rows), -(-K // 128)
+        if out is None:
+            out = _new(M, K, dtype, dev, stream)
+        if scales is None:
+            scales = _new(rows, cols, torch.float32, dev, stream)
+        ldq, lds = _matrix(out, "out", M, K, dtype, dev), _scales(scales, "scales", rows, cols, dev)
+        a = gemm_quantize_args_t(X.data_ptr(), out.data_ptr(), scales.data_ptr(), M, K, ldx, ldq, lds, dt_code, q_code, block_rows)
+        st = self._lib.gemm_run_quantize(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        if st != OK:
+            raise GemmError(st, "gemm_run_quantize")
+        return out, scales
+
+    def layer_norm(self, X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   eps: float = 1e-5, out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                   rstd: torch.Tensor | None = None, stream=None, _ptr=None) -> torch.Tensor:
+        """Y = (X - mean) * rstd * weight + bias over each row (gemm_run_layer_norm): X and Y (M x N) of one 16-bit type,
+        weight and bias (N) float32 or that type.  ``mean`` and ``rstd`` (M, float32), if given, receive the statistics;
+        ``out`` may be X itself.  Async on `stream`."""
+        dt, dev = X.dtype, self._index
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None or X.dim() != 2:
+            raise TypeError("X must be a 2-D float16 or bfloat16 tensor")
+        M, N = X.shape
+        ldx = _matrix(X, "X", M, N, dt, dev)
+        w_p = b_p = mean_p = rstd_p = w_code = b_code = 0
+        if weight is not None:
+            w_code, w_p = _vector(weight, "weight", N, dt, dev), weight.data_ptr()
+        if bias is not None:
+            b_code, b_p = _vector(bias, "bias", N, dt, dev), bias.data_ptr()
+        if mean is not None:
+            mean_p = _stat(mean, "mean", M, dev)
+        if rstd is not None:
+            rstd_p = _stat(rstd, "rstd", M, dev)
+        if out is None:
+            out = _new(M, N, dt, dev, stream)
+        ldy = _matrix(out, "out", M, N, dt, dev)
+        a = gemm_layer_norm_args_t(X.data_ptr(), out.data_ptr(), w_p, b_p, mean_p, rstd_p, M, N, ldx, ldy, dt_code, w_code,
+                                   b_code, eps)
+        st = self._lib.gemm_run_layer_norm(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        if st != OK:
+            raise GemmError(st, "gemm_run_layer_norm")
+        return out
+
+    def layer_norm_grad(self, dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                        dbias: torch.Tensor | None = None, beta: float = 0.0, stream=None, _ptr=None) -> torch.Tensor:
+        """dX of layer_norm, plus ``residual`` (gemm_run_layer_norm_grad): dY, X, residual and dX (M x N) of one 16-bit type,
+        mean and rstd (M, float32) as layer_norm kept them, weight (N) float32 or that type.  ``dweight`` and ``dbias`` (N,
+        float32 or that type), if given, become beta times themselves + the column sums.  ``out`` may be dY or
+        ``residual`` itself.  Async on `stream`."""
+        dt, dev = dY.dtype, self._index
+        dt_code = TORCH_TO_DTYPE.get(dt)
+        if dt_code is None or dY.dim() != 2:
+            raise TypeError("dY must be a 2-D float16 or bfloat16 tensor")
+        M, N = dY.shape
+        lddy, ldx = _matrix(dY, "dY", M, N, dt, dev), _matrix(X, "X", M, N, dt, dev)
+        mean_p, rstd_p = _stat(mean, "mean", M, dev), _stat(rstd, "rstd", M, dev)
+        res_p = w_p = dw_p = db_p = ws_p = ws_bytes = ldr = w_code = dw_code = db_code = 0
+        if weight is not None:
+            w_code, w_p = _vector(weight, "weight", N, dt, dev), weight.data_ptr()
+        if residual is not None:
+            ldr, res_p = _matrix(residual, "residual", M, N, dt, dev), residual.data_ptr()
+        if out is None:
+            out = _new(M, N, dt, dev, stream)
+        lddx = _matrix(out, "out", M, N, dt, dev)
+        if dweight is not None:
+            dw_code, dw_p = _vector(dweight, "dweight", N, dt, dev), dweight.data_ptr()
+        if dbias is not None:
+            db_code, db_p = _vector(dbias, "dbias", N, dt, dev), dbias.data_ptr()
+        if dw_p or db_p or N > 16384:
+            ws_bytes = _norm_bytes(M, N)
+            if ws_bytes > OWN_SUMS_BYTES:
+                ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
+                ws_p = ws.data_ptr()
+        a = gemm_layer_norm_grad_args_t(dY.data_ptr(), X.data_ptr(), res_p, mean_p, rstd_p, w_p, out.data_ptr(), dw_p, db_p,
+                                        ws_p, ws_bytes, M, N, lddy, ldx, ldr, lddx, dt_code, w_code, dw_code, db_code, beta)
+        st = self._lib.gemm_run_layer_norm_grad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        if st != OK:
+            raise GemmError(st, "gemm_run_layer_norm_grad")
+        return out
+
     def sync_status(self, stream=None) -> int:
         return int(self._lib.gemm_sync_status(self._h, _stream_ptr(stream) or None))
 
@@ -736,3 +1042,59 @@ def act_grad(dY: torch.Tensor, Z: torch.Tensor | None = None, act: str | None = 
     h, lock, ptr = _default_of(dY, stream)
     with lock:
         return h.act_grad(dY, Z, act, out, dbias, beta_bias, sums_only, stream, ptr)
+
+
+def linear_scaled(X: torch.Tensor, W: torch.Tensor, x_scales: torch.Tensor | None, w_scales: torch.Tensor | None,
+                  bias: torch.Tensor | None = None, act: str | None = None, residual: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                  out_dtype: torch.dtype | None = None, alpha: float = 1.0, stream=None) -> torch.Tensor:
+    """Gemm.linear_scaled on a default handle of the stream (see matmul)."""
+    h, lock, ptr = _default_of(X, stream)
+    with lock:
+        return h.linear_scaled(X, W, x_scales, w_scales, bias, act, residual, out, preact, out_dtype, alpha, stream, ptr)
+
+
+def linear_glu(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = "silu",
+               out: torch.Tensor | None = None, preact: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+               alpha: float = 1.0, x_scales: torch.Tensor | None = None, w_scales: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Gemm.linear_glu on a default handle of the stream (see matmul)."""
+    h, lock, ptr = _default_of(X, stream)
+    with lock:
+        return h.linear_glu(X, W, bias, act, out, preact, out_dtype, alpha, x_scales, w_scales, stream, ptr)
+
+
+def linear_glu_dgrad(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor, act: str | None = "silu",
+                     out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, alpha: float = 1.0,
+                     beta_bias: float = 0.0, stream=None) -> torch.Tensor:
+    """Gemm.linear_glu_dgrad on a default handle of the stream (see matmul)."""
+    h, lock, ptr = _default_of(dY, stream)
+    with lock:
+        return h.linear_glu_dgrad(dY, W, Z, act, out, dbias, alpha, beta_bias, stream, ptr)
+
+
+def quantize(X: torch.Tensor, block_rows: int = 1, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+             scales: torch.Tensor | None = None, stream=None):
+    """Gemm.quantize on a default handle of the stream (see matmul)."""
+    h, lock, ptr = _default_of(X, stream)
+    with lock:
+        return h.quantize(X, block_rows, dtype, out, scales, stream, ptr)
+
+
+def layer_norm(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, eps: float = 1e-5,
+               out: torch.Tensor | None = None, mean: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Gemm.layer_norm on a default handle of the stream (see matmul)."""
+    h, lock, ptr = _default_of(X, stream)
+    with lock:
+        return h.layer_norm(X, weight, bias, eps, out, mean, rstd, stream, ptr)
+
+
+def layer_norm_grad(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                    weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, dweight: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                    beta: float = 0.0, stream=None) -> torch.Tensor:
+    """Gemm.layer_norm_grad on a default handle of the stream (see matmul)."""
+    h, lock, ptr = _default_of(dY, stream)
+    with lock:
+        return h.layer_norm_grad(dY, X, mean, rstd, weight, residual, out, dweight, dbias, beta, stream, ptr)

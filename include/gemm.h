@@ -53,8 +53,8 @@ enum { GEMM_LAYOUT_NN = 0, GEMM_LAYOUT_TN = 1 };
 
 /* Element types.  F16 and BF16 serve as operand and output types; E4M3 and E5M2 (8-bit
  * floats: 1-4-3 with bias 7 and no infinities, 1-5-2 with bias 15) are operand types only,
- * accepted by gemm_run_ex and gemm_run_linear.  F32 is the type of biases, of bias gradients
- * and of weight gradients (the linear-layer entry points), never of A or B. */
+ * accepted by gemm_run_ex, gemm_run_linear, _glu and _scaled (and written by gemm_run_quantize).  F32 is
+ * the type of biases, of bias gradients and of weight gradients (the linear-layer entry points), never of A or B. */
 typedef int32_t gemm_dtype_t;
 enum { GEMM_DTYPE_F16 = 0, GEMM_DTYPE_BF16 = 1, GEMM_DTYPE_E4M3 = 2, GEMM_DTYPE_E5M2 = 3, GEMM_DTYPE_F32 = 4 };
 
@@ -495,6 +495,158 @@ gemm_status_t gemm_run_act_grad(gemm_handle_t h, const gemm_act_grad_args_t* arg
 /* Bytes of workspace for the column sums of an M x cols matrix: 4 * ceil(M / 32) * (cols rounded
  * up to 64); 0 when M or cols is 0. */
 int64_t gemm_bias_grad_workspace_bytes(int64_t M, int64_t cols);
+
+/* ---------------------------------------------------------------- gated feed-forward blocks
+ *
+ * What a block y = x + down(act(gate(n)) * up(n)), n = norm(x), takes beyond the linear layer's calls, trained in 16 bits
+ * and served in 8.  Activations, sums, alignment, aliasing, workspaces, options and status codes are those of the linear-layer
+ * section, except that gated products have no 128x128 tile (128x256 runs) and share no last tiles. */
+
+/* A gated layer: H = act(G) * U with G = alpha X Wg^T + bg, U = alpha X Wu^T + bu; H is rounded once, from the fp32 G and U.
+ *   - W: 2N x K, the rows of Wg above those of Wu; bias: 2N values (bg, then bu) of bias_dtype (F32, or out_dtype), or NULL.
+ *   - H: M x N.  Z: M x 2N, or NULL: receives G (columns 0 to N - 1) and U (columns N to 2N - 1).  So kept, a backward pass has
+ *     the gradients of both in one matrix too: with dZ from gemm_run_linear_glu_dgrad, dX = dZ W and dW = dZ^T X are
+ *     gemm_run_linear_dgrad and _wgrad of a layer of 2N outputs.  With Z, N must be a multiple of 8: both halves of a
+ *     row start on 16 bytes.
+ *   - dtype, out_dtype, alpha, K == 0, empty M and N: as for gemm_run_linear.
+ *   - x_scales, w_scales: 8-bit operands only, as for gemm_run_linear_scaled; w_scales has 2 ceil(N / 128) rows, first
+ *     those of Wg's blocks, then those of Wu's (each half's blocks start with its own row 0). */
+typedef struct {
+    const void* X;
+    const void* W;
+    void* H;
+    const void* bias;
+    void* Z;
+    const float* x_scales;
+    const float* w_scales;
+    int64_t M, N, K;
+    int64_t ldx, ldw, ldh, ldz, ld_xs, ld_ws;
+    gemm_dtype_t dtype;
+    gemm_dtype_t out_dtype;
+    gemm_dtype_t bias_dtype;
+    gemm_act_t act;
+    float alpha;
+} gemm_glu_args_t;
+
+gemm_status_t gemm_run_linear_glu(gemm_handle_t h, const gemm_glu_args_t* args, void* stream);
+
+/* Backward through the weights above a gated layer's H, and through the gate: with d = alpha dY W,
+ *   dZ = [d * U * act'(G) | d * act(G)], rounded, and dbias[n] = beta_bias * dbias[n] + sum over m of the fp32 dZ[m, n].
+ *   - dY: M x K, W: K x N (the layer that takes H: K outputs, N inputs), Z: M x 2N (kept by gemm_run_linear_glu), dZ:
+ *     M x 2N, all of type dtype (F16 or BF16).  N must be a multiple of 8.
+ *   - dbias: 2N values of dbias_dtype (F32, or dtype), or NULL; workspace as for gemm_run_linear_dgrad, with
+ *     gemm_bias_grad_workspace_bytes(M, 2 N).
+ *   - N == 0 is a no-op; with M == 0 dbias becomes beta_bias * dbias; with K == 0 d is zero. */
+typedef struct {
+    const void* dY;
+    const void* W;
+    const void* Z;
+    void* dZ;
+    void* dbias;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t M, N, K;
+    int64_t lddy, ldw, ldz, lddz;
+    gemm_dtype_t dtype;
+    gemm_dtype_t dbias_dtype;
+    gemm_act_t act;
+    float alpha;
+    float beta_bias;
+} gemm_glu_dgrad_args_t;
+
+gemm_status_t gemm_run_linear_glu_dgrad(gemm_handle_t h, const gemm_glu_dgrad_args_t* args, void* stream);
+
+/* gemm_run_linear of 8-bit operands with a scale for each block of 128:
+ *   z[m, n] = alpha sum over j of xs[m, j] ws[n / 128, j] (sum over k in [128 j, 128 j + 128) of X[m, k] W[n, k]) + bias[n].
+ *   - dtype: E4M3 or E5M2; the rest of args as for gemm_run_linear.
+ *   - x_scales: fp32, row m at x_scales + m * ld_xs; w_scales: fp32, row i (of the weights' rows [128 i, 128 i + 128)) at
+ *     w_scales + i * ld_ws; pitches of at least ceil(K / 128).  Either may be NULL: its scales are 1.
+ * Each block's product is summed on the tensor cores, scaled in fp32 and added to an fp32 sum with one rounding. */
+gemm_status_t gemm_run_linear_scaled(gemm_handle_t h, const gemm_linear_args_t* args, const float* x_scales, int64_t ld_xs,
+                                     const float* w_scales, int64_t ld_ws, void* stream);
+
+/* 8-bit values of X (M x K of dtype, F16 or BF16) and a scale for each block of block_rows x 128 elements (block_rows is 1 or
+ * 128; the last blocks of a row or column may be smaller).  With a the block's largest magnitude and F the largest number of
+ * q_dtype (448 for E4M3, 57344 for E5M2):
+ *   s = max(a / F, 2^-126),  r = 1 / s,  q = x r,
+ * each rounded to fp32 (to nearest even), q then to q_dtype (to nearest even; magnitudes over F become F).  So X is about
+ * Q times its scale.  A NaN makes every value of its block NaN; an infinity is a NaN among zeros whose scale is
+ * infinite, so that all of them stand for NaN.
+ *   - Q: M x K of q_dtype (E4M3 or E5M2); scales: row i (of the rows [block_rows i, block_rows (i + 1))) at scales + i *
+ *     lds, lds >= ceil(K / 128).  M == 0 or K == 0 is a no-op. */
+typedef struct {
+    const void* X;
+    void* Q;
+    float* scales;
+    int64_t M, K;
+    int64_t ldx, ldq, lds;
+    gemm_dtype_t dtype;
+    gemm_dtype_t q_dtype;
+    int32_t block_rows;
+} gemm_quantize_args_t;
+
+gemm_status_t gemm_run_quantize(gemm_handle_t h, const gemm_quantize_args_t* args, void* stream);
+
+/* Layer norm over each row: Y = (X - mean) rstd weight + bias, mean the row's mean, rstd = 1 / sqrt(v + eps), v the mean of
+ * (X - mean)^2; statistics in fp32.
+ *   - X, Y: M x N of type dtype (F16 or BF16); Y may be X itself (same pointer and pitch).
+ *   - weight, bias: N values of their dtype (F32, or dtype), or NULL (1, 0).  mean, rstd: M fp32 values each, or NULL:
+ *     receive the statistics, which a backward pass reads.  eps: finite, >= 0.
+ *   - M == 0 or N == 0 is a no-op. */
+typedef struct {
+    const void* X;
+    void* Y;
+    const void* weight;
+    const void* bias;
+    float* mean;
+    float* rstd;
+    int64_t M, N;
+    int64_t ldx, ldy;
+    gemm_dtype_t dtype;
+    gemm_dtype_t weight_dtype;
+    gemm_dtype_t bias_dtype;
+    float eps;
+} gemm_layer_norm_args_t;
+
+gemm_status_t gemm_run_layer_norm(gemm_handle_t h, const gemm_layer_norm_args_t* args, void* stream);
+
+/* Its backward pass.  With x^ = (X - mean) rstd and g = dY weight, means over the row:
+ *   dX = rstd (g - mean(g) - x^ mean(g x^)) + residual,
+ *   dweight[n] = beta dweight[n] + sum over m of dY x^,   dbias[n] = beta dbias[n] + sum over m of dY.
+ *   - dY, X, residual, dX: M x N of type dtype; residual (the gradient that reaches X past the norm) may be NULL.  dX may be
+ *     dY or the residual itself (same pointer and pitch).
+ *   - mean, rstd: as gemm_run_layer_norm kept them.  weight: N values of its dtype (F32, or dtype), or NULL (1).
+ *   - dweight, dbias: N values of their dtypes (F32, or dtype), or NULL; not read with beta == 0.
+ *   - workspace: gemm_layer_norm_grad_workspace_bytes(M, N) bytes, 16-byte aligned, that the call may overwrite until its
+ *     kernels are done (fewer: INVALID_ARG).  It may be NULL if those are at most GEMM_OWN_SUMS_BYTES, or
+ *     if neither dweight nor dbias is wanted and N is at most 16384.
+ *   - N == 0 is a no-op; with M == 0 dweight and dbias become beta times themselves. */
+typedef struct {
+    const void* dY;
+    const void* X;
+    const void* residual;
+    const float* mean;
+    const float* rstd;
+    const void* weight;
+    void* dX;
+    void* dweight;
+    void* dbias;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t M, N;
+    int64_t lddy, ldx, ldr, lddx;
+    gemm_dtype_t dtype;
+    gemm_dtype_t weight_dtype;
+    gemm_dtype_t dweight_dtype;
+    gemm_dtype_t dbias_dtype;
+    float beta;
+} gemm_layer_norm_grad_args_t;
+
+gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_grad_args_t* args, void* stream);
+
+/* Bytes of workspace for gemm_run_layer_norm_grad: 8 * min(M, 304) * (N rounded up to 64), and 8 M more where N is over
+ * 16384; 0 when M or N is 0. */
+int64_t gemm_layer_norm_grad_workspace_bytes(int64_t M, int64_t N);
 
 /* ---------------------------------------------------------------- status and version */
 

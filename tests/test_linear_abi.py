@@ -132,3 +132,36 @@ def test_module_functions_refuse_host_tensors(lib):
     for call in (lambda: lib.linear(x, x), lambda: lib.linear_dgrad(x, x), lambda: lib.linear_wgrad(x, x), lambda: lib.act_grad(x)):
         with pytest.raises(ValueError):
             call()
+
+
+GATED_STRUCTS = ["gemm_glu_args_t", "gemm_glu_dgrad_args_t", "gemm_quantize_args_t", "gemm_layer_norm_args_t",
+                 "gemm_layer_norm_grad_args_t"]
+
+
+def test_gated_structs_are_laid_out_as_the_c_compiler_does(lib, tmp_path, monkeypatch):
+    monkeypatch.setitem(globals(), "STRUCTS", GATED_STRUCTS)
+    test_structs_are_laid_out_as_the_c_compiler_does(lib, tmp_path)
+
+
+def test_gated_null_handles_and_arguments(lib):
+    so = lib.load()
+    for name, struct in zip(("gemm_run_linear_glu", "gemm_run_linear_glu_dgrad", "gemm_run_quantize", "gemm_run_layer_norm",
+                             "gemm_run_layer_norm_grad"), GATED_STRUCTS):
+        assert getattr(so, name)(None, None, None) == lib.ERR_INVALID_ARG
+        assert getattr(so, name)(None, ctypes.byref(getattr(lib, struct)()), None) == lib.ERR_INVALID_ARG
+    assert so.gemm_run_linear_scaled(None, None, None, 0, None, 0, None) == lib.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M,N,want", [(0, 5, 0), (5, 0, 0), (1, 1, 512), (65, 1000, 8 * 65 * 1024), (5000, 64, 8 * 304 * 64),
+                                      (7, 20000, 8 * 7 * 20032 + 56)])
+def test_norm_workspace_bytes(lib, M, N, want):
+    assert lib.layer_norm_grad_workspace_bytes(M, N) == want == lib._norm_bytes(M, N)
+
+
+def test_gated_module_functions_refuse_host_tensors(lib):
+    x, x8 = torch.zeros((8, 8), dtype=torch.float16), torch.zeros((8, 8), dtype=torch.float8_e4m3fn)
+    s = torch.zeros(8)
+    for call in (lambda: lib.linear_glu(x, x), lambda: lib.linear_glu_dgrad(x, x, x), lambda: lib.linear_scaled(x8, x8, None, None),
+                 lambda: lib.quantize(x), lambda: lib.layer_norm(x), lambda: lib.layer_norm_grad(x, x, s, s)):
+        with pytest.raises(ValueError):
+            call()
