@@ -4,6 +4,9 @@
 // Layer norm.  A row belongs to WARPS warps, CHUNKS times 8 elements (16 bytes) a lane, so statistics are taken in two passes
 // over registers: the mean, then the mean square of x - mean, without the cancellation of E[x^2] - mean^2.  Rows of more
 // elements than registers hold are read again for every pass.
+//   A block takes rows b, b + grid, ... and keeps the loads of the next ones in flight: every lane copies its own chunks of
+// the rows ahead into its own places of a ring in shared memory (cp.async), which it alone reads, so the ring needs no
+// barrier.
 //
 // Backward, with x^ = (x - mean) rstd and g = dy w:
 //   dx = rstd (g - mean(g) - x^ mean(g x^)) + residual,   dw = sum over rows of dy x^,   db = sum over rows of dy.
@@ -20,7 +23,10 @@
 namespace dtg {
 namespace linear {
 
-constexpr int kNormMaxBlocks = 304;     // rows of partial sums: two blocks on each of 152 SMs
+// Rows ahead whose loads are in flight, and blocks per SM (64 registers a thread; backward: 128).
+constexpr int kNormStages = 3, kNormGradStages = 2;
+constexpr int norm_blocks_per_sm(int threads) { return 1024 / threads; }
+constexpr int norm_grad_blocks_per_sm(int threads) { return 512 / threads; }
 constexpr int64_t kNormMaxHeld = 16384;  // longest row that is kept in registers
 
 // A parameter or gradient vector of fp32 or of the matrices' 16-bit type; null: absent.
@@ -89,6 +95,23 @@ __device__ __forceinline__ void store_row8(uint16_t* row, int64_t c, int64_t n, 
         if (c + e < n) row[c + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
 }
 
+// Start the copy of elements [c, c + 8) of a 16-bit row to 16 bytes of shared memory: zeros from column n on, which is not
+// read.
+__device__ __forceinline__ void copy_row8(uint32_t to, const uint16_t* row, int64_t c, int64_t n)
+{
+    const int64_t left = 2 * (n - c);
+    const int bytes = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(row + (left > 0 ? c : 0)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <bool BF16>
 __device__ __forceinline__ void unpack8(f32x2 (&v)[4], uint4 w)
 {
@@ -143,65 +166,81 @@ struct NormParams {
     float eps;
 };
 
-// ROWS rows per block (more than one: WARPS is 1).
+// ROWS rows per block at once (more than one: WARPS is 1).  Dynamic shared memory: kNormStages * CHUNKS * 16 bytes a thread.
 template <bool BF16, int WARPS, int CHUNKS, int ROWS>
-__global__ void __launch_bounds__(WARPS * ROWS * 32) layer_norm_kernel(const NormParams p)
+__global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * ROWS * 32)) layer_norm_kernel(const NormParams p)
 {
     static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
+    constexpr int kThreads = WARPS * ROWS * 32;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 shared[2][WARPS];
     const int t = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x;
+    const uint32_t mine = ptx::smem_addr(ring) + 16u * threadIdx.x;
+    auto slot = [&](int stage, int k) { return mine + 16u * kThreads * static_cast<uint32_t>(stage * CHUNKS + k); };
+    auto column = [&](int k) { return (k * WARPS * 32 + t) * int64_t(8); };
+    const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
+    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? threadIdx.x >> 5 : 0);
+    auto fetch = [&](int stage, int64_t r) {
+        if (r < p.M) {
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k) copy_row8(slot(stage, k), p.X + r * p.ldx, column(k), p.N);
+        }
+        copies_commit();
+    };
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    const int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? threadIdx.x >> 5 : 0);
-    if (row >= p.M) return;  // (a whole warp, and no barrier follows where rows are warps)
-    const uint16_t* const x = p.X + row * p.ldx;
-    uint4 raw[CHUNKS];
-    f32x2 v[CHUNKS][4];
-    f32x2 sum = 0;
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) raw[k] = load_row8(x, (k * WARPS * 32 + t) * int64_t(8), p.N);
-#pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) {
-        unpack8<BF16>(v[k], raw[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum = add2(sum, v[k][i]);
-    }
+    for (int st = 0; st < kNormStages; ++st) fetch(st, row + st * step);
     const float n = static_cast<float>(p.N);
-    const float mean = row_sums<WARPS>(make_float2(sum_of(sum), 0.0f), shared, 0).x / n;
-    float sq = 0.0f;
+    int stage = 0;
+    for (; row < p.M; row += step) {
+        copies_wait<kNormStages - 1>();
+        f32x2 v[CHUNKS][4];
+        f32x2 sum = 0;
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) {
-        const int64_t c = (k * WARPS * 32 + t) * int64_t(8);
-        f32x2 s = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[k][i] = add2(v[k][i], both(-mean));
-            if (c + 2 * i + 1 < p.N) {
-                s = fma2(v[k][i], v[k][i], s);
-            } else if (c + 2 * i < p.N) {
-                float lo, hi;
-                split(v[k][i], lo, hi);
-                sq = fmaf(lo, lo, sq);
-            }
+        for (int k = 0; k < CHUNKS; ++k) {
+            unpack8<BF16>(v[k], ld_shared_u4(slot(stage, k)));
+            sum = add2(sum, add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
         }
-        sq += sum_of(s);
-    }
-    const float rstd = 1.0f / sqrtf(row_sums<WARPS>(make_float2(sq, 0.0f), shared, 1).x / n + p.eps);
-    if (t == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    uint16_t* const y = p.Y + row * p.ldy;
+        // (Divided, not multiplied by 1 / n: a row of one value has exactly that mean, and no variance.)
+        const float mean = row_sums<WARPS>(make_float2(sum_of(sum), 0.0f), shared, 0).x / n;
+        // The sum has used what was in the slot.
+        fetch(stage, row + kNormStages * step);
+        stage = stage + 1 == kNormStages ? 0 : stage + 1;
+        f32x2 sq = 0;
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) {
-        const int64_t c = (k * WARPS * 32 + t) * int64_t(8);
-        if (c >= p.N) break;
-        f32x2 w[4], b[4];
-        load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
-        load_vector8<BF16>(b, p.b, c, p.N, 0.0f);
+        for (int k = 0; k < CHUNKS; ++k) {
+            const int64_t c = column(k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = fma2(mul2(v[k][i], both(rstd)), w[i], b[i]);
-        store_row8(y, c, p.N, round8<BF16>(b));
+            for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], both(-mean));
+            if (c + 8 > p.N) {  // nothing past the row's end counts
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    split(v[k][i], lo, hi);
+                    v[k][i] = pair(c + 2 * i < p.N ? lo : 0.0f, c + 2 * i + 1 < p.N ? hi : 0.0f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq = fma2(v[k][i], v[k][i], sq);
+        }
+        const float rstd = 1.0f / sqrtf(row_sums<WARPS>(make_float2(sum_of(sq), 0.0f), shared, 1).x / n + p.eps);
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        uint16_t* const y = p.Y + row * p.ldy;
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+            const int64_t c = column(k);
+            if (c >= p.N) break;
+            f32x2 w[4], b[4];
+            load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
+            load_vector8<BF16>(b, p.b, c, p.N, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = fma2(mul2(v[k][i], both(rstd)), w[i], b[i]);
+            store_row8(y, c, p.N, round8<BF16>(b));
+        }
     }
 }
 
@@ -276,36 +315,52 @@ __device__ __forceinline__ uint4 norm_dx8(const f32x2 (&g)[4], const f32x2 (&h)[
     return round8<BF16>(d);
 }
 
-// ROWS rows of a block at once (more than one: WARPS is 1), joined in shared memory at the end.
+// ROWS rows of a block at once (more than one: WARPS is 1), joined in shared memory at the end.  Dynamic shared memory:
+// kNormGradStages * 3 * CHUNKS * 16 bytes a thread, for dy, x and the residual.
 template <bool BF16, int WARPS, int CHUNKS, int ROWS>
-__global__ void __launch_bounds__(WARPS * ROWS * 32) layer_norm_grad_kernel(const NormGradParams p)
+__global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WARPS * ROWS * 32))
+    layer_norm_grad_kernel(const NormGradParams p)
 {
     static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
+    static_assert(kNormGradStages == 2, "row_sums takes the stage for its parity");
+    constexpr int kThreads = WARPS * ROWS * 32;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 shared[2][WARPS];
     const int t = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int slot = ROWS > 1 ? threadIdx.x >> 5 : 0;
+    const int group = ROWS > 1 ? threadIdx.x >> 5 : 0;
+    const uint32_t mine = ptx::smem_addr(ring) + 16u * threadIdx.x;
+    auto slot = [&](int stage, int which, int k) { return mine + 16u * kThreads * static_cast<uint32_t>((stage * 3 + which) * CHUNKS + k); };
+    auto column = [&](int k) { return (k * WARPS * 32 + t) * int64_t(8); };
+    const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
+    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + group;
+    auto fetch = [&](int stage, int64_t r) {
+        if (r < p.M) {
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k) {
+                copy_row8(slot(stage, 0, k), p.dY + r * p.lddy, column(k), p.N);
+                copy_row8(slot(stage, 1, k), p.X + r * p.ldx, column(k), p.N);
+                if (p.residual) copy_row8(slot(stage, 2, k), p.residual + r * p.ldr, column(k), p.N);
+            }
+        }
+        copies_commit();
+    };
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
+#pragma unroll
+    for (int st = 0; st < kNormGradStages; ++st) fetch(st, row + st * step);
     f32x2 dw[CHUNKS][4] = {}, db[CHUNKS][4] = {};
     const float inv_n = 1.0f / static_cast<float>(p.N);
-    int parity = 0;
-    for (int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + slot; row < p.M; row += gridDim.x * static_cast<int64_t>(ROWS)) {
-        uint4 dy[CHUNKS], x[CHUNKS];
-#pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = (k * WARPS * 32 + t) * int64_t(8);
-            dy[k] = load_row8(p.dY + row * p.lddy, c, p.N);
-            x[k] = load_row8(p.X + row * p.ldx, c, p.N);
-        }
+    int stage = 0;
+    for (; row < p.M; row += step) {
         const float mean = p.mean[row], rstd = p.rstd[row];
+        copies_wait<kNormGradStages - 1>();
         f32x2 s1 = 0, s2 = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = (k * WARPS * 32 + t) * int64_t(8);
             f32x2 g[4], h[4], w[4];
-            unpack8<BF16>(g, dy[k]);
-            unpack8<BF16>(h, x[k]);
-            load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
+            unpack8<BF16>(g, ld_shared_u4(slot(stage, 0, k)));
+            unpack8<BF16>(h, ld_shared_u4(slot(stage, 1, k)));
+            load_vector8<BF16>(w, p.w, column(k), p.N, 1.0f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // Past the row's end dy is 0, so x^ counts nowhere.
@@ -317,19 +372,18 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) layer_norm_grad_kernel(cons
                 s2 = fma2(g[i], h[i], s2);
             }
         }
-        float2 c12 = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared, parity);
-        parity ^= 1;
+        float2 c12 = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared, stage & 1);
         c12.x *= inv_n;
         c12.y *= inv_n;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = (k * WARPS * 32 + t) * int64_t(8);
+            const int64_t c = column(k);
             if (c >= p.N) break;
             f32x2 g[4], h[4], w[4];
             uint4 res = make_uint4(0, 0, 0, 0);
-            if (p.residual) res = load_row8(p.residual + row * p.ldr, c, p.N);
-            unpack8<BF16>(g, dy[k]);
-            unpack8<BF16>(h, x[k]);
+            if (p.residual) res = ld_shared_u4(slot(stage, 2, k));
+            unpack8<BF16>(g, ld_shared_u4(slot(stage, 0, k)));
+            unpack8<BF16>(h, ld_shared_u4(slot(stage, 1, k)));
             load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -338,6 +392,9 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) layer_norm_grad_kernel(cons
             }
             store_row8(p.dX + row * p.lddx, c, p.N, norm_dx8<BF16>(g, h, c12, rstd, p.residual != nullptr, res));
         }
+        // The stores have used what was in the slots.
+        fetch(stage, row + kNormGradStages * step);
+        stage = stage + 1 == kNormGradStages ? 0 : stage + 1;
     }
     if (!p.dw && !p.db) return;
     // This block's sums: of its one row group, or of ROWS warps by way of shared memory.
@@ -347,8 +404,8 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) layer_norm_grad_kernel(cons
         for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                parts[0][slot][(k * 32 + t) * 4 + i] = dw[k][i];
-                parts[1][slot][(k * 32 + t) * 4 + i] = db[k][i];
+                parts[0][group][(k * 32 + t) * 4 + i] = dw[k][i];
+                parts[1][group][(k * 32 + t) * 4 + i] = db[k][i];
             }
         __syncthreads();
         for (int e = threadIdx.x; e < 2 * CHUNKS * 32 * 4; e += ROWS * 32) {
@@ -472,20 +529,29 @@ __device__ __forceinline__ uint32_t to_f8x2(f32x2 v)
     return r;
 }
 
-// The largest magnitude of eight values, NaN if one of them is.
-template <bool BF16>
-__device__ __forceinline__ float largest8(uint4 raw)
+// Magnitudes of 16-bit floats order as their bits without the sign do, NaNs above infinity: the largest of two words' halves.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
-    f32x2 v[4];
-    unpack8<BF16>(v, raw);
-    float a = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        split(v[i], lo, hi);
-        a = max_nan(a, max_nan(fabsf(lo), fabsf(hi)));
-    }
-    return a;
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The largest magnitudes of eight values' even and odd ones.
+__device__ __forceinline__ uint32_t largest8(uint4 raw)
+{
+    constexpr uint32_t kNoSigns = 0x7FFF7FFFu;
+    return max_u16x2(max_u16x2(raw.x & kNoSigns, raw.y & kNoSigns), max_u16x2(raw.z & kNoSigns, raw.w & kNoSigns));
+}
+
+// The larger magnitude of a word's halves.
+template <bool BF16>
+__device__ __forceinline__ float larger_half(uint32_t w)
+{
+    f32x2 v = unpack2<BF16>(max_u16x2(w, w >> 16));
+    float lo, hi;
+    split(v, lo, hi);
+    return lo;
 }
 
 template <bool E5M2>
@@ -526,6 +592,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
     // Blocks of rows beyond the grid's second dimension are taken in turn.
     for (int64_t r0 = blockIdx.y * kBlockRows; r0 < p.M; r0 += gridDim.y * kBlockRows) {
         uint4 raw[kQuantRows];
+        uint32_t largest[kQuantRows];
 #pragma unroll
         for (int u = 0; u < kQuantRows; ++u) {
             const int64_t row = r0 + u * kQuantWarps + warp;
@@ -534,15 +601,24 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
         }
 #pragma unroll
         for (int u = 0; u < kQuantRows; ++u) {
-            const int64_t row = r0 + u * kQuantWarps + warp;
-            float a = largest8<BF16>(raw[u]);
+            largest[u] = largest8(raw[u]);
 #pragma unroll
-            for (int off = 8; off > 0; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, off));
-            const float s = scale_for<E5M2>(a);
-            if (row < p.M && c < p.K) {
-                store_f8x8<BF16, E5M2>(p.Q + row * p.ldq, c, p.K, raw[u], __frcp_rn(s));
-                if ((lane & 15) == 0) p.S[row * p.lds + c / kScaleCols] = s;
-            }
+            for (int off = 8; off > 0; off >>= 1) largest[u] = max_u16x2(largest[u], __shfl_xor_sync(0xFFFFFFFFu, largest[u], off));
+        }
+        // Lane u of a block's 16 divides for row u: one division and one reciprocal for all rows.
+        uint32_t own = largest[0];
+#pragma unroll
+        for (int u = 1; u < kQuantRows; ++u) own = (lane & 15) == u ? largest[u] : own;
+        const float s = scale_for<E5M2>(larger_half<BF16>(own)), inverse = __frcp_rn(s);
+        if ((lane & 15) < kQuantRows && (c - (lane & 15) * 8) < p.K) {
+            const int64_t row = r0 + (lane & 15) * kQuantWarps + warp;
+            if (row < p.M) p.S[row * p.lds + c / kScaleCols] = s;
+        }
+#pragma unroll
+        for (int u = 0; u < kQuantRows; ++u) {
+            const int64_t row = r0 + u * kQuantWarps + warp;
+            const float r = __shfl_sync(0xFFFFFFFFu, inverse, (lane & 16) + u);
+            if (row < p.M && c < p.K) store_f8x8<BF16, E5M2>(p.Q + row * p.ldq, c, p.K, raw[u], r);
         }
     }
 }
@@ -551,29 +627,29 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
 template <bool BF16, bool E5M2>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const QuantizeParams p)
 {
-    __shared__ float largest[8];
+    __shared__ uint32_t largest[8];
     const int64_t c = blockIdx.x * static_cast<int64_t>(kScaleCols) + (threadIdx.x & 15) * 8;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     for (int64_t rb = blockIdx.y; rb * kScaleCols < p.M; rb += gridDim.y) {
         const int64_t r0 = rb * kScaleCols + (threadIdx.x >> 4);
         uint4 raw[8];
-        float a = 0.0f;
+        uint32_t a = 0;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             raw[u] = make_uint4(0, 0, 0, 0);
             if (r0 + 16 * u < p.M) raw[u] = load_row8(p.X + (r0 + 16 * u) * p.ldx, c, p.K);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) a = max_nan(a, largest8<BF16>(raw[u]));
+        for (int u = 0; u < 8; ++u) a = max_u16x2(a, largest8(raw[u]));
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, off));
+        for (int off = 16; off > 0; off >>= 1) a = max_u16x2(a, __shfl_xor_sync(0xFFFFFFFFu, a, off));
         __syncthreads();  // the block before has been read
         if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = a;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < 8; ++w) a = max_nan(a, largest[w]);
-        const float s = scale_for<E5M2>(a), r = __frcp_rn(s);
+        for (int w = 0; w < 8; ++w) a = max_u16x2(a, largest[w]);
+        const float s = scale_for<E5M2>(larger_half<BF16>(a)), r = __frcp_rn(s);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (r0 + 16 * u < p.M && c < p.K) store_f8x8<BF16, E5M2>(p.Q + (r0 + 16 * u) * p.ldq, c, p.K, raw[u], r);

@@ -28,45 +28,77 @@ NormVector vector_of(const void* at, gemm_dtype_t t) { return {at, t == GEMM_DTY
 
 unsigned blocks_for(int64_t rows, int64_t per_block) { return static_cast<unsigned>(cdiv(rows, per_block)); }
 
-template <bool BF16>
-gemm_status_t launch_norm(const NormParams& p, cudaStream_t s)
+// A persistent kernel over M rows whose threads hold `slots` 16-byte places each of dynamic shared memory.
+template <class P>
+gemm_status_t launch_rows(gemm_handle_t h, void (*fn)(P), int slot, int64_t blocks, int threads, int slots, const P& p, cudaStream_t s)
 {
-    // Warps, 16-byte chunks a lane, and rows a block, by the row's length: short rows are a warp each.
-    if (p.N <= 256) return launch_after(&layer_norm_kernel<BF16, 1, 1, 8>, blocks_for(p.M, 8), 256, 0, s, p);
-    if (p.N <= 512) return launch_after(&layer_norm_kernel<BF16, 1, 2, 8>, blocks_for(p.M, 8), 256, 0, s, p);
-    if (p.N <= 1024) return launch_after(&layer_norm_kernel<BF16, 4, 1, 1>, blocks_for(p.M, 1), 128, 0, s, p);
-    if (p.N <= 2048) return launch_after(&layer_norm_kernel<BF16, 4, 2, 1>, blocks_for(p.M, 1), 128, 0, s, p);
-    if (p.N <= 4096) return launch_after(&layer_norm_kernel<BF16, 8, 2, 1>, blocks_for(p.M, 1), 256, 0, s, p);
-    if (p.N <= 8192) return launch_after(&layer_norm_kernel<BF16, 16, 2, 1>, blocks_for(p.M, 1), 512, 0, s, p);
-    if (p.N <= kNormMaxHeld) return launch_after(&layer_norm_kernel<BF16, 32, 2, 1>, blocks_for(p.M, 1), 1024, 0, s, p);
-    return launch_after(&layer_norm_wide_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
+    const int smem = 16 * slots * threads;
+    if (!h->dev.attrs_set[kNormSlot0 + slot]) {
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        h->dev.attrs_set[kNormSlot0 + slot] = true;
+    }
+    return launch_after(fn, static_cast<unsigned>(blocks), threads, static_cast<size_t>(smem), s, p);
 }
 
-// Rows of partial sums of dw and db.
-int64_t norm_grad_blocks(int64_t M) { return std::min<int64_t>(M, kNormMaxBlocks); }
+// The shape of the kernel for rows of N <= kNormMaxHeld: warps and 16-byte chunks a lane for a row, rows a block.  Short rows
+// are a warp each.  (Forward and backward have instantiations of their own, so that each keeps to its registers.)
+struct NormShape {
+    int warps, chunks, rows;
+    int threads() const { return 32 * warps * rows; }
+};
+constexpr NormShape kNormShapes[] = {{1, 1, 8}, {1, 2, 8}, {4, 1, 1}, {4, 2, 1}, {8, 2, 1}, {16, 2, 1}, {32, 2, 1}};
+constexpr NormShape kNormGradShapes[] = {{1, 1, 8}, {1, 2, 8}, {4, 1, 1}, {4, 2, 1}, {8, 2, 1}, {16, 2, 1}, {16, 4, 1}};
+constexpr int kNormKernels = 7;
+
+int shape_for(int64_t N)
+{
+    int i = 0;
+    for (int64_t n = 256; n < N; n *= 2) ++i;
+    return i;  // 256, 512, 1024, ..., 16384 elements
+}
 
 template <bool BF16>
-gemm_status_t launch_norm_grad(const NormGradParams& q, int64_t* blocks, cudaStream_t s)
+gemm_status_t launch_norm(gemm_handle_t h, const NormParams& p, cudaStream_t s)
+{
+    if (p.N > kNormMaxHeld) return launch_after(&layer_norm_wide_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
+    constexpr void (*kFn[kNormKernels])(const NormParams) = {
+        &layer_norm_kernel<BF16, 1, 1, 8>, &layer_norm_kernel<BF16, 1, 2, 8>,  &layer_norm_kernel<BF16, 4, 1, 1>, &layer_norm_kernel<BF16, 4, 2, 1>,
+        &layer_norm_kernel<BF16, 8, 2, 1>, &layer_norm_kernel<BF16, 16, 2, 1>, &layer_norm_kernel<BF16, 32, 2, 1>};
+    const int i = shape_for(p.N);
+    const NormShape shape = kNormShapes[i];
+    const int64_t blocks = std::min<int64_t>(cdiv(p.M, shape.rows), h->dev.num_sms * norm_blocks_per_sm(shape.threads()));
+    return launch_rows<NormParams>(h, kFn[i], i + kNormKernels * BF16, blocks, shape.threads(), kNormStages * shape.chunks, p, s);
+}
+
+// Most rows of partial sums of dw and db: blocks that run at once on 152 SMs (fewer SMs: fewer; more: no more).
+int64_t norm_grad_max_blocks(int64_t M, int64_t N)
+{
+    return std::min<int64_t>(M, 152 * (N > kNormMaxHeld ? 2 : norm_grad_blocks_per_sm(kNormGradShapes[shape_for(N)].threads())));
+}
+
+template <bool BF16>
+gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, cudaStream_t s)
 {
     NormGradParams p = q;
+    const int64_t most = norm_grad_max_blocks(p.M, p.N);
     if (p.N > kNormMaxHeld) {
         const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
         if (st != GEMM_OK) return st;
-        p.block_rows = cdiv(p.M, norm_grad_blocks(cdiv(p.M, 32)));
+        p.block_rows = cdiv(p.M, std::min(cdiv(p.M, 32), most));
         *blocks = cdiv(p.M, p.block_rows);
         return launch_after(&layer_norm_grad_wide_kernel<BF16>, dim3(blocks_for(p.N, kStripCols), static_cast<unsigned>(*blocks)),
                             kStripWarps * 32, 0, s, p);
     }
-    const int64_t rows = p.N <= 512 ? 8 : 1;  // of a block at once
-    *blocks = norm_grad_blocks(cdiv(p.M, rows));
-    const unsigned n = static_cast<unsigned>(*blocks);
-    if (p.N <= 256) return launch_after(&layer_norm_grad_kernel<BF16, 1, 1, 8>, n, 256, 0, s, p);
-    if (p.N <= 512) return launch_after(&layer_norm_grad_kernel<BF16, 1, 2, 8>, n, 256, 0, s, p);
-    if (p.N <= 1024) return launch_after(&layer_norm_grad_kernel<BF16, 4, 1, 1>, n, 128, 0, s, p);
-    if (p.N <= 2048) return launch_after(&layer_norm_grad_kernel<BF16, 4, 2, 1>, n, 128, 0, s, p);
-    if (p.N <= 4096) return launch_after(&layer_norm_grad_kernel<BF16, 8, 2, 1>, n, 256, 0, s, p);
-    if (p.N <= 8192) return launch_after(&layer_norm_grad_kernel<BF16, 16, 2, 1>, n, 512, 0, s, p);
-    return launch_after(&layer_norm_grad_kernel<BF16, 16, 4, 1>, n, 512, 0, s, p);
+    constexpr void (*kFn[kNormKernels])(const NormGradParams) = {
+        &layer_norm_grad_kernel<BF16, 1, 1, 8>, &layer_norm_grad_kernel<BF16, 1, 2, 8>,  &layer_norm_grad_kernel<BF16, 4, 1, 1>,
+        &layer_norm_grad_kernel<BF16, 4, 2, 1>, &layer_norm_grad_kernel<BF16, 8, 2, 1>, &layer_norm_grad_kernel<BF16, 16, 2, 1>,
+        &layer_norm_grad_kernel<BF16, 16, 4, 1>};
+    const int i = shape_for(p.N);
+    const NormShape shape = kNormGradShapes[i];
+    *blocks = std::min({cdiv(p.M, shape.rows), most, int64_t(h->dev.num_sms) * norm_grad_blocks_per_sm(shape.threads())});
+    return launch_rows<NormGradParams>(h, kFn[i], 2 * kNormKernels + i + kNormKernels * BF16, *blocks, shape.threads(),
+                                       3 * kNormGradStages * shape.chunks, p, s);
 }
 
 template <bool BF16, bool E5M2>
@@ -113,13 +145,13 @@ gemm_status_t gemm_run_layer_norm(gemm_handle_t h, const gemm_layer_norm_args_t*
     p.ldy = a.ldy;
     p.eps = a.eps;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return a.dtype == GEMM_DTYPE_BF16 ? launch_norm<true>(p, s) : launch_norm<false>(p, s);
+    return a.dtype == GEMM_DTYPE_BF16 ? launch_norm<true>(h, p, s) : launch_norm<false>(h, p, s);
 }
 
 int64_t gemm_layer_norm_grad_workspace_bytes(int64_t M, int64_t N)
 {
     if (M <= 0 || N <= 0) return 0;
-    return 8 * norm_grad_blocks(M) * sum_pitch(N) + (N > kNormMaxHeld ? 8 * M : 0);
+    return 8 * norm_grad_max_blocks(M, N) * sum_pitch(N) + (N > kNormMaxHeld ? 8 * M : 0);
 }
 
 gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_grad_args_t* args, void* stream)
@@ -156,7 +188,7 @@ gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_gr
     if (!g.ok) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float* const partials = a.workspace ? static_cast<float*>(a.workspace) : h->sums;
-    const int64_t pitch = sum_pitch(a.N), half = norm_grad_blocks(a.M) * pitch;
+    const int64_t pitch = sum_pitch(a.N), half = norm_grad_max_blocks(a.M, a.N) * pitch;
     int64_t blocks = 0;
     if (a.M > 0) {
         NormGradParams p;
@@ -178,7 +210,8 @@ gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_gr
         p.lddx = a.lddx;
         p.pitch = pitch;
         p.block_rows = 0;
-        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_norm_grad<true>(p, &blocks, s) : launch_norm_grad<false>(p, &blocks, s);
+        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_norm_grad<true>(h, p, &blocks, s)
+                                                             : launch_norm_grad<false>(h, p, &blocks, s);
         if (st != GEMM_OK) return st;
     }
     return launch_sums(partials, blocks, a.N, {a.dweight, a.dweight_dtype, a.beta}, {a.dbias, a.dbias_dtype, a.beta}, half, s);
