@@ -4,9 +4,10 @@
 // Layer norm.  A row belongs to WARPS warps, CHUNKS times 8 elements (16 bytes) a lane, so statistics are taken in two passes
 // over registers: the mean, then the mean square of x - mean, without the cancellation of E[x^2] - mean^2.  Rows of more
 // elements than registers hold are read again for every pass.
-//   A block takes rows b, b + grid, ... and keeps the loads of the next ones in flight: every lane copies its own chunks of
-// the rows ahead into its own places of a ring in shared memory (cp.async), which it alone reads, so the ring needs no
-// barrier.
+//   A block takes rows b, b + grid, ... and keeps the loads of the next ones in flight: every warp copies its own chunks of
+// the rows ahead into its own places of a ring in shared memory (cp.async, 16 bytes a lane), which it alone reads, so the ring
+// needs no barrier.  Of a warp's 256 columns lane l works on 4 l ... 4 l + 3 and 128 + 4 l ...: fp32 weights then are 16 bytes a
+// lane side by side (with 8 columns a lane every load of them touched twice the lines, and L1 was 72 % busy).
 //
 // Backward, with x^ = (x - mean) rstd and g = dy w:
 //   dx = rstd (g - mean(g) - x^ mean(g x^)) + residual,   dw = sum over rows of dy x^,   db = sum over rows of dy.
@@ -29,47 +30,63 @@ constexpr int norm_blocks_per_sm(int threads) { return 1024 / threads; }
 constexpr int norm_grad_blocks_per_sm(int threads) { return 512 / threads; }
 constexpr int64_t kNormMaxHeld = 16384;  // longest row that is kept in registers
 
-// A parameter or gradient vector of fp32 or of the matrices' 16-bit type; null: absent.
+// A parameter vector of fp32 or of the matrices' 16-bit type, and how it can be read.
+enum { kVecNone, kVecF32, kVec16, kVecF32Any, kVec16Any };  // absent; quads aligned to their size; any alignment
 struct NormVector {
     const void* at;
-    int32_t f32;
+    int32_t kind;
 };
 
-// Elements [c, c + 8) of a vector as fp32 pairs; `fill` where it is absent or past its n elements.
+// Elements c ... c + 3 of a vector (c a multiple of 4) as fp32 pairs; `fill` where it is absent or past its n elements.
+template <bool BF16>
+__device__ __forceinline__ void load_vector4(f32x2* v, const NormVector& vec, int32_t c, int32_t n, float fill)
+{
+    if (vec.kind == kVecF32 && c + 4 <= n) {
+        const float4 a = reinterpret_cast<const float4*>(vec.at)[c >> 2];
+        v[0] = pair(a.x, a.y);
+        v[1] = pair(a.z, a.w);
+    } else if (vec.kind == kVec16 && c + 4 <= n) {
+        const uint2 a = reinterpret_cast<const uint2*>(vec.at)[c >> 2];
+        v[0] = unpack2<BF16>(a.x);
+        v[1] = unpack2<BF16>(a.y);
+    } else {
+        float f[4];
+        const bool f32 = vec.kind == kVecF32 || vec.kind == kVecF32Any;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            f[e] = vec.kind == kVecNone || c + e >= n ? fill
+                   : f32                              ? static_cast<const float*>(vec.at)[c + e]
+                                                      : load16<BF16>(static_cast<const uint16_t*>(vec.at) + c + e);
+        v[0] = pair(f[0], f[1]);
+        v[1] = pair(f[2], f[3]);
+    }
+}
+
+// Elements [c, c + 8), likewise.
 template <bool BF16>
 __device__ __forceinline__ void load_vector8(f32x2 (&v)[4], const NormVector& vec, int64_t c, int64_t n, float fill)
 {
-    if (!vec.at || c >= n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = both(fill);
+    load_vector4<BF16>(v, vec, static_cast<int32_t>(c), static_cast<int32_t>(n), fill);
+    load_vector4<BF16>(v + 2, vec, static_cast<int32_t>(c) + 4, static_cast<int32_t>(n), fill);
+}
+
+// Columns c ... c + 3 of a 16-bit row to memory, none from n on.
+__device__ __forceinline__ void store_row4(uint16_t* row, int32_t c, int32_t n, uint32_t w0, uint32_t w1)
+{
+    if (c + 4 <= n) {
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(w0, w1);
         return;
     }
-    const int elem = vec.f32 ? 4 : 2;
-    const uint8_t* at = static_cast<const uint8_t*>(vec.at) + c * elem;
-    if (c + 8 <= n && (reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
-        if (vec.f32) {
-            const float4 a = reinterpret_cast<const float4*>(at)[0], b = reinterpret_cast<const float4*>(at)[1];
-            v[0] = pair(a.x, a.y);
-            v[1] = pair(a.z, a.w);
-            v[2] = pair(b.x, b.y);
-            v[3] = pair(b.z, b.w);
-        } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(at);
-            v[0] = unpack2<BF16>(w.x);
-            v[1] = unpack2<BF16>(w.y);
-            v[2] = unpack2<BF16>(w.z);
-            v[3] = unpack2<BF16>(w.w);
-        }
-        return;
-    }
-    float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f[e] = c + e >= n ? fill
-               : vec.f32  ? reinterpret_cast<const float*>(at)[e]
-                          : load16<BF16>(reinterpret_cast<const uint16_t*>(at) + e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+    for (int e = 0; e < 4; ++e)
+        if (c + e < n) row[c + e] = static_cast<uint16_t>((e < 2 ? w0 : w1) >> (16 * (e & 1)));
+}
+
+__device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 
 // Elements [c, c + 8) of a 16-bit row (16-byte aligned at c), zeros from column n on.
@@ -134,26 +151,45 @@ __device__ __forceinline__ float sum_of(f32x2 v)
     return lo + hi;
 }
 
-// The sums of two values over the WARPS warps of a row, for all of their threads.  `parity` alternates between calls, so that
-// one barrier a call keeps its writes apart from the reads of the call before.
+// The sum of a value (or of two) over the WARPS warps of a row, for all of their threads.  `shared` alternates between two
+// places from call to call, so that one barrier a call keeps its writes apart from the reads of the call before.
 template <int WARPS>
-__device__ __forceinline__ float2 row_sums(float2 v, float2 (*shared)[WARPS], int parity)
+__device__ __forceinline__ float row_sum(float v, float* shared)
 {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, off);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, off);
-    }
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     if constexpr (WARPS > 1) {
-        if ((threadIdx.x & 31) == 0) shared[parity][threadIdx.x >> 5] = v;
+        if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = shared[parity][0];
+        f32x2 s = 0;
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) {
-            v.x += shared[parity][w].x;
-            v.y += shared[parity][w].y;
+        for (int w = 0; w < WARPS; w += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(shared + w);
+            s = add2(s, add2(pair(f.x, f.y), pair(f.z, f.w)));
+        }
+        v = sum_of(s);
+    }
+    return v;
+}
+
+template <int WARPS>
+__device__ __forceinline__ float2 row_sums(float2 v, float2* shared)
+{
+    f32x2 s = pair(v.x, v.y);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s = add2(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    if constexpr (WARPS > 1) {
+        split(s, v.x, v.y);
+        if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+        __syncthreads();
+        s = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; w += 2) {
+            const float4 f = *reinterpret_cast<const float4*>(shared + w);
+            s = add2(s, add2(pair(f.x, f.y), pair(f.z, f.w)));
         }
     }
+    split(s, v.x, v.y);
     return v;
 }
 
@@ -166,24 +202,52 @@ struct NormParams {
     float eps;
 };
 
+// A warp's place in the ring for chunk k of a stage, and the columns of its lanes (see above).  `parts`: matrices in the ring.
+template <int WARPS, int CHUNKS, int ROWS>
+struct NormLanes {
+    static constexpr int kWarps = WARPS * ROWS;
+    uint32_t ring;
+    int warp, lane, in_row;  // of the block; of the warp; of the row's warps
+
+    __device__ __forceinline__ explicit NormLanes(const uint8_t* smem)
+        : ring(ptx::smem_addr(smem)), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), in_row(ROWS > 1 ? 0 : threadIdx.x >> 5)
+    {
+    }
+    __device__ __forceinline__ uint32_t place(int stage, int k) const { return ring + 512u * static_cast<uint32_t>((stage * CHUNKS + k) * kWarps + warp); }
+    __device__ __forceinline__ int32_t first(int k) const { return (k * WARPS + in_row) * 256; }
+    __device__ __forceinline__ int32_t quad(int k, int q) const { return first(k) + 128 * q + 4 * lane; }
+    __device__ __forceinline__ void copy(int stage, int k, const uint16_t* row, int32_t n) const
+    {
+        copy_row8(place(stage, k) + 16u * lane, row, first(k) + 8 * lane, n);
+    }
+    // This lane's eight values of a chunk.
+    template <bool BF16>
+    __device__ __forceinline__ void take(f32x2 (&v)[4], int stage, int k) const
+    {
+        const uint2 a = ld_shared_u2(place(stage, k) + 8u * lane), b = ld_shared_u2(place(stage, k) + 256u + 8u * lane);
+        v[0] = unpack2<BF16>(a.x);
+        v[1] = unpack2<BF16>(a.y);
+        v[2] = unpack2<BF16>(b.x);
+        v[3] = unpack2<BF16>(b.y);
+    }
+};
+
 // ROWS rows per block at once (more than one: WARPS is 1).  Dynamic shared memory: kNormStages * CHUNKS * 16 bytes a thread.
 template <bool BF16, int WARPS, int CHUNKS, int ROWS>
 __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * ROWS * 32)) layer_norm_kernel(const NormParams p)
 {
     static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
-    constexpr int kThreads = WARPS * ROWS * 32;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 shared[2][WARPS];
-    const int t = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x;
-    const uint32_t mine = ptx::smem_addr(ring) + 16u * threadIdx.x;
-    auto slot = [&](int stage, int k) { return mine + 16u * kThreads * static_cast<uint32_t>(stage * CHUNKS + k); };
-    auto column = [&](int k) { return (k * WARPS * 32 + t) * int64_t(8); };
+    __shared__ __align__(16) float shared[2][WARPS < 4 ? 4 : WARPS];
+    const NormLanes<WARPS, CHUNKS, ROWS> at(ring);
+    const int32_t N = static_cast<int32_t>(p.N);
     const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
-    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? threadIdx.x >> 5 : 0);
+    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? at.warp : 0);
     auto fetch = [&](int stage, int64_t r) {
         if (r < p.M) {
+            const uint16_t* const x = p.X + r * p.ldx;
 #pragma unroll
-            for (int k = 0; k < CHUNKS; ++k) copy_row8(slot(stage, k), p.X + r * p.ldx, column(k), p.N);
+            for (int k = 0; k < CHUNKS; ++k) at.copy(stage, k, x, N);
         }
         copies_commit();
     };
@@ -191,56 +255,59 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
     ptx::launch_dependents();
 #pragma unroll
     for (int st = 0; st < kNormStages; ++st) fetch(st, row + st * step);
-    const float n = static_cast<float>(p.N);
+    const float n = static_cast<float>(N);
     int stage = 0;
     for (; row < p.M; row += step) {
         copies_wait<kNormStages - 1>();
+        __syncwarp();
         f32x2 v[CHUNKS][4];
         f32x2 sum = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            unpack8<BF16>(v[k], ld_shared_u4(slot(stage, k)));
+            at.template take<BF16>(v[k], stage, k);
             sum = add2(sum, add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
         }
         // (Divided, not multiplied by 1 / n: a row of one value has exactly that mean, and no variance.)
-        const float mean = row_sums<WARPS>(make_float2(sum_of(sum), 0.0f), shared, 0).x / n;
-        // The sum has used what was in the slot.
+        const float mean = row_sum<WARPS>(sum_of(sum), shared[0]) / n;
+        // The sum has used what was in the warp's places.
         fetch(stage, row + kNormStages * step);
         stage = stage + 1 == kNormStages ? 0 : stage + 1;
         f32x2 sq = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = column(k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], both(-mean));
-            if (c + 8 > p.N) {  // nothing past the row's end counts
+            if (at.first(k) + 256 > N) {  // nothing past the row's end counts
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    const int32_t c = at.quad(k, i >> 1) + 2 * (i & 1);
                     float lo, hi;
                     split(v[k][i], lo, hi);
-                    v[k][i] = pair(c + 2 * i < p.N ? lo : 0.0f, c + 2 * i + 1 < p.N ? hi : 0.0f);
+                    v[k][i] = pair(c < N ? lo : 0.0f, c + 1 < N ? hi : 0.0f);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) sq = fma2(v[k][i], v[k][i], sq);
         }
-        const float rstd = 1.0f / sqrtf(row_sums<WARPS>(make_float2(sum_of(sq), 0.0f), shared, 1).x / n + p.eps);
-        if (t == 0) {
+        const float rstd = 1.0f / sqrtf(row_sum<WARPS>(sum_of(sq), shared[1]) / n + p.eps);
+        if (at.lane == 0 && at.in_row == 0) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
         uint16_t* const y = p.Y + row * p.ldy;
 #pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = column(k);
-            if (c >= p.N) break;
-            f32x2 w[4], b[4];
-            load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
-            load_vector8<BF16>(b, p.b, c, p.N, 0.0f);
+        for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = fma2(mul2(v[k][i], both(rstd)), w[i], b[i]);
-            store_row8(y, c, p.N, round8<BF16>(b));
-        }
+            for (int q = 0; q < 2; ++q) {
+                const int32_t c = at.quad(k, q);
+                if (c >= N) break;
+                f32x2 w[2], b[2];
+                load_vector4<BF16>(w, p.w, c, N, 1.0f);
+                load_vector4<BF16>(b, p.b, c, N, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) b[i] = fma2(mul2(v[k][2 * q + i], both(rstd)), w[i], b[i]);
+                store_row4(y, c, N, round2<BF16>(b[0]), round2<BF16>(b[1]));
+            }
     }
 }
 
@@ -249,7 +316,7 @@ constexpr int kWideWarps = 32;  // a row of any length per block, read again for
 template <bool BF16>
 __global__ void __launch_bounds__(kWideWarps * 32) layer_norm_wide_kernel(const NormParams p)
 {
-    __shared__ float2 shared[2][kWideWarps];
+    __shared__ __align__(16) float2 shared[2][kWideWarps];
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     const int64_t row = blockIdx.x, step = kWideWarps * 32 * int64_t(8);
@@ -261,7 +328,7 @@ __global__ void __launch_bounds__(kWideWarps * 32) layer_norm_wide_kernel(const 
         sum = add2(sum, add2(add2(v[0], v[1]), add2(v[2], v[3])));
     }
     const float n = static_cast<float>(p.N);
-    const float mean = row_sums<kWideWarps>(make_float2(sum_of(sum), 0.0f), shared, 0).x / n;
+    const float mean = row_sums<kWideWarps>(make_float2(sum_of(sum), 0.0f), shared[0]).x / n;
     float sq = 0.0f;
     for (int64_t c = c0; c < p.N; c += step) {
         unpack8<BF16>(v, load_row8(x, c, p.N));
@@ -273,7 +340,7 @@ __global__ void __launch_bounds__(kWideWarps * 32) layer_norm_wide_kernel(const 
             if (c + 2 * i + 1 < p.N) sq = fmaf(hi, hi, sq);
         }
     }
-    const float rstd = 1.0f / sqrtf(row_sums<kWideWarps>(make_float2(sq, 0.0f), shared, 1).x / n + p.eps);
+    const float rstd = 1.0f / sqrtf(row_sums<kWideWarps>(make_float2(sq, 0.0f), shared[1]).x / n + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -316,30 +383,32 @@ __device__ __forceinline__ uint4 norm_dx8(const f32x2 (&g)[4], const f32x2 (&h)[
 }
 
 // ROWS rows of a block at once (more than one: WARPS is 1), joined in shared memory at the end.  Dynamic shared memory:
-// kNormGradStages * 3 * CHUNKS * 16 bytes a thread, for dy, x and the residual.
+// kNormGradStages * 3 * CHUNKS * 16 bytes a thread, for dy, x and the residual.  With e = x - mean the row's sums are those of
+// g and g e, and dx = rstd g - rstd mean(g) - e rstd^2 mean(g e).
 template <bool BF16, int WARPS, int CHUNKS, int ROWS>
 __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WARPS * ROWS * 32))
     layer_norm_grad_kernel(const NormGradParams p)
 {
     static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
-    static_assert(kNormGradStages == 2, "row_sums takes the stage for its parity");
-    constexpr int kThreads = WARPS * ROWS * 32;
+    static_assert(kNormGradStages == 2, "row_sums takes the stage for its place");
+    constexpr bool kKeepW = CHUNKS <= 2;  // the weights stay in registers
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 shared[2][WARPS];
-    const int t = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int group = ROWS > 1 ? threadIdx.x >> 5 : 0;
-    const uint32_t mine = ptx::smem_addr(ring) + 16u * threadIdx.x;
-    auto slot = [&](int stage, int which, int k) { return mine + 16u * kThreads * static_cast<uint32_t>((stage * 3 + which) * CHUNKS + k); };
-    auto column = [&](int k) { return (k * WARPS * 32 + t) * int64_t(8); };
+    __shared__ __align__(16) float2 shared[2][WARPS < 2 ? 2 : WARPS];
+    const NormLanes<WARPS, 3 * CHUNKS, ROWS> at(ring);  // chunks of dy, then of x, then of the residual
+    const int32_t N = static_cast<int32_t>(p.N);
     const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
-    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + group;
+    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? at.warp : 0);
+    const bool has_res = p.residual != nullptr;
+    auto copy = [&](int stage, int which, int k, const uint16_t* from) {
+        copy_row8(at.place(stage, which * CHUNKS + k) + 16u * at.lane, from, at.first(k) + 8 * at.lane, N);
+    };
     auto fetch = [&](int stage, int64_t r) {
         if (r < p.M) {
 #pragma unroll
             for (int k = 0; k < CHUNKS; ++k) {
-                copy_row8(slot(stage, 0, k), p.dY + r * p.lddy, column(k), p.N);
-                copy_row8(slot(stage, 1, k), p.X + r * p.ldx, column(k), p.N);
-                if (p.residual) copy_row8(slot(stage, 2, k), p.residual + r * p.ldr, column(k), p.N);
+                copy(stage, 0, k, p.dY + r * p.lddy);
+                copy(stage, 1, k, p.X + r * p.ldx);
+                if (has_res) copy(stage, 2, k, p.residual + r * p.ldr);
             }
         }
         copies_commit();
@@ -348,85 +417,105 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
     ptx::launch_dependents();
 #pragma unroll
     for (int st = 0; st < kNormGradStages; ++st) fetch(st, row + st * step);
+    f32x2 kept[kKeepW ? CHUNKS : 1][4];
+    auto weights = [&](f32x2 (&w)[4], int k) {
+        load_vector4<BF16>(w, p.w, at.quad(k, 0), N, 1.0f);
+        load_vector4<BF16>(w + 2, p.w, at.quad(k, 1), N, 1.0f);
+    };
+    if constexpr (kKeepW) {
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) weights(kept[k], k);
+    }
     f32x2 dw[CHUNKS][4] = {}, db[CHUNKS][4] = {};
-    const float inv_n = 1.0f / static_cast<float>(p.N);
+    const float inv_n = 1.0f / static_cast<float>(N);
     int stage = 0;
     for (; row < p.M; row += step) {
         const float mean = p.mean[row], rstd = p.rstd[row];
         copies_wait<kNormGradStages - 1>();
+        __syncwarp();
         f32x2 s1 = 0, s2 = 0;
-#pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-            f32x2 g[4], h[4], w[4];
-            unpack8<BF16>(g, ld_shared_u4(slot(stage, 0, k)));
-            unpack8<BF16>(h, ld_shared_u4(slot(stage, 1, k)));
-            load_vector8<BF16>(w, p.w, column(k), p.N, 1.0f);
+        f32x2 g[4], e[4], w[4];
+        // g = dy w and e = x - mean of chunk k; dy stays in `dy`.
+        auto take = [&](int k, f32x2 (&dy)[4]) {
+            at.template take<BF16>(dy, stage, k);
+            at.template take<BF16>(e, stage, CHUNKS + k);
+            if constexpr (!kKeepW) weights(w, k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // Past the row's end dy is 0, so x^ counts nowhere.
-                h[i] = mul2(add2(h[i], both(-mean)), both(rstd));
-                dw[k][i] = fma2(g[i], h[i], dw[k][i]);
-                db[k][i] = add2(db[k][i], g[i]);
-                g[i] = mul2(g[i], w[i]);
+                e[i] = add2(e[i], both(-mean));
+                g[i] = mul2(dy[i], kKeepW ? kept[kKeepW ? k : 0][i] : w[i]);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+            f32x2 dy[4];
+            take(k, dy);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // Past the row's end dy is 0, so e counts nowhere.
+                dw[k][i] = fma2(mul2(e[i], both(rstd)), dy[i], dw[k][i]);
+                db[k][i] = add2(db[k][i], dy[i]);
                 s1 = add2(s1, g[i]);
-                s2 = fma2(g[i], h[i], s2);
+                s2 = fma2(g[i], e[i], s2);
             }
         }
-        float2 c12 = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared, stage & 1);
-        c12.x *= inv_n;
-        c12.y *= inv_n;
+        const float2 c = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared[stage]);
+        const f32x2 c1 = both(-rstd * (c.x * inv_n)), c2 = both(-rstd * (rstd * (rstd * (c.y * inv_n))));
+        uint16_t* const dx = p.dX + row * p.lddx;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = column(k);
-            if (c >= p.N) break;
-            f32x2 g[4], h[4], w[4];
-            uint4 res = make_uint4(0, 0, 0, 0);
-            if (p.residual) res = ld_shared_u4(slot(stage, 2, k));
-            unpack8<BF16>(g, ld_shared_u4(slot(stage, 0, k)));
-            unpack8<BF16>(h, ld_shared_u4(slot(stage, 1, k)));
-            load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
+            f32x2 dy[4];
+            take(k, dy);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[i] = mul2(add2(h[i], both(-mean)), both(rstd));
-                g[i] = mul2(g[i], w[i]);
+            for (int i = 0; i < 4; ++i) g[i] = fma2(e[i], c2, fma2(g[i], both(rstd), c1));
+            if (has_res) {
+                at.template take<BF16>(dy, stage, 2 * CHUNKS + k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[i] = add2(g[i], dy[i]);
             }
-            store_row8(p.dX + row * p.lddx, c, p.N, norm_dx8<BF16>(g, h, c12, rstd, p.residual != nullptr, res));
+            store_row4(dx, at.quad(k, 0), N, round2<BF16>(g[0]), round2<BF16>(g[1]));
+            store_row4(dx, at.quad(k, 1), N, round2<BF16>(g[2]), round2<BF16>(g[3]));
         }
-        // The stores have used what was in the slots.
+        __syncwarp();  // the warp has used what was in its places
         fetch(stage, row + kNormGradStages * step);
-        stage = stage + 1 == kNormGradStages ? 0 : stage + 1;
+        stage ^= 1;
     }
     if (!p.dw && !p.db) return;
-    // This block's sums: of its one row group, or of ROWS warps by way of shared memory.
+    // This block's sums: of its one row group, or of ROWS warps by way of shared memory.  (The pitch is a multiple of 64.)
+    auto put = [&](float* to, int32_t c, f32x2 lo, f32x2 hi) {
+        float f[4];
+        split(lo, f[0], f[1]);
+        split(hi, f[2], f[3]);
+        if (to && c < p.pitch) *reinterpret_cast<float4*>(to + blockIdx.x * p.pitch + c) = make_float4(f[0], f[1], f[2], f[3]);
+    };
     if constexpr (ROWS > 1) {
-        __shared__ f32x2 parts[2][ROWS][CHUNKS * 32 * 4];
+        __shared__ f32x2 parts[2][ROWS][CHUNKS][2][32][2];
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                parts[0][group][(k * 32 + t) * 4 + i] = dw[k][i];
-                parts[1][group][(k * 32 + t) * 4 + i] = db[k][i];
+                parts[0][at.warp][k][i >> 1][at.lane][i & 1] = dw[k][i];
+                parts[1][at.warp][k][i >> 1][at.lane][i & 1] = db[k][i];
             }
         __syncthreads();
-        for (int e = threadIdx.x; e < 2 * CHUNKS * 32 * 4; e += ROWS * 32) {
-            const int which = e / (CHUNKS * 32 * 4), at = e % (CHUNKS * 32 * 4);
-            f32x2 s = parts[which][0][at];
+        for (int e = threadIdx.x; e < 2 * CHUNKS * 2 * 32; e += ROWS * 32) {
+            const int l = e & 31, q = (e >> 5) & 1, k = (e >> 6) % CHUNKS, which = (e >> 6) / CHUNKS;
+            f32x2 lo = 0, hi = 0;
 #pragma unroll
-            for (int r = 1; r < ROWS; ++r) s = add2(s, parts[which][r][at]);
-            float* const to = which ? p.db : p.dw;
-            if (to && 2 * at < p.pitch) *reinterpret_cast<f32x2*>(to + blockIdx.x * p.pitch + 2 * at) = s;
+            for (int r = 0; r < ROWS; ++r) {
+                lo = add2(lo, parts[which][r][k][q][l][0]);
+                hi = add2(hi, parts[which][r][k][q][l][1]);
+            }
+            put(which ? p.db : p.dw, k * 256 + 128 * q + 4 * l, lo, hi);
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) {
-            const int64_t c = (k * WARPS * 32 + t) * int64_t(8);
-            if (c >= p.pitch) break;  // the pitch is a multiple of 64
+        for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (p.dw) *reinterpret_cast<f32x2*>(p.dw + blockIdx.x * p.pitch + c + 2 * i) = dw[k][i];
-                if (p.db) *reinterpret_cast<f32x2*>(p.db + blockIdx.x * p.pitch + c + 2 * i) = db[k][i];
+            for (int q = 0; q < 2; ++q) {
+                put(p.dw, at.quad(k, q), dw[k][2 * q], dw[k][2 * q + 1]);
+                put(p.db, at.quad(k, q), db[k][2 * q], db[k][2 * q + 1]);
             }
-        }
     }
 }
 
@@ -434,7 +523,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
 template <bool BF16>
 __global__ void __launch_bounds__(kWideWarps * 32) layer_norm_grad_means_kernel(const NormGradParams p)
 {
-    __shared__ float2 shared[2][kWideWarps];
+    __shared__ __align__(16) float2 shared[2][kWideWarps];
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     const int64_t row = blockIdx.x;
@@ -452,7 +541,7 @@ __global__ void __launch_bounds__(kWideWarps * 32) layer_norm_grad_means_kernel(
             s2 = fma2(g[i], mul2(add2(h[i], both(-mean)), both(rstd)), s2);
         }
     }
-    const float2 s = row_sums<kWideWarps>(make_float2(sum_of(s1), sum_of(s2)), shared, 0);
+    const float2 s = row_sums<kWideWarps>(make_float2(sum_of(s1), sum_of(s2)), shared[0]);
     const float inv_n = 1.0f / static_cast<float>(p.N);
     if (threadIdx.x == 0) p.row_means[row] = make_float2(s.x * inv_n, s.y * inv_n);
 }
@@ -582,7 +671,7 @@ __device__ __forceinline__ void store_f8x8(uint8_t* row, int64_t c, int64_t n, u
 constexpr int kQuantWarps = 8, kQuantRows = 4;
 
 template <bool BF16, bool E5M2>
-__global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const QuantizeParams p)
+__global__ void __launch_bounds__(kQuantWarps * 32, 5) quantize_rows_kernel(const QuantizeParams p)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = blockIdx.x * int64_t(256) + lane * 8;

@@ -24,7 +24,13 @@ void check_stat(Checks& c, const float* at)
     c.vector(at, GEMM_DTYPE_F32);
 }
 
-NormVector vector_of(const void* at, gemm_dtype_t t) { return {at, t == GEMM_DTYPE_F32}; }
+NormVector vector_of(const void* at, gemm_dtype_t t)
+{
+    if (!at) return {nullptr, kVecNone};
+    const bool f32 = t == GEMM_DTYPE_F32;
+    if ((reinterpret_cast<uintptr_t>(at) & (f32 ? 15u : 7u)) != 0) return {at, f32 ? kVecF32Any : kVec16Any};
+    return {at, f32 ? kVecF32 : kVec16};
+}
 
 unsigned blocks_for(int64_t rows, int64_t per_block) { return static_cast<unsigned>(cdiv(rows, per_block)); }
 
