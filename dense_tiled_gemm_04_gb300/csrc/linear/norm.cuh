@@ -24,10 +24,9 @@
 namespace dtg {
 namespace linear {
 
-// Rows ahead whose loads are in flight, and blocks per SM (64 registers a thread; backward: 128).
+// Rows ahead whose loads are in flight, and blocks per SM (128 registers a thread).
 constexpr int kNormStages = 3, kNormGradStages = 2;
-constexpr int norm_blocks_per_sm(int threads) { return 1024 / threads; }
-constexpr int norm_grad_blocks_per_sm(int threads) { return 512 / threads; }
+constexpr int norm_blocks_per_sm(int threads) { return 512 / threads; }
 constexpr int64_t kNormMaxHeld = 16384;  // longest row that is kept in registers
 
 // A parameter vector of fp32 or of the matrices' 16-bit type, and how it can be read.
@@ -38,17 +37,20 @@ struct NormVector {
 };
 
 // Elements c ... c + 3 of a vector (c a multiple of 4) as fp32 pairs; `fill` where it is absent or past its n elements.
-template <bool BF16>
+// FULL: quads are aligned and end inside it.
+template <bool BF16, bool FULL = false>
 __device__ __forceinline__ void load_vector4(f32x2* v, const NormVector& vec, int32_t c, int32_t n, float fill)
 {
-    if (vec.kind == kVecF32 && c + 4 <= n) {
+    if (vec.kind == kVecF32 && (FULL || c + 4 <= n)) {
         const float4 a = reinterpret_cast<const float4*>(vec.at)[c >> 2];
         v[0] = pair(a.x, a.y);
         v[1] = pair(a.z, a.w);
-    } else if (vec.kind == kVec16 && c + 4 <= n) {
+    } else if (vec.kind == kVec16 && (FULL || c + 4 <= n)) {
         const uint2 a = reinterpret_cast<const uint2*>(vec.at)[c >> 2];
         v[0] = unpack2<BF16>(a.x);
         v[1] = unpack2<BF16>(a.y);
+    } else if constexpr (FULL) {
+        v[0] = v[1] = both(fill);
     } else {
         float f[4];
         const bool f32 = vec.kind == kVecF32 || vec.kind == kVecF32Any;
@@ -71,9 +73,10 @@ __device__ __forceinline__ void load_vector8(f32x2 (&v)[4], const NormVector& ve
 }
 
 // Columns c ... c + 3 of a 16-bit row to memory, none from n on.
+template <bool FULL>
 __device__ __forceinline__ void store_row4(uint16_t* row, int32_t c, int32_t n, uint32_t w0, uint32_t w1)
 {
-    if (c + 4 <= n) {
+    if (FULL || c + 4 <= n) {
         *reinterpret_cast<uint2*>(row + c) = make_uint2(w0, w1);
         return;
     }
@@ -114,11 +117,15 @@ __device__ __forceinline__ void store_row8(uint16_t* row, int64_t c, int64_t n, 
 
 // Start the copy of elements [c, c + 8) of a 16-bit row to 16 bytes of shared memory: zeros from column n on, which is not
 // read.
-__device__ __forceinline__ void copy_row8(uint32_t to, const uint16_t* row, int64_t c, int64_t n)
+template <bool FULL>
+__device__ __forceinline__ void copy_row8(uint32_t to, const uint16_t* row, int32_t c, int32_t n)
 {
-    const int64_t left = 2 * (n - c);
-    const int bytes = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(row + (left > 0 ? c : 0)), "r"(bytes) : "memory");
+    if constexpr (FULL) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(row + c) : "memory");
+    } else {
+        const int left = n - c, bytes = left >= 8 ? 16 : left > 0 ? 2 * left : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(row + (left > 0 ? c : 0)), "r"(bytes) : "memory");
+    }
 }
 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -161,6 +168,7 @@ __device__ __forceinline__ float row_sum(float v, float* shared)
     if constexpr (WARPS > 1) {
         if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
         __syncthreads();
+        if constexpr (WARPS == 2) return shared[0] + shared[1];
         f32x2 s = 0;
 #pragma unroll
         for (int w = 0; w < WARPS; w += 4) {
@@ -193,6 +201,14 @@ __device__ __forceinline__ float2 row_sums(float2 v, float2* shared)
     return v;
 }
 
+// s / n, corrected by what the product with 1 / n leaves: a quotient that fp32 holds comes out exact, so a row of one value
+// has that mean, and no variance.
+__device__ __forceinline__ float over(float s, float n, float inv_n)
+{
+    const float q = s * inv_n;
+    return fmaf(fmaf(-q, n, s), inv_n, q);
+}
+
 struct NormParams {
     const uint16_t* X;
     uint16_t* Y;
@@ -216,9 +232,10 @@ struct NormLanes {
     __device__ __forceinline__ uint32_t place(int stage, int k) const { return ring + 512u * static_cast<uint32_t>((stage * CHUNKS + k) * kWarps + warp); }
     __device__ __forceinline__ int32_t first(int k) const { return (k * WARPS + in_row) * 256; }
     __device__ __forceinline__ int32_t quad(int k, int q) const { return first(k) + 128 * q + 4 * lane; }
-    __device__ __forceinline__ void copy(int stage, int k, const uint16_t* row, int32_t n) const
+    template <bool FULL>
+    __device__ __forceinline__ void copy(int stage, int place_k, int k, const uint16_t* row, int32_t n) const
     {
-        copy_row8(place(stage, k) + 16u * lane, row, first(k) + 8 * lane, n);
+        if (!FULL || first(k) < n) copy_row8<FULL>(place(stage, place_k) + 16u * lane, row, first(k) + 8 * lane, n);
     }
     // This lane's eight values of a chunk.
     template <bool BF16>
@@ -232,8 +249,9 @@ struct NormLanes {
     }
 };
 
-// ROWS rows per block at once (more than one: WARPS is 1).  Dynamic shared memory: kNormStages * CHUNKS * 16 bytes a thread.
-template <bool BF16, int WARPS, int CHUNKS, int ROWS>
+// ROWS rows per block at once (more than one: WARPS is 1).  FULL: rows are a multiple of 256, and weights and biases aligned.
+// Dynamic shared memory: kNormStages * CHUNKS * 16 bytes a thread.
+template <bool BF16, int WARPS, int CHUNKS, int ROWS, bool FULL>
 __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * ROWS * 32)) layer_norm_kernel(const NormParams p)
 {
     static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
@@ -247,7 +265,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
         if (r < p.M) {
             const uint16_t* const x = p.X + r * p.ldx;
 #pragma unroll
-            for (int k = 0; k < CHUNKS; ++k) at.copy(stage, k, x, N);
+            for (int k = 0; k < CHUNKS; ++k) at.template copy<FULL>(stage, k, k, x, N);
         }
         copies_commit();
     };
@@ -255,7 +273,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
     ptx::launch_dependents();
 #pragma unroll
     for (int st = 0; st < kNormStages; ++st) fetch(st, row + st * step);
-    const float n = static_cast<float>(N);
+    const float n = static_cast<float>(N), inv_n = 1.0f / n;
     int stage = 0;
     for (; row < p.M; row += step) {
         copies_wait<kNormStages - 1>();
@@ -264,20 +282,21 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
         f32x2 sum = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
+            if (FULL && at.first(k) >= N) break;
             at.template take<BF16>(v[k], stage, k);
             sum = add2(sum, add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
         }
-        // (Divided, not multiplied by 1 / n: a row of one value has exactly that mean, and no variance.)
-        const float mean = row_sum<WARPS>(sum_of(sum), shared[0]) / n;
+        const float mean = over(row_sum<WARPS>(sum_of(sum), shared[0]), n, inv_n);
         // The sum has used what was in the warp's places.
         fetch(stage, row + kNormStages * step);
         stage = stage + 1 == kNormStages ? 0 : stage + 1;
         f32x2 sq = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
+            if (FULL && at.first(k) >= N) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], both(-mean));
-            if (at.first(k) + 256 > N) {  // nothing past the row's end counts
+            if (!FULL && at.first(k) + 256 > N) {  // nothing past the row's end counts
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int32_t c = at.quad(k, i >> 1) + 2 * (i & 1);
@@ -289,25 +308,26 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
 #pragma unroll
             for (int i = 0; i < 4; ++i) sq = fma2(v[k][i], v[k][i], sq);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<WARPS>(sum_of(sq), shared[1]) / n + p.eps);
+        const float rstd = rsqrtf(over(row_sum<WARPS>(sum_of(sq), shared[1]), n, inv_n) + p.eps);
         if (at.lane == 0 && at.in_row == 0) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
         uint16_t* const y = p.Y + row * p.ldy;
 #pragma unroll
-        for (int k = 0; k < CHUNKS; ++k)
+        for (int k = 0; k < CHUNKS; ++k) {
+            if (at.first(k) >= N) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int32_t c = at.quad(k, q);
-                if (c >= N) break;
                 f32x2 w[2], b[2];
-                load_vector4<BF16>(w, p.w, c, N, 1.0f);
-                load_vector4<BF16>(b, p.b, c, N, 0.0f);
+                load_vector4<BF16, FULL>(w, p.w, c, N, 1.0f);
+                load_vector4<BF16, FULL>(b, p.b, c, N, 0.0f);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) b[i] = fma2(mul2(v[k][2 * q + i], both(rstd)), w[i], b[i]);
-                store_row4(y, c, N, round2<BF16>(b[0]), round2<BF16>(b[1]));
+                store_row4<FULL>(y, c, N, round2<BF16>(b[0]), round2<BF16>(b[1]));
             }
+        }
     }
 }
 
@@ -385,8 +405,8 @@ __device__ __forceinline__ uint4 norm_dx8(const f32x2 (&g)[4], const f32x2 (&h)[
 // ROWS rows of a block at once (more than one: WARPS is 1), joined in shared memory at the end.  Dynamic shared memory:
 // kNormGradStages * 3 * CHUNKS * 16 bytes a thread, for dy, x and the residual.  With e = x - mean the row's sums are those of
 // g and g e, and dx = rstd g - rstd mean(g) - e rstd^2 mean(g e).
-template <bool BF16, int WARPS, int CHUNKS, int ROWS>
-__global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WARPS * ROWS * 32))
+template <bool BF16, int WARPS, int CHUNKS, int ROWS, bool FULL>
+__global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * ROWS * 32))
     layer_norm_grad_kernel(const NormGradParams p)
 {
     static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
@@ -399,16 +419,13 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
     const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
     int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? at.warp : 0);
     const bool has_res = p.residual != nullptr;
-    auto copy = [&](int stage, int which, int k, const uint16_t* from) {
-        copy_row8(at.place(stage, which * CHUNKS + k) + 16u * at.lane, from, at.first(k) + 8 * at.lane, N);
-    };
     auto fetch = [&](int stage, int64_t r) {
         if (r < p.M) {
 #pragma unroll
             for (int k = 0; k < CHUNKS; ++k) {
-                copy(stage, 0, k, p.dY + r * p.lddy);
-                copy(stage, 1, k, p.X + r * p.ldx);
-                if (has_res) copy(stage, 2, k, p.residual + r * p.ldr);
+                at.template copy<FULL>(stage, k, k, p.dY + r * p.lddy, N);
+                at.template copy<FULL>(stage, CHUNKS + k, k, p.X + r * p.ldx, N);
+                if (has_res) at.template copy<FULL>(stage, 2 * CHUNKS + k, k, p.residual + r * p.ldr, N);
             }
         }
         copies_commit();
@@ -419,18 +436,29 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
     for (int st = 0; st < kNormGradStages; ++st) fetch(st, row + st * step);
     f32x2 kept[kKeepW ? CHUNKS : 1][4];
     auto weights = [&](f32x2 (&w)[4], int k) {
-        load_vector4<BF16>(w, p.w, at.quad(k, 0), N, 1.0f);
-        load_vector4<BF16>(w + 2, p.w, at.quad(k, 1), N, 1.0f);
+        load_vector4<BF16, FULL>(w, p.w, at.quad(k, 0), N, 1.0f);
+        load_vector4<BF16, FULL>(w + 2, p.w, at.quad(k, 1), N, 1.0f);
     };
     if constexpr (kKeepW) {
 #pragma unroll
-        for (int k = 0; k < CHUNKS; ++k) weights(kept[k], k);
+        for (int k = 0; k < CHUNKS; ++k)
+            if (!FULL || at.first(k) < N) weights(kept[k], k);
     }
     f32x2 dw[CHUNKS][4] = {}, db[CHUNKS][4] = {};
     const float inv_n = 1.0f / static_cast<float>(N);
     int stage = 0;
+    float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
+    auto fetch_stats = [&](int64_t r) {
+        if (r < p.M) {
+            next_mean = p.mean[r];
+            next_rstd = p.rstd[r];
+        }
+    };
+    fetch_stats(row);
     for (; row < p.M; row += step) {
-        const float mean = p.mean[row], rstd = p.rstd[row];
+        mean = next_mean;
+        rstd = next_rstd;
+        fetch_stats(row + step);
         copies_wait<kNormGradStages - 1>();
         __syncwarp();
         f32x2 s1 = 0, s2 = 0;
@@ -448,6 +476,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
         };
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
+            if (at.first(k) >= N) break;
             f32x2 dy[4];
             take(k, dy);
 #pragma unroll
@@ -464,6 +493,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
         uint16_t* const dx = p.dX + row * p.lddx;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
+            if (at.first(k) >= N) break;
             f32x2 dy[4];
             take(k, dy);
 #pragma unroll
@@ -473,8 +503,8 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_grad_blocks_per_sm(WAR
 #pragma unroll
                 for (int i = 0; i < 4; ++i) g[i] = add2(g[i], dy[i]);
             }
-            store_row4(dx, at.quad(k, 0), N, round2<BF16>(g[0]), round2<BF16>(g[1]));
-            store_row4(dx, at.quad(k, 1), N, round2<BF16>(g[2]), round2<BF16>(g[3]));
+            store_row4<FULL>(dx, at.quad(k, 0), N, round2<BF16>(g[0]), round2<BF16>(g[1]));
+            store_row4<FULL>(dx, at.quad(k, 1), N, round2<BF16>(g[2]), round2<BF16>(g[3]));
         }
         __syncwarp();  // the warp has used what was in its places
         fetch(stage, row + kNormGradStages * step);

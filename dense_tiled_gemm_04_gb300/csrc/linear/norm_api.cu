@@ -47,64 +47,88 @@ gemm_status_t launch_rows(gemm_handle_t h, void (*fn)(P), int slot, int64_t bloc
     return launch_after(fn, static_cast<unsigned>(blocks), threads, static_cast<size_t>(smem), s, p);
 }
 
-// The shape of the kernel for rows of N <= kNormMaxHeld: warps and 16-byte chunks a lane for a row, rows a block.  Short rows
-// are a warp each.  (Forward and backward have instantiations of their own, so that each keeps to its registers.)
+// The shape of the kernels for rows of N <= kNormMaxHeld, by steps of 256, 512, ... 16384: warps and chunks of 8 elements a lane
+// for a row, rows a block.  Few warps with many chunks each spend less on the sums across warps and wait less at barriers
+// (16384 x 8192 forward: 16 warps of 2 chunks 162 us); the backward kernel's sums of dw and db leave room for four.
 struct NormShape {
     int warps, chunks, rows;
     int threads() const { return 32 * warps * rows; }
 };
-constexpr NormShape kNormShapes[] = {{1, 1, 8}, {1, 2, 8}, {4, 1, 1}, {4, 2, 1}, {8, 2, 1}, {16, 2, 1}, {32, 2, 1}};
-constexpr NormShape kNormGradShapes[] = {{1, 1, 8}, {1, 2, 8}, {4, 1, 1}, {4, 2, 1}, {8, 2, 1}, {16, 2, 1}, {16, 4, 1}};
-constexpr int kNormKernels = 7;
+constexpr int kNormShapes = 7;
+constexpr NormShape kShape[kNormShapes] = {{1, 1, 4}, {1, 2, 4}, {1, 4, 4}, {1, 8, 4}, {2, 8, 1}, {4, 8, 1}, {8, 8, 1}};
+constexpr NormShape kGradShape[kNormShapes] = {{1, 1, 8}, {1, 2, 8}, {1, 4, 4}, {4, 2, 1}, {8, 2, 1}, {8, 4, 1}, {16, 4, 1}};
 
 int shape_for(int64_t N)
 {
     int i = 0;
     for (int64_t n = 256; n < N; n *= 2) ++i;
-    return i;  // 256, 512, 1024, ..., 16384 elements
+    return i;
+}
+
+bool quads(const NormVector& v) { return v.kind != kVecF32Any && v.kind != kVec16Any; }
+
+template <bool BF16, bool FULL, int I>
+constexpr auto norm_fn()
+{
+    return &layer_norm_kernel<BF16, kShape[I].warps, kShape[I].chunks, kShape[I].rows, FULL>;
+}
+
+template <bool BF16, bool FULL, int I>
+constexpr auto norm_grad_fn()
+{
+    return &layer_norm_grad_kernel<BF16, kGradShape[I].warps, kGradShape[I].chunks, kGradShape[I].rows, FULL>;
+}
+
+template <bool BF16, bool FULL>
+gemm_status_t launch_norm(gemm_handle_t h, const NormParams& p, cudaStream_t s)
+{
+    constexpr void (*kFn[kNormShapes])(const NormParams) = {norm_fn<BF16, FULL, 0>(), norm_fn<BF16, FULL, 1>(), norm_fn<BF16, FULL, 2>(),
+                                                            norm_fn<BF16, FULL, 3>(), norm_fn<BF16, FULL, 4>(), norm_fn<BF16, FULL, 5>(),
+                                                            norm_fn<BF16, FULL, 6>()};
+    const int i = shape_for(p.N);
+    const NormShape shape = kShape[i];
+    const int64_t blocks = std::min<int64_t>(cdiv(p.M, shape.rows), h->dev.num_sms * norm_blocks_per_sm(shape.threads()));
+    return launch_rows<NormParams>(h, kFn[i], i + kNormShapes * (2 * FULL + BF16), blocks, shape.threads(), kNormStages * shape.chunks, p, s);
 }
 
 template <bool BF16>
 gemm_status_t launch_norm(gemm_handle_t h, const NormParams& p, cudaStream_t s)
 {
     if (p.N > kNormMaxHeld) return launch_after(&layer_norm_wide_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
-    constexpr void (*kFn[kNormKernels])(const NormParams) = {
-        &layer_norm_kernel<BF16, 1, 1, 8>, &layer_norm_kernel<BF16, 1, 2, 8>,  &layer_norm_kernel<BF16, 4, 1, 1>, &layer_norm_kernel<BF16, 4, 2, 1>,
-        &layer_norm_kernel<BF16, 8, 2, 1>, &layer_norm_kernel<BF16, 16, 2, 1>, &layer_norm_kernel<BF16, 32, 2, 1>};
-    const int i = shape_for(p.N);
-    const NormShape shape = kNormShapes[i];
-    const int64_t blocks = std::min<int64_t>(cdiv(p.M, shape.rows), h->dev.num_sms * norm_blocks_per_sm(shape.threads()));
-    return launch_rows<NormParams>(h, kFn[i], i + kNormKernels * BF16, blocks, shape.threads(), kNormStages * shape.chunks, p, s);
+    return p.N % 256 == 0 && quads(p.w) && quads(p.b) ? launch_norm<BF16, true>(h, p, s) : launch_norm<BF16, false>(h, p, s);
 }
 
 // Most rows of partial sums of dw and db: blocks that run at once on 152 SMs (fewer SMs: fewer; more: no more).
 int64_t norm_grad_max_blocks(int64_t M, int64_t N)
 {
-    return std::min<int64_t>(M, 152 * (N > kNormMaxHeld ? 2 : norm_grad_blocks_per_sm(kNormGradShapes[shape_for(N)].threads())));
+    return std::min<int64_t>(M, 152 * (N > kNormMaxHeld ? 2 : norm_blocks_per_sm(kGradShape[shape_for(N)].threads())));
+}
+
+template <bool BF16, bool FULL>
+gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& p, int64_t* blocks, cudaStream_t s)
+{
+    constexpr void (*kFn[kNormShapes])(const NormGradParams) = {
+        norm_grad_fn<BF16, FULL, 0>(), norm_grad_fn<BF16, FULL, 1>(), norm_grad_fn<BF16, FULL, 2>(), norm_grad_fn<BF16, FULL, 3>(),
+        norm_grad_fn<BF16, FULL, 4>(), norm_grad_fn<BF16, FULL, 5>(), norm_grad_fn<BF16, FULL, 6>()};
+    const int i = shape_for(p.N);
+    const NormShape shape = kGradShape[i];
+    *blocks = std::min({cdiv(p.M, shape.rows), norm_grad_max_blocks(p.M, p.N), int64_t(h->dev.num_sms) * norm_blocks_per_sm(shape.threads())});
+    return launch_rows<NormGradParams>(h, kFn[i], i + kNormShapes * (4 + 2 * FULL + BF16), *blocks, shape.threads(),
+                                       3 * kNormGradStages * shape.chunks, p, s);
 }
 
 template <bool BF16>
 gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, cudaStream_t s)
 {
+    if (q.N <= kNormMaxHeld)
+        return q.N % 256 == 0 && quads(q.w) ? launch_norm_grad<BF16, true>(h, q, blocks, s) : launch_norm_grad<BF16, false>(h, q, blocks, s);
     NormGradParams p = q;
-    const int64_t most = norm_grad_max_blocks(p.M, p.N);
-    if (p.N > kNormMaxHeld) {
-        const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
-        if (st != GEMM_OK) return st;
-        p.block_rows = cdiv(p.M, std::min(cdiv(p.M, 32), most));
-        *blocks = cdiv(p.M, p.block_rows);
-        return launch_after(&layer_norm_grad_wide_kernel<BF16>, dim3(blocks_for(p.N, kStripCols), static_cast<unsigned>(*blocks)),
-                            kStripWarps * 32, 0, s, p);
-    }
-    constexpr void (*kFn[kNormKernels])(const NormGradParams) = {
-        &layer_norm_grad_kernel<BF16, 1, 1, 8>, &layer_norm_grad_kernel<BF16, 1, 2, 8>,  &layer_norm_grad_kernel<BF16, 4, 1, 1>,
-        &layer_norm_grad_kernel<BF16, 4, 2, 1>, &layer_norm_grad_kernel<BF16, 8, 2, 1>, &layer_norm_grad_kernel<BF16, 16, 2, 1>,
-        &layer_norm_grad_kernel<BF16, 16, 4, 1>};
-    const int i = shape_for(p.N);
-    const NormShape shape = kNormGradShapes[i];
-    *blocks = std::min({cdiv(p.M, shape.rows), most, int64_t(h->dev.num_sms) * norm_grad_blocks_per_sm(shape.threads())});
-    return launch_rows<NormGradParams>(h, kFn[i], 2 * kNormKernels + i + kNormKernels * BF16, *blocks, shape.threads(),
-                                       3 * kNormGradStages * shape.chunks, p, s);
+    const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
+    if (st != GEMM_OK) return st;
+    p.block_rows = cdiv(p.M, std::min(cdiv(p.M, 32), norm_grad_max_blocks(p.M, p.N)));
+    *blocks = cdiv(p.M, p.block_rows);
+    return launch_after(&layer_norm_grad_wide_kernel<BF16>, dim3(blocks_for(p.N, kStripCols), static_cast<unsigned>(*blocks)),
+                        kStripWarps * 32, 0, s, p);
 }
 
 template <bool BF16, bool E5M2>

@@ -234,7 +234,7 @@ def layer_norm_grad_workspace_bytes(M: int, N: int) -> int:
 
 def _norm_bytes(M: int, N: int) -> int:
     """layer_norm_grad_workspace_bytes without a call into the library."""
-    blocks = 608 if 512 < N <= 2048 else 152 if 4096 < N <= 16384 else 304
+    blocks = 608 if 512 < N <= 2048 else 152 if 8192 < N <= 16384 else 304
     return (8 * min(M, blocks) * (-(-N // 64) * 64) + (8 * M if N > 16384 else 0)) if M and N else 0
 
 

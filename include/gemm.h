@@ -645,7 +645,7 @@ typedef struct {
 gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_grad_args_t* args, void* stream);
 
 /* Bytes of workspace for gemm_run_layer_norm_grad: 8 * min(M, B) * (N rounded up to 64), B = 608 for N from 513 to 2048, 152
- * for N from 4097 to 16384, else 304; and 8 M more where N is over 16384; 0 when M or N is 0. */
+ * for N from 8193 to 16384, else 304; and 8 M more where N is over 16384; 0 when M or N is 0. */
 int64_t gemm_layer_norm_grad_workspace_bytes(int64_t M, int64_t N);
 
 /* ---------------------------------------------------------------- status and version */
