@@ -24,10 +24,10 @@
 namespace dtg {
 namespace linear {
 
-// Rows ahead whose loads are in flight, and blocks per SM (128 registers a thread).
-constexpr int kNormStages = 3, kNormGradStages = 2;
-constexpr int norm_blocks_per_sm(int threads) { return 512 / threads; }
-constexpr int64_t kNormMaxHeld = 16384;  // longest row that is kept in registers
+constexpr int kNormWarps = 16;       // most warps of a block of the forward kernel, one block per SM
+constexpr int kNormGradStages = 2;   // rows whose loads are in flight, backward
+constexpr int kNormGradThreads = 512;  // of an SM, backward: 128 registers each
+constexpr int64_t kNormMaxHeld = 16384, kNormGradMaxHeld = 8192;  // longest rows that are kept in registers
 
 // A parameter vector of fp32 or of the matrices' 16-bit type, and how it can be read.
 enum { kVecNone, kVecF32, kVec16, kVecF32Any, kVec16Any };  // absent; quads aligned to their size; any alignment
@@ -49,16 +49,14 @@ __device__ __forceinline__ void load_vector4(f32x2* v, const NormVector& vec, in
         const uint2 a = reinterpret_cast<const uint2*>(vec.at)[c >> 2];
         v[0] = unpack2<BF16>(a.x);
         v[1] = unpack2<BF16>(a.y);
-    } else if constexpr (FULL) {
-        v[0] = v[1] = both(fill);
     } else {
-        float f[4];
+        float f[4] = {fill, fill, fill, fill};
         const bool f32 = vec.kind == kVecF32 || vec.kind == kVecF32Any;
+        if (!FULL && vec.kind != kVecNone) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            f[e] = vec.kind == kVecNone || c + e >= n ? fill
-                   : f32                              ? static_cast<const float*>(vec.at)[c + e]
-                                                      : load16<BF16>(static_cast<const uint16_t*>(vec.at) + c + e);
+            for (int e = 0; e < 4; ++e)
+                if (c + e < n) f[e] = f32 ? static_cast<const float*>(vec.at)[c + e] : load16<BF16>(static_cast<const uint16_t*>(vec.at) + c + e);
+        }
         v[0] = pair(f[0], f[1]);
         v[1] = pair(f[2], f[3]);
     }
@@ -158,16 +156,19 @@ __device__ __forceinline__ float sum_of(f32x2 v)
     return lo + hi;
 }
 
-// The sum of a value (or of two) over the WARPS warps of a row, for all of their threads.  `shared` alternates between two
+// The sum of a value (or of two) over the WARPS warps of a row, warps [group * WARPS, (group + 1) * WARPS) of the block, for
+// all of their threads; they meet at a barrier of their own.  `shared` alternates between two
 // places from call to call, so that one barrier a call keeps its writes apart from the reads of the call before.
 template <int WARPS>
-__device__ __forceinline__ float row_sum(float v, float* shared)
+__device__ __forceinline__ float row_sum(float v, float* shared, int group)
 {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     if constexpr (WARPS > 1) {
-        if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-        __syncthreads();
+        shared += group * WARPS;
+        if ((threadIdx.x & 31) == 0) shared[(threadIdx.x >> 5) % WARPS] = v;
+        __syncwarp();
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(WARPS * 32) : "memory");
         if constexpr (WARPS == 2) return shared[0] + shared[1];
         f32x2 s = 0;
 #pragma unroll
@@ -181,15 +182,17 @@ __device__ __forceinline__ float row_sum(float v, float* shared)
 }
 
 template <int WARPS>
-__device__ __forceinline__ float2 row_sums(float2 v, float2* shared)
+__device__ __forceinline__ float2 row_sums(float2 v, float2* shared, int group)
 {
     f32x2 s = pair(v.x, v.y);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s = add2(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
     if constexpr (WARPS > 1) {
         split(s, v.x, v.y);
-        if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-        __syncthreads();
+        shared += group * WARPS;
+        if ((threadIdx.x & 31) == 0) shared[(threadIdx.x >> 5) % WARPS] = v;
+        __syncwarp();
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(WARPS * 32) : "memory");
         s = 0;
 #pragma unroll
         for (int w = 0; w < WARPS; w += 2) {
@@ -218,88 +221,81 @@ struct NormParams {
     float eps;
 };
 
-// A warp's place in the ring for chunk k of a stage, and the columns of its lanes (see above).  `parts`: matrices in the ring.
-template <int WARPS, int CHUNKS, int ROWS>
-struct NormLanes {
-    static constexpr int kWarps = WARPS * ROWS;
-    uint32_t ring;
-    int warp, lane, in_row;  // of the block; of the warp; of the row's warps
-
-    __device__ __forceinline__ explicit NormLanes(const uint8_t* smem)
-        : ring(ptx::smem_addr(smem)), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), in_row(ROWS > 1 ? 0 : threadIdx.x >> 5)
-    {
-    }
-    __device__ __forceinline__ uint32_t place(int stage, int k) const { return ring + 512u * static_cast<uint32_t>((stage * CHUNKS + k) * kWarps + warp); }
-    __device__ __forceinline__ int32_t first(int k) const { return (k * WARPS + in_row) * 256; }
-    __device__ __forceinline__ int32_t quad(int k, int q) const { return first(k) + 128 * q + 4 * lane; }
-    template <bool FULL>
-    __device__ __forceinline__ void copy(int stage, int place_k, int k, const uint16_t* row, int32_t n) const
-    {
-        if (!FULL || first(k) < n) copy_row8<FULL>(place(stage, place_k) + 16u * lane, row, first(k) + 8 * lane, n);
-    }
-    // This lane's eight values of a chunk.
-    template <bool BF16>
-    __device__ __forceinline__ void take(f32x2 (&v)[4], int stage, int k) const
-    {
-        const uint2 a = ld_shared_u2(place(stage, k) + 8u * lane), b = ld_shared_u2(place(stage, k) + 256u + 8u * lane);
-        v[0] = unpack2<BF16>(a.x);
-        v[1] = unpack2<BF16>(a.y);
-        v[2] = unpack2<BF16>(b.x);
-        v[3] = unpack2<BF16>(b.y);
-    }
-};
-
-// ROWS rows per block at once (more than one: WARPS is 1).  FULL: rows are a multiple of 256, and weights and biases aligned.
-// Dynamic shared memory: kNormStages * CHUNKS * 16 bytes a thread.
-template <bool BF16, int WARPS, int CHUNKS, int ROWS, bool FULL>
-__global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * ROWS * 32)) layer_norm_kernel(const NormParams p)
+__device__ __forceinline__ void st_shared_pairs(uint32_t addr, f32x2 a, f32x2 b)
 {
-    static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float shared[2][WARPS < 4 ? 4 : WARPS];
-    const NormLanes<WARPS, CHUNKS, ROWS> at(ring);
-    const int32_t N = static_cast<int32_t>(p.N);
-    const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
-    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? at.warp : 0);
+    asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
+}
+
+// Rows of a block's warps: `groups` of them at once, WARPS warps each.  The weights and biases are in shared memory as fp32: with
+// the ring there L1 has little room, and read through it they came from L2 for every row (16384 x 8192: 161 us).  FULL: rows are a
+// multiple of 256.  Dynamic shared memory: 8 bytes a column (rounded up to 256), then STAGES * CHUNKS * 512 bytes a warp.
+template <bool BF16, int WARPS, int CHUNKS, int STAGES, bool FULL>
+__global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const NormParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float shared[2][kNormWarps];
+    const int32_t N = static_cast<int32_t>(p.N), pitch = (N + 255) & ~255;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int group = warp / WARPS, in_row = warp % WARPS;
+    const uint32_t params = ptx::smem_addr(smem);  // weights, then biases
+    const uint32_t ring = params + 8u * pitch + 512u * warp;
+    auto place = [&](int stage, int k) { return ring + 512u * static_cast<uint32_t>((stage * CHUNKS + k) * warps); };
+    auto first = [&](int k) { return (k * WARPS + in_row) * 256; };
+    const int64_t step = gridDim.x * static_cast<int64_t>(warps / WARPS);
+    int64_t row = blockIdx.x * static_cast<int64_t>(warps / WARPS) + group;
     auto fetch = [&](int stage, int64_t r) {
         if (r < p.M) {
             const uint16_t* const x = p.X + r * p.ldx;
 #pragma unroll
-            for (int k = 0; k < CHUNKS; ++k) at.template copy<FULL>(stage, k, k, x, N);
+            for (int k = 0; k < CHUNKS; ++k)
+                if (first(k) < N) copy_row8<FULL>(place(stage, k) + 16u * lane, x, first(k) + 8 * lane, N);
         }
         copies_commit();
     };
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
 #pragma unroll
-    for (int st = 0; st < kNormStages; ++st) fetch(st, row + st * step);
+    for (int st = 0; st < STAGES; ++st) fetch(st, row + st * step);
+    for (int32_t c = 4 * threadIdx.x; c < pitch; c += 4 * blockDim.x) {
+        f32x2 w[2], b[2];
+        load_vector4<BF16>(w, p.w, c, N, 1.0f);
+        load_vector4<BF16>(b, p.b, c, N, 0.0f);
+        st_shared_pairs(params + 4u * c, w[0], w[1]);
+        st_shared_pairs(params + 4u * (pitch + c), b[0], b[1]);
+    }
+    __syncthreads();
     const float n = static_cast<float>(N), inv_n = 1.0f / n;
     int stage = 0;
     for (; row < p.M; row += step) {
-        copies_wait<kNormStages - 1>();
+        copies_wait<STAGES - 1>();
         __syncwarp();
         f32x2 v[CHUNKS][4];
         f32x2 sum = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            if (FULL && at.first(k) >= N) break;
-            at.template take<BF16>(v[k], stage, k);
-            sum = add2(sum, add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
+            if (first(k) >= N) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint2 a = ld_shared_u2(place(stage, k) + 256u * q + 8u * lane);
+                v[k][2 * q] = unpack2<BF16>(a.x);
+                v[k][2 * q + 1] = unpack2<BF16>(a.y);
+                sum = add2(sum, add2(v[k][2 * q], v[k][2 * q + 1]));
+            }
         }
-        const float mean = over(row_sum<WARPS>(sum_of(sum), shared[0]), n, inv_n);
+        const float mean = over(row_sum<WARPS>(sum_of(sum), shared[0], group), n, inv_n);
         // The sum has used what was in the warp's places.
-        fetch(stage, row + kNormStages * step);
-        stage = stage + 1 == kNormStages ? 0 : stage + 1;
+        fetch(stage, row + STAGES * step);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
         f32x2 sq = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            if (FULL && at.first(k) >= N) break;
+            if (first(k) >= N) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], both(-mean));
-            if (!FULL && at.first(k) + 256 > N) {  // nothing past the row's end counts
+            if (!FULL && first(k) + 256 > N) {  // nothing past the row's end counts
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int32_t c = at.quad(k, i >> 1) + 2 * (i & 1);
+                    const int32_t c = first(k) + 128 * (i >> 1) + 4 * lane + 2 * (i & 1);
                     float lo, hi;
                     split(v[k][i], lo, hi);
                     v[k][i] = pair(c < N ? lo : 0.0f, c + 1 < N ? hi : 0.0f);
@@ -308,72 +304,84 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
 #pragma unroll
             for (int i = 0; i < 4; ++i) sq = fma2(v[k][i], v[k][i], sq);
         }
-        const float rstd = rsqrtf(over(row_sum<WARPS>(sum_of(sq), shared[1]), n, inv_n) + p.eps);
-        if (at.lane == 0 && at.in_row == 0) {
+        const float rstd = rsqrtf(over(row_sum<WARPS>(sum_of(sq), shared[1], group), n, inv_n) + p.eps);
+        if (lane == 0 && in_row == 0) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
         uint16_t* const y = p.Y + row * p.ldy;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            if (at.first(k) >= N) break;
+            if (first(k) >= N) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int32_t c = at.quad(k, q);
-                f32x2 w[2], b[2];
-                load_vector4<BF16, FULL>(w, p.w, c, N, 1.0f);
-                load_vector4<BF16, FULL>(b, p.b, c, N, 0.0f);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) b[i] = fma2(mul2(v[k][2 * q + i], both(rstd)), w[i], b[i]);
-                store_row4<FULL>(y, c, N, round2<BF16>(b[0]), round2<BF16>(b[1]));
+                const int32_t c = first(k) + 128 * q + 4 * lane;
+                const float4 w = ld_shared_f4(params + 4u * c), b = ld_shared_f4(params + 4u * (pitch + c));
+                const f32x2 lo = fma2(mul2(v[k][2 * q], both(rstd)), pair(w.x, w.y), pair(b.x, b.y));
+                const f32x2 hi = fma2(mul2(v[k][2 * q + 1], both(rstd)), pair(w.z, w.w), pair(b.z, b.w));
+                store_row4<FULL>(y, c, N, round2<BF16>(lo), round2<BF16>(hi));
             }
         }
     }
 }
 
-constexpr int kWideWarps = 32;  // a row of any length per block, read again for each pass
+// A row of any length per block, read again (from L2) for each pass.
+constexpr int kWideWarps = 16, kWideUnroll = 4;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kWideWarps * 32) layer_norm_wide_kernel(const NormParams p)
+__global__ void __launch_bounds__(kWideWarps * 32, 1) layer_norm_wide_kernel(const NormParams p)
 {
-    __shared__ __align__(16) float2 shared[2][kWideWarps];
+    __shared__ __align__(16) float shared[2][kWideWarps];
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    const int64_t row = blockIdx.x, step = kWideWarps * 32 * int64_t(8);
+    constexpr int64_t kStep = kWideWarps * 32 * int64_t(8);
+    const int64_t row = blockIdx.x;
     const uint16_t* const x = p.X + row * p.ldx;
-    const int64_t c0 = threadIdx.x * int64_t(8);
-    f32x2 v[4], sum = 0;
-    for (int64_t c = c0; c < p.N; c += step) {
-        unpack8<BF16>(v, load_row8(x, c, p.N));
-        sum = add2(sum, add2(add2(v[0], v[1]), add2(v[2], v[3])));
-    }
-    const float n = static_cast<float>(p.N);
-    const float mean = row_sums<kWideWarps>(make_float2(sum_of(sum), 0.0f), shared[0]).x / n;
-    float sq = 0.0f;
-    for (int64_t c = c0; c < p.N; c += step) {
-        unpack8<BF16>(v, load_row8(x, c, p.N));
+    // f(c, v) on every eight values from column c on, zeros past the row's end; kWideUnroll loads at once.
+    auto pass = [&](auto f) {
+        for (int64_t c0 = threadIdx.x * int64_t(8); c0 < p.N; c0 += kWideUnroll * kStep) {
+            uint4 raw[kWideUnroll];
+#pragma unroll
+            for (int u = 0; u < kWideUnroll; ++u) raw[u] = load_row8(x, c0 + u * kStep, p.N);
+#pragma unroll
+            for (int u = 0; u < kWideUnroll; ++u) {
+                f32x2 v[4];
+                unpack8<BF16>(v, raw[u]);
+                f(c0 + u * kStep, v);
+            }
+        }
+    };
+    f32x2 sum = 0;
+    pass([&](int64_t, f32x2 (&v)[4]) { sum = add2(sum, add2(add2(v[0], v[1]), add2(v[2], v[3]))); });
+    const float n = static_cast<float>(p.N), inv_n = 1.0f / n;
+    const float mean = over(row_sum<kWideWarps>(sum_of(sum), shared[0], 0), n, inv_n);
+    f32x2 sq = 0;
+    pass([&](int64_t c, f32x2 (&v)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            split(add2(v[i], both(-mean)), lo, hi);
-            if (c + 2 * i < p.N) sq = fmaf(lo, lo, sq);
-            if (c + 2 * i + 1 < p.N) sq = fmaf(hi, hi, sq);
+            f32x2 e = add2(v[i], both(-mean));
+            if (c + 8 > p.N) {
+                float lo, hi;
+                split(e, lo, hi);
+                e = pair(c + 2 * i < p.N ? lo : 0.0f, c + 2 * i + 1 < p.N ? hi : 0.0f);
+            }
+            sq = fma2(e, e, sq);
         }
-    }
-    const float rstd = 1.0f / sqrtf(row_sums<kWideWarps>(make_float2(sq, 0.0f), shared[1]).x / n + p.eps);
+    });
+    const float rstd = rsqrtf(over(row_sum<kWideWarps>(sum_of(sq), shared[1], 0), n, inv_n) + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    for (int64_t c = c0; c < p.N; c += step) {
+    pass([&](int64_t c, f32x2 (&v)[4]) {
+        if (c >= p.N) return;
         f32x2 w[4], b[4];
-        unpack8<BF16>(v, load_row8(x, c, p.N));
         load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
         load_vector8<BF16>(b, p.b, c, p.N, 0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[i] = fma2(mul2(add2(v[i], both(-mean)), both(rstd)), w[i], b[i]);
         store_row8(p.Y + row * p.ldy, c, p.N, round8<BF16>(b));
-    }
+    });
 }
 
 struct NormGradParams {
@@ -387,46 +395,35 @@ struct NormGradParams {
     int64_t block_rows;  // layer_norm_grad_wide_kernel: rows per block
 };
 
-// dx of eight elements from those of g (mean of g: c1, of g x^: c2), x^ and the residual.
-template <bool BF16>
-__device__ __forceinline__ uint4 norm_dx8(const f32x2 (&g)[4], const f32x2 (&h)[4], float2 c, float rstd, bool has_res, uint4 res)
-{
-    f32x2 d[4], r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = mul2(fma2(h[i], both(-c.y), add2(g[i], both(-c.x))), both(rstd));
-    if (has_res) {
-        unpack8<BF16>(r, res);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = add2(d[i], r[i]);
-    }
-    return round8<BF16>(d);
-}
-
-// ROWS rows of a block at once (more than one: WARPS is 1), joined in shared memory at the end.  Dynamic shared memory:
-// kNormGradStages * 3 * CHUNKS * 16 bytes a thread, for dy, x and the residual.  With e = x - mean the row's sums are those of
-// g and g e, and dx = rstd g - rstd mean(g) - e rstd^2 mean(g e).
-template <bool BF16, int WARPS, int CHUNKS, int ROWS, bool FULL>
-__global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * ROWS * 32))
+// GROUPS rows of a block at once, WARPS warps each, whose sums are joined in shared memory at the end.  Dynamic shared memory:
+// kNormGradStages * 3 * CHUNKS * 512 bytes a warp, for dy, x and the residual.  With e = x - mean the row's sums are those of g
+// and g e, and dx = rstd g - rstd mean(g) - e rstd^2 mean(g e).
+template <bool BF16, int WARPS, int CHUNKS, int GROUPS, bool FULL>
+__global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS * GROUPS * 32))
     layer_norm_grad_kernel(const NormGradParams p)
 {
-    static_assert(ROWS == 1 || WARPS == 1, "a block's barrier covers one row");
     static_assert(kNormGradStages == 2, "row_sums takes the stage for its place");
-    constexpr bool kKeepW = CHUNKS <= 2;  // the weights stay in registers
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float2 shared[2][WARPS < 2 ? 2 : WARPS];
-    const NormLanes<WARPS, 3 * CHUNKS, ROWS> at(ring);  // chunks of dy, then of x, then of the residual
+    constexpr int kWarps = WARPS * GROUPS;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float2 shared[2][kWarps];
     const int32_t N = static_cast<int32_t>(p.N);
-    const int64_t step = gridDim.x * static_cast<int64_t>(ROWS);
-    int64_t row = blockIdx.x * static_cast<int64_t>(ROWS) + (ROWS > 1 ? at.warp : 0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / WARPS, in_row = warp % WARPS;
+    const uint32_t ring = ptx::smem_addr(smem) + 512u * warp;
+    auto place = [&](int stage, int which, int k) { return ring + 512u * static_cast<uint32_t>(((stage * 3 + which) * CHUNKS + k) * kWarps); };
+    auto first = [&](int k) { return (k * WARPS + in_row) * 256; };
+    const int64_t step = gridDim.x * static_cast<int64_t>(GROUPS);
+    int64_t row = blockIdx.x * static_cast<int64_t>(GROUPS) + group;
     const bool has_res = p.residual != nullptr;
     auto fetch = [&](int stage, int64_t r) {
         if (r < p.M) {
 #pragma unroll
-            for (int k = 0; k < CHUNKS; ++k) {
-                at.template copy<FULL>(stage, k, k, p.dY + r * p.lddy, N);
-                at.template copy<FULL>(stage, CHUNKS + k, k, p.X + r * p.ldx, N);
-                if (has_res) at.template copy<FULL>(stage, 2 * CHUNKS + k, k, p.residual + r * p.ldr, N);
-            }
+            for (int k = 0; k < CHUNKS; ++k)
+                if (first(k) < N) {
+                    copy_row8<FULL>(place(stage, 0, k) + 16u * lane, p.dY + r * p.lddy, first(k) + 8 * lane, N);
+                    copy_row8<FULL>(place(stage, 1, k) + 16u * lane, p.X + r * p.ldx, first(k) + 8 * lane, N);
+                    if (has_res) copy_row8<FULL>(place(stage, 2, k) + 16u * lane, p.residual + r * p.ldr, first(k) + 8 * lane, N);
+                }
         }
         copies_commit();
     };
@@ -434,19 +431,6 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
     ptx::launch_dependents();
 #pragma unroll
     for (int st = 0; st < kNormGradStages; ++st) fetch(st, row + st * step);
-    f32x2 kept[kKeepW ? CHUNKS : 1][4];
-    auto weights = [&](f32x2 (&w)[4], int k) {
-        load_vector4<BF16, FULL>(w, p.w, at.quad(k, 0), N, 1.0f);
-        load_vector4<BF16, FULL>(w + 2, p.w, at.quad(k, 1), N, 1.0f);
-    };
-    if constexpr (kKeepW) {
-#pragma unroll
-        for (int k = 0; k < CHUNKS; ++k)
-            if (!FULL || at.first(k) < N) weights(kept[k], k);
-    }
-    f32x2 dw[CHUNKS][4] = {}, db[CHUNKS][4] = {};
-    const float inv_n = 1.0f / static_cast<float>(N);
-    int stage = 0;
     float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
     auto fetch_stats = [&](int64_t r) {
         if (r < p.M) {
@@ -455,6 +439,22 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
         }
     };
     fetch_stats(row);
+    f32x2 w[CHUNKS][4];
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) load_vector4<BF16>(&w[k][2 * q], p.w, first(k) + 128 * q + 4 * lane, N, 1.0f);
+    f32x2 dw[CHUNKS][4] = {}, db[CHUNKS][4] = {};
+    const float inv_n = 1.0f / static_cast<float>(N);
+    int stage = 0;
+    auto take = [&](f32x2 (&v)[4], int which, int k) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint2 a = ld_shared_u2(place(stage, which, k) + 256u * q + 8u * lane);
+            v[2 * q] = unpack2<BF16>(a.x);
+            v[2 * q + 1] = unpack2<BF16>(a.y);
+        }
+    };
     for (; row < p.M; row += step) {
         mean = next_mean;
         rstd = next_rstd;
@@ -462,125 +462,135 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32, norm_blocks_per_sm(WARPS * 
         copies_wait<kNormGradStages - 1>();
         __syncwarp();
         f32x2 s1 = 0, s2 = 0;
-        f32x2 g[4], e[4], w[4];
-        // g = dy w and e = x - mean of chunk k; dy stays in `dy`.
-        auto take = [&](int k, f32x2 (&dy)[4]) {
-            at.template take<BF16>(dy, stage, k);
-            at.template take<BF16>(e, stage, CHUNKS + k);
-            if constexpr (!kKeepW) weights(w, k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                e[i] = add2(e[i], both(-mean));
-                g[i] = mul2(dy[i], kKeepW ? kept[kKeepW ? k : 0][i] : w[i]);
-            }
-        };
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            if (at.first(k) >= N) break;
-            f32x2 dy[4];
-            take(k, dy);
+            if (first(k) >= N) break;
+            f32x2 dy[4], e[4];
+            take(dy, 0, k);
+            take(e, 1, k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // Past the row's end dy is 0, so e counts nowhere.
+                e[i] = add2(e[i], both(-mean));
                 dw[k][i] = fma2(mul2(e[i], both(rstd)), dy[i], dw[k][i]);
                 db[k][i] = add2(db[k][i], dy[i]);
-                s1 = add2(s1, g[i]);
-                s2 = fma2(g[i], e[i], s2);
+                const f32x2 g = mul2(dy[i], w[k][i]);
+                s1 = add2(s1, g);
+                s2 = fma2(g, e[i], s2);
             }
         }
-        const float2 c = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared[stage]);
+        const float2 c = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared[stage], group);
         const f32x2 c1 = both(-rstd * (c.x * inv_n)), c2 = both(-rstd * (rstd * (rstd * (c.y * inv_n))));
         uint16_t* const dx = p.dX + row * p.lddx;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
-            if (at.first(k) >= N) break;
-            f32x2 dy[4];
-            take(k, dy);
+            if (first(k) >= N) break;
+            f32x2 d[4], e[4];
+            take(d, 0, k);
+            take(e, 1, k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = fma2(e[i], c2, fma2(g[i], both(rstd), c1));
+            for (int i = 0; i < 4; ++i) d[i] = fma2(add2(e[i], both(-mean)), c2, fma2(mul2(d[i], w[k][i]), both(rstd), c1));
             if (has_res) {
-                at.template take<BF16>(dy, stage, 2 * CHUNKS + k);
+                take(e, 2, k);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) g[i] = add2(g[i], dy[i]);
+                for (int i = 0; i < 4; ++i) d[i] = add2(d[i], e[i]);
             }
-            store_row4<FULL>(dx, at.quad(k, 0), N, round2<BF16>(g[0]), round2<BF16>(g[1]));
-            store_row4<FULL>(dx, at.quad(k, 1), N, round2<BF16>(g[2]), round2<BF16>(g[3]));
+            store_row4<FULL>(dx, first(k) + 4 * lane, N, round2<BF16>(d[0]), round2<BF16>(d[1]));
+            store_row4<FULL>(dx, first(k) + 128 + 4 * lane, N, round2<BF16>(d[2]), round2<BF16>(d[3]));
         }
         __syncwarp();  // the warp has used what was in its places
         fetch(stage, row + kNormGradStages * step);
         stage ^= 1;
     }
     if (!p.dw && !p.db) return;
-    // This block's sums: of its one row group, or of ROWS warps by way of shared memory.  (The pitch is a multiple of 64.)
+    // This block's sums: the groups' added in shared memory, in the ring's place.  (The pitch is a multiple of 64.)
     auto put = [&](float* to, int32_t c, f32x2 lo, f32x2 hi) {
         float f[4];
         split(lo, f[0], f[1]);
         split(hi, f[2], f[3]);
         if (to && c < p.pitch) *reinterpret_cast<float4*>(to + blockIdx.x * p.pitch + c) = make_float4(f[0], f[1], f[2], f[3]);
     };
-    if constexpr (ROWS > 1) {
-        __shared__ f32x2 parts[2][ROWS][CHUNKS][2][32][2];
+    if constexpr (GROUPS > 1) {
+        constexpr int kQuads = WARPS * CHUNKS * 64;  // of a group's columns: (chunk, half, lane), a warp's side by side
+        static_assert(GROUPS * kQuads * 16 <= kNormGradStages * 3 * CHUNKS * 512 * kWarps, "the sums of one vector fit the ring");
+        f32x2* const parts = reinterpret_cast<f32x2*>(smem);
+        copies_wait<0>();
 #pragma unroll
-        for (int k = 0; k < CHUNKS; ++k)
+        for (int which = 0; which < 2; ++which) {
+            float* const to = which ? p.db : p.dw;
+            __syncthreads();  // the ring, and the first vector's sums, are done with
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                parts[0][at.warp][k][i >> 1][at.lane][i & 1] = dw[k][i];
-                parts[1][at.warp][k][i >> 1][at.lane][i & 1] = db[k][i];
+            for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    parts[2 * (group * kQuads + (k * WARPS + in_row) * 64 + (i >> 1) * 32 + lane) + (i & 1)] = which ? db[k][i] : dw[k][i];
+            __syncthreads();
+            for (int e = threadIdx.x; e < kQuads; e += kWarps * 32) {
+                f32x2 lo = 0, hi = 0;
+#pragma unroll
+                for (int r = 0; r < GROUPS; ++r) {
+                    lo = add2(lo, parts[2 * (r * kQuads + e)]);
+                    hi = add2(hi, parts[2 * (r * kQuads + e) + 1]);
+                }
+                put(to, (e >> 6) * 256 + 128 * ((e >> 5) & 1) + 4 * (e & 31), lo, hi);
             }
-        __syncthreads();
-        for (int e = threadIdx.x; e < 2 * CHUNKS * 2 * 32; e += ROWS * 32) {
-            const int l = e & 31, q = (e >> 5) & 1, k = (e >> 6) % CHUNKS, which = (e >> 6) / CHUNKS;
-            f32x2 lo = 0, hi = 0;
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                lo = add2(lo, parts[which][r][k][q][l][0]);
-                hi = add2(hi, parts[which][r][k][q][l][1]);
-            }
-            put(which ? p.db : p.dw, k * 256 + 128 * q + 4 * l, lo, hi);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                put(p.dw, at.quad(k, q), dw[k][2 * q], dw[k][2 * q + 1]);
-                put(p.db, at.quad(k, q), db[k][2 * q], db[k][2 * q + 1]);
+                put(p.dw, first(k) + 128 * q + 4 * lane, dw[k][2 * q], dw[k][2 * q + 1]);
+                put(p.db, first(k) + 128 * q + 4 * lane, db[k][2 * q], db[k][2 * q + 1]);
             }
     }
 }
 
 // Rows that registers do not hold: first the means of every row, then dx and the sums by strips of columns.
+constexpr int kMeansWarps = 8, kMeansUnroll = 4;
+
 template <bool BF16>
-__global__ void __launch_bounds__(kWideWarps * 32) layer_norm_grad_means_kernel(const NormGradParams p)
+__global__ void __launch_bounds__(kMeansWarps * 32, 4) layer_norm_grad_means_kernel(const NormGradParams p)
 {
-    __shared__ __align__(16) float2 shared[2][kWideWarps];
+    __shared__ __align__(16) float2 shared[kMeansWarps];
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     const int64_t row = blockIdx.x;
     const float mean = p.mean[row], rstd = p.rstd[row];
     f32x2 s1 = 0, s2 = 0;
-    for (int64_t c = threadIdx.x * int64_t(8); c < p.N; c += kWideWarps * 32 * int64_t(8)) {
-        f32x2 g[4], h[4], w[4];
-        unpack8<BF16>(g, load_row8(p.dY + row * p.lddy, c, p.N));
-        unpack8<BF16>(h, load_row8(p.X + row * p.ldx, c, p.N));
-        load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
+    constexpr int64_t kStep = kMeansWarps * 32 * int64_t(8);
+    for (int64_t c0 = threadIdx.x * int64_t(8); c0 < p.N; c0 += kMeansUnroll * kStep) {
+        uint4 dy[kMeansUnroll], x[kMeansUnroll];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            g[i] = mul2(g[i], w[i]);
-            s1 = add2(s1, g[i]);
-            s2 = fma2(g[i], mul2(add2(h[i], both(-mean)), both(rstd)), s2);
+        for (int u = 0; u < kMeansUnroll; ++u) {
+            dy[u] = load_row8(p.dY + row * p.lddy, c0 + u * kStep, p.N);
+            x[u] = load_row8(p.X + row * p.ldx, c0 + u * kStep, p.N);
+        }
+#pragma unroll
+        for (int u = 0; u < kMeansUnroll; ++u) {
+            if (c0 + u * kStep >= p.N) break;
+            f32x2 g[4], h[4], w[4];
+            unpack8<BF16>(g, dy[u]);
+            unpack8<BF16>(h, x[u]);
+            load_vector8<BF16>(w, p.w, c0 + u * kStep, p.N, 1.0f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[i] = mul2(g[i], w[i]);
+                s1 = add2(s1, g[i]);
+                s2 = fma2(g[i], mul2(add2(h[i], both(-mean)), both(rstd)), s2);
+            }
         }
     }
-    const float2 s = row_sums<kWideWarps>(make_float2(sum_of(s1), sum_of(s2)), shared[0]);
+    const float2 s = row_sums<kMeansWarps>(make_float2(sum_of(s1), sum_of(s2)), shared, 0);
     const float inv_n = 1.0f / static_cast<float>(p.N);
     if (threadIdx.x == 0) p.row_means[row] = make_float2(s.x * inv_n, s.y * inv_n);
 }
 
-constexpr int kStripWarps = 8;
-constexpr int kStripCols = 256;
+// A block has 256 columns of block_rows rows, a warp every eighth of them, two at a time.
+constexpr int kStripWarps = 8, kStripCols = 256, kStripRows = 2;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kStripWarps * 32) layer_norm_grad_wide_kernel(const NormGradParams p)
+__global__ void __launch_bounds__(kStripWarps * 32, 2) layer_norm_grad_wide_kernel(const NormGradParams p)
 {
     __shared__ f32x2 parts[2][kStripWarps][kStripCols / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -590,22 +600,45 @@ __global__ void __launch_bounds__(kStripWarps * 32) layer_norm_grad_wide_kernel(
     f32x2 w[4], dw[4] = {}, db[4] = {};
     load_vector8<BF16>(w, p.w, c, p.N, 1.0f);
     const int64_t r0 = blockIdx.y * p.block_rows, r1 = r0 + p.block_rows < p.M ? r0 + p.block_rows : p.M;
+    const bool has_res = p.residual != nullptr;
     if (c < p.N)
-        for (int64_t row = r0 + warp; row < r1; row += kStripWarps) {
-            const float mean = p.mean[row], rstd = p.rstd[row];
-            f32x2 g[4], h[4];
-            uint4 res = make_uint4(0, 0, 0, 0);
-            unpack8<BF16>(g, load_row8(p.dY + row * p.lddy, c, p.N));
-            unpack8<BF16>(h, load_row8(p.X + row * p.ldx, c, p.N));
-            if (p.residual) res = load_row8(p.residual + row * p.ldr, c, p.N);
+        for (int64_t row0 = r0 + warp; row0 < r1; row0 += kStripRows * kStripWarps) {
+            uint4 dy[kStripRows], x[kStripRows], res[kStripRows];
+            float mean[kStripRows], rstd[kStripRows];
+            float2 means[kStripRows];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[i] = mul2(add2(h[i], both(-mean)), both(rstd));
-                dw[i] = fma2(g[i], h[i], dw[i]);
-                db[i] = add2(db[i], g[i]);
-                g[i] = mul2(g[i], w[i]);
+            for (int u = 0; u < kStripRows; ++u) {
+                const int64_t row = row0 + u * kStripWarps;
+                if (row >= r1) break;
+                dy[u] = load_row8(p.dY + row * p.lddy, c, p.N);
+                x[u] = load_row8(p.X + row * p.ldx, c, p.N);
+                res[u] = has_res ? load_row8(p.residual + row * p.ldr, c, p.N) : make_uint4(0, 0, 0, 0);
+                mean[u] = p.mean[row];
+                rstd[u] = p.rstd[row];
+                means[u] = p.row_means[row];
             }
-            store_row8(p.dX + row * p.lddx, c, p.N, norm_dx8<BF16>(g, h, p.row_means[row], rstd, p.residual != nullptr, res));
+#pragma unroll
+            for (int u = 0; u < kStripRows; ++u) {
+                const int64_t row = row0 + u * kStripWarps;
+                if (row >= r1) break;
+                f32x2 g[4], h[4], d[4];
+                unpack8<BF16>(g, dy[u]);
+                unpack8<BF16>(h, x[u]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = mul2(add2(h[i], both(-mean[u])), both(rstd[u]));
+                    dw[i] = fma2(g[i], h[i], dw[i]);
+                    db[i] = add2(db[i], g[i]);
+                    g[i] = mul2(g[i], w[i]);
+                    d[i] = mul2(fma2(h[i], both(-means[u].y), add2(g[i], both(-means[u].x))), both(rstd[u]));
+                }
+                if (has_res) {
+                    unpack8<BF16>(h, res[u]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = add2(d[i], h[i]);
+                }
+                store_row8(p.dX + row * p.lddx, c, p.N, round8<BF16>(d));
+            }
         }
     if (!p.dw && !p.db) return;
 #pragma unroll

@@ -34,29 +34,32 @@ NormVector vector_of(const void* at, gemm_dtype_t t)
 
 unsigned blocks_for(int64_t rows, int64_t per_block) { return static_cast<unsigned>(cdiv(rows, per_block)); }
 
-// A persistent kernel over M rows whose threads hold `slots` 16-byte places each of dynamic shared memory.
+// A persistent kernel over rows.
 template <class P>
-gemm_status_t launch_rows(gemm_handle_t h, void (*fn)(P), int slot, int64_t blocks, int threads, int slots, const P& p, cudaStream_t s)
+gemm_status_t launch_rows(gemm_handle_t h, void (*fn)(P), int slot, int64_t blocks, int threads, int smem, int smem_max, const P& p, cudaStream_t s)
 {
-    const int smem = 16 * slots * threads;
     if (!h->dev.attrs_set[kNormSlot0 + slot]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) != cudaSuccess)
             return GEMM_ERR_CUDA;
         h->dev.attrs_set[kNormSlot0 + slot] = true;
     }
     return launch_after(fn, static_cast<unsigned>(blocks), threads, static_cast<size_t>(smem), s, p);
 }
 
-// The shape of the kernels for rows of N <= kNormMaxHeld, by steps of 256, 512, ... 16384: warps and chunks of 8 elements a lane
-// for a row, rows a block.  Few warps with many chunks each spend less on the sums across warps and wait less at barriers
-// (16384 x 8192 forward: 16 warps of 2 chunks 162 us); the backward kernel's sums of dw and db leave room for four.
+// The shapes of the kernels for rows that registers hold, by steps of 256, 512, ... columns: warps and chunks of 8 elements a
+// lane for a row; forward: rows whose loads are in flight; backward: rows a block.  Few warps with many chunks each spend less on
+// the sums across warps and wait less at barriers; the backward kernel's sums of dw and db leave room for two chunks (with four
+// its weights came from L2 for every row: 8192 x 8192 125 us).
 struct NormShape {
-    int warps, chunks, rows;
-    int threads() const { return 32 * warps * rows; }
+    int warps, chunks, stages;
 };
-constexpr int kNormShapes = 7;
-constexpr NormShape kShape[kNormShapes] = {{1, 1, 4}, {1, 2, 4}, {1, 4, 4}, {1, 8, 4}, {2, 8, 1}, {4, 8, 1}, {8, 8, 1}};
-constexpr NormShape kGradShape[kNormShapes] = {{1, 1, 8}, {1, 2, 8}, {1, 4, 4}, {4, 2, 1}, {8, 2, 1}, {8, 4, 1}, {16, 4, 1}};
+constexpr int kNormShapes = 7, kNormGradShapes = 6;
+constexpr NormShape kShape[kNormShapes] = {{1, 1, 4}, {1, 2, 4}, {1, 4, 3}, {1, 8, 2}, {2, 8, 2}, {4, 8, 2}, {8, 8, 1}};
+struct NormGradShape {
+    int warps, chunks, groups;
+    int threads() const { return 32 * warps * groups; }
+};
+constexpr NormGradShape kGradShape[kNormGradShapes] = {{1, 1, 8}, {1, 2, 8}, {2, 2, 4}, {4, 2, 2}, {8, 2, 1}, {16, 2, 1}};
 
 int shape_for(int64_t N)
 {
@@ -65,18 +68,16 @@ int shape_for(int64_t N)
     return i;
 }
 
-bool quads(const NormVector& v) { return v.kind != kVecF32Any && v.kind != kVec16Any; }
-
 template <bool BF16, bool FULL, int I>
 constexpr auto norm_fn()
 {
-    return &layer_norm_kernel<BF16, kShape[I].warps, kShape[I].chunks, kShape[I].rows, FULL>;
+    return &layer_norm_kernel<BF16, kShape[I].warps, kShape[I].chunks, kShape[I].stages, FULL>;
 }
 
 template <bool BF16, bool FULL, int I>
 constexpr auto norm_grad_fn()
 {
-    return &layer_norm_grad_kernel<BF16, kGradShape[I].warps, kGradShape[I].chunks, kGradShape[I].rows, FULL>;
+    return &layer_norm_grad_kernel<BF16, kGradShape[I].warps, kGradShape[I].chunks, kGradShape[I].groups, FULL>;
 }
 
 template <bool BF16, bool FULL>
@@ -87,43 +88,47 @@ gemm_status_t launch_norm(gemm_handle_t h, const NormParams& p, cudaStream_t s)
                                                             norm_fn<BF16, FULL, 6>()};
     const int i = shape_for(p.N);
     const NormShape shape = kShape[i];
-    const int64_t blocks = std::min<int64_t>(cdiv(p.M, shape.rows), h->dev.num_sms * norm_blocks_per_sm(shape.threads()));
-    return launch_rows<NormParams>(h, kFn[i], i + kNormShapes * (2 * FULL + BF16), blocks, shape.threads(), kNormStages * shape.chunks, p, s);
+    // Few rows are spread over the SMs before a block takes several; eight warps at least bring in weights and biases.
+    const int64_t most = kNormWarps / shape.warps, groups = std::min(most, std::max(cdiv(p.M, h->dev.num_sms), int64_t(8) / shape.warps));
+    const int64_t blocks = std::min<int64_t>(cdiv(p.M, groups), h->dev.num_sms);
+    const auto smem = [&](int64_t columns, int64_t warps) { return static_cast<int>(8 * columns + 512 * shape.stages * shape.chunks * warps); };
+    return launch_rows<NormParams>(h, kFn[i], i + kNormShapes * (2 * FULL + BF16), blocks, static_cast<int>(32 * shape.warps * groups),
+                                   smem(cdiv(p.N, 256) * 256, shape.warps * groups), smem(int64_t(256) << i, kNormWarps), p, s);
 }
 
 template <bool BF16>
 gemm_status_t launch_norm(gemm_handle_t h, const NormParams& p, cudaStream_t s)
 {
     if (p.N > kNormMaxHeld) return launch_after(&layer_norm_wide_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
-    return p.N % 256 == 0 && quads(p.w) && quads(p.b) ? launch_norm<BF16, true>(h, p, s) : launch_norm<BF16, false>(h, p, s);
+    return p.N % 256 == 0 ? launch_norm<BF16, true>(h, p, s) : launch_norm<BF16, false>(h, p, s);
 }
 
 // Most rows of partial sums of dw and db: blocks that run at once on 152 SMs (fewer SMs: fewer; more: no more).
 int64_t norm_grad_max_blocks(int64_t M, int64_t N)
 {
-    return std::min<int64_t>(M, 152 * (N > kNormMaxHeld ? 2 : norm_blocks_per_sm(kGradShape[shape_for(N)].threads())));
+    return std::min<int64_t>(M, N > 4096 && N <= kNormGradMaxHeld ? 152 : 304);
 }
 
 template <bool BF16, bool FULL>
 gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& p, int64_t* blocks, cudaStream_t s)
 {
-    constexpr void (*kFn[kNormShapes])(const NormGradParams) = {
-        norm_grad_fn<BF16, FULL, 0>(), norm_grad_fn<BF16, FULL, 1>(), norm_grad_fn<BF16, FULL, 2>(), norm_grad_fn<BF16, FULL, 3>(),
-        norm_grad_fn<BF16, FULL, 4>(), norm_grad_fn<BF16, FULL, 5>(), norm_grad_fn<BF16, FULL, 6>()};
+    constexpr void (*kFn[kNormGradShapes])(const NormGradParams) = {norm_grad_fn<BF16, FULL, 0>(), norm_grad_fn<BF16, FULL, 1>(),
+                                                                    norm_grad_fn<BF16, FULL, 2>(), norm_grad_fn<BF16, FULL, 3>(),
+                                                                    norm_grad_fn<BF16, FULL, 4>(), norm_grad_fn<BF16, FULL, 5>()};
     const int i = shape_for(p.N);
-    const NormShape shape = kGradShape[i];
-    *blocks = std::min({cdiv(p.M, shape.rows), norm_grad_max_blocks(p.M, p.N), int64_t(h->dev.num_sms) * norm_blocks_per_sm(shape.threads())});
-    return launch_rows<NormGradParams>(h, kFn[i], i + kNormShapes * (4 + 2 * FULL + BF16), *blocks, shape.threads(),
-                                       3 * kNormGradStages * shape.chunks, p, s);
+    const NormGradShape shape = kGradShape[i];
+    *blocks = std::min({cdiv(p.M, shape.groups), norm_grad_max_blocks(p.M, p.N), int64_t(h->dev.num_sms) * (kNormGradThreads / shape.threads())});
+    const int smem = 3 * kNormGradStages * shape.chunks * 16 * shape.threads();
+    return launch_rows<NormGradParams>(h, kFn[i], i + kNormShapes * (4 + 2 * FULL + BF16), *blocks, shape.threads(), smem, smem, p, s);
 }
 
 template <bool BF16>
 gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, cudaStream_t s)
 {
-    if (q.N <= kNormMaxHeld)
-        return q.N % 256 == 0 && quads(q.w) ? launch_norm_grad<BF16, true>(h, q, blocks, s) : launch_norm_grad<BF16, false>(h, q, blocks, s);
+    if (q.N <= kNormGradMaxHeld)
+        return q.N % 256 == 0 ? launch_norm_grad<BF16, true>(h, q, blocks, s) : launch_norm_grad<BF16, false>(h, q, blocks, s);
     NormGradParams p = q;
-    const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kWideWarps * 32, 0, s, p);
+    const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kMeansWarps * 32, 0, s, p);
     if (st != GEMM_OK) return st;
     p.block_rows = cdiv(p.M, std::min(cdiv(p.M, 32), norm_grad_max_blocks(p.M, p.N)));
     *blocks = cdiv(p.M, p.block_rows);
@@ -181,7 +186,7 @@ gemm_status_t gemm_run_layer_norm(gemm_handle_t h, const gemm_layer_norm_args_t*
 int64_t gemm_layer_norm_grad_workspace_bytes(int64_t M, int64_t N)
 {
     if (M <= 0 || N <= 0) return 0;
-    return 8 * norm_grad_max_blocks(M, N) * sum_pitch(N) + (N > kNormMaxHeld ? 8 * M : 0);
+    return 8 * norm_grad_max_blocks(M, N) * sum_pitch(N) + (N > kNormGradMaxHeld ? 8 * M : 0);
 }
 
 gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_grad_args_t* args, void* stream)
@@ -206,7 +211,7 @@ gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_gr
         check_stat(c, a.mean);
         check_stat(c, a.rstd);
         const int64_t need = gemm_layer_norm_grad_workspace_bytes(a.M, a.N);
-        if ((sums || a.N > kNormMaxHeld) && (a.workspace || need > GEMM_OWN_SUMS_BYTES)) {
+        if ((sums || a.N > kNormGradMaxHeld) && (a.workspace || need > GEMM_OWN_SUMS_BYTES)) {
             if (!a.workspace || a.workspace_bytes < need)
                 c.add(GEMM_ERR_INVALID_ARG);
             else if ((reinterpret_cast<uintptr_t>(a.workspace) & 15u) != 0)

@@ -234,8 +234,8 @@ def layer_norm_grad_workspace_bytes(M: int, N: int) -> int:
 
 def _norm_bytes(M: int, N: int) -> int:
     """layer_norm_grad_workspace_bytes without a call into the library."""
-    blocks = 608 if 512 < N <= 2048 else 152 if 8192 < N <= 16384 else 304
-    return (8 * min(M, blocks) * (-(-N // 64) * 64) + (8 * M if N > 16384 else 0)) if M and N else 0
+    blocks = 152 if 4096 < N <= 8192 else 304
+    return (8 * min(M, blocks) * (-(-N // 64) * 64) + (8 * M if N > 8192 else 0)) if M and N else 0
 
 
 def tile_coord(tile: int, tiles_m: int, tiles_n: int, group_m: int):
@@ -955,7 +955,7 @@ class Gemm:
             dw_code, dw_p = _vector(dweight, "dweight", N, dt, dev), dweight.data_ptr()
         if dbias is not None:
             db_code, db_p = _vector(dbias, "dbias", N, dt, dev), dbias.data_ptr()
-        if dw_p or db_p or N > 16384:
+        if dw_p or db_p or N > 8192:
             ws_bytes = _norm_bytes(M, N)
             if ws_bytes > OWN_SUMS_BYTES:
                 ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)

@@ -619,7 +619,7 @@ gemm_status_t gemm_run_layer_norm(gemm_handle_t h, const gemm_layer_norm_args_t*
  *   - dweight, dbias: N values of their dtypes (F32, or dtype), or NULL; not read with beta == 0.
  *   - workspace: gemm_layer_norm_grad_workspace_bytes(M, N) bytes, 16-byte aligned, that the call may overwrite until its
  *     kernels are done (fewer: INVALID_ARG).  It may be NULL if those are at most GEMM_OWN_SUMS_BYTES, or
- *     if neither dweight nor dbias is wanted and N is at most 16384.
+ *     if neither dweight nor dbias is wanted and N is at most 8192.
  *   - N == 0 is a no-op; with M == 0 dweight and dbias become beta times themselves. */
 typedef struct {
     const void* dY;
@@ -644,8 +644,8 @@ typedef struct {
 
 gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_grad_args_t* args, void* stream);
 
-/* Bytes of workspace for gemm_run_layer_norm_grad: 8 * min(M, B) * (N rounded up to 64), B = 608 for N from 513 to 2048, 152
- * for N from 8193 to 16384, else 304; and 8 M more where N is over 16384; 0 when M or N is 0. */
+/* Bytes of workspace for gemm_run_layer_norm_grad: 8 * min(M, B) * (N rounded up to 64), B = 152 for N from 4097 to 8192,
+ * else 304; and 8 M more where N is over 8192; 0 when M or N is 0. */
 int64_t gemm_layer_norm_grad_workspace_bytes(int64_t M, int64_t N);
 
 /* ---------------------------------------------------------------- status and version */
