@@ -376,6 +376,8 @@ struct Watchdog {
                                          int kb) const
     {
         if (ptx::mbar_try_wait(bar, parity)) return true;
+        // A first sleep before the clock is read: reading it takes longer than most waits.
+        if (ptx::mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
         const uint64_t t0 = ptx::globaltimer_ns();
         for (;;) {
             // Sleep until the phase completes (or kWaitSleepNs passes): a waiting warp must

@@ -329,7 +329,7 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     const int64_t cols = q.mode == dtg::linear::kGlu ? 256 * cdiv(q.cols, 128) : q.cols;
     int config = pick_config(o, h->dev, q.rows, cols, q.depth);
     if (config == GEMM_CONFIG_128x64) config = GEMM_CONFIG_128x128;
-    if (gated(q) && config == GEMM_CONFIG_128x128) config = GEMM_CONFIG_128x256;
+    if ((gated(q) || q.scaled) && config == GEMM_CONFIG_128x128) config = GEMM_CONFIG_128x256;  // (their only one-CTA tile)
     // CTA pairs from 2/5 of a tile per SM on, where gemm_run asks for 1/2: on 64 pair tiles 512 x 8192 x 8192 takes 46.8
     // us against 57.7 in 128 x 256 tiles, 1024 x 4096 x 4096 27.0 and 30.7; on 32 256 x 8192 x 8192 46.2 and 40.8.
     if (o.config == GEMM_CONFIG_AUTO && cdiv(q.rows, 256) * cdiv(cols, 256) * 5 >= 2 * h->dev.num_sms)

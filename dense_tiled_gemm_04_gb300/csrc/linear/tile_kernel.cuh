@@ -109,8 +109,8 @@ struct TileSmem {
     static constexpr int kStgOff = STAGES * kStageBytes;
     static constexpr int kStgBufs = STG_BUFS;
     static constexpr int kBarOff = kStgOff + kTileEpiWarps * STG_BUFS * kTileStgBytes;
-    // full, empty, acc_full[2], acc_empty[2], drain, pre-activation boxes per staging buffer
-    static constexpr int kNumBars = 2 * STAGES + 5 + kTileEpiWarps * (STG_BUFS < 2 ? 2 : STG_BUFS);
+    // full, empty, acc_full[2], acc_empty[2], drain[2], pre-activation boxes per staging buffer
+    static constexpr int kNumBars = 2 * STAGES + 6 + kTileEpiWarps * (STG_BUFS < 2 ? 2 : STG_BUFS);
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kTotal = kMiscOff + 16;  // tmem slot, abort flag, stream-K "last" flag
     static constexpr int kAlloc = kTotal + 1024;  // slack for aligning the base to 1 KB
@@ -338,6 +338,8 @@ __device__ __forceinline__ void tile_coord32(uint32_t t, const KernelParams& p, 
     tm = first_m + (r - tn * rows);
 }
 
+__device__ const float kUnitScale = 1.0f;
+
 // IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward ... kGluDgrad;
 // SUMS: the contraction runs in chunks that are summed in registers; CLUSTER: 1 (one CTA) or 2 (a CTA pair); SCALED:
 // 8-bit operands with a scale for each block of 128: every K block is a chunk, multiplied by its scales as it is
@@ -376,8 +378,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto acce_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 5 + STG_BUFS * w + b); };  // dgrad: box loaded
+    auto drain_bar = [&](int w) { return bar0 + 8u * (2 * STAGES + 4 + w); };
+    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 6 + STG_BUFS * w + b); };  // dgrad: box loaded
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int32_t* const abort_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 4);
     volatile int32_t* const last_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 8);
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ptx::mbar_init(accf_bar(b), 1);
             ptx::mbar_init(acce_bar(b), kTileEpiWarps * kRanks);
         }
-        ptx::mbar_init(drain_bar, 1);
+        for (int w = 0; w < 2; ++w) ptx::mbar_init(drain_bar(w), 1);
         if constexpr (MODE == kDgrad || MODE == kGluDgrad)
             for (int w = 0; w < kTileEpiWarps; ++w)
                 for (int b = 0; b < STG_BUFS; ++b) ptx::mbar_init(in_bar(w, b), 1);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int s = 0; s < STAGES; ++s)
                     if (armed_mask & (1u << s)) wd.drain(full_bar(s), (armed_parity >> s) & 1u);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || (SCALED && warp == kMmaWarp + 1)) {
         if (lane == 0 && leader) {
             // ---------------------------------------------------------------- MMA issuer
             uint32_t idesc = idesc_mma<T::kFormat, BT, kTileM, BN>() | (AT ? 1u << 15 : 0u);
@@ -523,11 +525,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             WorkIter it(p, unit, units);
             int64_t tile;
             int kb0, kb1;
+            // SCALED: every K block is a chunk, whose waits, MMAs and commits take one thread longer (630 cycles) than the MMAs
+            // themselves (512).  Two warps take turns, each with an accumulator of its own.
+            const int mma_warp = SCALED ? warp - kMmaWarp : 0;
+            [[maybe_unused]] int turn = 0;
             while (!aborted && it.next(p, tile, kb0, kb1)) {
                 // A loop over chunks around one over K blocks: with the chunk's wait and commit as conditions inside a
                 // single loop, each K block's issue took about 60 cycles longer (8192^3 bf16: 623 against 563 us).
                 const int n = kb1 - kb0;
                 for (int c0 = 0; c0 < n && !aborted;) {
+                    if constexpr (SCALED) {
+                        const bool mine = turn == mma_warp;
+                        turn ^= 1;
+                        if (!mine) {
+                            ++c0;
+                            if (++stage == STAGES) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                            continue;
+                        }
+                        acc = mma_warp;
+                    }
                     if (!wd.wait(acce_bar(acc), acc_phase ^ 1u, kRoleMma, tile, -1)) {
                         aborted = true;
                         break;
@@ -581,16 +600,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         ptx::mma_commit_cta1(accf_bar(acc));
                     c0 = c1;
                     acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
+                    if (SCALED || acc == 0) acc_phase ^= 1u;
                 }
             }
             if (aborted) {
                 // Let every MMA issued so far finish before the TMEM is released.
                 if constexpr (PAIR)
-                    ptx::mma_commit_pair(drain_bar, static_cast<uint16_t>(1u << rank));
+                    ptx::mma_commit_pair(drain_bar(mma_warp), static_cast<uint16_t>(1u << rank));
                 else
-                    ptx::mma_commit_cta1(drain_bar);
-                wd.drain(drain_bar, 0);
+                    ptx::mma_commit_cta1(drain_bar(mma_warp));
+                wd.drain(drain_bar(mma_warp), 0);
             }
         }
         __syncwarp();
@@ -904,14 +923,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if constexpr (GLU) return static_cast<uint32_t>((q * 32 / kWarpN) * kTileN + half * kWarpN + q * 32 % kWarpN);
             return static_cast<uint32_t>(half * CW + q * 32);
         };
-        // SCALED: the factors of K block kb for this thread's row, of the warp's columns (of g and of u).
-        auto load_scales = [&](int kb, float& fg, float& fu) {
+        // SCALED: the scales of K block kb for this thread's row and the warp's columns, which lie inside one block of 128 of the
+        // weights' rows (gated: of Wg's and of Wu's).
+        struct Scales {
+            float x = 1.0f, w = 1.0f, w_up = 1.0f;
+        };
+        // Absent scales, and those of rows and columns past the edges, are a 1 that is read at every K block.
+        const float *xs_at = &kUnitScale, *ws_at = &kUnitScale, *wu_at = &kUnitScale;
+        int xs_step = 0, ws_step = 0;
+        auto point_at_scales = [&]() {
             const int64_t row = static_cast<int64_t>(cur.y) + lane;
-            const int64_t block = cur.x >> 7;  // 128 columns of a weight's block: a warp's lie inside one
-            const float xs = p.x_scales && row < p.M ? p.x_scales[row * p.ld_xs + kb] : 1.0f;
-            const bool w = p.w_scales && cur.x < p.N;
-            fg = xs * (w ? p.w_scales[block * p.ld_ws + kb] : 1.0f);
-            if constexpr (GLU) fu = xs * (w ? p.w_scales[p.up_scales + block * p.ld_ws + kb] : 1.0f);
+            const bool x = p.x_scales && row < p.M, w = p.w_scales && cur.x < p.N;
+            xs_at = x ? p.x_scales + row * p.ld_xs : &kUnitScale;
+            ws_at = w ? p.w_scales + (cur.x >> 7) * p.ld_ws : &kUnitScale;
+            if constexpr (GLU) wu_at = w ? ws_at + p.up_scales : &kUnitScale;
+            xs_step = x;
+            ws_step = w;
+        };
+        auto load_scales = [&](int kb) {
+            Scales f;
+            f.x = __ldg(xs_at + kb * xs_step);
+            f.w = __ldg(ws_at + kb * ws_step);
+            if constexpr (GLU) f.w_up = __ldg(wu_at + kb * ws_step);
+            return f;
         };
         // 64 columns of the accumulator: TMEM -> v.
         auto load_acc = [&](float* v, uint32_t taddr) {
@@ -931,8 +965,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ptx::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
+                // (Nothing in memory is handed over: a release at cluster scope would wait for the warp's loads and stores.)
                 if constexpr (PAIR)
-                    ptx::mbar_arrive_cluster(ptx::mapa_shared(acce_bar(acc), 0u));
+                    ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(acce_bar(acc), 0u));
                 else
                     ptx::mbar_arrive(acce_bar(acc));
             }
@@ -1006,15 +1041,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 bool ok = true;
 #pragma unroll
                 for (int i = 0; i < CW; ++i) s[i] = 0.0f;
-                [[maybe_unused]] float next_g = 1.0f, next_u = 1.0f;  // SCALED: loaded a K block ahead
+                // SCALED: the scales of a K block, loaded two blocks ahead.
+                [[maybe_unused]] Scales next, after;
                 auto block_at = [&](int i) { return cur.rev ? kb1 - 1 - (i - kb0) : i; };
                 if constexpr (SCALED) {
-                    if (kb0 < kb1) load_scales(block_at(kb0), next_g, next_u);
+                    point_at_scales();
+                    if (kb0 < kb1) next = load_scales(block_at(kb0));
+                    if (kb0 + 1 < kb1) after = load_scales(block_at(kb0 + 1));
                 }
                 for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
-                    [[maybe_unused]] const f32x2 fg = both(next_g), fu = both(next_u);
+                    [[maybe_unused]] float fg, fu;
                     if constexpr (SCALED) {
-                        if (kb + 1 < kb1) load_scales(block_at(kb + 1), next_g, next_u);
+                        fg = next.x * next.w;
+                        fu = next.x * next.w_up;
+                        next = after;
+                        if (kb + 2 < kb1) after = load_scales(block_at(kb + 2));
                     }
                     ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1026,17 +1067,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             uint32_t v[32];
                             ptx::tmem_ld_32x32b_x32(tacc + acc_col(q), v);
                             ptx::tmem_wait_ld();
+                            if (q == CW / 32 - 1) release_acc();
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                const f32x2 sum = pair(s[q * 32 + i], s[q * 32 + i + 1]);
-                                const f32x2 add = pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                                if constexpr (SCALED)
-                                    split(fma2(GLU && q * 32 >= CW / 2 ? fu : fg, add, sum), s[q * 32 + i], s[q * 32 + i + 1]);
-                                else
-                                    split(add2(sum, add), s[q * 32 + i], s[q * 32 + i + 1]);
+                                if constexpr (SCALED) {
+                                    const float f = GLU && q * 32 >= CW / 2 ? fu : fg;
+                                    s[q * 32 + i] = fmaf(f, __uint_as_float(v[i]), s[q * 32 + i]);
+                                    s[q * 32 + i + 1] = fmaf(f, __uint_as_float(v[i + 1]), s[q * 32 + i + 1]);
+                                } else {
+                                    split(add2(pair(s[q * 32 + i], s[q * 32 + i + 1]),
+                                               pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))),
+                                          s[q * 32 + i], s[q * 32 + i + 1]);
+                                }
                             }
                         }
-                        release_acc();
                     }
                     acc ^= 1;
                     if (acc == 0) acc_phase ^= 1u;

@@ -35,8 +35,7 @@ template <int OUT>
 KernelChoice scaled_choice(int config)
 {
     if (config == 3) return tile_choice<256, 6, 2, OUT, kForward, true, 2, true>(3);
-    if (config == 1) return tile_choice<256, 4, 2, OUT, kForward, true, 1, true>(1);
-    return tile_choice<128, 6, 2, OUT, kForward, true, 1, true>(2);
+    return tile_choice<256, 4, 2, OUT, kForward, true, 1, true>(1);
 }
 
 // Gated forward: a pair or (any other config) one CTA with 256 accumulator columns, 128 of each half.
