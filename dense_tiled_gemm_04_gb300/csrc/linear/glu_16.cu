@@ -5,8 +5,8 @@ namespace dtg {
 namespace linear {
 KernelChoice glu_16(int config, bool bf16, bool sums)
 {
-    if (bf16) return sums ? glu_choice<1, kOutBf16, true, false>(config) : glu_choice<1, kOutBf16, false, false>(config);
-    return sums ? glu_choice<0, kOutF16, true, false>(config) : glu_choice<0, kOutF16, false, false>(config);
+    if (bf16) return sums ? glu_choice<1, kOutBf16, true>(config) : glu_choice<1, kOutBf16, false>(config);
+    return sums ? glu_choice<0, kOutF16, true>(config) : glu_choice<0, kOutF16, false>(config);
 }
 }  // namespace linear
 }  // namespace dtg

@@ -5,7 +5,7 @@ namespace dtg {
 namespace linear {
 KernelChoice glu_scaled(int config, bool out_bf16)
 {
-    return out_bf16 ? glu_choice<2, kOutBf16, true, true>(config) : glu_choice<2, kOutF16, true, true>(config);
+    return out_bf16 ? scaled_choice<kOutBf16, kGlu>(config) : scaled_choice<kOutF16, kGlu>(config);
 }
 }  // namespace linear
 }  // namespace dtg

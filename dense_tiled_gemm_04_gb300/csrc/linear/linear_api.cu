@@ -325,15 +325,17 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     if (planned != GEMM_OK) return planned;
     if (few.tokens) return launch_cluster(h, q, few, sum_rows, stream);
     if (sum_rows) *sum_rows = cdiv(q.rows, kSumRows);
-    // Columns of accumulators: a gated tile has 128 of each half, however few of them the output has.
-    const int64_t cols = q.mode == dtg::linear::kGlu ? 256 * cdiv(q.cols, 128) : q.cols;
+    // Columns of accumulators: a gated tile has 128 (scaled: 64) of each half, however few of them the output has.
+    const int64_t half = q.scaled ? 64 : 128;
+    const int64_t cols = q.mode == dtg::linear::kGlu ? 2 * half * cdiv(q.cols, half) : q.cols;
     int config = pick_config(o, h->dev, q.rows, cols, q.depth);
     if (config == GEMM_CONFIG_128x64) config = GEMM_CONFIG_128x128;
-    if ((gated(q) || q.scaled) && config == GEMM_CONFIG_128x128) config = GEMM_CONFIG_128x256;  // (their only one-CTA tile)
     // CTA pairs from 2/5 of a tile per SM on, where gemm_run asks for 1/2: on 64 pair tiles 512 x 8192 x 8192 takes 46.8
     // us against 57.7 in 128 x 256 tiles, 1024 x 4096 x 4096 27.0 and 30.7; on 32 256 x 8192 x 8192 46.2 and 40.8.
     if (o.config == GEMM_CONFIG_AUTO && cdiv(q.rows, 256) * cdiv(cols, 256) * 5 >= 2 * h->dev.num_sms)
         config = GEMM_CONFIG_256x256;
+    // The only one-CTA tiles of scaled (128 x 128) and of gated (128 x 256) kernels.
+    if (config != GEMM_CONFIG_256x256 && (q.scaled || gated(q))) config = q.scaled ? GEMM_CONFIG_128x128 : GEMM_CONFIG_128x256;
     const KernelChoice kc = tile_kernel(q, config);
     const int slot = tile_slot(q, kc.config);
     if (!h->dev.attrs_set[slot]) {
@@ -374,8 +376,9 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     dtg::linear::TileMaps<dtg::linear::kGlu> maps;  // (the others' begin alike; gated dgrad's has the same six)
     CUtensorMap &tA = maps.A, &tB = maps.B, &tC = maps.C, &tZ = maps.Z, &t5 = maps.B_up, &t6 = maps.Z_up;
     const auto out_map = [&](const void* at, int64_t ld, CUtensorMap* map) {
-        // Boxes of the output and of what is read or kept beside it; gated dgrad's are half as wide.
-        const bool half = q.mode == dtg::linear::kGluDgrad;
+        // Boxes of the output and of what is read or kept beside it; those of gated dgrad and scaled gated forward are
+        // half as wide.
+        const bool half = q.mode == dtg::linear::kGluDgrad || (q.mode == dtg::linear::kGlu && q.scaled);
         return get_tmap(nullptr, at, q.cols, q.rows, ld * oe, static_cast<uint32_t>((half ? 64 : 128) / oe), 32, q.out, map,
                         half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     };
@@ -390,7 +393,7 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
         return GEMM_ERR_CUDA;
     if (q.depth > 0) {
         const bool at = q.mode == dtg::linear::kWgrad, bt = q.mode != dtg::linear::kForward && q.mode != dtg::linear::kGlu;
-        const uint32_t b_box = q.mode == dtg::linear::kGlu ? 128u : static_cast<uint32_t>(kc.b_box);
+        const uint32_t b_box = q.mode == dtg::linear::kGlu ? static_cast<uint32_t>(half) : static_cast<uint32_t>(kc.b_box);
         if (!(at ? get_tmap(nullptr, q.A, q.rows, q.depth, q.lda * eb, nb, sk, q.in, &tA)
                  : get_tmap(nullptr, q.A, q.depth, q.rows, q.lda * eb, sk, dtg::kBM, q.in, &tA)) ||
             !(bt ? get_tmap(nullptr, q.B, q.cols, q.depth, q.ldb * eb, nb, sk, q.in, &tB)

@@ -109,8 +109,8 @@ struct TileSmem {
     static constexpr int kStgOff = STAGES * kStageBytes;
     static constexpr int kStgBufs = STG_BUFS;
     static constexpr int kBarOff = kStgOff + kTileEpiWarps * STG_BUFS * kTileStgBytes;
-    // full, empty, acc_full[2], acc_empty[2], drain[2], pre-activation boxes per staging buffer
-    static constexpr int kNumBars = 2 * STAGES + 6 + kTileEpiWarps * (STG_BUFS < 2 ? 2 : STG_BUFS);
+    // full, empty, acc_full[4], acc_empty[4], drain[2], pre-activation boxes per staging buffer
+    static constexpr int kNumBars = 2 * STAGES + 10 + kTileEpiWarps * (STG_BUFS < 2 ? 2 : STG_BUFS);
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kTotal = kMiscOff + 16;  // tmem slot, abort flag, stream-K "last" flag
     static constexpr int kAlloc = kTotal + 1024;  // slack for aligning the base to 1 KB
@@ -295,6 +295,28 @@ __device__ __forceinline__ void store_rows(const uint32_t (&h)[32], int32_t x, i
     store_box_now(tm, stg, x, y, lane);
 }
 
+// The same for a box of 32 16-bit columns (64-byte swizzle).
+__device__ __forceinline__ void store_half_rows(const uint32_t (&h)[16], int32_t x, int32_t y, int lane, uint32_t stg,
+                                                const CUtensorMap* tm, void* base, int64_t ld, int32_t M, int32_t N)
+{
+    if (N % 8 != 0 && x + 32 > N) {
+        const int64_t row = static_cast<int64_t>(y) + lane;
+        if (row < M) {
+            uint16_t* const dst = static_cast<uint16_t*>(base) + row * ld + x;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (x + e < N) dst[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
+        }
+        return;
+    }
+    if (lane == 0) ptx::bulk_wait_group_read<0>();  // the last store has read the buffer
+    __syncwarp();
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        ptx::st_shared_v4(half_box_chunk(stg, lane, ch), h[4 * ch], h[4 * ch + 1], h[4 * ch + 2], h[4 * ch + 3]);
+    store_box_now(tm, stg, x, y, lane);
+}
+
 // Sums over the warp's 32 rows of 64 columns held one row per lane: lane l ends with columns 2l, 2l + 1
 // in v[0], v[1].  Each step exchanges half of the columns still held with the lane `off` away.
 __device__ __forceinline__ void sum_rows(float* v, int lane)
@@ -352,8 +374,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     static_assert(IN <= 3 && (BN == 128 || BN == 256), "dense operands, 64 or 128 columns per epilogue warp");
     static_assert(MODE == kForward || MODE == kGlu || !T::kF8, "8-bit operands: forward only");
     static_assert(OUT != kOutF32 || (MODE == kWgrad && SUMS), "fp32 output: weight gradients only");
-    static_assert(!SCALED || (IN == 2 && SUMS), "scales meet the products in the registers' sums");
-    static_assert((MODE != kGlu && MODE != kGluDgrad) || BN == 256, "gated: a box of 64 columns of both halves per warp");
+    static_assert(!SCALED || (IN == 2 && SUMS && BN == 128), "scales meet the products in the registers' sums");
+    static_assert(MODE != kGluDgrad || BN == 256, "two pairs of boxes per warp");
     static_assert(MODE != kDgrad || STG_BUFS == 2, "dgrad alternates between two buffers");
     const CUtensorMap &tmA = maps.A, &tmB = maps.B, &tmC = maps.C, &tmZ = maps.Z;
     constexpr bool GLU = MODE == kGlu;
@@ -366,7 +388,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int CW = BN / 2;                 // accumulator columns per epilogue warp
     constexpr int kTileN = GLU ? BN / 2 : BN;  // output columns of a tile
     constexpr int kWarpN = kTileN / 2;         // ... and of an epilogue warp
-    constexpr uint32_t kTmemCols = 2 * BN;
+    // Accumulators.  SCALED: a chunk is one K block, and from the last of its MMAs to the first of those that take its accumulator
+    // again there are some 1200 cycles of commits, arrivals and wake-ups beside the draining; with two accumulators of 256 columns
+    // that halved the speed (8192^3: 501 us), four of 128 cover it.
+    constexpr int kAccs = SCALED ? 4 : 2;
+    constexpr uint32_t kTmemCols = kAccs * BN;
     using L = TileSmem<kBRows, STAGES, STG_BUFS>;
 
     extern __shared__ uint8_t smem_raw[];
@@ -377,9 +403,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
-    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-    auto drain_bar = [&](int w) { return bar0 + 8u * (2 * STAGES + 4 + w); };
-    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 6 + STG_BUFS * w + b); };  // dgrad: box loaded
+    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 4 + b); };
+    auto drain_bar = [&](int w) { return bar0 + 8u * (2 * STAGES + 8 + w); };
+    auto in_bar = [&](int w, int b) { return bar0 + 8u * (2 * STAGES + 10 + STG_BUFS * w + b); };  // dgrad: box loaded
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int32_t* const abort_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 4);
     volatile int32_t* const last_flag = reinterpret_cast<volatile int32_t*>(smem + L::kMiscOff + 8);
@@ -396,7 +422,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ptx::mbar_init(full_bar(s), 1);
             ptx::mbar_init(empty_bar(s), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kAccs; ++b) {
             ptx::mbar_init(accf_bar(b), 1);
             ptx::mbar_init(acce_bar(b), kTileEpiWarps * kRanks);
         }
@@ -525,28 +551,51 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             WorkIter it(p, unit, units);
             int64_t tile;
             int kb0, kb1;
-            // SCALED: every K block is a chunk, whose waits, MMAs and commits take one thread longer (630 cycles) than the MMAs
-            // themselves (512).  Two warps take turns, each with an accumulator of its own.
             const int mma_warp = SCALED ? warp - kMmaWarp : 0;
-            [[maybe_unused]] int turn = 0;
+            [[maybe_unused]] uint32_t chunk = 0;
             while (!aborted && it.next(p, tile, kb0, kb1)) {
+                if constexpr (SCALED) {
+                    // Every K block is a chunk.  One thread's waits, MMAs and commits for it take longer (630 cycles) than its MMAs
+                    // themselves, so two warps take turns.
+                    for (int i = kb0; i < kb1; ++i, ++chunk) {
+                        if ((chunk & 1u) == static_cast<uint32_t>(mma_warp)) {
+                            const int a = chunk & 3u;
+                            const uint32_t sa = base + stage * L::kStageBytes;
+                            const uint32_t sb = sa + L::kABytes;
+                            if (!wd.wait(full_bar(stage), phase, kRoleMma, tile, i) ||
+                                !wd.wait(acce_bar(a), ((chunk >> 2) & 1u) ^ 1u, kRoleMma, tile, i)) {
+                                aborted = true;
+                                break;
+                            }
+                            ptx::tc_fence_after_sync();
+                            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * BN);
+#pragma unroll
+                            for (int k = 0; k < T::kStageK / T::kMmaK; ++k) {
+                                const uint64_t adesc = smem_desc_sw128(sa + k * 32, 16, 1024), bdesc = smem_desc_sw128(sb + k * 32, 16, 1024);
+                                if constexpr (PAIR)
+                                    ptx::mma_f8_pair(d_tmem, adesc, bdesc, idesc, k != 0);
+                                else
+                                    ptx::mma_f8_cta1(d_tmem, adesc, bdesc, idesc, k != 0);
+                            }
+                            if constexpr (PAIR) {
+                                ptx::mma_commit_pair(accf_bar(a), 0x3);
+                                ptx::mma_commit_pair(empty_bar(stage), 0x3);
+                            } else {
+                                ptx::mma_commit_cta1(accf_bar(a));
+                                ptx::mma_commit_cta1(empty_bar(stage));
+                            }
+                        }
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    continue;
+                }
                 // A loop over chunks around one over K blocks: with the chunk's wait and commit as conditions inside a
                 // single loop, each K block's issue took about 60 cycles longer (8192^3 bf16: 623 against 563 us).
                 const int n = kb1 - kb0;
                 for (int c0 = 0; c0 < n && !aborted;) {
-                    if constexpr (SCALED) {
-                        const bool mine = turn == mma_warp;
-                        turn ^= 1;
-                        if (!mine) {
-                            ++c0;
-                            if (++stage == STAGES) {
-                                stage = 0;
-                                phase ^= 1u;
-                            }
-                            continue;
-                        }
-                        acc = mma_warp;
-                    }
                     if (!wd.wait(acce_bar(acc), acc_phase ^ 1u, kRoleMma, tile, -1)) {
                         aborted = true;
                         break;
@@ -600,7 +649,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         ptx::mma_commit_cta1(accf_bar(acc));
                     c0 = c1;
                     acc ^= 1;
-                    if (SCALED || acc == 0) acc_phase ^= 1u;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
             }
             if (aborted) {
@@ -664,15 +713,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         Item cur = {}, nxt = {};
         bool more_items = false;  // nxt is an item
 
-        // w = alpha v + bias over 64 columns from column x of C on.
-        auto with_bias = [&](f32x2 (&w)[32], const float* v, const void* bias, int32_t x) {
+        // w = alpha v + bias over the PAIRS * 2 (64 or 32) columns from column x of C on.
+        auto with_bias = [&](auto& w, const float* v, const void* bias, int32_t x) {
+            constexpr int PAIRS = sizeof(w) / sizeof(f32x2);
             const f32x2 alpha = both(p.alpha);
             if (bias) {
-                // The box's 64 biases go through the staging buffer, from which all lanes read them.
+                // The box's biases go through the staging buffer, from which all lanes read them.
                 if (lane == 0) ptx::bulk_wait_group_read<0>();
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < PAIRS / 16; ++e) {
                     const int32_t c = x + lane + 32 * e;
                     float f = 0.0f;
                     if (c < p.N)
@@ -681,7 +731,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < PAIRS / 2; ++i) {
                     const float4 f = ld_shared_f4(stg + 16 * i);
                     w[2 * i] = fma2(alpha, pair(v[4 * i], v[4 * i + 1]), pair(f.x, f.y));
                     w[2 * i + 1] = fma2(alpha, pair(v[4 * i + 2], v[4 * i + 3]), pair(f.z, f.w));
@@ -689,29 +739,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
             } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
+                for (int i = 0; i < PAIRS; ++i) w[i] = mul2(alpha, pair(v[2 * i], v[2 * i + 1]));
             }
         };
 
-        // Gated forward on 64 columns of this thread's row: vg, vu hold the products' sums.
+        // Gated forward on a box of this thread's row, 64 columns (SCALED: 32): vg, vu hold the products' sums.
         auto finish_glu = [&](const float* vg, const float* vu, int32_t x, int32_t y) {
-            f32x2 g[32], u[32];
-            uint32_t h[32];
+            constexpr int PAIRS = SCALED ? 16 : 32;
+            f32x2 g[PAIRS], u[PAIRS];
+            uint32_t h[PAIRS];
             with_bias(g, vg, p.bias, x);
             with_bias(u, vu, p.bias_up, x);
             if constexpr (GLU) {
+                auto store = [&](const CUtensorMap* tm, void* base, int64_t ld) {
+                    if constexpr (SCALED)
+                        store_half_rows(h, x, y, lane, stg, tm, base, ld, p.M, p.N);
+                    else
+                        store_rows<2>(h, x, y, lane, stg, tm, base, ld, p.M, p.N);
+                };
                 if (p.Z) {  // (N is a multiple of 8 then: no masked stores)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(g[i]);
-                    store_rows<2>(h, x, y, lane, stg, &tmZ, p.Z, p.ldz, p.M, p.N);
+                    for (int i = 0; i < PAIRS; ++i) h[i] = round2<kBf16>(g[i]);
+                    store(&tmZ, p.Z, p.ldz);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(u[i]);
-                    store_rows<2>(h, x, y, lane, stg, &maps.Z_up, p.Z, p.ldz, p.M, p.N);
+                    for (int i = 0; i < PAIRS; ++i) h[i] = round2<kBf16>(u[i]);
+                    store(&maps.Z_up, p.Z, p.ldz);
                 }
                 DTG_ACT_SWITCH(p.act, {
-                    _Pragma("unroll") for (int i = 0; i < 32; ++i) h[i] = round2<kBf16>(mul2(act_value2<ACT>(g[i]), u[i]));
+                    _Pragma("unroll") for (int i = 0; i < PAIRS; ++i) h[i] = round2<kBf16>(mul2(act_value2<ACT>(g[i]), u[i]));
                 });
-                store_rows<2>(h, x, y, lane, stg, &tmC, p.C, p.ldc, p.M, p.N);
+                store(&tmC, p.C, p.ldc);
             }
         };
 
@@ -923,29 +980,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if constexpr (GLU) return static_cast<uint32_t>((q * 32 / kWarpN) * kTileN + half * kWarpN + q * 32 % kWarpN);
             return static_cast<uint32_t>(half * CW + q * 32);
         };
-        // SCALED: the scales of K block kb for this thread's row and the warp's columns, which lie inside one block of 128 of the
-        // weights' rows (gated: of Wg's and of Wu's).
-        struct Scales {
-            float x = 1.0f, w = 1.0f, w_up = 1.0f;
-        };
-        // Absent scales, and those of rows and columns past the edges, are a 1 that is read at every K block.
-        const float *xs_at = &kUnitScale, *ws_at = &kUnitScale, *wu_at = &kUnitScale;
-        int xs_step = 0, ws_step = 0;
-        auto point_at_scales = [&]() {
+        // SCALED: adds the item's K blocks, each times its scales, to s.  A chunk is one block, 256 cycles of MMAs, so everything
+        // around the loads and sums counts: the barrier of the next block is asked for, and its factors are made, among the sums
+        // of this one; scales are loaded two blocks ahead; the arrival is predicated, not branched to.
+        // Absent scales, and those of rows and columns past the edges, are a 1 that is read at every block.
+        auto add_scaled = [&](float* s, int kb0, int kb1) -> bool {
             const int64_t row = static_cast<int64_t>(cur.y) + lane;
-            const bool x = p.x_scales && row < p.M, w = p.w_scales && cur.x < p.N;
-            xs_at = x ? p.x_scales + row * p.ld_xs : &kUnitScale;
-            ws_at = w ? p.w_scales + (cur.x >> 7) * p.ld_ws : &kUnitScale;
-            if constexpr (GLU) wu_at = w ? ws_at + p.up_scales : &kUnitScale;
-            xs_step = x;
-            ws_step = w;
-        };
-        auto load_scales = [&](int kb) {
-            Scales f;
-            f.x = __ldg(xs_at + kb * xs_step);
-            f.w = __ldg(ws_at + kb * ws_step);
-            if constexpr (GLU) f.w_up = __ldg(wu_at + kb * ws_step);
-            return f;
+            const bool has_x = p.x_scales && row < p.M, has_w = p.w_scales && cur.x < p.N;
+            const int first = cur.rev ? kb1 - 1 : kb0, x_step = has_x ? (cur.rev ? -1 : 1) : 0, w_step = has_w ? (cur.rev ? -1 : 1) : 0;
+            // (The warp's columns lie inside one block of 128 of the weights' rows; gated: of Wg's and of Wu's.)
+            const float* x_at = has_x ? p.x_scales + row * p.ld_xs + first : &kUnitScale;
+            const float* w_at = has_w ? p.w_scales + (cur.x >> 7) * p.ld_ws + first : &kUnitScale;
+            const float* u_at = GLU && has_w ? w_at + p.up_scales : &kUnitScale;
+            float x1 = __ldg(x_at), w1 = __ldg(w_at), u1 = GLU ? __ldg(u_at) : 1.0f;  // of the next block
+            float fg = x1 * w1, fu = x1 * u1;
+            auto advance = [&](bool more) {
+                if (more) {
+                    x_at += x_step;
+                    w_at += w_step;
+                    if constexpr (GLU) u_at += w_step;
+                }
+            };
+            advance(kb0 + 1 < kb1);
+            x1 = __ldg(x_at);
+            w1 = __ldg(w_at);
+            if constexpr (GLU) u1 = __ldg(u_at);
+            const uint32_t tacc = tmem_base + lane_off;
+            // A wait that ran out does not leave the loop (the launch is being abandoned, and what is added counts nowhere): with
+            // a second way out the sums were moved to other registers and back in every turn.
+            bool ready = false, ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!__all_sync(0xFFFFFFFFu, ready) && ok) ok = wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, cur.tile, kb);
+                __syncwarp();
+                ptx::tc_fence_after_sync();
+                const int next_acc = (acc + 1) & (kAccs - 1);
+                const uint32_t next_phase = next_acc == 0 ? acc_phase ^ 1u : acc_phase;
+                float next_fg = 1.0f, next_fu = 1.0f;
+#pragma unroll
+                for (int q = 0; q < CW / 32; ++q) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(tacc + static_cast<uint32_t>(acc * BN) + acc_col(q), v);
+                    ptx::tmem_wait_ld();
+                    if (q == 0) {
+                        next_fg = x1 * w1;
+                        if constexpr (GLU) next_fu = x1 * u1;
+                        advance(kb + 2 < kb1);
+                        x1 = __ldg(x_at);
+                        w1 = __ldg(w_at);
+                        if constexpr (GLU) u1 = __ldg(u_at);
+                    }
+                    if (q == CW / 32 - 1) {
+                        ptx::tc_fence_before_sync();
+                        ptx::mbar_arrive_relaxed_if(PAIR ? ptx::mapa_shared(acce_bar(acc), 0u) : acce_bar(acc), lane == 0);
+                        ready = ptx::mbar_test_wait(accf_bar(next_acc), next_phase);
+                    }
+                    const float f = GLU && q * 32 >= CW / 2 ? fu : fg;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[q * 32 + i] = fmaf(f, __uint_as_float(v[i]), s[q * 32 + i]);
+                }
+                fg = next_fg;
+                fu = next_fu;
+                acc = next_acc;
+                acc_phase = next_phase;
+            }
+            return __all_sync(0xFFFFFFFFu, ok);
         };
         // 64 columns of the accumulator: TMEM -> v.
         auto load_acc = [&](float* v, uint32_t taddr) {
@@ -1041,49 +1139,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 bool ok = true;
 #pragma unroll
                 for (int i = 0; i < CW; ++i) s[i] = 0.0f;
-                // SCALED: the scales of a K block, loaded two blocks ahead.
-                [[maybe_unused]] Scales next, after;
-                auto block_at = [&](int i) { return cur.rev ? kb1 - 1 - (i - kb0) : i; };
                 if constexpr (SCALED) {
-                    point_at_scales();
-                    if (kb0 < kb1) next = load_scales(block_at(kb0));
-                    if (kb0 + 1 < kb1) after = load_scales(block_at(kb0 + 1));
-                }
-                for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
-                    [[maybe_unused]] float fg, fu;
-                    if constexpr (SCALED) {
-                        fg = next.x * next.w;
-                        fu = next.x * next.w_up;
-                        next = after;
-                        if (kb + 2 < kb1) after = load_scales(block_at(kb + 2));
-                    }
-                    ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (ok) {
-                        ptx::tc_fence_after_sync();
-                        const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN);
+                    if (kb0 < kb1) ok = add_scaled(s, kb0, kb1);
+                } else {
+                    for (int kb = kb0; kb < kb1; kb += p.chunk_kb) {
+                        ok = ok && wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (ok) {
+                            ptx::tc_fence_after_sync();
+                            const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN);
 #pragma unroll
-                        for (int q = 0; q < CW / 32; ++q) {
-                            uint32_t v[32];
-                            ptx::tmem_ld_32x32b_x32(tacc + acc_col(q), v);
-                            ptx::tmem_wait_ld();
-                            if (q == CW / 32 - 1) release_acc();
+                            for (int q = 0; q < CW / 32; ++q) {
+                                uint32_t v[32];
+                                ptx::tmem_ld_32x32b_x32(tacc + acc_col(q), v);
+                                ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                if constexpr (SCALED) {
-                                    const float f = GLU && q * 32 >= CW / 2 ? fu : fg;
-                                    s[q * 32 + i] = fmaf(f, __uint_as_float(v[i]), s[q * 32 + i]);
-                                    s[q * 32 + i + 1] = fmaf(f, __uint_as_float(v[i + 1]), s[q * 32 + i + 1]);
-                                } else {
+                                for (int i = 0; i < 32; i += 2)
                                     split(add2(pair(s[q * 32 + i], s[q * 32 + i + 1]),
                                                pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))),
                                           s[q * 32 + i], s[q * 32 + i + 1]);
-                                }
                             }
+                            release_acc();
                         }
+                        acc ^= 1;
+                        if (acc == 0) acc_phase ^= 1u;
                     }
-                    acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
                 }
                 if (!tile_epi_and(ok)) return false;
                 if (!whole && other_is_in(tr, parts)) {

@@ -30,20 +30,21 @@ KernelChoice tile_choice_for(int config)
     return tile_choice<128, 6 - kLess, IN, OUT, MODE, SUMS, 1>(2);
 }
 
-// 8-bit operands with block scales.
-template <int OUT>
+// 8-bit operands with block scales: tiles of 128 accumulator columns (gated: 64 of each half), a pair or (any other config)
+// one CTA.
+template <int OUT, int MODE>
 KernelChoice scaled_choice(int config)
 {
-    if (config == 3) return tile_choice<256, 6, 2, OUT, kForward, true, 2, true>(3);
-    return tile_choice<256, 4, 2, OUT, kForward, true, 1, true>(1);
+    if (config == 3) return tile_choice<128, 8, 2, OUT, MODE, true, 2, true>(3);
+    return tile_choice<128, 6, 2, OUT, MODE, true, 1, true>(2);
 }
 
-// Gated forward: a pair or (any other config) one CTA with 256 accumulator columns, 128 of each half.
-template <int IN, int OUT, bool SUMS, bool SCALED>
+// Gated forward, 16-bit operands: a pair or one CTA with 256 accumulator columns, 128 of each half.
+template <int IN, int OUT, bool SUMS>
 KernelChoice glu_choice(int config)
 {
-    if (config == 3) return tile_choice<256, 6, IN, OUT, kGlu, SUMS, 2, SCALED>(3);
-    return tile_choice<256, 4, IN, OUT, kGlu, SUMS, 1, SCALED>(1);
+    if (config == 3) return tile_choice<256, 6, IN, OUT, kGlu, SUMS, 2>(3);
+    return tile_choice<256, 4, IN, OUT, kGlu, SUMS, 1>(1);
 }
 
 // Gated dgrad: three staging buffers per warp in a pair, two beside one CTA's wider stages.

@@ -58,6 +58,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // As mbar_try_wait, but a thread whose phase is not yet complete may stay suspended for
 // up to `hint_ns` nanoseconds (it resumes as soon as the phase completes), instead of
 // spinning and taking issue slots from the warps it shares a scheduler with.
@@ -316,6 +330,17 @@ __device__ __forceinline__ void cluster_sync()
 }
 
 // Arrive once on an mbarrier that may live in another CTA of the cluster.
+// The same, predicated; also on a barrier of this CTA (a shared::cta address is one of shared::cluster).
+__device__ __forceinline__ void mbar_arrive_relaxed_if(uint32_t cluster_addr, bool yes)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(cluster_addr),
+        "r"(yes ? 1u : 0u)
+        : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
