@@ -207,7 +207,9 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
     if (tokens == 128) {
         const bool few = 4 * tiles <= dev.num_sms;
         if (!few && (tiles > dev.num_sms || kb <= 16)) return GEMM_OK;
-        // (Gated and scaled kernels have 64 tokens at most.)
+        // Gated and scaled kernels have 64 tokens at most; scaled ones take their tiles where those are not few (128 x 8192 x 8192
+        // 20.1 us, 30.8 on clusters; 256 x 4096 x 4096 15.9 and 19.7; but 128 x 4096 x 4096 15.7 and 14.1).
+        if (!few && q.scaled) return GEMM_OK;
         if ((few && q.mode != dtg::linear::kWgrad) || gated(q) || q.scaled) {
             tokens = 64;
             tiles = cdiv(q.cols, features) * cdiv(q.rows, tokens);
@@ -325,9 +327,9 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     if (planned != GEMM_OK) return planned;
     if (few.tokens) return launch_cluster(h, q, few, sum_rows, stream);
     if (sum_rows) *sum_rows = cdiv(q.rows, kSumRows);
-    // Columns of accumulators: a gated tile has 128 (scaled: 64) of each half, however few of them the output has.
-    const int64_t half = q.scaled ? 64 : 128;
-    const int64_t cols = q.mode == dtg::linear::kGlu ? 2 * half * cdiv(q.cols, half) : q.cols;
+    // Columns of accumulators: a gated tile has 128 of each half (scaled in one CTA: 64), however few of them the output has.
+    const auto columns = [&](int64_t half) { return q.mode == dtg::linear::kGlu ? 2 * half * cdiv(q.cols, half) : q.cols; };
+    int64_t cols = columns(128);
     int config = pick_config(o, h->dev, q.rows, cols, q.depth);
     if (config == GEMM_CONFIG_128x64) config = GEMM_CONFIG_128x128;
     // CTA pairs from 2/5 of a tile per SM on, where gemm_run asks for 1/2: on 64 pair tiles 512 x 8192 x 8192 takes 46.8
@@ -336,6 +338,8 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
         config = GEMM_CONFIG_256x256;
     // The only one-CTA tiles of scaled (128 x 128) and of gated (128 x 256) kernels.
     if (config != GEMM_CONFIG_256x256 && (q.scaled || gated(q))) config = q.scaled ? GEMM_CONFIG_128x128 : GEMM_CONFIG_128x256;
+    const int64_t half = q.scaled && config != GEMM_CONFIG_256x256 ? 64 : 128;
+    cols = columns(half);
     const KernelChoice kc = tile_kernel(q, config);
     const int slot = tile_slot(q, kc.config);
     if (!h->dev.attrs_set[slot]) {
@@ -376,11 +380,11 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     dtg::linear::TileMaps<dtg::linear::kGlu> maps;  // (the others' begin alike; gated dgrad's has the same six)
     CUtensorMap &tA = maps.A, &tB = maps.B, &tC = maps.C, &tZ = maps.Z, &t5 = maps.B_up, &t6 = maps.Z_up;
     const auto out_map = [&](const void* at, int64_t ld, CUtensorMap* map) {
-        // Boxes of the output and of what is read or kept beside it; those of gated dgrad and scaled gated forward are
-        // half as wide.
-        const bool half = q.mode == dtg::linear::kGluDgrad || (q.mode == dtg::linear::kGlu && q.scaled);
-        return get_tmap(nullptr, at, q.cols, q.rows, ld * oe, static_cast<uint32_t>((half ? 64 : 128) / oe), 32, q.out, map,
-                        half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+        // Boxes of the output and of what is read or kept beside it; those of gated dgrad and of a gated tile of
+        // 64 columns are half as wide.
+        const bool narrow = q.mode == dtg::linear::kGluDgrad || (q.mode == dtg::linear::kGlu && half == 64);
+        return get_tmap(nullptr, at, q.cols, q.rows, ld * oe, static_cast<uint32_t>((narrow ? 64 : 128) / oe), 32, q.out, map,
+                        narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     };
     const auto up = [&](const void* at) { return static_cast<const uint16_t*>(at) + q.cols; };  // the other half of g, u
     if (!out_map(q.C, q.ldc, &tC)) return GEMM_ERR_CUDA;

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     static_assert(IN <= 3 && (BN == 128 || BN == 256), "dense operands, 64 or 128 columns per epilogue warp");
     static_assert(MODE == kForward || MODE == kGlu || !T::kF8, "8-bit operands: forward only");
     static_assert(OUT != kOutF32 || (MODE == kWgrad && SUMS), "fp32 output: weight gradients only");
-    static_assert(!SCALED || (IN == 2 && SUMS && BN == 128), "scales meet the products in the registers' sums");
+    static_assert(!SCALED || (IN == 2 && SUMS), "scales meet the products in the registers' sums");
     static_assert(MODE != kGluDgrad || BN == 256, "two pairs of boxes per warp");
     static_assert(MODE != kDgrad || STG_BUFS == 2, "dgrad alternates between two buffers");
     const CUtensorMap &tmA = maps.A, &tmB = maps.B, &tmC = maps.C, &tmZ = maps.Z;
@@ -389,9 +389,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kTileN = GLU ? BN / 2 : BN;  // output columns of a tile
     constexpr int kWarpN = kTileN / 2;         // ... and of an epilogue warp
     // Accumulators.  SCALED: a chunk is one K block, and from the last of its MMAs to the first of those that take its accumulator
-    // again there are some 1200 cycles of commits, arrivals and wake-ups beside the draining; with two accumulators of 256 columns
-    // that halved the speed (8192^3: 501 us), four of 128 cover it.
-    constexpr int kAccs = SCALED ? 4 : 2;
+    // again there are some 1200 cycles of commits, arrivals and wake-ups beside the draining.  A pair's two accumulators of 256
+    // columns do not cover that (8192^3 457 us, 293 unscaled), but four of 128 cost more in what every chunk costs (583 us); one
+    // CTA takes four, which leaves a few tiles' long contractions the shorter chain (256 x 8192 x 8192 25.9 us, 31.0 with two).
+    constexpr int kAccs = SCALED ? 512 / BN : 2;
     constexpr uint32_t kTmemCols = kAccs * BN;
     using L = TileSmem<kBRows, STAGES, STG_BUFS>;
 
@@ -555,15 +556,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             [[maybe_unused]] uint32_t chunk = 0;
             while (!aborted && it.next(p, tile, kb0, kb1)) {
                 if constexpr (SCALED) {
-                    // Every K block is a chunk.  One thread's waits, MMAs and commits for it take longer (630 cycles) than its MMAs
-                    // themselves, so two warps take turns.
+                    // Every K block is a chunk, which takes one thread 630 cycles (waits, MMAs, commits), more than its MMAs run (512
+                    // for 256 columns): two warps take turns.  What the accumulator's barrier holds up comes last before the MMAs,
+                    // and their commit to it first after them (8192^3 497 us in the other order, 457 in this).
                     for (int i = kb0; i < kb1; ++i, ++chunk) {
                         if ((chunk & 1u) == static_cast<uint32_t>(mma_warp)) {
-                            const int a = chunk & 3u;
+                            const int a = chunk % kAccs;
                             const uint32_t sa = base + stage * L::kStageBytes;
                             const uint32_t sb = sa + L::kABytes;
                             if (!wd.wait(full_bar(stage), phase, kRoleMma, tile, i) ||
-                                !wd.wait(acce_bar(a), ((chunk >> 2) & 1u) ^ 1u, kRoleMma, tile, i)) {
+                                !wd.wait(acce_bar(a), ((chunk / kAccs) & 1u) ^ 1u, kRoleMma, tile, i)) {
                                 aborted = true;
                                 break;
                             }
@@ -743,16 +745,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
 
-        // Gated forward on a box of this thread's row, 64 columns (SCALED: 32): vg, vu hold the products' sums.
+        // Gated forward on a box of this thread's row, 64 columns (of a 128-column tile: 32): vg, vu hold the products' sums.
         auto finish_glu = [&](const float* vg, const float* vu, int32_t x, int32_t y) {
-            constexpr int PAIRS = SCALED ? 16 : 32;
+            constexpr int PAIRS = kWarpN / 2;
             f32x2 g[PAIRS], u[PAIRS];
             uint32_t h[PAIRS];
             with_bias(g, vg, p.bias, x);
             with_bias(u, vu, p.bias_up, x);
             if constexpr (GLU) {
                 auto store = [&](const CUtensorMap* tm, void* base, int64_t ld) {
-                    if constexpr (SCALED)
+                    if constexpr (PAIRS == 16)
                         store_half_rows(h, x, y, lane, stg, tm, base, ld, p.M, p.N);
                     else
                         store_rows<2>(h, x, y, lane, stg, tm, base, ld, p.M, p.N);

@@ -30,12 +30,12 @@ KernelChoice tile_choice_for(int config)
     return tile_choice<128, 6 - kLess, IN, OUT, MODE, SUMS, 1>(2);
 }
 
-// 8-bit operands with block scales: tiles of 128 accumulator columns (gated: 64 of each half), a pair or (any other config)
-// one CTA.
+// 8-bit operands with block scales: a pair with 256 accumulator columns (gated: 128 of each half) or (any other config) one CTA
+// with 128.
 template <int OUT, int MODE>
 KernelChoice scaled_choice(int config)
 {
-    if (config == 3) return tile_choice<128, 8, 2, OUT, MODE, true, 2, true>(3);
+    if (config == 3) return tile_choice<256, 6, 2, OUT, MODE, true, 2, true>(3);
     return tile_choice<128, 6, 2, OUT, MODE, true, 1, true>(2);
 }
 
