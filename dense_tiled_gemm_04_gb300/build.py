@@ -34,7 +34,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "sm103_p
                                                      "host/handle.cuh", "linear/activation.cuh",
                                                      "linear/elementwise.cuh", "linear/tile_kernel.cuh",
                                                      "linear/tile_set.cuh", "linear/cluster_kernel.cuh",
-                                                     "linear/cluster_set.cuh", "linear/api_common.cuh", "linear/norm.cuh")] + [
+                                                     "linear/cluster_set.cuh", "linear/api_common.cuh", "linear/norm.cuh", "linear/sums.cuh")] + [
     os.path.join(INCLUDE, "gemm.h")]
 OBJ_DIR = os.path.join(HERE, "_build")
 

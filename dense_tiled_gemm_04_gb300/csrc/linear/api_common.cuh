@@ -9,6 +9,7 @@
 
 #include "gemm.h"
 #include "host/handle.cuh"
+#include "sums.cuh"
 
 namespace dtg {
 namespace host {
@@ -84,6 +85,11 @@ struct SumVector {
     gemm_dtype_t type;
     float beta;
 };
+
+inline linear::BiasGrad bias_grad(const SumVector& v)
+{
+    return {v.to, v.type == GEMM_DTYPE_F32 ? linear::kOutF32 : (v.type == GEMM_DTYPE_BF16 ? linear::kOutBf16 : linear::kOutF16), v.beta};
+}
 
 // One vector, or two (from `offset` floats on) in one launch; a null `to` is left out.
 gemm_status_t launch_sums(const float* partials, int64_t rows, int64_t cols, const SumVector& first, const SumVector& second,

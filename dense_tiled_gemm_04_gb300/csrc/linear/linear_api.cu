@@ -19,11 +19,6 @@ using dtg::KernelChoice;
 namespace dtg {
 namespace host {
 
-static linear::BiasGrad bias_grad(const SumVector& v)
-{
-    return {v.to, v.type == GEMM_DTYPE_F32 ? linear::kOutF32 : (v.type == GEMM_DTYPE_BF16 ? linear::kOutBf16 : linear::kOutF16), v.beta};
-}
-
 gemm_status_t launch_sums(const float* partials, int64_t rows, int64_t cols, const SumVector& first, const SumVector& second,
                           int64_t offset, cudaStream_t s)
 {
@@ -79,14 +74,24 @@ bool gated(const Product& q) { return q.mode == dtg::linear::kGlu || q.mode == d
 // its sum per product (see tile_kernel.cuh).  Where an fp32 result is wanted, 12 blocks of 64 keep that under 1e-6.  A
 // result that is rounded to 16 bits takes up to 128 blocks as one chain, whose 1e-5 is 1/25 of fp16's half spacing where
 // that is smallest; a longer contraction is cut into chains of at most that.
-constexpr int64_t kChunkBlocks = 12, kLongChunkBlocks = 128;
+// A gated layer's column sums, of values that are rounded to 16 bits beside them, take 32 blocks as one chain (2.5e-6): summed in
+// registers 16384 x 8192 x 1024 takes 332 us, as one chain 275.
+constexpr int64_t kChunkBlocks = 12, kGatedChunkBlocks = 32, kLongChunkBlocks = 128;
 
 bool fp32_result(const Product& q) { return q.out == GEMM_DTYPE_F32 || q.partials; }
 int64_t k_blocks(const Product& q) { return cdiv(q.depth, is_f8(q.in) ? 128 : 64); }
-int64_t chunk_limit(const Product& q) { return q.scaled ? 1 : fp32_result(q) ? kChunkBlocks : kLongChunkBlocks; }
+int64_t chunk_limit(const Product& q)
+{
+    if (q.mode == dtg::linear::kGluDgrad && q.partials) return kGatedChunkBlocks;
+    return q.scaled ? 1 : fp32_result(q) ? kChunkBlocks : kLongChunkBlocks;
+}
 
 // Whether a product takes the tile kernel that sums chunks in registers.
-bool summed(const Product& q) { return fp32_result(q) || q.scaled || k_blocks(q) > kLongChunkBlocks; }
+bool summed(const Product& q)
+{
+    if (q.mode == dtg::linear::kGluDgrad && q.partials) return k_blocks(q) > kGatedChunkBlocks;
+    return fp32_result(q) || q.scaled || k_blocks(q) > kLongChunkBlocks;
+}
 
 KernelChoice tile_kernel(const Product& q, int config)
 {
@@ -206,10 +211,11 @@ gemm_status_t plan_cluster(const LaunchOptions& o, DeviceState& dev, const Produ
     const int64_t slots = 2 * dev.num_sms;
     if (tokens == 128) {
         const bool few = 4 * tiles <= dev.num_sms;
-        if (!few && (tiles > dev.num_sms || kb <= 16)) return GEMM_OK;
         // Gated and scaled kernels have 64 tokens at most; scaled ones take their tiles where those are not few (128 x 8192 x 8192
         // 20.1 us, 30.8 on clusters; 256 x 4096 x 4096 15.9 and 19.7; but 128 x 4096 x 4096 15.7 and 14.1).
-        if (!few && q.scaled) return GEMM_OK;
+        // Gated ones, whose tiles are twice as wide, do from half a tile per SM on (256 hidden 2048 over 1024: 7.9 us, 9.7 in tiles;
+        // 512 x 2048 over 2048: 15.2 and 14.0; backward 1003 x 1000 over 520: 15.8 and 16.5, 512 x 4096 over 1024: 19.8 and 16.1).
+        if (!few && (q.scaled || (gated(q) ? 2 * tiles > dev.num_sms : tiles > dev.num_sms || kb <= 16))) return GEMM_OK;
         if ((few && q.mode != dtg::linear::kWgrad) || gated(q) || q.scaled) {
             tokens = 64;
             tiles = cdiv(q.cols, features) * cdiv(q.rows, tokens);

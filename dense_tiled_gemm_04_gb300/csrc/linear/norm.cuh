@@ -19,7 +19,7 @@
 // NaN or an infinity makes every value of its block stand for NaN (s is NaN; or s is infinite, r is 0 and finite values are 0).
 #pragma once
 
-#include "tile_kernel.cuh"
+#include "sums.cuh"
 
 namespace dtg {
 namespace linear {
@@ -52,10 +52,10 @@ __device__ __forceinline__ void load_vector4(f32x2* v, const NormVector& vec, in
     } else {
         float f[4] = {fill, fill, fill, fill};
         const bool f32 = vec.kind == kVecF32 || vec.kind == kVecF32Any;
-        if (!FULL && vec.kind != kVecNone) {
+        if constexpr (!FULL) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (c + e < n) f[e] = f32 ? static_cast<const float*>(vec.at)[c + e] : load16<BF16>(static_cast<const uint16_t*>(vec.at) + c + e);
+                if (vec.kind != kVecNone && c + e < n) f[e] = f32 ? static_cast<const float*>(vec.at)[c + e] : load16<BF16>(static_cast<const uint16_t*>(vec.at) + c + e);
         }
         v[0] = pair(f[0], f[1]);
         v[1] = pair(f[2], f[3]);
@@ -169,14 +169,17 @@ __device__ __forceinline__ float row_sum(float v, float* shared, int group)
         if ((threadIdx.x & 31) == 0) shared[(threadIdx.x >> 5) % WARPS] = v;
         __syncwarp();
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(WARPS * 32) : "memory");
-        if constexpr (WARPS == 2) return shared[0] + shared[1];
-        f32x2 s = 0;
+        if constexpr (WARPS == 2) {
+            v = shared[0] + shared[1];
+        } else {
+            f32x2 s = 0;
 #pragma unroll
-        for (int w = 0; w < WARPS; w += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(shared + w);
-            s = add2(s, add2(pair(f.x, f.y), pair(f.z, f.w)));
+            for (int w = 0; w < WARPS; w += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(shared + w);
+                s = add2(s, add2(pair(f.x, f.y), pair(f.z, f.w)));
+            }
+            v = sum_of(s);
         }
-        v = sum_of(s);
     }
     return v;
 }
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const No
 constexpr int kWideWarps = 16, kWideUnroll = 4;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kWideWarps * 32, 1) layer_norm_wide_kernel(const NormParams p)
+__global__ void __launch_bounds__(kWideWarps * 32, 2) layer_norm_wide_kernel(const NormParams p)
 {
     __shared__ __align__(16) float shared[2][kWideWarps];
     ptx::grid_dependency_wait();
@@ -390,6 +393,9 @@ struct NormGradParams {
     NormVector w;
     uint16_t* dX;
     float *dw, *db;    // partial sums: a row of `pitch` per block; null: not wanted
+    // Few blocks: the last of them to finish adds the partial sums itself, in block order, and saves a launch.  null: none does.
+    int32_t* arrived;  // zero before and after
+    BiasGrad dw_out, db_out;
     float2* row_means;  // rows that registers do not hold: (mean(g), mean(g x^))
     int64_t M, N, lddy, ldx, ldr, lddx, pitch;
     int64_t block_rows;  // layer_norm_grad_wide_kernel: rows per block
@@ -544,6 +550,34 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
                 put(p.db, first(k) + 128 * q + 4 * lane, db[k][2 * q], db[k][2 * q + 1]);
             }
     }
+    if (!p.arrived) return;
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(p.arrived, 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const int32_t quads = (N + 3) >> 2;
+    for (int32_t i = threadIdx.x; i < 2 * quads; i += kWarps * 32) {
+        const bool second = i >= quads;
+        const int32_t c = 4 * (second ? i - quads : i);
+        const float* from = second ? p.db : p.dw;
+        if (!from) continue;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (unsigned b = 0; b < gridDim.x; ++b) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(from + b * p.pitch + c));
+            s[0] += f.x;
+            s[1] += f.y;
+            s[2] += f.z;
+            s[3] += f.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < N) write_bias_grad(second ? p.db_out : p.dw_out, c + e, s[e]);
+    }
+    if (threadIdx.x == 0) *p.arrived = 0;  // ready for the next launch
 }
 
 // Rows that registers do not hold: first the means of every row, then dx and the sums by strips of columns.

@@ -110,23 +110,30 @@ int64_t norm_grad_max_blocks(int64_t M, int64_t N)
 }
 
 template <bool BF16, bool FULL>
-gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& p, int64_t* blocks, cudaStream_t s)
+gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, bool* summed, cudaStream_t s)
 {
     constexpr void (*kFn[kNormGradShapes])(const NormGradParams) = {norm_grad_fn<BF16, FULL, 0>(), norm_grad_fn<BF16, FULL, 1>(),
                                                                     norm_grad_fn<BF16, FULL, 2>(), norm_grad_fn<BF16, FULL, 3>(),
                                                                     norm_grad_fn<BF16, FULL, 4>(), norm_grad_fn<BF16, FULL, 5>()};
-    const int i = shape_for(p.N);
+    const int i = shape_for(q.N);
     const NormGradShape shape = kGradShape[i];
-    *blocks = std::min({cdiv(p.M, shape.groups), norm_grad_max_blocks(p.M, p.N), int64_t(h->dev.num_sms) * (kNormGradThreads / shape.threads())});
+    *blocks = std::min({cdiv(q.M, shape.groups), norm_grad_max_blocks(q.M, q.N), int64_t(h->dev.num_sms) * (kNormGradThreads / shape.threads())});
+    // Up to 32 blocks the last one adds their sums (65 x 1000 fp16: 10.2 us with a second launch, whose host part it saves).
+    NormGradParams p = q;
+    if (*blocks <= 32 && (p.dw || p.db)) {
+        p.arrived = h->ws.counters;
+        *summed = true;
+    }
     const int smem = 3 * kNormGradStages * shape.chunks * 16 * shape.threads();
     return launch_rows<NormGradParams>(h, kFn[i], i + kNormShapes * (4 + 2 * FULL + BF16), *blocks, shape.threads(), smem, smem, p, s);
 }
 
+// summed: set where the kernel has written dw and db itself, not only `blocks` rows of partial sums.
 template <bool BF16>
-gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, cudaStream_t s)
+gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, bool* summed, cudaStream_t s)
 {
     if (q.N <= kNormGradMaxHeld)
-        return q.N % 256 == 0 ? launch_norm_grad<BF16, true>(h, q, blocks, s) : launch_norm_grad<BF16, false>(h, q, blocks, s);
+        return q.N % 256 == 0 ? launch_norm_grad<BF16, true>(h, q, blocks, summed, s) : launch_norm_grad<BF16, false>(h, q, blocks, summed, s);
     NormGradParams p = q;
     const gemm_status_t st = launch_after(&layer_norm_grad_means_kernel<BF16>, blocks_for(p.M, 1), kMeansWarps * 32, 0, s, p);
     if (st != GEMM_OK) return st;
@@ -224,9 +231,11 @@ gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_gr
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float* const partials = a.workspace ? static_cast<float*>(a.workspace) : h->sums;
     const int64_t pitch = sum_pitch(a.N), half = norm_grad_max_blocks(a.M, a.N) * pitch;
+    const SumVector dw{a.dweight, a.dweight_dtype, a.beta}, db{a.dbias, a.dbias_dtype, a.beta};
     int64_t blocks = 0;
+    bool summed = false;
     if (a.M > 0) {
-        NormGradParams p;
+        NormGradParams p = {};
         p.dY = static_cast<const uint16_t*>(a.dY);
         p.X = static_cast<const uint16_t*>(a.X);
         p.residual = static_cast<const uint16_t*>(a.residual);
@@ -244,12 +253,13 @@ gemm_status_t gemm_run_layer_norm_grad(gemm_handle_t h, const gemm_layer_norm_gr
         p.ldr = a.ldr;
         p.lddx = a.lddx;
         p.pitch = pitch;
-        p.block_rows = 0;
-        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_norm_grad<true>(h, p, &blocks, s)
-                                                             : launch_norm_grad<false>(h, p, &blocks, s);
+        p.dw_out = bias_grad(dw);
+        p.db_out = bias_grad(db);
+        const gemm_status_t st = a.dtype == GEMM_DTYPE_BF16 ? launch_norm_grad<true>(h, p, &blocks, &summed, s)
+                                                             : launch_norm_grad<false>(h, p, &blocks, &summed, s);
         if (st != GEMM_OK) return st;
     }
-    return launch_sums(partials, blocks, a.N, {a.dweight, a.dweight_dtype, a.beta}, {a.dbias, a.dbias_dtype, a.beta}, half, s);
+    return summed ? GEMM_OK : launch_sums(partials, blocks, a.N, dw, db, half, s);
 }
 
 gemm_status_t gemm_run_quantize(gemm_handle_t h, const gemm_quantize_args_t* args, void* stream)

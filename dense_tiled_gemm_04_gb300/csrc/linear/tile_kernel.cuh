@@ -1293,16 +1293,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // Bring the lines of `in` that this warp will read for `nxt` into L2, an item ahead.
         auto prefetch_in = [&]() {
             const int64_t row = static_cast<int64_t>(nxt.y) + lane;
-            if (!p.in || !nxt.inside || row >= p.M) return;
+            // (Not for a gated layer's g and u: 16384 x 8192 x 1024 without sums 257 us with them, 238 without.)
+            if (MODE == kGluDgrad || !p.in || !nxt.inside || row >= p.M) return;
             constexpr int kElem = OUT == kOutF32 ? 4 : 2;
             const uint8_t* line = static_cast<const uint8_t*>(p.in) + (row * p.ldin + nxt.x) * kElem;
 #pragma unroll
             for (int b = 0; b < CW * kElem / 128; ++b)
-                if (nxt.x + b * (128 / kElem) < p.N) {
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
-                    if constexpr (MODE == kGluDgrad)  // u, N columns after g
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128 + static_cast<int64_t>(p.N) * kElem));
-                }
+                if (nxt.x + b * (128 / kElem) < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + b * 128));
         };
         more_items = next_item(nxt);
         if (more_items) prefetch_in();

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -129,6 +130,19 @@ class gemm_layer_norm_grad_args_t(ctypes.Structure):
                 ("dbias_dtype", ctypes.c_int32), ("beta", ctypes.c_float)]
 
 
+def _packer(cls):
+    """A function that lays a structure's fields out as bytes, in a third of the time that making a ctypes structure takes."""
+    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_linear, _pack_glu, _pack_glu_dgrad, _pack_quantize, _pack_layer_norm, _pack_layer_norm_grad = map(
+    _packer, (gemm_linear_args_t, gemm_glu_args_t, gemm_glu_dgrad_args_t, gemm_quantize_args_t, gemm_layer_norm_args_t,
+              gemm_layer_norm_grad_args_t))
+
+
 class GemmError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -177,12 +191,12 @@ def load() -> ctypes.CDLL:
         "gemm_run_linear_wgrad": ([p, ctypes.POINTER(gemm_wgrad_args_t), p], i32),
         "gemm_run_act_grad": ([p, ctypes.POINTER(gemm_act_grad_args_t), p], i32),
         "gemm_bias_grad_workspace_bytes": ([i64, i64], i64),
-        "gemm_run_linear_glu": ([p, ctypes.POINTER(gemm_glu_args_t), p], i32),
-        "gemm_run_linear_glu_dgrad": ([p, ctypes.POINTER(gemm_glu_dgrad_args_t), p], i32),
-        "gemm_run_linear_scaled": ([p, ctypes.POINTER(gemm_linear_args_t), p, i64, p, i64, p], i32),
-        "gemm_run_quantize": ([p, ctypes.POINTER(gemm_quantize_args_t), p], i32),
-        "gemm_run_layer_norm": ([p, ctypes.POINTER(gemm_layer_norm_args_t), p], i32),
-        "gemm_run_layer_norm_grad": ([p, ctypes.POINTER(gemm_layer_norm_grad_args_t), p], i32),
+        "gemm_run_linear_glu": ([p, p, p], i32),
+        "gemm_run_linear_glu_dgrad": ([p, p, p], i32),
+        "gemm_run_linear_scaled": ([p, p, p, i64, p, i64, p], i32),
+        "gemm_run_quantize": ([p, p, p], i32),
+        "gemm_run_layer_norm": ([p, p, p], i32),
+        "gemm_run_layer_norm_grad": ([p, p, p], i32),
         "gemm_layer_norm_grad_workspace_bytes": ([i64, i64], i64),
         "gemm_status_string": ([i32], ctypes.c_char_p),
         "gemm_api_version": ([], i32),
@@ -781,9 +795,9 @@ class Gemm:
         if out is None:
             out = _new(M, N, out_dtype, dev, stream)
         ldy = _matrix(out, "out", M, N, out_dtype, dev)
-        a = gemm_linear_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
+        a = _pack_linear(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
                                ldz, in_code, out_code, bias_code, _act(act), alpha)
-        st = self._lib.gemm_run_linear_scaled(self._h, ctypes.byref(a), xs_p, ld_xs, ws_p, ld_ws,
+        st = self._lib.gemm_run_linear_scaled(self._h, a, xs_p, ld_xs, ws_p, ld_ws,
                                               _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_linear_scaled")
@@ -828,9 +842,9 @@ class Gemm:
         if out is None:
             out = _new(M, N, out_dtype, dev, stream)
         ldh = _matrix(out, "out", M, N, out_dtype, dev)
-        a = gemm_glu_args_t(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, z_p, xs_p, ws_p, M, N, K, ldx, ldw, ldh, ldz, ld_xs,
+        a = _pack_glu(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, z_p, xs_p, ws_p, M, N, K, ldx, ldw, ldh, ldz, ld_xs,
                             ld_ws, in_code, out_code, bias_code, _act(act), alpha)
-        st = self._lib.gemm_run_linear_glu(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        st = self._lib.gemm_run_linear_glu(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_linear_glu")
         return out
@@ -861,9 +875,9 @@ class Gemm:
             if ws_bytes > OWN_SUMS_BYTES:
                 ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
                 ws_p = ws.data_ptr()
-        a = gemm_glu_dgrad_args_t(dY.data_ptr(), W.data_ptr(), Z.data_ptr(), out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy,
+        a = _pack_glu_dgrad(dY.data_ptr(), W.data_ptr(), Z.data_ptr(), out.data_ptr(), db_p, ws_p, ws_bytes, M, N, K, lddy,
                                   ldw, ldz, lddz, dt_code, db_code, code, alpha, beta_bias)
-        st = self._lib.gemm_run_linear_glu_dgrad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        st = self._lib.gemm_run_linear_glu_dgrad(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_linear_glu_dgrad")
         return out
@@ -891,8 +905,8 @@ class Gemm:
         if scales is None:
             scales = _new(rows, cols, torch.float32, dev, stream)
         ldq, lds = _matrix(out, "out", M, K, dtype, dev), _scales(scales, "scales", rows, cols, dev)
-        a = gemm_quantize_args_t(X.data_ptr(), out.data_ptr(), scales.data_ptr(), M, K, ldx, ldq, lds, dt_code, q_code, block_rows)
-        st = self._lib.gemm_run_quantize(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        a = _pack_quantize(X.data_ptr(), out.data_ptr(), scales.data_ptr(), M, K, ldx, ldq, lds, dt_code, q_code, block_rows)
+        st = self._lib.gemm_run_quantize(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_quantize")
         return out, scales
@@ -921,9 +935,9 @@ class Gemm:
         if out is None:
             out = _new(M, N, dt, dev, stream)
         ldy = _matrix(out, "out", M, N, dt, dev)
-        a = gemm_layer_norm_args_t(X.data_ptr(), out.data_ptr(), w_p, b_p, mean_p, rstd_p, M, N, ldx, ldy, dt_code, w_code,
+        a = _pack_layer_norm(X.data_ptr(), out.data_ptr(), w_p, b_p, mean_p, rstd_p, M, N, ldx, ldy, dt_code, w_code,
                                    b_code, eps)
-        st = self._lib.gemm_run_layer_norm(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        st = self._lib.gemm_run_layer_norm(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_layer_norm")
         return out
@@ -960,9 +974,9 @@ class Gemm:
             if ws_bytes > OWN_SUMS_BYTES:
                 ws = _new(1, ws_bytes // 4, torch.float32, dev, stream)
                 ws_p = ws.data_ptr()
-        a = gemm_layer_norm_grad_args_t(dY.data_ptr(), X.data_ptr(), res_p, mean_p, rstd_p, w_p, out.data_ptr(), dw_p, db_p,
+        a = _pack_layer_norm_grad(dY.data_ptr(), X.data_ptr(), res_p, mean_p, rstd_p, w_p, out.data_ptr(), dw_p, db_p,
                                         ws_p, ws_bytes, M, N, lddy, ldx, ldr, lddx, dt_code, w_code, dw_code, db_code, beta)
-        st = self._lib.gemm_run_layer_norm_grad(self._h, ctypes.byref(a), _stream_of(stream, dev) if _ptr is None else _ptr)
+        st = self._lib.gemm_run_layer_norm_grad(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
             raise GemmError(st, "gemm_run_layer_norm_grad")
         return out
