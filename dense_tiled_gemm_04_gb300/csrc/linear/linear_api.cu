@@ -74,22 +74,17 @@ bool gated(const Product& q) { return q.mode == dtg::linear::kGlu || q.mode == d
 // its sum per product (see tile_kernel.cuh).  Where an fp32 result is wanted, 12 blocks of 64 keep that under 1e-6.  A
 // result that is rounded to 16 bits takes up to 128 blocks as one chain, whose 1e-5 is 1/25 of fp16's half spacing where
 // that is smallest; a longer contraction is cut into chains of at most that.
-// A gated layer's column sums, of values that are rounded to 16 bits beside them, take 32 blocks as one chain (2.5e-6): summed in
-// registers 16384 x 8192 x 1024 takes 332 us, as one chain 275.
-constexpr int64_t kChunkBlocks = 12, kGatedChunkBlocks = 32, kLongChunkBlocks = 128;
+constexpr int64_t kChunkBlocks = 12, kLongChunkBlocks = 128;
 
 bool fp32_result(const Product& q) { return q.out == GEMM_DTYPE_F32 || q.partials; }
 int64_t k_blocks(const Product& q) { return cdiv(q.depth, is_f8(q.in) ? 128 : 64); }
-int64_t chunk_limit(const Product& q)
-{
-    if (q.mode == dtg::linear::kGluDgrad && q.partials) return kGatedChunkBlocks;
-    return q.scaled ? 1 : fp32_result(q) ? kChunkBlocks : kLongChunkBlocks;
-}
+int64_t chunk_limit(const Product& q) { return q.scaled ? 1 : fp32_result(q) ? kChunkBlocks : kLongChunkBlocks; }
 
 // Whether a product takes the tile kernel that sums chunks in registers.
+// (A gated layer's column sums are joined box by box: one chunk needs no sums in registers.)
 bool summed(const Product& q)
 {
-    if (q.mode == dtg::linear::kGluDgrad && q.partials) return k_blocks(q) > kGatedChunkBlocks;
+    if (q.mode == dtg::linear::kGluDgrad && k_blocks(q) <= kChunkBlocks) return false;
     return fp32_result(q) || q.scaled || k_blocks(q) > kLongChunkBlocks;
 }
 
@@ -386,9 +381,9 @@ gemm_status_t launch_product(gemm_handle_t h, const Product& q, int64_t* sum_row
     dtg::linear::TileMaps<dtg::linear::kGlu> maps;  // (the others' begin alike; gated dgrad's has the same six)
     CUtensorMap &tA = maps.A, &tB = maps.B, &tC = maps.C, &tZ = maps.Z, &t5 = maps.B_up, &t6 = maps.Z_up;
     const auto out_map = [&](const void* at, int64_t ld, CUtensorMap* map) {
-        // Boxes of the output and of what is read or kept beside it; those of gated dgrad and of a gated tile of
-        // 64 columns are half as wide.
-        const bool narrow = q.mode == dtg::linear::kGluDgrad || (q.mode == dtg::linear::kGlu && half == 64);
+        // Boxes of the output and of what is read or kept beside it; those of a gated tile of 64 columns are half
+        // as wide.
+        const bool narrow = q.mode == dtg::linear::kGlu && half == 64;
         return get_tmap(nullptr, at, q.cols, q.rows, ld * oe, static_cast<uint32_t>((narrow ? 64 : 128) / oe), 32, q.out, map,
                         narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     };

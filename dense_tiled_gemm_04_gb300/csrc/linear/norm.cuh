@@ -51,8 +51,8 @@ __device__ __forceinline__ void load_vector4(f32x2* v, const NormVector& vec, in
         v[1] = unpack2<BF16>(a.y);
     } else {
         float f[4] = {fill, fill, fill, fill};
-        const bool f32 = vec.kind == kVecF32 || vec.kind == kVecF32Any;
         if constexpr (!FULL) {
+            const bool f32 = vec.kind == kVecF32 || vec.kind == kVecF32Any;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (vec.kind != kVecNone && c + e < n) f[e] = f32 ? static_cast<const float*>(vec.at)[c + e] : load16<BF16>(static_cast<const uint16_t*>(vec.at) + c + e);
@@ -74,13 +74,15 @@ __device__ __forceinline__ void load_vector8(f32x2 (&v)[4], const NormVector& ve
 template <bool FULL>
 __device__ __forceinline__ void store_row4(uint16_t* row, int32_t c, int32_t n, uint32_t w0, uint32_t w1)
 {
-    if (FULL || c + 4 <= n) {
+    if constexpr (FULL) {
         *reinterpret_cast<uint2*>(row + c) = make_uint2(w0, w1);
-        return;
-    }
+    } else if (c + 4 <= n) {
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(w0, w1);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (c + e < n) row[c + e] = static_cast<uint16_t>((e < 2 ? w0 : w1) >> (16 * (e & 1)));
+        for (int e = 0; e < 4; ++e)
+            if (c + e < n) row[c + e] = static_cast<uint16_t>((e < 2 ? w0 : w1) >> (16 * (e & 1)));
+    }
 }
 
 __device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr)
@@ -184,7 +186,7 @@ __device__ __forceinline__ float row_sum(float v, float* shared, int group)
     return v;
 }
 
-template <int WARPS>
+template <int WARPS, bool ALONE>
 __device__ __forceinline__ float2 row_sums(float2 v, float2* shared, int group)
 {
     f32x2 s = pair(v.x, v.y);
@@ -192,10 +194,15 @@ __device__ __forceinline__ float2 row_sums(float2 v, float2* shared, int group)
     for (int off = 16; off > 0; off >>= 1) s = add2(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
     if constexpr (WARPS > 1) {
         split(s, v.x, v.y);
-        shared += group * WARPS;
-        if ((threadIdx.x & 31) == 0) shared[(threadIdx.x >> 5) % WARPS] = v;
-        __syncwarp();
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(WARPS * 32) : "memory");
+        if constexpr (ALONE) {  // the block's only row
+            if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+            __syncthreads();
+        } else {
+            shared += group * WARPS;
+            if ((threadIdx.x & 31) == 0) shared[(threadIdx.x >> 5) % WARPS] = v;
+            __syncwarp();
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(WARPS * 32) : "memory");
+        }
         s = 0;
 #pragma unroll
         for (int w = 0; w < WARPS; w += 2) {
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
     __shared__ __align__(16) float2 shared[2][kWarps];
     const int32_t N = static_cast<int32_t>(p.N);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = warp / WARPS, in_row = warp % WARPS;
+    const int group = GROUPS == 1 ? 0 : warp / WARPS, in_row = GROUPS == 1 ? warp : warp % WARPS;
     const uint32_t ring = ptx::smem_addr(smem) + 512u * warp;
     auto place = [&](int stage, int which, int k) { return ring + 512u * static_cast<uint32_t>(((stage * 3 + which) * CHUNKS + k) * kWarps); };
     auto first = [&](int k) { return (k * WARPS + in_row) * 256; };
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
                 s2 = fma2(g, e[i], s2);
             }
         }
-        const float2 c = row_sums<WARPS>(make_float2(sum_of(s1), sum_of(s2)), shared[stage], group);
+        const float2 c = row_sums<WARPS, GROUPS == 1>(make_float2(sum_of(s1), sum_of(s2)), shared[stage], group);
         const f32x2 c1 = both(-rstd * (c.x * inv_n)), c2 = both(-rstd * (rstd * (rstd * (c.y * inv_n))));
         uint16_t* const dx = p.dX + row * p.lddx;
 #pragma unroll
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(kMeansWarps * 32, 4) layer_norm_grad_means_ker
             }
         }
     }
-    const float2 s = row_sums<kMeansWarps>(make_float2(sum_of(s1), sum_of(s2)), shared, 0);
+    const float2 s = row_sums<kMeansWarps, true>(make_float2(sum_of(s1), sum_of(s2)), shared, 0);
     const float inv_n = 1.0f / static_cast<float>(p.N);
     if (threadIdx.x == 0) p.row_means[row] = make_float2(s.x * inv_n, s.y * inv_n);
 }

@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     static_assert(OUT != kOutF32 || (MODE == kWgrad && SUMS), "fp32 output: weight gradients only");
     static_assert(!SCALED || (IN == 2 && SUMS), "scales meet the products in the registers' sums");
     static_assert(MODE != kGluDgrad || BN == 256, "two pairs of boxes per warp");
-    static_assert(MODE != kDgrad || STG_BUFS == 2, "dgrad alternates between two buffers");
+    static_assert((MODE != kDgrad && MODE != kGluDgrad) || STG_BUFS == 2, "dgrad alternates between two buffers, gated dgrad fills both");
     const CUtensorMap &tmA = maps.A, &tmB = maps.B, &tmC = maps.C, &tmZ = maps.Z;
     constexpr bool GLU = MODE == kGlu;
     constexpr bool PAIR = CLUSTER == 2;
@@ -684,14 +684,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // bytes of 32 rows at a time, they bound the kernel: 16384 x 1024 x 8192 relu 233 us against 176 without.)
         int in_buf = 0;                        // buffer of the next box
         uint32_t in_phase = 0, in_flight = 0;  // per buffer: parity its barrier completes next; a load is pending
-        // A gated layer's boxes are 32 columns wide: g in the first half of a buffer, u in the second.
+        // Gated: g in the first buffer, u in the second.
         auto load_in = [&](int buf, int32_t x, int32_t y) {
             in_flight |= 1u << buf;
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(in_bar(ew, buf), kTileStgBytes);
+                ptx::mbar_arrive_expect_tx(in_bar(ew, buf), (MODE == kGluDgrad ? 2 : 1) * kTileStgBytes);
                 ptx::tma_load_2d(stg + buf * kTileStgBytes, &tmZ, x, y, in_bar(ew, buf));
-                if constexpr (MODE == kGluDgrad)
-                    ptx::tma_load_2d(stg + buf * kTileStgBytes + kTileStgBytes / 2, &maps.Z_up, x, y, in_bar(ew, buf));
+                if constexpr (MODE == kGluDgrad) ptx::tma_load_2d(stg + kTileStgBytes, &maps.Z_up, x, y, in_bar(ew, buf));
             }
         };
         // A work item as this warp sees it: columns from x, rows from y of C; inside: it has some of both.
@@ -774,80 +773,84 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
 
-        // Gated dgrad on 32 columns of this thread's row: v holds d's sums.  g and u come by TMA (see load_in), the next box's
-        // while this one is worked on; their gradients are written over them and leave from there.  N is a multiple of 8:
-        // TMA clips every box exactly.
+        // Gated dgrad on 64 columns of this thread's row: v holds d's sums, and is overwritten.  g and u come by TMA into the warp's
+        // two staging buffers, their gradients are written over them and leave from there, and the next box's g and u are asked
+        // for as soon as the stores have read the buffers.  (Boxes of 32 columns in two pairs of buffers hid that wait, but
+        // took twice the TMA's rows, which then bound the kernel: 16384 x 8192 x 1024 238 us without sums, 311 with.)  N is a
+        // multiple of 8: TMA clips every box exactly.
         auto finish_glu_dgrad = [&](float* v, int32_t x, int32_t y) {
             if constexpr (MODE == kGluDgrad) {
-                const uint32_t buf = stg + in_buf * kTileStgBytes;
-                auto free_for = [&](int b, int32_t lx, int32_t ly) {  // the store that left from buffer b has read it; load it
-                    if (lane == 0) ptx::bulk_wait_group_read<STG_BUFS - 2>();
+                auto load_next = [&](int32_t lx, int32_t ly) {
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
                     __syncwarp();
-                    load_in(b, lx, ly);
+                    load_in(0, lx, ly);
                 };
-                if (!(in_flight & (1u << in_buf))) {
-                    if (lane == 0) ptx::bulk_wait_group_read<STG_BUFS - 1>();
-                    __syncwarp();
-                    load_in(in_buf, x, y);
-                }
-                const int next = in_buf + 1 == STG_BUFS ? 0 : in_buf + 1;
-                const bool same_tile = x + 32 < p.N && x - cur.x + 32 < CW;
-                if (same_tile)
-                    free_for(next, x + 32, y);
-                else if (more_items && nxt.inside)
-                    free_for(next, nxt.x, nxt.y);
-                const bool in = wd.wait(in_bar(ew, in_buf), (in_phase >> in_buf) & 1u, kRoleEpilogue, -1, 0);
+                if (!in_flight) load_next(x, y);
+                const bool in = wd.wait(in_bar(ew, 0), in_phase & 1u, kRoleEpilogue, -1, 0);
                 if (!__all_sync(0xFFFFFFFFu, in)) return;  // recorded: the launch is being abandoned
-                in_phase ^= 1u << in_buf;
-                in_flight &= ~(1u << in_buf);
+                in_phase ^= 1u;
+                in_flight = 0;
                 const f32x2 alpha = both(p.alpha);
                 const bool row_in = y + lane < p.M;
-                float du[32];  // v becomes dG
-                DTG_ACT_SWITCH(p.act, {
-                    _Pragma("unroll") for (int ch = 0; ch < 4; ++ch)
-                    {
-                        const uint32_t at_g = half_box_chunk(buf, lane, ch), at_u = at_g + kTileStgBytes / 2;
-                        const uint4 gw = ld_shared_u4(at_g), uw = ld_shared_u4(at_u);
-                        const uint32_t gi[4] = {gw.x, gw.y, gw.z, gw.w}, ui[4] = {uw.x, uw.y, uw.z, uw.w};
-                        uint32_t hg[4], hu[4];
-                        _Pragma("unroll") for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                for (int half_box = 0; half_box < 2; ++half_box) {
+                    float du[32];  // v's first 32 become dG
+                    DTG_ACT_SWITCH(p.act, {
+                        _Pragma("unroll") for (int ch = 0; ch < 4; ++ch)
                         {
-                            const int c = 8 * ch + 2 * i;
-                            const f32x2 d = mul2(alpha, pair(v[c], v[c + 1]));
-                            f32x2 value, slope;
-                            act_both2<ACT>(unpack2<kBf16>(gi[i]), value, slope);
-                            const f32x2 a = mul2(mul2(d, unpack2<kBf16>(ui[i])), slope), b = mul2(d, value);
-                            hg[i] = round2<kBf16>(a);
-                            hu[i] = round2<kBf16>(b);
-                            split(a, v[c], v[c + 1]);
-                            split(b, du[c], du[c + 1]);
+                            const uint32_t at_g = box_chunk(stg, lane, 4 * half_box + ch), at_u = at_g + kTileStgBytes;
+                            const uint4 gw = ld_shared_u4(at_g), uw = ld_shared_u4(at_u);
+                            const uint32_t gi[4] = {gw.x, gw.y, gw.z, gw.w}, ui[4] = {uw.x, uw.y, uw.z, uw.w};
+                            uint32_t hg[4], hu[4];
+                            _Pragma("unroll") for (int i = 0; i < 4; ++i)
+                            {
+                                const int c = 8 * ch + 2 * i;
+                                const f32x2 d = mul2(alpha, pair(v[c], v[c + 1]));
+                                f32x2 value, slope;
+                                act_both2<ACT>(unpack2<kBf16>(gi[i]), value, slope);
+                                const f32x2 a = mul2(mul2(d, unpack2<kBf16>(ui[i])), slope), b = mul2(d, value);
+                                hg[i] = round2<kBf16>(a);
+                                hu[i] = round2<kBf16>(b);
+                                split(a, v[c], v[c + 1]);
+                                split(b, du[c], du[c + 1]);
+                            }
+                            ptx::st_shared_v4(at_g, hg[0], hg[1], hg[2], hg[3]);
+                            ptx::st_shared_v4(at_u, hu[0], hu[1], hu[2], hu[3]);
                         }
-                        ptx::st_shared_v4(at_g, hg[0], hg[1], hg[2], hg[3]);
-                        ptx::st_shared_v4(at_u, hu[0], hu[1], hu[2], hu[3]);
+                    });
+                    if (half_box == 1) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::tma_store_2d(&tmC, stg, x, y);
+                            ptx::tma_store_2d(&maps.C_up, stg + kTileStgBytes, x, y);
+                            ptx::bulk_commit_group();
+                        }
                     }
-                });
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::tma_store_2d(&tmC, buf, x, y);
-                    ptx::tma_store_2d(&maps.C_up, buf + kTileStgBytes / 2, x, y);
-                    ptx::bulk_commit_group();
-                }
-                in_buf = next;
-                if (p.partials) {
-                    // Rows past M are not part of the sums (an infinite weight makes them NaN).
-                    if (!row_in) {
+                    if (p.partials) {
+                        // Rows past M are not part of the sums (an infinite weight makes them NaN).
+                        if (!row_in) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = du[i] = 0.0f;
+                            for (int i = 0; i < 32; ++i) v[i] = du[i] = 0.0f;
+                        }
+                        sum_rows32(v, lane);
+                        sum_rows32(du, lane);
+                        const int32_t c = x + 32 * half_box + lane;
+                        if (c < p.N) {
+                            float* const sums = p.partials + static_cast<int64_t>(y >> 5) * p.pitch + c;
+                            sums[0] = v[0];
+                            sums[p.N] = du[0];
+                        }
                     }
-                    sum_rows32(v, lane);
-                    sum_rows32(du, lane);
-                    if (x + lane < p.N) {
-                        float* const sums = p.partials + static_cast<int64_t>(y >> 5) * p.pitch + x + lane;
-                        sums[0] = v[0];
-                        sums[p.N] = du[0];
+                    if (half_box == 0) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = v[32 + i];
                     }
                 }
+                if (x + 64 < p.N && x - cur.x + 64 < CW)
+                    load_next(x + 64, y);
+                else if (more_items && nxt.inside)
+                    load_next(nxt.x, nxt.y);
             }
         };
 
@@ -1127,6 +1130,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         };
 
+        // Whether this warp's wait was met.  Where tiles are shared out the eight warps decide together, since they meet at barriers
+        // for the joins; elsewhere each goes its own way, up to a tile ahead of the slowest (gated dgrad 16384 x 8192 x 1024: warps
+        // waited 5000 of a tile's 18000 cycles for one another).
+        const bool shared_out = p.dp_tiles != p.num_tiles;
+        auto carry_on = [&](bool ok) { return shared_out ? tile_epi_and(ok) : __all_sync(0xFFFFFFFFu, ok) != 0; };
+
         // The item `cur`; false when the launch is being abandoned.
         auto one_item = [&]() -> bool {
             const int64_t tile = cur.tile;
@@ -1167,7 +1176,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         if (acc == 0) acc_phase ^= 1u;
                     }
                 }
-                if (!tile_epi_and(ok)) return false;
+                if (!carry_on(ok)) return false;
                 if (!whole && other_is_in(tr, parts)) {
                     const float4* f4 = slot_f4(sk_slot(p, first_unit + (unit == first_unit ? 1 : 0), tr));
 #pragma unroll
@@ -1192,9 +1201,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (y < p.M && x0 < p.N) finish_glu(&s[0], &s[CW / 2], x0, y);
                 } else if constexpr (MODE == kGluDgrad) {
                     if (y < p.M) {
+                        // A rolled loop that moves the sums up by a box: with a copy of the code (five activations) for each 32 columns
+                        // 4096^3 took 130 us, so 117.
+#pragma unroll 1
+                        for (int b = 0; b < CW / 64; ++b) {
+                            if (x0 + b * 64 < p.N) {
+                                float v[64];
 #pragma unroll
-                        for (int b = 0; b < CW / 32; ++b)
-                            if (x0 + b * 32 < p.N) finish_glu_dgrad(&s[b * 32], x0 + b * 32, y);
+                                for (int i = 0; i < 64; ++i) v[i] = s[i];
+                                finish_glu_dgrad(v, x0 + b * 64, y);
+                            }
+#pragma unroll
+                            for (int i = 0; i < CW - 64; ++i) s[i] = s[i + 64];
+                        }
                     }
                 } else if (y < p.M) {
                     constexpr int kBox = OUT == kOutF32 ? 32 : 64;
@@ -1205,7 +1224,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             } else {
                 // One chunk: every box goes straight from the accumulator (or from the parts) to the output.
                 const bool ok = kb0 == kb1 || wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, tile, kb0);
-                if (!tile_epi_and(ok)) return false;
+                if (!carry_on(ok)) return false;
                 ptx::tc_fence_after_sync();
                 const uint32_t tacc = tmem_base + lane_off + static_cast<uint32_t>(acc * BN + half * CW);
                 float v[64];
@@ -1223,20 +1242,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (y < p.M && x0 < p.N) finish_glu(v, u, x0, y);
                 } else if constexpr (MODE == kGluDgrad) {  // (always a whole tile)
 #pragma unroll 1
-                    for (int b = 0; b < CW / 32; ++b) {
+                    for (int b = 0; b < CW / 64; ++b) {
                         if (kb0 == kb1) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                            for (int i = 0; i < 64; ++i) v[i] = 0.0f;
                         } else {
-                            uint32_t a[32];
-                            __syncwarp();
-                            ptx::tmem_ld_32x32b_x32(tacc + b * 32, a);
-                            ptx::tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
-                            if (b == CW / 32 - 1) release_acc();
+                            load_acc(v, tacc + b * 64);
+                            if (b == CW / 64 - 1) release_acc();
                         }
-                        if (y < p.M && x0 + b * 32 < p.N) finish_glu_dgrad(v, x0 + b * 32, y);
+                        if (y < p.M && x0 + b * 64 < p.N) finish_glu_dgrad(v, x0 + b * 64, y);
                     }
                 } else if (whole) {
 #pragma unroll 1

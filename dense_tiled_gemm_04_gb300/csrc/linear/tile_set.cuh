@@ -47,8 +47,7 @@ KernelChoice glu_choice(int config)
     return tile_choice<256, 4, IN, OUT, kGlu, SUMS, 1>(1);
 }
 
-// Gated dgrad: a ring stage given for two staging buffers per warp, each of g's and u's 32 columns (three buffers and four
-// stages: 16384 x 8192 x 1024 273 us, so 256; 4096^3 110.6 and 99.6).
+// Gated dgrad: a ring stage given for g's and u's staging buffers.
 template <int IN, int OUT, bool SUMS>
 KernelChoice glu_dgrad_choice(int config)
 {
