@@ -643,7 +643,8 @@ gemm_status_t gemm_create(gemm_handle_t* out, int device)
     h->dev.num_sms = sms;
     // Stream-K workspace, sized for the largest plan any configuration makes on this
     // device: 2 slots per work unit of 128 x 256 fp32 per CTA, and an arrival counter per
-    // stream-K tile (at most two waves of tiles) and CTA.
+    // stream-K tile (at most two waves of tiles) and CTA.  One counter more is the layer norm's, whose kernels give up on
+    // nothing: an abandoned product leaves it alone.
     h->ws.partial_floats = static_cast<size_t>(2 * sms) * dtg::kBM * 256;
     h->ws.counter_count = 4 * static_cast<int64_t>(sms);
     // Allocating and clearing are allowed while a stream is being captured (by this thread or another): the calls below
@@ -655,8 +656,8 @@ gemm_status_t gemm_create(gemm_handle_t* out, int device)
         cudaMalloc(&h->d_err, 4 * sizeof(int32_t)) == cudaSuccess &&
         cudaMemsetAsync(h->d_err, 0, 4 * sizeof(int32_t), s) == cudaSuccess &&
         cudaMalloc(&h->ws.partials, h->ws.partial_floats * sizeof(float)) == cudaSuccess &&
-        cudaMalloc(&h->ws.counters, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t)) == cudaSuccess &&
-        cudaMemsetAsync(h->ws.counters, 0, static_cast<size_t>(h->ws.counter_count) * sizeof(int32_t), s) == cudaSuccess &&
+        cudaMalloc(&h->ws.counters, static_cast<size_t>(h->ws.counter_count + 1) * sizeof(int32_t)) == cudaSuccess &&
+        cudaMemsetAsync(h->ws.counters, 0, static_cast<size_t>(h->ws.counter_count + 1) * sizeof(int32_t), s) == cudaSuccess &&
         cudaMalloc(&h->sums, GEMM_OWN_SUMS_BYTES) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
     if (s) cudaStreamDestroy(s);
     if (!ok) {

@@ -400,7 +400,7 @@ struct NormGradParams {
     NormVector w;
     uint16_t* dX;
     float *dw, *db;    // partial sums: a row of `pitch` per block; null: not wanted
-    // Few blocks: the last of them to finish adds the partial sums itself, in block order, and saves a launch.  null: none does.
+    // JOIN, few blocks: the last of them to finish adds the partial sums itself, in block order, and saves a launch.
     int32_t* arrived;  // zero before and after
     BiasGrad dw_out, db_out;
     float2* row_means;  // rows that registers do not hold: (mean(g), mean(g x^))
@@ -411,7 +411,8 @@ struct NormGradParams {
 // GROUPS rows of a block at once, WARPS warps each, whose sums are joined in shared memory at the end.  Dynamic shared memory:
 // kNormGradStages * 3 * CHUNKS * 512 bytes a warp, for dy, x and the residual.  With e = x - mean the row's sums are those of g
 // and g e, and dx = rstd g - rstd mean(g) - e rstd^2 mean(g e).
-template <bool BF16, int WARPS, int CHUNKS, int GROUPS, bool FULL>
+// JOIN: see NormGradParams (an instantiation of its own: with the joining's registers 16384 x 4096 took 94 us, without 89).
+template <bool BF16, int WARPS, int CHUNKS, int GROUPS, bool FULL, bool JOIN>
 __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS * GROUPS * 32))
     layer_norm_grad_kernel(const NormGradParams p)
 {
@@ -557,34 +558,35 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
                 put(p.db, first(k) + 128 * q + 4 * lane, db[k][2 * q], db[k][2 * q + 1]);
             }
     }
-    if (!p.arrived) return;
-    __shared__ bool last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.arrived, 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    const int32_t quads = (N + 3) >> 2;
-    for (int32_t i = threadIdx.x; i < 2 * quads; i += kWarps * 32) {
-        const bool second = i >= quads;
-        const int32_t c = 4 * (second ? i - quads : i);
-        const float* from = second ? p.db : p.dw;
-        if (!from) continue;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (JOIN) {
+        __shared__ bool last;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) last = atomicAdd(p.arrived, 1) == static_cast<int>(gridDim.x) - 1;
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+        const int32_t quads = (N + 3) >> 2;
+        for (int32_t i = threadIdx.x; i < 2 * quads; i += kWarps * 32) {
+            const bool second = i >= quads;
+            const int32_t c = 4 * (second ? i - quads : i);
+            const float* from = second ? p.db : p.dw;
+            if (!from) continue;
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-        for (unsigned b = 0; b < gridDim.x; ++b) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(from + b * p.pitch + c));
-            s[0] += f.x;
-            s[1] += f.y;
-            s[2] += f.z;
-            s[3] += f.w;
-        }
+            for (unsigned b = 0; b < gridDim.x; ++b) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(from + b * p.pitch + c));
+                s[0] += f.x;
+                s[1] += f.y;
+                s[2] += f.z;
+                s[3] += f.w;
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < N) write_bias_grad(second ? p.db_out : p.dw_out, c + e, s[e]);
+            for (int e = 0; e < 4; ++e)
+                if (c + e < N) write_bias_grad(second ? p.db_out : p.dw_out, c + e, s[e]);
+        }
+        if (threadIdx.x == 0) *p.arrived = 0;  // ready for the next launch
     }
-    if (threadIdx.x == 0) *p.arrived = 0;  // ready for the next launch
 }
 
 // Rows that registers do not hold: first the means of every row, then dx and the sums by strips of columns.

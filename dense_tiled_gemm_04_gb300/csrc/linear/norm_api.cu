@@ -74,10 +74,10 @@ constexpr auto norm_fn()
     return &layer_norm_kernel<BF16, kShape[I].warps, kShape[I].chunks, kShape[I].stages, FULL>;
 }
 
-template <bool BF16, bool FULL, int I>
+template <bool BF16, bool FULL, bool JOIN, int I>
 constexpr auto norm_grad_fn()
 {
-    return &layer_norm_grad_kernel<BF16, kGradShape[I].warps, kGradShape[I].chunks, kGradShape[I].groups, FULL>;
+    return &layer_norm_grad_kernel<BF16, kGradShape[I].warps, kGradShape[I].chunks, kGradShape[I].groups, FULL, JOIN>;
 }
 
 template <bool BF16, bool FULL>
@@ -112,20 +112,22 @@ int64_t norm_grad_max_blocks(int64_t M, int64_t N)
 template <bool BF16, bool FULL>
 gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t* blocks, bool* summed, cudaStream_t s)
 {
-    constexpr void (*kFn[kNormGradShapes])(const NormGradParams) = {norm_grad_fn<BF16, FULL, 0>(), norm_grad_fn<BF16, FULL, 1>(),
-                                                                    norm_grad_fn<BF16, FULL, 2>(), norm_grad_fn<BF16, FULL, 3>(),
-                                                                    norm_grad_fn<BF16, FULL, 4>(), norm_grad_fn<BF16, FULL, 5>()};
+    constexpr void (*kFn[2][kNormGradShapes])(const NormGradParams) = {
+        {norm_grad_fn<BF16, FULL, false, 0>(), norm_grad_fn<BF16, FULL, false, 1>(), norm_grad_fn<BF16, FULL, false, 2>(),
+         norm_grad_fn<BF16, FULL, false, 3>(), norm_grad_fn<BF16, FULL, false, 4>(), norm_grad_fn<BF16, FULL, false, 5>()},
+        {norm_grad_fn<BF16, FULL, true, 0>(), norm_grad_fn<BF16, FULL, true, 1>(), norm_grad_fn<BF16, FULL, true, 2>(),
+         norm_grad_fn<BF16, FULL, true, 3>(), norm_grad_fn<BF16, FULL, true, 4>(), norm_grad_fn<BF16, FULL, true, 5>()}};
     const int i = shape_for(q.N);
     const NormGradShape shape = kGradShape[i];
     *blocks = std::min({cdiv(q.M, shape.groups), norm_grad_max_blocks(q.M, q.N), int64_t(h->dev.num_sms) * (kNormGradThreads / shape.threads())});
     // Up to 32 blocks the last one adds their sums (65 x 1000 fp16: 10.2 us with a second launch, whose host part it saves).
     NormGradParams p = q;
     if (*blocks <= 32 && (p.dw || p.db)) {
-        p.arrived = h->ws.counters;
+        p.arrived = h->ws.counters + h->ws.counter_count;  // its own
         *summed = true;
     }
     const int smem = 3 * kNormGradStages * shape.chunks * 16 * shape.threads();
-    return launch_rows<NormGradParams>(h, kFn[i], i + kNormShapes * (4 + 2 * FULL + BF16), *blocks, shape.threads(), smem, smem, p, s);
+    return launch_rows<NormGradParams>(h, kFn[*summed][i], i + kNormShapes * (4 + 4 * *summed + 2 * FULL + BF16), *blocks, shape.threads(), smem, smem, p, s);
 }
 
 // summed: set where the kernel has written dw and db itself, not only `blocks` rows of partial sums.

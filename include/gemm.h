@@ -500,7 +500,8 @@ int64_t gemm_bias_grad_workspace_bytes(int64_t M, int64_t cols);
  *
  * What a block y = x + down(act(gate(n)) * up(n)), n = norm(x), takes beyond the linear layer's calls, trained in 16 bits
  * and served in 8.  Activations, sums, alignment, aliasing, workspaces, options and status codes are those of the linear-layer
- * section, except that gated products have no 128x128 tile (128x256 runs) and share no last tiles. */
+ * section, except that gated products share no last tiles, and that the only one-CTA tile is 128x256 for gated products of 16-bit
+ * operands and 128x128 for 8-bit operands with block scales (of a gated layer: 64 columns of each half). */
 
 /* A gated layer: H = act(G) * U with G = alpha X Wg^T + bg, U = alpha X Wu^T + bu; H is rounded once, from the fp32 G and U.
  *   - W: 2N x K, the rows of Wg above those of Wu; bias: 2N values (bg, then bu) of bias_dtype (F32, or out_dtype), or NULL.
