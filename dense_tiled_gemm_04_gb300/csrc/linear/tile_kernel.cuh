@@ -39,6 +39,11 @@
 // instructions a cycle -- two warps per scheduler waiting on fixed latencies, TMEM and shared memory.  Sixteen warps,
 // loads a tile ahead, coalesced plain stores without the proxy fence, and rolled loops were slower.
 //
+// kGlu with z kept runs as a linear layer of 2N outputs does (4096 x 4096 over 4096: 139 us, 143).  kGluDgrad, 16384 x 8192 over
+// 1024: 228 us without sums (4.9 TB/s; 167 at the copy rate), 288 with them, whose chunks go through registers and whose
+// exchanges take a quarter of the epilogue.  Block scales, e4m3: 4096^3 74 us (unscaled 46), bound by the round trip of a
+// 256-column accumulator: 512 cycles of MMAs, 630 of draining, some 1000 of commits, arrivals and wake-ups.
+//
 // Column sums (kDgrad): the 32 lanes' rows are summed by five exchange steps that halve the columns
 // a lane holds each time, which leaves two finished columns per lane and a fixed order of additions.
 #pragma once
@@ -51,7 +56,7 @@ namespace linear {
 
 constexpr int kForward = 0, kDgrad = 1, kWgrad = 2, kGlu = 3, kGluDgrad = 4;
 constexpr int kOutF16 = 0, kOutBf16 = 1, kOutF32 = 2;
-// Warps 0-3: producer, MMA and two idle ones; warps 4-11: epilogue.  setmaxnreg moves registers
+// Warps 0-3: producer, MMA (SCALED: two of them) and idle ones; warps 4-11: epilogue.  setmaxnreg moves registers
 // between them by warpgroup: the block starts with 384 x 168 = 64512, the first four warps go down
 // to 64, the epilogue's eight up to 216 (128 x 64 + 256 x 216 = 63488).
 constexpr int kTileThreads = 384;
@@ -1011,8 +1016,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             w1 = __ldg(w_at);
             if constexpr (GLU) u1 = __ldg(u_at);
             const uint32_t tacc = tmem_base + lane_off;
-            // A wait that ran out does not leave the loop (the launch is being abandoned, and what is added counts nowhere): with
-            // a second way out the sums were moved to other registers and back in every turn.
+            // A wait that ran out does not leave the loop: the launch is being abandoned, and what is added counts nowhere.
             bool ready = false, ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!__all_sync(0xFFFFFFFFu, ready) && ok) ok = wd.wait(accf_bar(acc), acc_phase, kRoleEpilogue, cur.tile, kb);

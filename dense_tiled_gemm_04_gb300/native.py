@@ -374,6 +374,14 @@ def _padded_output(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Te
     return t if ld == cols else t[:, :cols]
 
 
+def _output(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype, device: int, stream):
+    """An output argument, a new one where it is None, and its leading dimension."""
+    if out is None:
+        out = _new(rows, cols, dtype, device, stream)
+        return out, out.stride(0)
+    return out, _matrix(out, "out", rows, cols, dtype, device)
+
+
 class Gemm:
     """A library handle bound to one CUDA device.
 
@@ -792,9 +800,7 @@ class Gemm:
             ldr, res_p = _matrix(residual, "residual", M, N, out_dtype, dev), residual.data_ptr()
         if preact is not None:
             ldz, z_p = _matrix(preact, "preact", M, N, out_dtype, dev), preact.data_ptr()
-        if out is None:
-            out = _new(M, N, out_dtype, dev, stream)
-        ldy = _matrix(out, "out", M, N, out_dtype, dev)
+        out, ldy = _output(out, M, N, out_dtype, dev, stream)
         a = _pack_linear(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, res_p, z_p, M, N, K, ldx, ldw, ldy, ldr,
                                ldz, in_code, out_code, bias_code, _act(act), alpha)
         st = self._lib.gemm_run_linear_scaled(self._h, a, xs_p, ld_xs, ws_p, ld_ws,
@@ -839,9 +845,7 @@ class Gemm:
             ld_xs, xs_p = _scales(x_scales, "x_scales", M, -(-K // 128), dev), x_scales.data_ptr()
         if w_scales is not None:
             ld_ws, ws_p = _scales(w_scales, "w_scales", 2 * -(-N // 128), -(-K // 128), dev), w_scales.data_ptr()
-        if out is None:
-            out = _new(M, N, out_dtype, dev, stream)
-        ldh = _matrix(out, "out", M, N, out_dtype, dev)
+        out, ldh = _output(out, M, N, out_dtype, dev, stream)
         a = _pack_glu(X.data_ptr(), W.data_ptr(), out.data_ptr(), bias_p, z_p, xs_p, ws_p, M, N, K, ldx, ldw, ldh, ldz, ld_xs,
                             ld_ws, in_code, out_code, bias_code, _act(act), alpha)
         st = self._lib.gemm_run_linear_glu(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
@@ -865,9 +869,7 @@ class Gemm:
         (M, K), N = dY.shape, W.shape[1]
         lddy, ldw = _matrix(dY, "dY", M, K, dt, dev), _matrix(W, "W", K, N, dt, dev)
         ldz = _matrix(Z, "Z", M, 2 * N, dt, dev)
-        if out is None:
-            out = _new(M, 2 * N, dt, dev, stream)
-        lddz = _matrix(out, "out", M, 2 * N, dt, dev)
+        out, lddz = _output(out, M, 2 * N, dt, dev, stream)
         db_p = db_code = ws_p = ws_bytes = 0
         if dbias is not None:
             db_code, db_p = _vector(dbias, "dbias", 2 * N, dt, dev), dbias.data_ptr()
@@ -900,11 +902,12 @@ class Gemm:
         if q_code is None or q_code <= DTYPE_BF16:
             raise TypeError("Q must be float8_e4m3fn or float8_e5m2")
         ldx, rows, cols = _matrix(X, "X", M, K, dt, dev), -(-M // block_rows), -(-K // 128)
-        if out is None:
-            out = _new(M, K, dtype, dev, stream)
+        out, ldq = _output(out, M, K, dtype, dev, stream)
         if scales is None:
             scales = _new(rows, cols, torch.float32, dev, stream)
-        ldq, lds = _matrix(out, "out", M, K, dtype, dev), _scales(scales, "scales", rows, cols, dev)
+            lds = scales.stride(0)
+        else:
+            lds = _scales(scales, "scales", rows, cols, dev)
         a = _pack_quantize(X.data_ptr(), out.data_ptr(), scales.data_ptr(), M, K, ldx, ldq, lds, dt_code, q_code, block_rows)
         st = self._lib.gemm_run_quantize(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
         if st != OK:
@@ -932,9 +935,7 @@ class Gemm:
             mean_p = _stat(mean, "mean", M, dev)
         if rstd is not None:
             rstd_p = _stat(rstd, "rstd", M, dev)
-        if out is None:
-            out = _new(M, N, dt, dev, stream)
-        ldy = _matrix(out, "out", M, N, dt, dev)
+        out, ldy = _output(out, M, N, dt, dev, stream)
         a = _pack_layer_norm(X.data_ptr(), out.data_ptr(), w_p, b_p, mean_p, rstd_p, M, N, ldx, ldy, dt_code, w_code,
                                    b_code, eps)
         st = self._lib.gemm_run_layer_norm(self._h, a, _stream_of(stream, dev) if _ptr is None else _ptr)
@@ -962,9 +963,7 @@ class Gemm:
             w_code, w_p = _vector(weight, "weight", N, dt, dev), weight.data_ptr()
         if residual is not None:
             ldr, res_p = _matrix(residual, "residual", M, N, dt, dev), residual.data_ptr()
-        if out is None:
-            out = _new(M, N, dt, dev, stream)
-        lddx = _matrix(out, "out", M, N, dt, dev)
+        out, lddx = _output(out, M, N, dt, dev, stream)
         if dweight is not None:
             dw_code, dw_p = _vector(dweight, "dweight", N, dt, dev), dweight.data_ptr()
         if dbias is not None:
