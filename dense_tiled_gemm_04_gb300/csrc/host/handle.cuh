@@ -22,7 +22,7 @@ constexpr int kLinearTileKernels = 34, kLinearOperators = 24;
 constexpr int kLinearTileSlots = 3 * kLinearTileKernels;     // tile kernels: operators, types and sums x tiles
 constexpr int kLinearClusterSlots = 4 * kLinearOperators;  // cluster kernels: operators and types x token sizes
 constexpr int kNormSlot0 = kLinearSlot0 + kLinearTileSlots + kLinearClusterSlots;
-constexpr int kNumSlots = kNormSlot0 + 84;   // layer norm, forward and backward (joining or not): types x row lengths x FULL
+constexpr int kNumSlots = kNormSlot0 + 96;   // layer norm, forward and backward (joining or not): types x row lengths x FULL
 constexpr int64_t kMinStreamKBlocks = 8;   // default shortest stream-K share (GEMM_OPT_SK_MIN_BLOCKS)
 constexpr int64_t kMinSplitBlocks = 32;    // default shortest share of a split under one wave (GEMM_OPT_SPLIT_MIN_BLOCKS)
 

@@ -14,8 +14,8 @@
 // A block takes rows b, b + grid, ...; every lane adds its columns' dw and db in registers over all of them, and writes
 // one row of partial sums per block, which column_sum_kernel adds in a fixed order.
 //
-// Measured (one GB300, inputs larger than L2; the copy rate is 6.7 TB/s): forward 16384 x 8192 bf16 94.6 us (5.7 TB/s), from 512 to
-// 16384 columns 5.3 to 6.1 TB/s over 64 M elements; backward 16384 x 4096 with residual 89 us (6.0 TB/s), from 256 to 8192 columns
+// Measured (one GB300, inputs larger than L2; the copy rate is 6.7 TB/s): forward 16384 x 8192 bf16 83 us (6.5 TB/s), from 256 to
+// 16384 columns 5.1 to 6.6 TB/s over 128 M elements; backward 16384 x 4096 with residual 86 us (6.2 TB/s), from 256 to 8192 columns
 // 4.3 to 5.9; longer rows by strips 2.3 (they are read twice); rows under 256 columns leave lanes idle (64 columns: 1.1 and 1.4).
 // Quantization 8192 x 8192 38.4 us (5.2 TB/s): issue and latency, 80 instructions for 8 elements a lane.
 //
@@ -30,6 +30,7 @@ namespace dtg {
 namespace linear {
 
 constexpr int kNormWarps = 16;       // most warps of a block of the forward kernel, one block per SM
+constexpr int kNormMaxStages = 3;    // most rows of a warp whose loads are in flight, forward
 constexpr int kNormGradStages = 2;   // rows whose loads are in flight, backward
 constexpr int kNormGradThreads = 512;  // of an SM, backward: 128 registers each
 constexpr int64_t kNormMaxHeld = 16384, kNormGradMaxHeld = 8192;  // longest rows that are kept in registers
@@ -139,6 +140,18 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// All but the newest n groups, n < kNormMaxStages.
+__device__ __forceinline__ void copies_wait(int n)
+{
+    static_assert(kNormMaxStages == 3, "a case for each");
+    if (n == 0)
+        copies_wait<0>();
+    else if (n == 1)
+        copies_wait<1>();
+    else
+        copies_wait<2>();
+}
+
 template <bool BF16>
 __device__ __forceinline__ void unpack8(f32x2 (&v)[4], uint4 w)
 {
@@ -232,6 +245,7 @@ struct NormParams {
     NormVector w, b;
     int64_t M, N, ldx, ldy;
     float eps;
+    int32_t stages;  // rows of a warp whose loads are in flight
 };
 
 __device__ __forceinline__ void st_shared_pairs(uint32_t addr, f32x2 a, f32x2 b)
@@ -241,8 +255,8 @@ __device__ __forceinline__ void st_shared_pairs(uint32_t addr, f32x2 a, f32x2 b)
 
 // Rows of a block's warps: `groups` of them at once, WARPS warps each.  The weights and biases are in shared memory as fp32: with
 // the ring there L1 has little room, and read through it they came from L2 for every row (16384 x 8192: 161 us).  FULL: rows are a
-// multiple of 256.  Dynamic shared memory: 8 bytes a column (rounded up to 256), then STAGES * CHUNKS * 512 bytes a warp.
-template <bool BF16, int WARPS, int CHUNKS, int STAGES, bool FULL>
+// multiple of 256.  Dynamic shared memory: 8 bytes a column (rounded up to 256), then stages * CHUNKS * 512 bytes a warp.
+template <bool BF16, int WARPS, int CHUNKS, bool FULL>
 __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -267,8 +281,8 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const No
     };
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-#pragma unroll
-    for (int st = 0; st < STAGES; ++st) fetch(st, row + st * step);
+    const int stages = p.stages;
+    for (int st = 0; st < stages; ++st) fetch(st, row + st * step);
     for (int32_t c = 4 * threadIdx.x; c < pitch; c += 4 * blockDim.x) {
         f32x2 w[2], b[2];
         load_vector4<BF16>(w, p.w, c, N, 1.0f);
@@ -280,7 +294,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const No
     const float n = static_cast<float>(N), inv_n = 1.0f / n;
     int stage = 0;
     for (; row < p.M; row += step) {
-        copies_wait<STAGES - 1>();
+        copies_wait(stages - 1);
         __syncwarp();
         f32x2 v[CHUNKS][4];
         f32x2 sum = 0;
@@ -297,8 +311,8 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const No
         }
         const float mean = over(row_sum<WARPS>(sum_of(sum), shared[0], group), n, inv_n);
         // The sum has used what was in the warp's places.
-        fetch(stage, row + STAGES * step);
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        fetch(stage, row + stages * step);
+        stage = stage + 1 == stages ? 0 : stage + 1;
         f32x2 sq = 0;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {

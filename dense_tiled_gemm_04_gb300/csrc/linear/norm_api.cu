@@ -47,14 +47,21 @@ gemm_status_t launch_rows(gemm_handle_t h, void (*fn)(P), int slot, int64_t bloc
 }
 
 // The shapes of the kernels for rows that registers hold, by steps of 256, 512, ... columns: warps and chunks of 8 elements a
-// lane for a row; forward: rows whose loads are in flight; backward: rows a block.  Few warps with many chunks each spend less on
-// the sums across warps and wait less at barriers; the backward kernel's sums of dw and db leave room for two chunks (with four
-// its weights came from L2 for every row: 8192 x 8192 125 us).
+// lane for a row; backward: rows a block.  Few warps with many chunks each spend less on the sums across warps and wait less at
+// barriers; the backward kernel's sums of dw and db leave room for two chunks (with four its weights came from L2 for every row:
+// 8192 x 8192 125 us).  Forward rows that fill eight warps of four chunks take those: 16384 x 8192 83 us, on four of eight 89; but
+// 7168 columns 89 and 84.
 struct NormShape {
-    int warps, chunks, stages;
+    int warps, chunks;
 };
-constexpr int kNormShapes = 7, kNormGradShapes = 6;
-constexpr NormShape kShape[kNormShapes] = {{1, 1, 4}, {1, 2, 4}, {1, 4, 3}, {1, 8, 2}, {2, 8, 2}, {4, 8, 2}, {8, 8, 1}};
+constexpr int kNormShapes = 8, kNormGradShapes = 6;
+constexpr NormShape kShape[kNormShapes] = {{1, 1}, {1, 2}, {1, 4}, {1, 8}, {2, 8}, {4, 8}, {8, 8}, {8, 4}};
+constexpr int kNormFilled = 7;  // its index
+constexpr int kNormSmem = 229376;  // dynamic, beside the row sums
+// Bytes of an SM's rows in flight that are enough: the fewest rows ahead that pass it, up to three.  More only spreads DRAM's
+// reads among its writes (128 M elements in rows of 7168: one row 84 us, two 95; 8192 on eight warps of four chunks: one 98, two
+// 83, four 87; 1000: one 95, two 85).
+constexpr int64_t kNormInFlight = 41500;
 struct NormGradShape {
     int warps, chunks, groups;
     int threads() const { return 32 * warps * groups; }
@@ -71,7 +78,7 @@ int shape_for(int64_t N)
 template <bool BF16, bool FULL, int I>
 constexpr auto norm_fn()
 {
-    return &layer_norm_kernel<BF16, kShape[I].warps, kShape[I].chunks, kShape[I].stages, FULL>;
+    return &layer_norm_kernel<BF16, kShape[I].warps, kShape[I].chunks, FULL>;
 }
 
 template <bool BF16, bool FULL, bool JOIN, int I>
@@ -81,19 +88,22 @@ constexpr auto norm_grad_fn()
 }
 
 template <bool BF16, bool FULL>
-gemm_status_t launch_norm(gemm_handle_t h, const NormParams& p, cudaStream_t s)
+gemm_status_t launch_norm(gemm_handle_t h, const NormParams& q, cudaStream_t s)
 {
     constexpr void (*kFn[kNormShapes])(const NormParams) = {norm_fn<BF16, FULL, 0>(), norm_fn<BF16, FULL, 1>(), norm_fn<BF16, FULL, 2>(),
                                                             norm_fn<BF16, FULL, 3>(), norm_fn<BF16, FULL, 4>(), norm_fn<BF16, FULL, 5>(),
-                                                            norm_fn<BF16, FULL, 6>()};
-    const int i = shape_for(p.N);
+                                                            norm_fn<BF16, FULL, 6>(), norm_fn<BF16, FULL, 7>()};
+    NormParams p = q;
+    const int i = p.N > 7680 && p.N <= 8192 ? kNormFilled : shape_for(p.N);
     const NormShape shape = kShape[i];
     // Few rows are spread over the SMs before a block takes several; eight warps at least bring in weights and biases.
     const int64_t most = kNormWarps / shape.warps, groups = std::min(most, std::max(cdiv(p.M, h->dev.num_sms), int64_t(8) / shape.warps));
     const int64_t blocks = std::min<int64_t>(cdiv(p.M, groups), h->dev.num_sms);
-    const auto smem = [&](int64_t columns, int64_t warps) { return static_cast<int>(8 * columns + 512 * shape.stages * shape.chunks * warps); };
+    const int64_t params = 8 * cdiv(p.N, 256) * 256, row = 512 * shape.chunks * shape.warps * groups;
+    const int64_t wish = kNormInFlight / (most * 2 * p.N) + 1, fit = (kNormSmem - params) / row;
+    p.stages = static_cast<int32_t>(std::min({wish, fit, int64_t(kNormMaxStages)}));
     return launch_rows<NormParams>(h, kFn[i], i + kNormShapes * (2 * FULL + BF16), blocks, static_cast<int>(32 * shape.warps * groups),
-                                   smem(cdiv(p.N, 256) * 256, shape.warps * groups), smem(int64_t(256) << i, kNormWarps), p, s);
+                                   static_cast<int>(params + p.stages * row), kNormSmem, p, s);
 }
 
 template <bool BF16>
