@@ -17,7 +17,7 @@
 // Measured (one GB300, inputs larger than L2; the copy rate is 6.7 TB/s): forward 16384 x 8192 bf16 83 us (6.5 TB/s), from 256 to
 // 16384 columns 5.1 to 6.6 TB/s over 128 M elements; backward 16384 x 4096 with residual 86 us (6.2 TB/s), from 256 to 8192 columns
 // 4.3 to 5.9; longer rows by strips 2.3 (they are read twice); rows under 256 columns leave lanes idle (64 columns: 1.1 and 1.4).
-// Quantization 8192 x 8192 38.4 us (5.2 TB/s): issue and latency, 80 instructions for 8 elements a lane.
+// Quantization 8192 x 8192 33.5 us (6.0 TB/s), in 128 x 128 blocks 37.
 //
 // 8 bits.  For each block of 1 x 128 or 128 x 128 elements: s = max(a / F, 2^-126), a the largest magnitude, F the
 // type's largest number; q = x r rounded to nearest even, r = 1 / s and x r rounded to fp32.  The bound on s keeps r finite.  A
@@ -723,6 +723,9 @@ struct QuantizeParams {
     uint8_t* Q;
     float* S;
     int64_t M, K, ldx, ldq, lds;
+    // quantize_rows_kernel: strips of 256 columns; a block's next box is step_rows rows and step_strips strips on.
+    int64_t step_rows;
+    int32_t strips, step_strips;
 };
 
 constexpr int kScaleCols = 128;
@@ -790,27 +793,44 @@ __device__ __forceinline__ void store_f8x8(uint8_t* row, int64_t c, int64_t n, u
     }
 }
 
-// A scale for every 128 elements of a row: 16 lanes a block, two blocks and kQuantRows rows a warp.
-constexpr int kQuantWarps = 8, kQuantRows = 4;
+// A scale for every 128 elements of a row: 16 lanes a block of them, two such blocks and kQuantRows rows a warp.  As many thread
+// blocks as run at once take boxes of 32 rows by 256 columns in turn, along the rows first, with the next box's loads in flight
+// (8192 x 8192: 33.5 us; a thread block for every box 38.6, for every 16 rows of four warps 37.0).
+constexpr int kQuantWarps = 8, kQuantRows = 4, kQuantBlocks = 4;  // kQuantBlocks: of an SM
 
 template <bool BF16, bool E5M2>
-__global__ void __launch_bounds__(kQuantWarps * 32, 5) quantize_rows_kernel(const QuantizeParams p)
+__global__ void __launch_bounds__(kQuantWarps * 32, kQuantBlocks) quantize_rows_kernel(const QuantizeParams p)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t c = blockIdx.x * int64_t(256) + lane * 8;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    constexpr int64_t kBlockRows = kQuantWarps * kQuantRows;
-    // Blocks of rows beyond the grid's second dimension are taken in turn.
-    for (int64_t r0 = blockIdx.y * kBlockRows; r0 < p.M; r0 += gridDim.y * kBlockRows) {
-        uint4 raw[kQuantRows];
-        uint32_t largest[kQuantRows];
+    uint4 ahead[kQuantRows];
+    auto load = [&](int64_t r0, int64_t c) {
 #pragma unroll
         for (int u = 0; u < kQuantRows; ++u) {
             const int64_t row = r0 + u * kQuantWarps + warp;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (row < p.M) raw[u] = load_row8(p.X + row * p.ldx, c, p.K);
+            ahead[u] = make_uint4(0, 0, 0, 0);
+            if (row < p.M) ahead[u] = load_row8(p.X + row * p.ldx, c, p.K);
         }
+    };
+    // (The grid has no more blocks than there are boxes.)
+    int32_t strip = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(p.strips));
+    int64_t next_r0 = blockIdx.x / static_cast<uint32_t>(p.strips) * int64_t(kQuantWarps * kQuantRows);
+    int64_t next_c = strip * int64_t(256) + lane * 8;
+    load(next_r0, next_c);
+    while (next_r0 < p.M) {
+        const int64_t r0 = next_r0, c = next_c;
+        uint4 raw[kQuantRows];
+        uint32_t largest[kQuantRows];
+#pragma unroll
+        for (int u = 0; u < kQuantRows; ++u) raw[u] = ahead[u];
+        next_r0 += p.step_rows;
+        if ((strip += p.step_strips) >= p.strips) {
+            strip -= p.strips;
+            next_r0 += kQuantWarps * kQuantRows;
+        }
+        next_c = strip * int64_t(256) + lane * 8;
+        load(next_r0, next_c);
 #pragma unroll
         for (int u = 0; u < kQuantRows; ++u) {
             largest[u] = largest8(raw[u]);

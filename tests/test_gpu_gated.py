@@ -411,6 +411,20 @@ def test_quantize(g, M, K, dtype, q, rows):
     same(new_q.float(), want_q.float()), same(new_s, want_s)
 
 
+@pytest.mark.parametrize("M,K", [(1100, 5000), (20000, 264), (9800, 512), (3, 160000), (70, 80001), (2432, 8192)])
+def test_quantize_many_boxes(g, M, K):
+    # More boxes of 32 x 256 than blocks run at once: a block's boxes lie on one strip of columns, or wander over them.
+    r = gen(M + K)
+    X = matrix(r, M, K, BF16)
+    want_q, want_s = gref.quantize(X, 1, E4M3)
+    out, S = Guarded(M, K, E4M3), torch.full((M + 1, want_s.shape[1] + 2), 5.0, device="cuda")
+    g.quantize(X, 1, out=out.t, scales=S[:M, :want_s.shape[1]])
+    same(S[:M, :want_s.shape[1]], want_s, "scales")
+    same(out.t.float(), want_q.float(), "values")
+    out.check()
+    assert bool((S[-1] == 5).all()) and bool((S[:, -2:] == 5).all())
+
+
 @pytest.mark.parametrize("rows", [1, 128])
 @pytest.mark.parametrize("q", [E4M3, E5M2])
 def test_quantize_special_values(g, rows, q):
@@ -459,6 +473,21 @@ def test_layer_norm(g, M, N, dtype):
     g.layer_norm(buf.t, w, b, eps=1e-3, out=buf.t)
     same(buf.t, g.layer_norm(X, w, b, eps=1e-3), "in place")
     buf.check()
+
+
+@pytest.mark.parametrize("M,N", [(1300, 7936), (611, 8000), (9800, 200), (5000, 768), (2600, 1024), (650, 5120), (611, 10240),
+                                 (460, 12296)])
+def test_layer_norm_rows_ahead(g, M, N):
+    # Every warp takes several rows, one to three of them in flight.
+    r = gen(M + N)
+    X, w, b = matrix(r, M, N, BF16), vector(r, N, F32), vector(r, N, F32)
+    Y = Guarded(M, N, BF16)
+    g.layer_norm(X, w, b, eps=1e-3, out=Y.t)
+    gref.assert_within(Y.t, gref.layer_norm(X, w, b, 1e-3, BF16)[0], "Y")
+    Y.check()
+    buf = Guarded(M, N, BF16, init=X)
+    g.layer_norm(buf.t, w, b, eps=1e-3, out=buf.t)
+    same(buf.t, Y.t, "in place")
 
 
 def test_layer_norm_of_a_large_mean(g):
