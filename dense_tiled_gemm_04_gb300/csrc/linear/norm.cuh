@@ -427,7 +427,7 @@ struct NormGradParams {
 
 // GROUPS rows of a block at once, WARPS warps each, whose sums are joined in shared memory at the end.  Dynamic shared memory:
 // kNormGradStages * 3 * CHUNKS * 512 bytes a warp, for dy, x and the residual.  With e = x - mean the row's sums are those of g
-// and g e, and dx = rstd g - rstd mean(g) - e rstd^2 mean(g e).
+// and g e, and dx = rstd (g - mean(g) - e rstd^2 mean(g e)).
 // JOIN: see NormGradParams (an instantiation of its own: with the joining's registers 16384 x 4096 took 94 us, without 89).
 template <bool BF16, int WARPS, int CHUNKS, int GROUPS, bool FULL, bool JOIN>
 __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS * GROUPS * 32))
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
 #pragma unroll
         for (int q = 0; q < 2; ++q) load_vector4<BF16>(&w[k][2 * q], p.w, first(k) + 128 * q + 4 * lane, N, 1.0f);
     f32x2 dw[CHUNKS][4] = {}, db[CHUNKS][4] = {};
-    const float inv_n = 1.0f / static_cast<float>(N);
+    const float n = static_cast<float>(N), inv_n = 1.0f / n;
     int stage = 0;
     auto take = [&](f32x2 (&v)[4], int which, int k) {
 #pragma unroll
@@ -511,7 +511,9 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
             }
         }
         const float2 c = row_sums<WARPS, GROUPS == 1>(make_float2(sum_of(s1), sum_of(s2)), shared[stage], group);
-        const f32x2 c1 = both(-rstd * (c.x * inv_n)), c2 = both(-rstd * (rstd * (rstd * (c.y * inv_n))));
+        // g - mean(g) first, g rounded as for the mean (a mere product would be contracted with the subtraction): a row of one
+        // column leaves exactly the residual.
+        const f32x2 c1 = both(-over(c.x, n, inv_n)), c2 = both(-rstd * (rstd * over(c.y, n, inv_n)));
         uint16_t* const dx = p.dX + row * p.lddx;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
@@ -520,11 +522,14 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
             take(d, 0, k);
             take(e, 1, k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = fma2(add2(e[i], both(-mean)), c2, fma2(mul2(d[i], w[k][i]), both(rstd), c1));
+            for (int i = 0; i < 4; ++i) d[i] = fma2(add2(e[i], both(-mean)), c2, add2(fma2(d[i], w[k][i], both(0.0f)), c1));
             if (has_res) {
                 take(e, 2, k);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = add2(d[i], e[i]);
+                for (int i = 0; i < 4; ++i) d[i] = fma2(d[i], both(rstd), e[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], both(rstd));
             }
             store_row4<FULL>(dx, first(k) + 4 * lane, N, round2<BF16>(d[0]), round2<BF16>(d[1]));
             store_row4<FULL>(dx, first(k) + 128 + 4 * lane, N, round2<BF16>(d[2]), round2<BF16>(d[3]));

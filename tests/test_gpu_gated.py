@@ -573,6 +573,18 @@ def test_layer_norm_grad_against_differences(g):
             assert abs(terms.sum().item() - want) <= 2.0 ** -11 * terms.abs().sum().item() + 1e-4, i
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_layer_norm_grad_of_one_column(g, dtype):
+    # The norm of one column is its bias, whatever X: nothing but the residual reaches dX, however large rstd is.
+    r = gen(5)
+    dY, X, res, w = matrix(r, 50, 1, dtype), matrix(r, 50, 1, dtype), matrix(r, 50, 1, dtype), vector(r, 1, F32)
+    mean, rstd = torch.empty(50, device="cuda"), torch.empty(50, device="cuda")
+    g.layer_norm(X, w, eps=1e-5, mean=mean, rstd=rstd)
+    assert bool((rstd > 300).all())
+    same(g.layer_norm_grad(dY, X, mean, rstd, w, residual=res), res)
+    assert bool((g.layer_norm_grad(dY, X, mean, rstd, w) == 0).all())
+
+
 def test_layer_norm_grad_no_rows(g):
     dw, db = torch.ones(24, device="cuda"), torch.full((24,), 2.0, device="cuda")
     none = torch.zeros((0, 24), dtype=F16, device="cuda")
