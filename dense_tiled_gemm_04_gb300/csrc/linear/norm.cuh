@@ -231,11 +231,11 @@ __device__ __forceinline__ float2 row_sums(float2 v, float2* shared, int group)
 }
 
 // s / n, corrected by what the product with 1 / n leaves: a quotient that fp32 holds comes out exact, so a row of one value
-// has that mean, and no variance.
+// has that mean, and no variance.  (An infinite quotient leaves inf - inf, NaN: it stands as it is.)
 __device__ __forceinline__ float over(float s, float n, float inv_n)
 {
     const float q = s * inv_n;
-    return fmaf(fmaf(-q, n, s), inv_n, q);
+    return isinf(q) ? q : fmaf(fmaf(-q, n, s), inv_n, q);
 }
 
 struct NormParams {
@@ -427,7 +427,8 @@ struct NormGradParams {
 
 // GROUPS rows of a block at once, WARPS warps each, whose sums are joined in shared memory at the end.  Dynamic shared memory:
 // kNormGradStages * 3 * CHUNKS * 512 bytes a warp, for dy, x and the residual.  With e = x - mean the row's sums are those of g
-// and g e, and dx = rstd (g - mean(g) - e rstd^2 mean(g e)).
+// and (g rstd) e, and dx = rstd (g - mean(g) - e rstd mean(g rstd e)).  (Sums of g e leave fp32's range where rstd is 0; past a row's
+// end, where g is 0, e rstd may.)
 // JOIN: see NormGradParams (an instantiation of its own: with the joining's registers 16384 x 4096 took 94 us, without 89).
 template <bool BF16, int WARPS, int CHUNKS, int GROUPS, bool FULL, bool JOIN>
 __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS * GROUPS * 32))
@@ -507,13 +508,13 @@ __global__ void __launch_bounds__(WARPS * GROUPS * 32, kNormGradThreads / (WARPS
                 db[k][i] = add2(db[k][i], dy[i]);
                 const f32x2 g = mul2(dy[i], w[k][i]);
                 s1 = add2(s1, g);
-                s2 = fma2(g, e[i], s2);
+                s2 = fma2(mul2(g, both(rstd)), e[i], s2);
             }
         }
         const float2 c = row_sums<WARPS, GROUPS == 1>(make_float2(sum_of(s1), sum_of(s2)), shared[stage], group);
         // g - mean(g) first, g rounded as for the mean (a mere product would be contracted with the subtraction): a row of one
         // column leaves exactly the residual.
-        const f32x2 c1 = both(-over(c.x, n, inv_n)), c2 = both(-rstd * (rstd * over(c.y, n, inv_n)));
+        const f32x2 c1 = both(-over(c.x, n, inv_n)), c2 = both(-rstd * over(c.y, n, inv_n));
         uint16_t* const dx = p.dX + row * p.lddx;
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {

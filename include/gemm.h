@@ -589,7 +589,8 @@ typedef struct {
 gemm_status_t gemm_run_quantize(gemm_handle_t h, const gemm_quantize_args_t* args, void* stream);
 
 /* Layer norm over each row: Y = (X - mean) rstd weight + bias, mean the row's mean, rstd = 1 / sqrt(v + eps), v the mean of
- * (X - mean)^2; statistics in fp32.
+ * (X - mean)^2; statistics in fp32.  Where the sum behind the mean or v is over fp32's range, that is infinite: an infinite v gives
+ * an rstd of 0, so Y is the bias (and, backward, X^ is 0); an infinite mean gives NaN, as a row with an infinity or a NaN does.
  *   - X, Y: M x N of type dtype (F16 or BF16); Y may be X itself (same pointer and pitch).
  *   - weight, bias: N values of their dtype (F32, or dtype), or NULL (1, 0).  mean, rstd: M fp32 values each, or NULL:
  *     receive the statistics, which a backward pass reads.  eps: finite, >= 0.

@@ -512,6 +512,23 @@ def test_layer_norm_special_rows(g):
         same(Y[4], b.half())
 
 
+@pytest.mark.parametrize("N", [8, 200, 1024, 3000, 8192, 9000, 20000])
+def test_layer_norm_beyond_the_range_of_its_sums(g, N):
+    # Finite values whose squares' sum is over fp32's range: v is infinite, so rstd is 0 and Y the bias; a sum that is infinite
+    # is the mean.  The rows beside them keep their values.
+    r = gen(8)
+    X, b = matrix(r, 5, N, BF16), vector(r, N, F32)
+    want = g.layer_norm(X, None, b)
+    X[1] *= 1e25
+    X[3, N // 2] = float("-inf")
+    mean, rstd = torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    Y = g.layer_norm(X, None, b, mean=mean, rstd=rstd)
+    same(Y[1], b.to(BF16))
+    assert rstd[1].item() == 0 and bool(mean[1].isfinite())
+    assert mean[3].item() == float("-inf") and bool(Y[3].isnan().all()) and bool(rstd[3].isnan())
+    same(Y[[0, 2, 4]], want[[0, 2, 4]])
+
+
 @pytest.mark.parametrize("M,N", NORMS + [(700, 200), (2500, 72)])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_layer_norm_grad(g, M, N, dtype):
@@ -546,6 +563,40 @@ def test_layer_norm_grad(g, M, N, dtype):
         g.layer_norm_grad(buf.t if source == "dY" else dY, X, mean, rstd, w, residual=res if source == "dY" else buf.t, out=buf.t)
         same(buf.t, g.layer_norm_grad(dY, X, mean, rstd, w, residual=res), "in place of " + source)
         buf.check()
+
+
+@pytest.mark.parametrize("M,N", [(6, 64), (700, 500), (400, 3000), (320, 8192), (9, 9000)])
+def test_layer_norm_grad_special_rows(g, M, N):
+    # A NaN or infinity of X or dY reaches its own row of dX alone (and the sums of its columns); where rstd is 0, since the
+    # squares' sum was over fp32's range, x^ is 0: dX is the residual, and nothing comes to dw.
+    r = gen(9)
+    dY, X, res, w = matrix(r, M, N, BF16), matrix(r, M, N, BF16), matrix(r, M, N, BF16), vector(r, N, F32)
+    stats = torch.empty((2, M), device="cuda")
+
+    def grad(dY, X):
+        g.layer_norm(X, mean=stats[0], rstd=stats[1])
+        dw, db = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+        return g.layer_norm_grad(dY, X, stats[0], stats[1], w, residual=res, dweight=dw, dbias=db), dw, db
+
+    want, _, db = grad(dY, X)
+    huge = Guarded(M, N, BF16, init=X).t
+    huge[2] = torch.where(torch.arange(N, device="cuda") % 4 < 2, 2e38, -2e38).to(BF16)  # (its sum stays in range)
+    zeroed = Guarded(M, N, BF16, init=dY).t
+    zeroed[2] = 0
+    dX, dw, db_huge = grad(dY, huge)
+    assert stats[1, 2].item() == 0
+    same(dX[2], res[2], "rstd of 0")
+    same(db_huge, db, "db")
+    others = torch.arange(M, device="cuda") != 2
+    same(dX[others], want[others], "beside it")
+    same(dw, grad(zeroed, X)[1], "dw without the row")
+    X[1, 3], X[4, N - 1], dY[3, N // 2] = float("nan"), float("inf"), float("inf")
+    dX, _, db = grad(dY, X)
+    others[[1, 3, 4]] = False
+    others[2] = True
+    same(dX[others], want[others], "beside NaN and infinities")
+    assert bool(dX[[1, 4]].isnan().all()) and bool((~dX[3].isfinite()).any())
+    assert db[N // 2].item() == float("inf") and bool(db[torch.arange(N, device="cuda") != N // 2].isfinite().all())
 
 
 def test_layer_norm_grad_against_differences(g):
