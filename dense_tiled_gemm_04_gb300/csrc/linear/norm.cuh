@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(kMeansWarps * 32, 4) layer_norm_grad_means_ker
             for (int i = 0; i < 4; ++i) {
                 g[i] = mul2(g[i], w[i]);
                 s1 = add2(s1, g[i]);
-                s2 = fma2(g[i], mul2(add2(h[i], both(-mean)), both(rstd)), s2);
+                // (Past the row's end g is 0, and (x - mean) rstd may be infinite.)
+                s2 = fma2(mul2(g[i], both(rstd)), add2(h[i], both(-mean)), s2);
             }
         }
     }

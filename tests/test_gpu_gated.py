@@ -599,6 +599,22 @@ def test_layer_norm_grad_special_rows(g, M, N):
     assert db[N // 2].item() == float("inf") and bool(db[torch.arange(N, device="cuda") != N // 2].isfinite().all())
 
 
+@pytest.mark.parametrize("N", [100, 500, 3001, 9001])
+def test_layer_norm_grad_of_a_constant_row_far_from_zero(g, N):
+    # X - mean is 0; past a ragged row's end it is -mean, and that times rstd is over fp32's range: it must not count.
+    r = gen(10)
+    dY, X, w = matrix(r, 5, N, BF16), matrix(r, 5, N, BF16), vector(r, N, F32)
+    X[1] = 3e34
+    mean, rstd = torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    g.layer_norm(X, eps=1e-12, mean=mean, rstd=rstd)
+    same(mean[1].double(), X[1, 0].double())
+    assert (mean[1] * rstd[1]).item() == float("inf")
+    dw, db = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    dX = g.layer_norm_grad(dY, X, mean, rstd, w, dweight=dw, dbias=db)
+    x, a, b = gref.layer_norm_grad(dY, X, mean, rstd, w, None, BF16, (F32, F32))
+    gref.assert_within(dX, x, "dX"), gref.assert_within(dw, a, "dw"), gref.assert_within(db, b, "db")
+
+
 def test_layer_norm_grad_against_differences(g):
     # L = sum(C * norm(x) w + b) along a direction of x, w and b, by central differences in fp64; dX is rounded to fp16
     # (2^-11 of each term), the differences are off by h^2 times third derivatives (under 100 in sum here).
