@@ -178,6 +178,15 @@ __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// A load through the coherent path.  The stream's previous kernel may write what is read while this one has started and waits for
+// it, so the path for memory that is constant over a kernel's life (__ldg) is not open.
+__device__ __forceinline__ float ld_global_f32(const float* at)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at));
+    return v;
+}
+
 // The two 16-bit floats of a word, in fp32.
 template <bool BF16>
 __device__ __forceinline__ f32x2 unpack2(uint32_t w)
@@ -372,8 +381,6 @@ __device__ __forceinline__ void tile_coord32(uint32_t t, const KernelParams& p, 
     tn = r / rows;
     tm = first_m + (r - tn * rows);
 }
-
-__device__ const float kUnitScale = 1.0f;
 
 // IN: operand type (Operand<IN>: 0 fp16, 1 bf16, 2 E4M3, 3 E5M2); OUT: kOut*; MODE: kForward ... kGluDgrad;
 // SUMS: the contraction runs in chunks that are summed in registers; CLUSTER: 1 (one CTA) or 2 (a CTA pair); SCALED:
@@ -1000,28 +1007,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // SCALED: adds the item's K blocks, each times its scales, to s.  A chunk is one block, 256 cycles of MMAs, so everything
         // around the loads and sums counts: the barrier of the next block is asked for, and its factors are made, among the sums
         // of this one; scales are loaded two blocks ahead; the arrival is predicated, not branched to.
-        // Absent scales, and those of rows and columns past the edges, are a 1 that is read at every block.
+        // Absent scales, and those of rows and columns past the edges, are a 1 that is not read.
         auto add_scaled = [&](float* s, int kb0, int kb1) -> bool {
             const int64_t row = static_cast<int64_t>(cur.y) + lane;
             const bool has_x = p.x_scales && row < p.M, has_w = p.w_scales && cur.x < p.N;
-            const int first = cur.rev ? kb1 - 1 : kb0, x_step = has_x ? (cur.rev ? -1 : 1) : 0, w_step = has_w ? (cur.rev ? -1 : 1) : 0;
+            const int first = cur.rev ? kb1 - 1 : kb0, step = cur.rev ? -1 : 1;
             // (The warp's columns lie inside one block of 128 of the weights' rows; gated: of Wg's and of Wu's.)
-            const float* x_at = has_x ? p.x_scales + row * p.ld_xs + first : &kUnitScale;
-            const float* w_at = has_w ? p.w_scales + (cur.x >> 7) * p.ld_ws + first : &kUnitScale;
-            const float* u_at = GLU && has_w ? w_at + p.up_scales : &kUnitScale;
-            float x1 = __ldg(x_at), w1 = __ldg(w_at), u1 = GLU ? __ldg(u_at) : 1.0f;  // of the next block
+            const float* x_at = p.x_scales + row * p.ld_xs + first;
+            const float* w_at = p.w_scales + (cur.x >> 7) * p.ld_ws + first;
+            float x1 = 1.0f, w1 = 1.0f, u1 = 1.0f;  // of the next block
+            auto load = [&]() {
+                if (has_x) x1 = ld_global_f32(x_at);
+                if (has_w) {
+                    w1 = ld_global_f32(w_at);
+                    if constexpr (GLU) u1 = ld_global_f32(w_at + p.up_scales);
+                }
+                __syncwarp();  // (has_x differs where the warp's rows end)
+            };
+            load();
             float fg = x1 * w1, fu = x1 * u1;
             auto advance = [&](bool more) {
                 if (more) {
-                    x_at += x_step;
-                    w_at += w_step;
-                    if constexpr (GLU) u_at += w_step;
+                    x_at += step;
+                    w_at += step;
                 }
             };
             advance(kb0 + 1 < kb1);
-            x1 = __ldg(x_at);
-            w1 = __ldg(w_at);
-            if constexpr (GLU) u1 = __ldg(u_at);
+            load();
             const uint32_t tacc = tmem_base + lane_off;
             // A wait that ran out does not leave the loop: the launch is being abandoned, and what is added counts nowhere.
             bool ready = false, ok = true;
@@ -1041,9 +1053,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         next_fg = x1 * w1;
                         if constexpr (GLU) next_fu = x1 * u1;
                         advance(kb + 2 < kb1);
-                        x1 = __ldg(x_at);
-                        w1 = __ldg(w_at);
-                        if constexpr (GLU) u1 = __ldg(u_at);
+                        load();
                     }
                     if (q == CW / 32 - 1) {
                         ptx::tc_fence_before_sync();
