@@ -565,6 +565,34 @@ def test_layer_norm_grad(g, M, N, dtype):
         buf.check()
 
 
+# Lengths of every shape of the kernel, ragged and full, with rows enough that a group of warps takes four or more (on 152 SMs), and
+# not the same number in every group.
+GRAD_LOOPS = [(9800, 200), (9900, 256), (9801, 500), (9901, 512), (5003, 1000), (5001, 1024), (2605, 2000), (2603, 2048), (1301, 3000),
+              (1303, 4096), (801, 5000), (803, 8192)]
+
+
+@pytest.mark.parametrize("M,N", GRAD_LOOPS)
+def test_layer_norm_grad_rows_ahead(g, M, N):
+    # The places of the rows in flight are filled again and again, their statistics fetched a row ahead.
+    r = gen(M + N)
+    for dtype, with_res in ((BF16, True), (F16, False)):
+        X = matrix(r, M, N, dtype, scale=2.0)
+        X += torch.randn((M, 1), generator=r, device="cuda").to(dtype)
+        mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        g.layer_norm(X, eps=1e-2, mean=mean, rstd=rstd)
+        dY, w, res = matrix(r, M, N, dtype), vector(r, N, F32), matrix(r, M, N, dtype, pad=2) if with_res else None
+        dX, dw, db = Guarded(M, N, dtype), Guarded(1, N, F32), Guarded(1, N, F32)
+        g.layer_norm_grad(dY, X, mean, rstd, w, residual=res, out=dX.t, dweight=dw.t[0], dbias=db.t[0])
+        x, a, b = gref.layer_norm_grad(dY, X, mean, rstd, w, res, dtype, (F32, F32))
+        gref.assert_within(dX.t, x, "dX"), gref.assert_within(dw.t[0], a, "dw"), gref.assert_within(db.t[0], b, "db")
+        dX.check(), dw.check(), db.check()
+        for source in ("dY", "residual") if with_res else ("dY",):
+            buf = Guarded(M, N, dtype, init=dY if source == "dY" else res)
+            g.layer_norm_grad(buf.t if source == "dY" else dY, X, mean, rstd, w, residual=res if source == "dY" else buf.t, out=buf.t)
+            same(buf.t, dX.t, "in place of " + source)
+            buf.check()
+
+
 @pytest.mark.parametrize("M,N", [(6, 64), (700, 500), (400, 3000), (320, 8192), (9, 9000)])
 def test_layer_norm_grad_special_rows(g, M, N):
     # A NaN or infinity of X or dY reaches its own row of dX alone (and the sums of its columns); where rstd is 0, since the
