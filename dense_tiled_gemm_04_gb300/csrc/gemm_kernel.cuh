@@ -376,7 +376,8 @@ struct Watchdog {
                                          int kb) const
     {
         if (ptx::mbar_try_wait(bar, parity)) return true;
-        // A first sleep before the clock is read: reading it takes longer than most waits.
+        // A first sleep before the clock is read: reading it takes longer than most waits (block-scaled 4096^3 74.8 us, 76.3 without;
+        // 8192^3 bf16, ragged and one-token calls the same either way).
         if (ptx::mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
         const uint64_t t0 = ptx::globaltimer_ns();
         for (;;) {

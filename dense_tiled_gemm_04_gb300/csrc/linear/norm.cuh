@@ -1,9 +1,9 @@
-// Layer norm, forward and backward, and the rounding of matrices to 8 bits with block scales.  All are bound by memory: every
-// kernel reads its inputs once, keeps them in registers, and writes its outputs once.
+// Layer norm, forward and backward, and the rounding of matrices to 8 bits with block scales.  All are bound by memory: the
+// kernels read their inputs once, keep them in registers, and write their outputs once, but for the layer norm of rows longer than
+// registers hold (over 16384 columns forward, 8192 backward), which are read three times, and twice.
 //
 // Layer norm.  A row belongs to WARPS warps, CHUNKS times 8 elements (16 bytes) a lane, so statistics are taken in two passes
-// over registers: the mean, then the mean square of x - mean, without the cancellation of E[x^2] - mean^2.  Rows of more
-// elements than registers hold are read again for every pass.
+// over registers: the mean, then the mean square of x - mean, without the cancellation of E[x^2] - mean^2.
 //   A block takes rows b, b + grid, ... and keeps the loads of the next ones in flight: every warp copies its own chunks of
 // the rows ahead into its own places of a ring in shared memory (cp.async, 16 bytes a lane), which it alone reads, so the ring
 // needs no barrier.  Of a warp's 256 columns lane l works on 4 l ... 4 l + 3 and 128 + 4 l ...: fp32 weights then are 16 bytes a
@@ -14,10 +14,12 @@
 // A block takes rows b, b + grid, ...; every lane adds its columns' dw and db in registers over all of them, and writes
 // one row of partial sums per block, which column_sum_kernel adds in a fixed order.
 //
-// Measured (one GB300, inputs larger than L2; the copy rate is 6.7 TB/s): forward 16384 x 8192 bf16 83 us (6.5 TB/s), from 256 to
-// 16384 columns 5.1 to 6.6 TB/s over 128 M elements; backward 16384 x 4096 with residual 86 us (6.2 TB/s), from 256 to 8192 columns
-// 4.3 to 5.9; longer rows by strips 2.3 (they are read twice); rows under 256 columns leave lanes idle (64 columns: 1.1 and 1.4).
-// Quantization 8192 x 8192 33.5 us (6.0 TB/s), in 128 x 128 blocks 37.
+// Measured (one GB300, inputs larger than L2; the copy rate is 6.7 TB/s; bytes counted once each), over 64 to 128 M elements: forward
+// 16384 x 8192 bf16 83 us (6.5 TB/s), from 256 to 16384 columns 5.1 to 6.5 TB/s, longer rows 2.5 to 2.7 (20480, 65536 columns);
+// backward 16384 x 4096 with residual 85 us (6.3 TB/s), from 256 to 8192 columns with residual 5.8 to 6.8, longer rows 3.3 with and 2.3
+// to 2.7 without; rows under 256 columns leave lanes idle: 128 columns 2.2 forward and 2.8 backward without residual, 64 1.1 and
+// 1.4.  Quantization 8192 x 8192 33.4 us (6.0 TB/s), in 128 x 128 blocks 37.8; where the last strip of 256 columns is thin, 100000 x
+// 520 44 us (3.5) and 260000 x 200 49 us (3.2).
 //
 // 8 bits.  For each block of 1 x 128 or 128 x 128 elements: s = max(a / F, 2^-126), a the largest magnitude, F the
 // type's largest number; q = x r rounded to nearest even, r = 1 / s and x r rounded to fp32.  The bound on s keeps r finite.  A
@@ -254,8 +256,8 @@ __device__ __forceinline__ void st_shared_pairs(uint32_t addr, f32x2 a, f32x2 b)
 }
 
 // Rows of a block's warps: `groups` of them at once, WARPS warps each.  The weights and biases are in shared memory as fp32: with
-// the ring there L1 has little room, and read through it they came from L2 for every row (16384 x 8192: 161 us).  FULL: rows are a
-// multiple of 256.  Dynamic shared memory: 8 bytes a column (rounded up to 256), then stages * CHUNKS * 512 bytes a warp.
+// the ring there L1 has little room, and read through it they came from L2 for every row.  FULL: rows are a multiple of 256.
+// Dynamic shared memory: 8 bytes a column (rounded up to 256), then stages * CHUNKS * 512 bytes a warp.
 template <bool BF16, int WARPS, int CHUNKS, bool FULL>
 __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_kernel(const NormParams p)
 {

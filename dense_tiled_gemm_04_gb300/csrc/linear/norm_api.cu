@@ -50,7 +50,7 @@ gemm_status_t launch_rows(gemm_handle_t h, void (*fn)(P), int slot, int64_t bloc
 // lane for a row; backward: rows a block.  Few warps with many chunks each spend less on the sums across warps and wait less at
 // barriers; the backward kernel's sums of dw and db leave room for two chunks (with four its weights came from L2 for every row:
 // 8192 x 8192 125 us).  Forward rows that fill eight warps of four chunks take those: 16384 x 8192 83 us, on four of eight 89; but
-// 7168 columns 89 and 84.
+// 7168 columns 89 and 84, and what lies between is not measured; nor are eight warps of fewer chunks for shorter rows.
 struct NormShape {
     int warps, chunks;
 };
@@ -58,9 +58,10 @@ constexpr int kNormShapes = 8, kNormGradShapes = 6;
 constexpr NormShape kShape[kNormShapes] = {{1, 1}, {1, 2}, {1, 4}, {1, 8}, {2, 8}, {4, 8}, {8, 8}, {8, 4}};
 constexpr int kNormFilled = 7;  // its index
 constexpr int kNormSmem = 229376;  // dynamic, beside the row sums
-// Bytes of an SM's rows in flight that are enough: the fewest rows ahead that pass it, up to three.  More only spreads DRAM's
-// reads among its writes (128 M elements in rows of 7168: one row 84 us, two 95; 8192 on eight warps of four chunks: one 98, two
-// 83, four 87; 1000: one 95, two 85).
+// Bytes of an SM's rows in flight that are enough: the fewest rows ahead that pass it, up to three, of a block with as many groups
+// of warps as one can have (few rows have fewer, and are done before it matters).  More only spreads DRAM's reads among its
+// writes (128 M elements in rows of 7168: one row 84 us, two 95; 8192 on eight warps of four chunks: one 98, two 83, four 87;
+// 1000: one 95, two 85: any bound from 32769 to 57343 chooses the better of each).
 constexpr int64_t kNormInFlight = 41500;
 struct NormGradShape {
     int warps, chunks, groups;
@@ -130,7 +131,8 @@ gemm_status_t launch_norm_grad(gemm_handle_t h, const NormGradParams& q, int64_t
     const int i = shape_for(q.N);
     const NormGradShape shape = kGradShape[i];
     *blocks = std::min({cdiv(q.M, shape.groups), norm_grad_max_blocks(q.M, q.N), int64_t(h->dev.num_sms) * (kNormGradThreads / shape.threads())});
-    // Up to 32 blocks the last one adds their sums (65 x 1000 fp16: 10.2 us with a second launch, whose host part it saves).
+    // Up to 32 blocks the last one adds their sums (65 x 1000 fp16, 17 blocks: 8.7 us, 10.2 with a second launch, whose host part it
+    // saves).  What that block reads grows with the row's length too, to 2 MB at 32 x 8192; those sizes are not measured.
     NormGradParams p = q;
     if (*blocks <= 32 && (p.dw || p.db)) {
         p.arrived = h->ws.counters + h->ws.counter_count;  // its own

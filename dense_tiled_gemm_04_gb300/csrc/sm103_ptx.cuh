@@ -329,8 +329,9 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrive once on an mbarrier that may live in another CTA of the cluster.
-// The same, predicated; also on a barrier of this CTA (a shared::cta address is one of shared::cluster).
+// Relaxed arrivals, on an mbarrier that may live in another CTA of the cluster (or in this one: a shared::cta address is one of
+// shared::cluster).  They hand over no memory: they only free TMEM that the warp has read, after tcgen05.wait::ld and the fence before
+// thread synchronisation.  This one is predicated.
 __device__ __forceinline__ void mbar_arrive_relaxed_if(uint32_t cluster_addr, bool yes)
 {
     asm volatile(
@@ -346,6 +347,7 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Arrive once on an mbarrier that may live in another CTA of the cluster, releasing what this thread has written to memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");

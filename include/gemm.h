@@ -378,8 +378,8 @@ gemm_status_t gemm_run_noalloc(const void* A, const void* B, void* C,
  * Sums run in fp32, in an order that depends on the sizes and the handle's options alone, so a
  * call's results do not change from one call to the next.  The tensor core truncates as it adds: a
  * chain of n 16-bit products is short by about 1.2e-9 n of its value.  Chains end after 768 products
- * where a result or a column sum is fp32, after 8192 (8-bit operands: 16384) where it is rounded
- * to 16 bits; longer contractions add chains in fp32, rounding to nearest.  Every matrix is row-major, with the
+ * where a result or a column sum is fp32, after 8192 (8-bit operands: 16384; with block scales, and in gated layers: 128) where
+ * it is rounded to 16 bits; longer contractions add chains in fp32, rounding to nearest.  Every matrix is row-major, with the
  * alignment rules of gemm_run (bases of 16 bytes; row pitches that are multiples of 16 bytes);
  * bias and dbias are dense vectors of any alignment their type allows; a dimension over
  * 2^31 - 512 is UNSUPPORTED.  An output may not
@@ -511,7 +511,8 @@ int64_t gemm_bias_grad_workspace_bytes(int64_t M, int64_t cols);
  *     row start on 16 bytes.
  *   - dtype, out_dtype, alpha, K == 0, empty M and N: as for gemm_run_linear.
  *   - x_scales, w_scales: 8-bit operands only, as for gemm_run_linear_scaled; w_scales has 2 ceil(N / 128) rows, first
- *     those of Wg's blocks, then those of Wu's (each half's blocks start with its own row 0). */
+ *     those of Wg's blocks, then those of Wu's (each half's blocks start with its own row 0).  8-bit operands without scales
+ *     take the same kernels, with scales of 1, at nearly the same time. */
 typedef struct {
     const void* X;
     const void* W;
@@ -562,7 +563,8 @@ gemm_status_t gemm_run_linear_glu_dgrad(gemm_handle_t h, const gemm_glu_dgrad_ar
  *   - dtype: E4M3 or E5M2; the rest of args as for gemm_run_linear.
  *   - x_scales: fp32, row m at x_scales + m * ld_xs; w_scales: fp32, row i (of the weights' rows [128 i, 128 i + 128)) at
  *     w_scales + i * ld_ws; pitches of at least ceil(K / 128).  Either may be NULL: its scales are 1.
- * Each block's product is summed on the tensor cores, scaled in fp32 and added to an fp32 sum with one rounding. */
+ * Each block's product is summed on the tensor cores, multiplied by xs ws (rounded to fp32, so within fp32's range) and added to an
+ * fp32 sum with one rounding. */
 gemm_status_t gemm_run_linear_scaled(gemm_handle_t h, const gemm_linear_args_t* args, const float* x_scales, int64_t ld_xs,
                                      const float* w_scales, int64_t ld_ws, void* stream);
 
