@@ -39,8 +39,8 @@
 // instructions a cycle -- two warps per scheduler waiting on fixed latencies, TMEM and shared memory.  Sixteen warps,
 // loads a tile ahead, coalesced plain stores without the proxy fence, and rolled loops were slower.
 //
-// kGlu with z kept runs as a linear layer of 2N outputs does (4096 x 4096 over 4096: 139 us, 143; without z 142).  kGluDgrad, 16384 x 8192 over
-// 1024: 228 us without sums (4.9 TB/s; 167 at the copy rate), 288 with them, whose chunks go through registers and whose
+// kGlu with z kept runs as a linear layer of 2N outputs does (4096 x 4096 over 4096: 139 us, 143; without z 142).  kGluDgrad,
+// 16384 x 8192 over 1024: 228 us without sums (4.9 TB/s; 167 at the copy rate), 288 with them, whose chunks go through registers and whose
 // exchanges take a quarter of the epilogue.  Block scales, e4m3: 4096^3 75 us (unscaled 46), bound by the round trip of a
 // 256-column accumulator: 512 cycles of MMAs, 630 of draining, some 1000 of commits, arrivals and wake-ups.  Gated with block scales
 // 4096 x 4096 over 4096 125 us, back to back 143, likewise (a linear layer of 2N outputs without scales 82).
@@ -1005,8 +1005,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if constexpr (GLU) return static_cast<uint32_t>((q * 32 / kWarpN) * kTileN + half * kWarpN + q * 32 % kWarpN);
             return static_cast<uint32_t>(half * CW + q * 32);
         };
-        // SCALED: adds the item's K blocks, each times its scales, to s.  A chunk is one block, 256 (a pair: 512) cycles of MMAs, so everything
-        // around the loads and sums counts: the barrier of the next block is asked for, and its factors are made, among the sums
+        // SCALED: adds the item's K blocks, each times its scales, to s.  A chunk is one block, 256 cycles of MMAs (a pair: 512), so
+        // everything around the loads and sums counts: the barrier of the next block is asked for, and its factors are made, among the sums
         // of this one; scales are loaded two blocks ahead; the arrival is predicated, not branched to.
         // Absent scales, and those of rows and columns past the edges, are a 1 that is not read.
         auto add_scaled = [&](float* s, int kb0, int kb1) -> bool {
@@ -1343,7 +1343,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             cur = nxt;
             more_items = next_item(nxt);
             if (more_items) prefetch_in();
-            if (!one_item()) break;  // (where tiles are shared out all eight warps leave together; else each when its own wait fails)
+            if (!one_item()) break;  // (all eight warps together where tiles are shared out, else each when its own wait fails)
         }
         if constexpr (MODE == kDgrad || MODE == kGluDgrad)  // after an abandoned launch: a load may still be on its way
             for (int b = 0; b < STG_BUFS; ++b)

@@ -22,7 +22,7 @@ LAYOUTS = {"NN": LAYOUT_NN, "TN": LAYOUT_TN}
 DTYPES = {"f16": DTYPE_F16, "bf16": DTYPE_BF16, "e4m3": DTYPE_E4M3, "e5m2": DTYPE_E5M2}
 KINDS = {"dense": 0, "block_scaled": 1, "sparse24": 2}  # gemm_kind_t
 TORCH_TO_DTYPE = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
-# 8-bit operand types (gemm_run_ex only).
+# With the 8-bit operand types (gemm_run_ex, gemm_run_mx and the forward linear-layer calls).
 TORCH_TO_DTYPE_EX = {**TORCH_TO_DTYPE, torch.float8_e4m3fn: DTYPE_E4M3, torch.float8_e5m2: DTYPE_E5M2}
 # Biases, bias gradients and weight gradients (the linear-layer entry points).
 TORCH_TO_DTYPE_F32 = {**TORCH_TO_DTYPE, torch.float32: DTYPE_F32}
